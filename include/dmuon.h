@@ -434,6 +434,191 @@ dmuon_status dmuon_adamw_flat(void* param, const void* grad, float* exp_avg, flo
                               int32_t param_dtype, int32_t grad_dtype, float lr, float beta1, float beta2,
                               float eps, float weight_decay, int32_t step, void* stream);
 
+/*
+ * ---- The language-model head: losses with their gradients, without the logits
+ *
+ * The parameters the Muon predicate leaves out include the head ("DMuon"
+ * project docs, section "DMuon 能做什么": everything else goes to AdamW), and
+ * every gradient a step consumes starts at the head's loss. These calls take
+ * the head's input and weight and return the loss of each token and the
+ * gradients of both, working through the vocabulary in pieces: the
+ * tokens x vocab matrix of logits never exists.
+ *
+ *   hidden   H, tokens x dim, bf16 (row pitch ld_hidden elements)
+ *   weight   W, vocab x dim, bf16 (row pitch ld_weight elements)
+ *   z[t][v] = sum_d H[t][d] * W[v][d], fp32 accumulation, kept in fp32
+ *
+ * A dmuon_head_t is made once per (max_tokens, vocab, dim, max_top) and bound to
+ * a caller-owned workspace, like a plan; one call uses the workspace at a time
+ * (calls on several streams must be ordered by the caller), and nothing in it
+ * is kept from one call for the next except the status word.
+ *
+ * H, W and their gradients start on 16 bytes, and their row pitches are
+ * multiples of 8 elements and at least dim.
+ */
+typedef struct dmuon_head_s* dmuon_head_t;
+
+/*
+ * dmuon_head_create - host only. 1 <= max_tokens <= 2^20, 1 <= vocab <= 2^22,
+ * 1 <= dim <= 2^16; max_top (0..256) is the longest teacher list a
+ * distillation call may pass (0: none).
+ */
+dmuon_status dmuon_head_create(int64_t max_tokens, int64_t vocab, int64_t dim, int32_t max_top, dmuon_head_t* out);
+
+/* Bytes of device workspace the head needs (host only). */
+dmuon_status dmuon_head_workspace_bytes(dmuon_head_t head, size_t* bytes);
+
+/*
+ * dmuon_head_bind - attach a caller-owned device workspace (1024-byte aligned,
+ * its contents need not be initialised) and clear the status word in it,
+ * asynchronously on stream. Errors as dmuon_plan_bind.
+ */
+dmuon_status dmuon_head_bind(dmuon_head_t head, void* d_workspace, size_t bytes, void* stream);
+
+/*
+ * dmuon_head_xent - softmax cross entropy of each token against its target:
+ *
+ *   lse[t]  = log sum_v exp(z[t][v])
+ *   loss[t] = lse[t] - z[t][targets[t]]
+ *
+ *  targets   device, tokens int64. A target outside 0..vocab-1 (-100, say)
+ *            marks a token that does not count: its loss is 0.
+ *  tokens    0..max_tokens; 0 is a no-op.
+ *  loss, lse device, tokens floats each.
+ *
+ * The target's share of the sum is kept apart from the others', so that the
+ * loss of a token predicted with near certainty keeps its leading digits.
+ * Asynchronous on stream, no allocation, deterministic.
+ */
+dmuon_status dmuon_head_xent(dmuon_head_t head, const void* hidden, int64_t ld_hidden, const void* weight,
+                             int64_t ld_weight, const int64_t* targets, int64_t tokens, float* loss, float* lse,
+                             void* stream);
+
+/*
+ * dmuon_head_xent_backward - gradients of sum_t grad_loss[t] * loss[t]:
+ *
+ *   dz[t][v] = grad_loss[t] * (exp(z[t][v] - lse[t]) - [v == targets[t]])   (0 for a token that does not count)
+ *   dH = dz W,  dW = dz^T H
+ *
+ *  lse        device, tokens floats, as dmuon_head_xent wrote them.
+ *  grad_loss  device, tokens floats (1/n for a mean over n tokens).
+ *  dhidden    device, tokens x dim bf16, pitch ld_dhidden, or NULL: not wanted.
+ *  dweight    device, vocab x dim bf16, pitch ld_dweight, or NULL: not wanted
+ *             (a frozen head). Overwritten, also when tokens is 0.
+ *
+ * z is formed again, piece by piece, and dz is rounded to bf16 once, as the
+ * operand of two tensor-core products that accumulate in fp32 over the whole
+ * vocabulary (dH) and all tokens (dW).
+ */
+dmuon_status dmuon_head_xent_backward(dmuon_head_t head, const void* hidden, int64_t ld_hidden, const void* weight,
+                                      int64_t ld_weight, const int64_t* targets, int64_t tokens, const float* lse,
+                                      const float* grad_loss, void* dhidden, int64_t ld_dhidden, void* dweight,
+                                      int64_t ld_dweight, void* stream);
+
+/*
+ * dmuon_head_distill - distillation from a teacher's top logits: the divergence
+ * of the student's distribution over the whole vocabulary from the teacher's
+ * over its list, both at a temperature:
+ *
+ *   q[t] = softmax(top_logits[t] / temperature) over the list's entries
+ *   p[t] = softmax(z[t] / temperature) over the vocabulary
+ *   lse[t]  = log sum_v exp(z[t][v] / temperature)
+ *   loss[t] = temperature^2 * sum_k q[t][k] * (log q[t][k] - log p[t][top_ids[t][k]])
+ *
+ *  top_ids     device, tokens x top int64, contiguous, any order. An entry
+ *              whose id is outside 0..vocab-1 or whose logit is -infinity is
+ *              not in the list; a row without entries has loss 0. The ids of a
+ *              row should differ; entries that share one add up.
+ *  top_logits  device, tokens x top fp32, contiguous.
+ *  top         1..max_top.
+ *  temperature > 0, finite.
+ */
+dmuon_status dmuon_head_distill(dmuon_head_t head, const void* hidden, int64_t ld_hidden, const void* weight,
+                                int64_t ld_weight, const int64_t* top_ids, const float* top_logits, int32_t top,
+                                float temperature, int64_t tokens, float* loss, float* lse, void* stream);
+
+/*
+ * dmuon_head_distill_backward - gradients of sum_t grad_loss[t] * loss[t]:
+ *
+ *   dz[t][v] = grad_loss[t] * temperature * (p[t][v] - q[t][v])   (0 for a row without entries)
+ *
+ * lse as dmuon_head_distill wrote it; the rest as dmuon_head_xent_backward.
+ */
+dmuon_status dmuon_head_distill_backward(dmuon_head_t head, const void* hidden, int64_t ld_hidden, const void* weight,
+                                         int64_t ld_weight, const int64_t* top_ids, const float* top_logits,
+                                         int32_t top, float temperature, int64_t tokens, const float* lse,
+                                         const float* grad_loss, void* dhidden, int64_t ld_dhidden, void* dweight,
+                                         int64_t ld_dweight, void* stream);
+
+/* As dmuon_read_device_status, for the head's status word (DMUON_DEV_WAIT_TIMEOUT). */
+dmuon_status dmuon_head_read_device_status(dmuon_head_t head, void* stream, uint32_t* bits);
+
+/* Free the host-side head (the workspace stays the caller's). NULL is a no-op. */
+void dmuon_head_destroy(dmuon_head_t head);
+
+/*
+ * ---- Tokens to experts and back
+ *
+ * What a mixture-of-experts layer does around its experts' products, whose
+ * matrices are the largest sets Muon owns ("DMuon" project docs, section
+ * "DMuon 能做什么": one owner per expert projection). Assignment i = t*top + k
+ * sends token t to expert expert_ids[i]; an id outside 0..experts-1 marks an
+ * assignment that is dropped. Rows are ordered by expert and, within one, by
+ * assignment.
+ *
+ *   offsets[e]  rows offsets[e] .. offsets[e+1]-1 belong to expert e
+ *   dest[i]     the row of assignment i, -1 when dropped
+ *   source[r]   the assignment of row r, -1 past the last row in use
+ *
+ * Asynchronous on stream, no allocation, deterministic (no atomics whose order
+ * could show).
+ */
+
+/* Bytes of scratch dmuon_route_sort needs for up to these sizes (host only):
+ * 0 <= tokens, 1 <= top <= 64, tokens*top <= 2^30, 1 <= experts <= 4096. */
+dmuon_status dmuon_route_workspace_bytes(int64_t tokens, int32_t top, int32_t experts, size_t* bytes);
+
+/*
+ * dmuon_route_sort - order the assignments by expert.
+ *  expert_ids  device, tokens x top int64, contiguous.
+ *  dest, source  device, tokens*top int32 each;  offsets  device, experts+1 int32.
+ *  d_workspace   device scratch, 256-byte aligned, free again when the call's work is done.
+ */
+dmuon_status dmuon_route_sort(const int64_t* expert_ids, int64_t tokens, int32_t top, int32_t experts, int32_t* dest,
+                              int32_t* source, int32_t* offsets, void* d_workspace, size_t bytes, void* stream);
+
+/*
+ * dmuon_route_dispatch - the experts' input: xs[r] = x[source[r] / top], zeros
+ * for rows not in use.
+ *  x   device, tokens x dim of dtype (DMUON_F32/DMUON_BF16), row pitch ld_x.
+ *  xs  device, tokens*top x dim, contiguous.
+ * Any dim >= 1; rows that start on 16 bytes and are whole 16-byte pieces move
+ * 16 bytes at a time, others element by element.
+ */
+dmuon_status dmuon_route_dispatch(const void* x, int64_t ld_x, const int32_t* dest, const int32_t* source, int64_t tokens,
+                                  int32_t top, int64_t dim, int32_t dtype, void* xs, void* stream);
+
+/*
+ * dmuon_route_combine - the layer's output: y[t] = sum_k weights[t][k] * ys[dest[t][k]],
+ * fp32 sums in the order of k, rounded once. Dropped assignments add nothing.
+ *  weights  device, tokens x top fp32, or NULL: all 1. With NULL it is also the
+ *           gradient of dmuon_route_dispatch (ys = the gradient of xs).
+ *  y        device, tokens x dim, row pitch ld_y.
+ */
+dmuon_status dmuon_route_combine(const void* ys, const float* weights, const int32_t* dest, int64_t tokens, int32_t top,
+                                 int64_t dim, int32_t dtype, void* y, int64_t ld_y, void* stream);
+
+/*
+ * dmuon_route_combine_backward - gradients of dmuon_route_combine:
+ *   dys[dest[t][k]] = weights[t][k] * dy[t]   (zeros for rows not in use)
+ *   dweights[t][k]  = sum_d dy[t][d] * ys[dest[t][k]][d]   (0 when dropped)
+ *  dy        device, tokens x dim, row pitch ld_dy.
+ *  dys       device, tokens*top x dim, contiguous;  dweights  device, tokens x top fp32.
+ */
+dmuon_status dmuon_route_combine_backward(const void* dy, int64_t ld_dy, const void* ys, const float* weights,
+                                          const int32_t* dest, const int32_t* source, int64_t tokens, int32_t top,
+                                          int64_t dim, int32_t dtype, void* dys, float* dweights, void* stream);
+
 /* Free the host-side plan (the workspace stays the caller's). NULL is a no-op. */
 void dmuon_plan_destroy(dmuon_plan_t plan);
 

@@ -1,0 +1,105 @@
+// head.h - structures shared by the host side of the head's losses (head.cu) and their kernels.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "dmuon.h"
+
+namespace dmuon {
+namespace head {
+
+using bf16 = __nv_bfloat16;
+
+// The forward pass reduces each token's logits over groups of 128 vocabulary entries.
+constexpr int kGroup = 128;
+constexpr int kMaxTop = 256;
+
+// What the loss wants of a token's logits. Cross entropy: one entry, targets[t]. Distillation: a
+// list per token, sorted by id and padded with ids >= vocab, and its probabilities.
+struct Wanted {
+  const int64_t* targets;  // cross entropy (then ids, q, count are nullptr)
+  const int32_t* ids;      // [tokens][top], ascending
+  const float* q;          // [tokens][top]
+  const int32_t* count;    // [tokens]: entries in the list
+  int32_t top;             // row pitch of ids, q and picked
+  int32_t vocab;
+};
+
+// One group's share of a token's softmax sum: sum of exp(z - peak), over the entries that are not wanted.
+struct alignas(8) Part {
+  float peak;
+  float sum;
+};
+
+struct LogitParams {
+  const bf16* hidden;
+  const bf16* weight;
+  int64_t ld_hidden, ld_weight;
+  int64_t tokens;
+  int32_t vocab, dim;
+  float scale;             // 1 / temperature
+  Wanted want;
+  // forward
+  Part* parts;             // [groups][tokens]
+  float* picked;           // [tokens][want.top]: scaled logits of the wanted entries
+  // backward: entries v0 .. v0 + width - 1
+  int32_t v0, width;
+  const float* lse;
+  const float* grad;
+  bf16* dz;                // [tokens][ld_dz]
+  int64_t ld_dz;
+};
+
+struct GradParams {
+  const bf16* hidden;
+  const bf16* weight;
+  int64_t ld_hidden, ld_weight;
+  int64_t tokens;
+  int32_t dim;
+  int32_t v0, width;
+  const bf16* dz;
+  int64_t ld_dz;
+  int32_t first;           // this piece starts the sum in dh_acc
+  float* dh_acc;           // [tokens][dim] or nullptr
+  bf16* dweight;           // or nullptr
+  int64_t ld_dweight;
+};
+
+struct RowParams {
+  int64_t tokens;
+  int32_t vocab;
+  Wanted want;
+  const Part* parts;
+  int32_t groups;
+  const float* picked;
+  const float* entropy;    // [tokens]: sum_k q log q (distillation)
+  float temperature;
+  float* loss;
+  float* lse;
+};
+
+struct TeacherParams {
+  const int64_t* ids;
+  const float* logits;
+  int64_t tokens;
+  int32_t top, vocab;
+  float scale;
+  int32_t* out_ids;
+  float* out_q;
+  int32_t* out_count;
+  float* out_entropy;
+};
+
+cudaError_t launch_logits(const LogitParams& p, cudaStream_t s);
+cudaError_t launch_dz(const LogitParams& p, cudaStream_t s);
+cudaError_t launch_grads(const GradParams& p, cudaStream_t s);
+cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t s);
+cudaError_t launch_rows(const RowParams& p, cudaStream_t s);
+cudaError_t launch_round(const float* acc, int64_t tokens, int32_t dim, bf16* out, int64_t ld_out, cudaStream_t s);
+
+}  // namespace head
+}  // namespace dmuon

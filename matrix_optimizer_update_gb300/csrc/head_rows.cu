@@ -1,0 +1,198 @@
+// head_rows.cu - the per-token work of the head's losses beside the products:
+// the teacher's list sorted and turned into probabilities, and the groups'
+// partial sums joined into the loss.
+#include <algorithm>
+#include <cmath>
+
+#include "head.h"
+
+namespace dmuon {
+namespace head {
+namespace {
+
+constexpr float kNegInf = -INFINITY;
+
+// ------------------------------------------------------------------ teacher
+// One block per token, one thread per entry of a list padded to a power of two
+// (at most 256): a bitonic sort by id in shared memory, then the softmax over
+// the entries that count. Entries that do not count sort last, with id vocab.
+__global__ void teacher_kernel(const __grid_constant__ TeacherParams p) {
+  extern __shared__ unsigned char raw[];
+  const int n = blockDim.x;
+  int* id = reinterpret_cast<int*>(raw);
+  float* lg = reinterpret_cast<float*>(id + n);
+  __shared__ float red[8];
+  const int64_t t = blockIdx.x;
+  const int k = threadIdx.x;
+  int my = p.vocab;
+  float l = kNegInf;
+  if (k < p.top) {
+    const int64_t v = p.ids[t * p.top + k];
+    const float x = p.logits[t * p.top + k];
+    if (v >= 0 && v < p.vocab && x != kNegInf) {
+      my = static_cast<int>(v);
+      l = x;
+    }
+  }
+  id[k] = my;
+  lg[k] = l;
+  __syncthreads();
+  for (int size = 2; size <= n; size <<= 1) {
+    for (int d = size >> 1; d > 0; d >>= 1) {
+      const int o = k ^ d;
+      if (o > k) {
+        const bool up = (k & size) == 0;
+        const int a = id[k], b = id[o];
+        // entries of equal id keep an order of their own (by logit), so that the result does not
+        // depend on the order they came in
+        const bool swap = up ? (a > b || (a == b && lg[k] > lg[o])) : (a < b || (a == b && lg[k] < lg[o]));
+        if (swap) {
+          id[k] = b;
+          id[o] = a;
+          const float x = lg[k];
+          lg[k] = lg[o];
+          lg[o] = x;
+        }
+      }
+      __syncthreads();
+    }
+  }
+  const int lane = k & 31, warp = k >> 5, warps = (n + 31) >> 5;
+  auto reduce = [&](float v, bool max) {
+    for (int d = 16; d > 0; d >>= 1) {
+      const float o = __shfl_xor_sync(0xffffffffu, v, d);
+      v = max ? fmaxf(v, o) : v + o;
+    }
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = red[0];
+    for (int w = 1; w < warps; ++w) v = max ? fmaxf(v, red[w]) : v + red[w];
+    __syncthreads();
+    return v;
+  };
+  const bool on = id[k] < p.vocab;
+  l = lg[k];
+  // a NaN logit makes its whole row NaN through the sum
+  const float best = reduce(on ? l : kNegInf, true);
+  const float e = on ? expf((l - best) * p.scale) : 0.f;
+  const float sum = reduce(e, false);
+  const float q = on ? e / sum : 0.f;
+  const float ent = reduce(q > 0.f ? q * logf(q) : q, false);
+  const float count = reduce(on ? 1.f : 0.f, false);
+  if (k < p.top) {
+    p.out_ids[t * p.top + k] = id[k];
+    p.out_q[t * p.top + k] = q;
+  }
+  if (k == 0) {
+    p.out_count[t] = static_cast<int>(count);
+    p.out_entropy[t] = ent;
+  }
+}
+
+// ------------------------------------------------------------------ rows
+// One block per token. The sum over the vocabulary is kept in two shares, of
+// the wanted entries and of all others, so that a loss that is small beside
+// the logits is formed from their ratio (log1p) and not as a difference.
+constexpr int kRowThreads = 128;
+
+__device__ __forceinline__ void join(float& peak, float& sum, float peak2, float sum2) {
+  const float m = fmaxf(peak, peak2);
+  if (m == kNegInf) return;  // neither has anything
+  sum = sum * expf(peak - m) + sum2 * expf(peak2 - m);
+  peak = m;
+}
+
+__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ RowParams p) {
+  __shared__ float s_peak[kRowThreads / 32], s_sum[kRowThreads / 32];
+  const int64_t t = blockIdx.x;
+  float peak = kNegInf, sum = 0.f;
+  for (int g = threadIdx.x; g < p.groups; g += kRowThreads) {
+    const Part q = p.parts[int64_t(g) * p.tokens + t];
+    join(peak, sum, q.peak, q.sum);
+  }
+  for (int d = 16; d > 0; d >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, peak, d), s2 = __shfl_xor_sync(0xffffffffu, sum, d);
+    join(peak, sum, m2, s2);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    s_peak[threadIdx.x >> 5] = peak;
+    s_sum[threadIdx.x >> 5] = sum;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < kRowThreads / 32; ++w) join(peak, sum, s_peak[w], s_sum[w]);
+  // peak, sum: the others. Now the wanted entries.
+  float hit_peak = kNegInf, hit = 0.f, dot = 0.f;
+  const float* z = p.picked + t * p.want.top;
+  int n;
+  if (p.want.targets != nullptr) {
+    const int64_t y = p.want.targets[t];
+    n = y >= 0 && y < p.vocab;
+    if (n) {
+      hit_peak = z[0];
+      hit = 1.f;
+      dot = z[0];
+    }
+  } else {
+    n = p.want.count[t];
+    const int32_t* id = p.want.ids + t * p.want.top;
+    const float* q = p.want.q + t * p.want.top;
+    for (int k = 0; k < n; ++k) hit_peak = fmaxf(hit_peak, z[k]);
+    for (int k = 0; k < n; ++k) {
+      if (k == 0 || id[k] != id[k - 1]) hit += expf(z[k] - hit_peak);
+      dot = fmaf(q[k], z[k] - hit_peak, dot);
+    }
+  }
+  if (n == 0) {
+    p.lse[t] = peak + logf(sum);
+    p.loss[t] = 0.f;
+    return;
+  }
+  const float lse_hit = hit_peak + logf(hit);
+  const float ratio = sum * expf(peak - hit_peak) / hit;
+  float lse, rest;  // rest = lse - lse_hit
+  if (ratio < 1.f) {
+    rest = log1pf(ratio);
+    lse = lse_hit + rest;
+  } else {
+    lse = peak + logf(sum + hit * expf(hit_peak - peak));
+    rest = lse - lse_hit;
+  }
+  p.lse[t] = lse;
+  if (p.want.targets != nullptr) {
+    p.loss[t] = rest;
+  } else {
+    // sum_k q log q - q (z - hit_peak) + log(hit): the divergence within the list; rest: of the list's share
+    const float within = p.entropy[t] - dot + logf(hit);
+    p.loss[t] = (within + rest) * p.temperature * p.temperature;
+  }
+}
+
+__global__ void __launch_bounds__(256) round_kernel(const float* acc, int64_t n, int32_t dim, bf16* out, int64_t ld) {
+  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x)
+    out[i / dim * ld + i % dim] = __float2bfloat16_rn(acc[i]);
+}
+
+}  // namespace
+
+cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t s) {
+  int n = 32;
+  while (n < p.top) n <<= 1;
+  teacher_kernel<<<static_cast<unsigned>(p.tokens), n, 8 * n, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_rows(const RowParams& p, cudaStream_t s) {
+  rows_kernel<<<static_cast<unsigned>(p.tokens), kRowThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_round(const float* acc, int64_t tokens, int32_t dim, bf16* out, int64_t ld_out, cudaStream_t s) {
+  const int64_t n = tokens * dim;
+  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 8192));
+  round_kernel<<<blocks, 256, 0, s>>>(acc, n, dim, out, ld_out);
+  return cudaGetLastError();
+}
+
+}  // namespace head
+}  // namespace dmuon

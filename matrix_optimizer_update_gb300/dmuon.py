@@ -51,6 +51,11 @@ EXPORTS = (
     "dmuon_profile_begin", "dmuon_profile_end", "dmuon_profile_cta_times", "dmuon_read_cta_times",
     "dmuon_plan_costs", "dmuon_launch_count",
     "dmuon_selftest_wait_timeout", "dmuon_momentum_norm_noalloc", "dmuon_assign_owners", "dmuon_adamw_flat",
+    "dmuon_head_create", "dmuon_head_workspace_bytes", "dmuon_head_bind", "dmuon_head_xent",
+    "dmuon_head_xent_backward", "dmuon_head_distill", "dmuon_head_distill_backward",
+    "dmuon_head_read_device_status", "dmuon_head_destroy",
+    "dmuon_route_workspace_bytes", "dmuon_route_sort", "dmuon_route_dispatch", "dmuon_route_combine",
+    "dmuon_route_combine_backward",
     "dmuon_plan_destroy", "dmuon_last_error", "dmuon_version",
 )
 
@@ -105,6 +110,21 @@ def lib():
         "dmuon_assign_owners": (i32, [ctypes.POINTER(Shape), i32, i32, ctypes.POINTER(ctypes.c_double), i32,
                                       ctypes.POINTER(i32), ctypes.POINTER(ctypes.c_double)]),
         "dmuon_adamw_flat": (i32, [vp, vp, vp, vp, i64, i32, i32, f32, f32, f32, f32, f32, i32, vp]),
+        "dmuon_head_create": (i32, [i64, i64, i64, i32, ctypes.POINTER(vp)]),
+        "dmuon_head_workspace_bytes": (i32, [vp, ctypes.POINTER(sz)]),
+        "dmuon_head_bind": (i32, [vp, vp, sz, vp]),
+        "dmuon_head_xent": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, vp, vp]),
+        "dmuon_head_xent_backward": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp]),
+        "dmuon_head_distill": (i32, [vp, vp, i64, vp, i64, vp, vp, i32, f32, i64, vp, vp, vp]),
+        "dmuon_head_distill_backward": (i32, [vp, vp, i64, vp, i64, vp, vp, i32, f32, i64, vp, vp, vp, i64, vp, i64,
+                                              vp]),
+        "dmuon_head_read_device_status": (i32, [vp, vp, ctypes.POINTER(u32)]),
+        "dmuon_head_destroy": (None, [vp]),
+        "dmuon_route_workspace_bytes": (i32, [i64, i32, i32, ctypes.POINTER(sz)]),
+        "dmuon_route_sort": (i32, [vp, i64, i32, i32, vp, vp, vp, vp, sz, vp]),
+        "dmuon_route_dispatch": (i32, [vp, i64, vp, vp, i64, i32, i64, i32, vp, vp]),
+        "dmuon_route_combine": (i32, [vp, vp, vp, i64, i32, i64, i32, vp, i64, vp]),
+        "dmuon_route_combine_backward": (i32, [vp, i64, vp, vp, vp, vp, i64, i32, i64, i32, vp, vp, vp]),
         "dmuon_plan_destroy": (None, [vp]),
         "dmuon_last_error": (ctypes.c_char_p, []),
         "dmuon_version": (i32, []),
@@ -322,3 +342,288 @@ class Muon:
                        [t.data_ptr() for t in grads] if not isinstance(grads[0], int) else grads,
                        [t.data_ptr() for t in momenta] if not isinstance(momenta[0], int) else momenta,
                        lr, mu, nesterov, s.cuda_stream)
+
+
+# --------------------------------------------------------------------------
+# losses of the language-model head, and routing to experts
+# --------------------------------------------------------------------------
+
+def _want(ok: bool, msg: str):
+    if not ok:
+        raise DmuonError(ERR_INVALID_ARG, msg)
+
+
+def _rows(t, dim, dtype, name, rows=None):
+    """A CUDA matrix whose rows lie contiguous (any row pitch); returns that pitch."""
+    _want(t.is_cuda and t.dtype == dtype and t.dim() == 2 and t.shape[1] == dim and
+          (rows is None or t.shape[0] == rows) and (t.shape[1] <= 1 or t.stride(1) == 1),
+          f"{name} must be a CUDA {dtype} tensor of shape [{'rows' if rows is None else rows}, {dim}] "
+          "with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], -(-t.shape[1] // 8) * 8)
+
+
+def _flat(t, shape, dtype, name):
+    _want(t.is_cuda and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
+          f"{name} must be a contiguous CUDA {dtype} tensor of shape {list(shape)}")
+
+
+class _on:
+    """Run a call on ``stream``: what it allocates belongs to that stream, and what it is given stays
+    alive until the stream is done with it."""
+
+    def __init__(self, stream, *tensors):
+        import torch
+        here = torch.cuda.current_stream()
+        self.stream = here if stream is None else stream
+        self.other = None
+        if self.stream != here:
+            self.other = torch.cuda.stream(self.stream)
+            for t in tensors:
+                if t is not None and t.is_cuda:
+                    t.record_stream(self.stream)
+
+    def __enter__(self):
+        if self.other is not None:
+            self.other.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.other is not None:
+            self.other.__exit__(*exc)
+
+
+class Head:
+    """Losses of a language model's head with their gradients, without the logits.
+
+    One object per (max_tokens, vocab, dim, max_top), with its workspace from
+    torch; one call uses it at a time. ``hidden`` is [tokens, dim] and
+    ``weight`` [vocab, dim], both bf16 with rows that start on 16 bytes;
+    losses, log sums and their gradients are fp32 [tokens]. See
+    include/dmuon.h for the formulas.
+    """
+
+    def __init__(self, handle, max_tokens, vocab, dim, max_top):
+        self._h = handle
+        self.max_tokens, self.vocab, self.dim, self.max_top = max_tokens, vocab, dim, max_top
+        self.workspace = None
+
+    @classmethod
+    def create(cls, max_tokens, vocab, dim, *, max_top=0, device=None, stream=None):
+        import torch
+        h = ctypes.c_void_p()
+        _check(lib().dmuon_head_create(int(max_tokens), int(vocab), int(dim), int(max_top), ctypes.byref(h)))
+        self = cls(h, int(max_tokens), int(vocab), int(dim), int(max_top))
+        nbytes = self.workspace_bytes()
+        with _on(stream) as s:
+            ws = torch.empty(nbytes + 1024, dtype=torch.uint8, device=device or "cuda")
+            self.bind((ws.data_ptr() + 1023) // 1024 * 1024, nbytes, s)
+        self.workspace = ws
+        return self
+
+    def workspace_bytes(self) -> int:
+        n = ctypes.c_size_t()
+        _check(lib().dmuon_head_workspace_bytes(self._h, ctypes.byref(n)))
+        return n.value
+
+    def bind(self, d_workspace: int, nbytes: int, stream: int = 0):
+        _check(lib().dmuon_head_bind(self._h, ctypes.c_void_p(d_workspace), nbytes, ctypes.c_void_p(stream)))
+
+    def _inputs(self, hidden, weight):
+        import torch
+        lh = _rows(hidden, self.dim, torch.bfloat16, "hidden")
+        lw = _rows(weight, self.dim, torch.bfloat16, "weight", self.vocab)
+        return hidden.data_ptr(), lh, weight.data_ptr(), lw
+
+    def _teacher(self, top_ids, top_logits, tokens):
+        import torch
+        _want(top_ids.dim() == 2, "top_ids must be [tokens, top]")
+        _flat(top_ids, (tokens, top_ids.shape[1]), torch.int64, "top_ids")
+        _flat(top_logits, top_ids.shape, torch.float32, "top_logits")
+        return top_ids.data_ptr(), top_logits.data_ptr(), top_ids.shape[1]
+
+    def _grads(self, hidden, weight, dhidden, dweight):
+        """Gradient tensors (made where True, left out where False or None) with addresses and pitches."""
+        import torch
+        out = []
+        for want, like, name in ((dhidden, hidden, "dhidden"), (dweight, weight, "dweight")):
+            if want is True:
+                want = torch.empty(like.shape[0], -(-self.dim // 8) * 8, dtype=like.dtype,
+                                   device=like.device)[:, :self.dim]
+            elif want is False:
+                want = None
+            ld = 0 if want is None else _rows(want, self.dim, torch.bfloat16, name, like.shape[0])
+            out += [want, None if want is None else want.data_ptr(), ld]
+        return out
+
+    def xent(self, hidden, weight, targets, *, stream=None):
+        """(loss, lse) per token; targets int64, one outside the vocabulary does not count."""
+        import torch
+        n = hidden.shape[0]
+        _flat(targets, (n,), torch.int64, "targets")
+        args = self._inputs(hidden, weight)
+        with _on(stream, hidden, weight, targets, self.workspace) as s:
+            loss, lse = (torch.empty(n, dtype=torch.float32, device=hidden.device) for _ in range(2))
+            _check(lib().dmuon_head_xent(self._h, *args, targets.data_ptr(), n, loss.data_ptr(), lse.data_ptr(), s))
+        return loss, lse
+
+    def xent_backward(self, hidden, weight, targets, lse, grad_loss, *, dhidden=True, dweight=True, stream=None):
+        """(dhidden, dweight) of sum(grad_loss * loss). Either may be a tensor to write into, or False."""
+        import torch
+        n = hidden.shape[0]
+        _flat(targets, (n,), torch.int64, "targets")
+        _flat(lse, (n,), torch.float32, "lse")
+        _flat(grad_loss, (n,), torch.float32, "grad_loss")
+        args = self._inputs(hidden, weight)
+        with _on(stream, hidden, weight, targets, lse, grad_loss, self.workspace) as s:
+            dh, ph, lh, dw, pw, lw = self._grads(hidden, weight, dhidden, dweight)
+            _check(lib().dmuon_head_xent_backward(self._h, *args, targets.data_ptr(), n, lse.data_ptr(),
+                                                  grad_loss.data_ptr(), ph, lh, pw, lw, s))
+        return dh, dw
+
+    def distill(self, hidden, weight, top_ids, top_logits, temperature=1.0, *, stream=None):
+        """(loss, lse) per token against a teacher's top logits; ids int64 and logits fp32, both [tokens, top]."""
+        import torch
+        n = hidden.shape[0]
+        ids, lg, k = self._teacher(top_ids, top_logits, n)
+        args = self._inputs(hidden, weight)
+        with _on(stream, hidden, weight, top_ids, top_logits, self.workspace) as s:
+            loss, lse = (torch.empty(n, dtype=torch.float32, device=hidden.device) for _ in range(2))
+            _check(lib().dmuon_head_distill(self._h, *args, ids, lg, k, float(temperature), n, loss.data_ptr(),
+                                            lse.data_ptr(), s))
+        return loss, lse
+
+    def distill_backward(self, hidden, weight, top_ids, top_logits, temperature, lse, grad_loss, *, dhidden=True,
+                         dweight=True, stream=None):
+        """(dhidden, dweight) of sum(grad_loss * loss), as xent_backward."""
+        import torch
+        n = hidden.shape[0]
+        ids, lg, k = self._teacher(top_ids, top_logits, n)
+        _flat(lse, (n,), torch.float32, "lse")
+        _flat(grad_loss, (n,), torch.float32, "grad_loss")
+        args = self._inputs(hidden, weight)
+        with _on(stream, hidden, weight, top_ids, top_logits, lse, grad_loss, self.workspace) as s:
+            dh, ph, lh, dw, pw, lw = self._grads(hidden, weight, dhidden, dweight)
+            _check(lib().dmuon_head_distill_backward(self._h, *args, ids, lg, k, float(temperature), n,
+                                                     lse.data_ptr(), grad_loss.data_ptr(), ph, lh, pw, lw, s))
+        return dh, dw
+
+    def read_device_status(self, stream: int = 0) -> int:
+        b = ctypes.c_uint32()
+        _check(lib().dmuon_head_read_device_status(self._h, ctypes.c_void_p(stream), ctypes.byref(b)))
+        return b.value
+
+    def destroy(self):
+        if self._h is not None and self._h.value:
+            lib().dmuon_head_destroy(self._h)
+        self._h = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+@dataclass
+class Route:
+    """Rows of the assignments in expert order (see include/dmuon.h)."""
+
+    dest: object     # [tokens, top] int32: the assignment's row, -1 when dropped
+    source: object   # [tokens * top] int32: the row's assignment, -1 for rows not in use
+    offsets: object  # [experts + 1] int32: the experts' first rows
+
+
+class Router:
+    """Tokens to experts and back, for up to ``max_tokens`` tokens with ``top`` experts each.
+
+    Holds the sort's scratch (torch-allocated; one sort uses it at a time).
+    Rows are bf16 or fp32, weights fp32 [tokens, top].
+    """
+
+    def __init__(self, max_tokens, top, experts, workspace):
+        self.max_tokens, self.top, self.experts, self.workspace = max_tokens, top, experts, workspace
+
+    @classmethod
+    def create(cls, max_tokens, top, experts, *, device=None):
+        import torch
+        n = ctypes.c_size_t()
+        _check(lib().dmuon_route_workspace_bytes(int(max_tokens), int(top), int(experts), ctypes.byref(n)))
+        return cls(int(max_tokens), int(top), int(experts),
+                   torch.empty(n.value, dtype=torch.uint8, device=device or "cuda"))
+
+    def sort(self, expert_ids, *, stream=None) -> Route:
+        """Order the assignments by expert; expert_ids int64 [tokens, top], one outside 0..experts-1 is dropped."""
+        import torch
+        _want(expert_ids.dim() == 2 and expert_ids.shape[0] <= self.max_tokens,
+              f"expert_ids must be [tokens <= {self.max_tokens}, {self.top}]")
+        t = expert_ids.shape[0]
+        _flat(expert_ids, (t, self.top), torch.int64, "expert_ids")
+        with _on(stream, expert_ids, self.workspace) as s:
+            dev = expert_ids.device
+            dest = torch.empty(t, self.top, dtype=torch.int32, device=dev)
+            source = torch.empty(t * self.top, dtype=torch.int32, device=dev)
+            offsets = torch.empty(self.experts + 1, dtype=torch.int32, device=dev)
+            _check(lib().dmuon_route_sort(expert_ids.data_ptr(), t, self.top, self.experts, dest.data_ptr(),
+                                          source.data_ptr(), offsets.data_ptr(), self.workspace.data_ptr(),
+                                          self.workspace.numel(), s))
+        return Route(dest, source, offsets)
+
+    def _row_type(self, t, name):
+        import torch
+        kinds = {torch.bfloat16: BF16, torch.float32: F32}
+        _want(t.dtype in kinds and t.dim() == 2, f"{name} must be a bf16 or fp32 matrix")
+        return kinds[t.dtype]
+
+    def _route(self, route, tokens):
+        import torch
+        _flat(route.dest, (tokens, self.top), torch.int32, "route.dest")
+        _flat(route.source, (tokens * self.top,), torch.int32, "route.source")
+
+    def dispatch(self, x, route, *, stream=None):
+        """xs [tokens * top, dim]: x's rows in expert order, zeros in rows not in use."""
+        import torch
+        kind = self._row_type(x, "x")
+        t, dim = x.shape
+        ld = _rows(x, dim, x.dtype, "x")
+        self._route(route, t)
+        with _on(stream, x, route.dest, route.source) as s:
+            xs = torch.empty(t * self.top, dim, dtype=x.dtype, device=x.device)
+            _check(lib().dmuon_route_dispatch(x.data_ptr(), ld, route.dest.data_ptr(), route.source.data_ptr(), t,
+                                              self.top, dim, kind, xs.data_ptr(), s))
+        return xs
+
+    def combine(self, ys, weights, route, *, stream=None):
+        """y [tokens, dim]: the sum of each token's expert rows, times weights (fp32 [tokens, top], or None: 1)."""
+        import torch
+        kind = self._row_type(ys, "ys")
+        t, dim = route.dest.shape[0], ys.shape[1]
+        self._route(route, t)
+        _flat(ys, (t * self.top, dim), ys.dtype, "ys")
+        if weights is not None:
+            _flat(weights, (t, self.top), torch.float32, "weights")
+        with _on(stream, ys, weights, route.dest) as s:
+            y = torch.empty(t, dim, dtype=ys.dtype, device=ys.device)
+            _check(lib().dmuon_route_combine(ys.data_ptr(), None if weights is None else weights.data_ptr(),
+                                             route.dest.data_ptr(), t, self.top, dim, kind, y.data_ptr(), dim, s))
+        return y
+
+    def combine_backward(self, dy, ys, weights, route, *, stream=None):
+        """(dys, dweights) of combine."""
+        import torch
+        kind = self._row_type(ys, "ys")
+        t, dim = route.dest.shape[0], ys.shape[1]
+        self._route(route, t)
+        _flat(ys, (t * self.top, dim), ys.dtype, "ys")
+        _flat(weights, (t, self.top), torch.float32, "weights")
+        ld = _rows(dy, dim, ys.dtype, "dy", t)
+        with _on(stream, dy, ys, weights, route.dest, route.source) as s:
+            dys = torch.empty_like(ys)
+            dw = torch.empty_like(weights)
+            _check(lib().dmuon_route_combine_backward(dy.data_ptr(), ld, ys.data_ptr(), weights.data_ptr(),
+                                                      route.dest.data_ptr(), route.source.data_ptr(), t, self.top,
+                                                      dim, kind, dys.data_ptr(), dw.data_ptr(), s))
+        return dys, dw
+
+    def dispatch_backward(self, dxs, route, *, stream=None):
+        """dx [tokens, dim]: the gradient of dispatch, the sum of each token's rows of dxs."""
+        return self.combine(dxs, None, route, stream=stream)
