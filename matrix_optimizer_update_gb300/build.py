@@ -20,7 +20,7 @@ BUILD = os.path.join(PKG, "_build")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdmuon.so")
 SOURCES = ["api.cu", "momentum.cu", "tc_ns.cu", "tc_ns2.cu", "simt_ns.cu", "noalloc.cu", "owners.cpp", "adamw.cu",
-           "head.cu", "head_rows.cu", "head_simple.cu", "route.cu"]
+           "head.cu", "head_rows.cu", "head_mma.cu", "route.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

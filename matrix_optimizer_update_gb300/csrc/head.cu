@@ -21,6 +21,8 @@ constexpr size_t kAlign = 1024;
 // dz exists for one piece of the vocabulary at a time: as many entries as keep it within these bytes.
 constexpr int64_t kPieceBytes = int64_t(512) << 20;
 constexpr int64_t kPieceStep = 256;
+constexpr int64_t kMaxSlices = 152;
+constexpr int64_t kSliceBytes = 2 * kMaxSlices * 256 * 256 * 4;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -50,7 +52,12 @@ struct dmuon_head_s {
   size_t off_status = 0, off_parts = 0, off_picked = 0, off_ids = 0, off_q = 0, off_count = 0, off_entropy = 0,
          off_dz = 0, off_acc = 0, bytes = 0;
   char* ws = nullptr;
-  int device = -1;
+  int device = -1, pairs = 0;
+
+  head::Pipe pipe() const {
+    unsigned* words = reinterpret_cast<unsigned*>(ws + off_status);
+    return {words, words + 32, reinterpret_cast<float*>(words + 48), pairs};
+  }
 };
 
 namespace {
@@ -167,7 +174,7 @@ dmuon_status forward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, cons
   head::LogitParams p = logit_params(H, hidden, ld_hidden, weight, ld_weight, tokens, L, w);
   p.parts = reinterpret_cast<head::Part*>(H->ws + H->off_parts);
   p.picked = reinterpret_cast<float*>(H->ws + H->off_picked);
-  cudaError_t e = head::launch_logits(p, s);
+  cudaError_t e = head::launch_logits(p, H->pipe(), s);
   if (e != cudaSuccess) return cuda_refuse(e, "logits kernel");
   head::RowParams r{};
   r.tokens = tokens;
@@ -216,22 +223,31 @@ dmuon_status backward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, con
   g.ld_hidden = ld_hidden;
   g.ld_weight = ld_weight;
   g.tokens = tokens;
+  g.vocab = p.vocab;
   g.dim = p.dim;
   g.dz = p.dz;
   g.ld_dz = p.ld_dz;
-  g.dh_acc = dhidden != nullptr ? reinterpret_cast<float*>(H->ws + H->off_acc) : nullptr;
+  g.gscale = L.temperature;
+  g.slices = head::dh_slices(tokens, H->dim, std::min(H->piece, H->vocab), dweight != nullptr, H->pairs);
+  const bool direct = H->vocab <= H->piece && g.slices.count == 1;
+  if (dhidden != nullptr && direct) {
+    g.dhidden = static_cast<head::bf16*>(dhidden);
+    g.ld_dhidden = ld_dhidden;
+  } else if (dhidden != nullptr) {
+    g.dh_acc = reinterpret_cast<float*>(H->ws + H->off_acc);
+  }
   g.dweight = static_cast<head::bf16*>(dweight);
   g.ld_dweight = ld_dweight;
   for (int64_t v0 = 0; v0 < H->vocab; v0 += H->piece) {
     p.v0 = g.v0 = static_cast<int32_t>(v0);
     p.width = g.width = static_cast<int32_t>(std::min(H->piece, H->vocab - v0));
     g.first = v0 == 0;
-    if ((e = head::launch_dz(p, s)) != cudaSuccess) return cuda_refuse(e, "dz kernel");
-    if ((e = head::launch_grads(g, s)) != cudaSuccess) return cuda_refuse(e, "gradient kernel");
+    if ((e = head::launch_dz(p, H->pipe(), s)) != cudaSuccess) return cuda_refuse(e, "dz kernel");
+    if ((e = head::launch_grads(g, H->pipe(), s)) != cudaSuccess) return cuda_refuse(e, "gradient kernel");
   }
-  if (dhidden != nullptr &&
-      (e = head::launch_round(g.dh_acc, tokens, g.dim, static_cast<head::bf16*>(dhidden), ld_dhidden, s)) !=
-          cudaSuccess)
+  if (g.dh_acc != nullptr &&
+      (e = head::launch_round(g.dh_acc, g.slices.count, tokens, g.dim, g.gscale, H->pipe().gmax,
+                              static_cast<head::bf16*>(dhidden), ld_dhidden, s)) != cudaSuccess)
     return cuda_refuse(e, "rounding kernel");
   return ok();
 }
@@ -268,7 +284,9 @@ extern "C" dmuon_status dmuon_head_create(int64_t max_tokens, int64_t vocab, int
   H->off_count = take(max_top > 0 ? 4 * max_tokens : 0);
   H->off_entropy = take(max_top > 0 ? 4 * max_tokens : 0);
   H->off_dz = take(2 * max_tokens * H->piece);
-  H->off_acc = take(4 * max_tokens * dim);
+  // dH's sums: one set where tokens are many; up to 2 x 76 tiles of 256 x 256 where K is cut into slices
+  const int64_t row = 4 * head::acc_pitch(dim);
+  H->off_acc = take(std::max(row * max_tokens, std::min(row * max_tokens * kMaxSlices, kSliceBytes)));
   H->bytes = at;
   *out = H;
   return ok();
@@ -285,7 +303,7 @@ extern "C" dmuon_status dmuon_head_bind(dmuon_head_t H, void* d_workspace, size_
   H->ws = nullptr;
   if (d_workspace == nullptr || misaligned(d_workspace, kAlign) || bytes < H->bytes)
     return refuse(DMUON_ERR_WORKSPACE, "workspace is NULL, not 1024-byte aligned or smaller than %zu bytes", H->bytes);
-  int device = -1, major = 0, minor = 0;
+  int device = -1, major = 0, minor = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return cuda_refuse(e, "cudaGetDevice");
   cudaPointerAttributes pa;
@@ -295,7 +313,8 @@ extern "C" dmuon_status dmuon_head_bind(dmuon_head_t H, void* d_workspace, size_
     return refuse(DMUON_ERR_WORKSPACE, "workspace is not device memory of the current device %d", device);
   }
   if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device)) != cudaSuccess ||
-      (e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device)) != cudaSuccess)
+      (e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device)) != cudaSuccess ||
+      (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device)) != cudaSuccess)
     return cuda_refuse(e, "cudaDeviceGetAttribute");
   if (major != 10 || minor != 3)
     return refuse(DMUON_ERR_UNSUPPORTED, "the head's losses need an sm_103 GPU (found sm_%d%d)", major, minor);
@@ -304,6 +323,7 @@ extern "C" dmuon_status dmuon_head_bind(dmuon_head_t H, void* d_workspace, size_
     return cuda_refuse(e, "clearing the status word");
   H->ws = static_cast<char*>(d_workspace);
   H->device = device;
+  H->pairs = sms / 2;
   return ok();
 }
 

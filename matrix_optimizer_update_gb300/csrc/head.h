@@ -54,20 +54,40 @@ struct LogitParams {
   int64_t ld_dz;
 };
 
+// What the tensor-core launches share: words in the workspace, and the SM pairs they run on.
+struct Pipe {
+  unsigned* status;
+  unsigned* sched;         // two words, zero between launches
+  float* gmax;             // the largest |grad| of a backward call; dz is relative to it
+  int pairs;
+};
+
+// The cut of dH's K (a piece's entries) into slices of nk stages.
+struct Slices {
+  int32_t nk, count;
+};
+
 struct GradParams {
   const bf16* hidden;
   const bf16* weight;
   int64_t ld_hidden, ld_weight;
   int64_t tokens;
-  int32_t dim;
+  int32_t vocab, dim;
   int32_t v0, width;
   const bf16* dz;
   int64_t ld_dz;
-  int32_t first;           // this piece starts the sum in dh_acc
-  float* dh_acc;           // [tokens][dim] or nullptr
+  float gscale;            // gradients = gscale * gmax * (products of dz)
+  // dH: straight into dhidden (one piece, one slice), or into sums of fp32, or neither
+  bf16* dhidden;
+  int64_t ld_dhidden;
+  float* dh_acc;           // [slices.count][tokens][acc_pitch(dim)]
+  Slices slices;           // as the call's first (widest) piece has them
+  int32_t first;           // this piece starts the sums
   bf16* dweight;           // or nullptr
   int64_t ld_dweight;
 };
+
+inline int64_t acc_pitch(int64_t dim) { return (dim + 7) / 8 * 8; }
 
 struct RowParams {
   int64_t tokens;
@@ -94,12 +114,15 @@ struct TeacherParams {
   float* out_entropy;
 };
 
-cudaError_t launch_logits(const LogitParams& p, cudaStream_t s);
-cudaError_t launch_dz(const LogitParams& p, cudaStream_t s);
-cudaError_t launch_grads(const GradParams& p, cudaStream_t s);
+cudaError_t launch_logits(const LogitParams& p, const Pipe& pipe, cudaStream_t s);
+cudaError_t launch_dz(const LogitParams& p, const Pipe& pipe, cudaStream_t s);
+Slices dh_slices(int64_t tokens, int64_t dim, int64_t width, bool dweight, int pairs);
+cudaError_t launch_grads(const GradParams& p, const Pipe& pipe, cudaStream_t s);
 cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t s);
 cudaError_t launch_rows(const RowParams& p, cudaStream_t s);
-cudaError_t launch_round(const float* acc, int64_t tokens, int32_t dim, bf16* out, int64_t ld_out, cudaStream_t s);
+// out = bf16(gscale * *gmax * the sum of the slices of acc)
+cudaError_t launch_round(const float* acc, int slices, int64_t tokens, int32_t dim, float gscale, const float* gmax,
+                         bf16* out, int64_t ld_out, cudaStream_t s);
 
 }  // namespace head
 }  // namespace dmuon

@@ -1,0 +1,779 @@
+// head_mma.cu - the products of the head's losses on the tensor cores:
+// 256 x 256 output tiles on pairs of SMs (two-SM UMMA, tcgen05 cta_group::2),
+// operands staged by TMA, fp32 accumulators in TMEM.
+//
+// Three launches share the pipeline and differ in operands and epilogue:
+//  logits  z = H W^T, tile 256 tokens x 256 vocabulary entries. The epilogue
+//          keeps, per token and 128 entries, the largest logit and the sum of
+//          exponentials below it, and takes out the logits the loss asks for:
+//          z itself is never stored.
+//  dz      the same product for one piece of the vocabulary; the epilogue turns
+//          it into the loss's gradient with respect to z, in bf16.
+//  grads   both gradients of a piece: dH += dz W (K = the piece's entries) and
+//          dW = dz^T H (K = the tokens), one list of tiles.
+// Every one is bound by the tensor cores once tokens are many (256 x 256 x K on
+// a pair: 32 KB of operands per SM for 4.2 MFLOP).
+//
+// Roles in a CTA: warp 0 loads (and, in the leader, claims tiles from a counter
+// and hands them to its peer), warp 1 issues the MMAs (leader only), warps 2 to
+// 9 drain the accumulators, of which there are two, so that one tile's epilogue
+// runs under the next tile's products. All waits are bounded (ptx.cuh).
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include <cudaTypedefs.h>
+
+#include "head.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace dmuon {
+namespace head {
+namespace {
+
+constexpr int kTile = 256;                     // rows and columns of a pair's tile
+constexpr int kStep = 64;                      // K per stage
+constexpr uint32_t kHalf = 128 * kStep * 2;    // a CTA's 128 rows (or columns) of an operand, one stage
+constexpr int kStages = 6;
+constexpr int kThreads = 320;
+constexpr int kEpiWarps = 8;
+constexpr int kBox = 32 * 64;                  // staging box of a TMA store: 32 rows of 64 bytes
+constexpr int kRing = 8;
+constexpr uint32_t kRingReaders = 2 + 2 * kEpiWarps;
+constexpr uint32_t kTmemCols = 2 * kTile;
+constexpr int64_t kWaitNs = 2000000000LL;
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum Mode { kLogits, kDz, kGrads };
+
+struct Params {
+  CUtensorMap a[2], b[2];  // [1]: the second kind of tile of a grads launch (dW)
+  CUtensorMap out[2];      // dz; dH (bf16) or its fp32 sums; dW
+  // tiles
+  int32_t items;
+  int32_t rows, cols;      // logits, dz: tiles along the tokens and the vocabulary
+  int32_t nk;              // K stages per tile
+  // grads: dH tiles come first (the longer ones), `slices` parts of K each, then dW tiles
+  int32_t dh_items, dh_rows, dh_nk, slices, slice_nk;
+  int32_t dim_tiles;
+  int32_t chunked;         // dim is a multiple of 64: one copy brings two 64-column blocks
+  int32_t dh_direct;       // dH is complete: store bf16; else add into fp32 sums
+  int32_t first;           // ... of which this is the first piece (store, not add)
+  float gscale;            // factor of the gradients beside *gmax
+  float* gmax;             // largest |grad|: dz holds gradients relative to it
+  LogitParams l;
+  unsigned* sched;         // [0] tiles claimed, [1] CTAs done; both zero between launches
+  unsigned* status;
+};
+
+struct Shared {
+  uint64_t full[kStages];
+  uint64_t empty[kStages];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t mma_done;
+  uint64_t ring_full[kRing];
+  uint64_t ring_empty[kRing];
+  int ring[kRing];
+  uint32_t tmem;
+  int abort_flag;
+  float red[kEpiWarps];
+};
+static_assert(sizeof(Shared) <= 1024, "barriers must fit their 1 KB");
+
+// Instruction descriptor as ptx::idesc_bf16, with A MN-major too (bit 15).
+__host__ __device__ constexpr uint32_t idesc(bool a_mn, bool b_mn) {
+  return ptx::idesc_bf16(kTile, kTile, b_mn) | (a_mn ? (1u << 15) : 0u);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Keeps results below 2^-126: gradients of entries far down the tail, which sums may still be made of.
+__device__ __forceinline__ float ex2_full(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(ptx::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+
+// Adds a staged fp32 box to global memory, element by element.
+__device__ __forceinline__ void tma_add_3d(const void* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(ptx::smem_u32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
+// Staging boxes have 64-byte rows; piece c of row r sits at piece c ^ ((r >> 1) & 3) (64-byte swizzle).
+__device__ __forceinline__ uint4* piece(uint8_t* box, int r, int c) {
+  return reinterpret_cast<uint4*>(box + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+struct Where {
+  int kind;        // grads: 0 = dH, 1 = dW
+  int row, col;    // tile coordinates
+  int slice;
+  int k0, nk;      // K stages
+};
+
+// Tiles of logits and dz: bands of 8 token blocks, the vocabulary within a band, so that the 76 pairs at
+// work share the band's H (8 x 256 rows) and about ten blocks of W.
+constexpr int kBand = 8;
+
+template <int MODE>
+__device__ __forceinline__ Where where_is(const Params& p, int w) {
+  Where x;
+  x.kind = 0;
+  x.slice = 0;
+  x.k0 = 0;
+  if (MODE != kGrads) {
+    const int band = w / (kBand * p.cols);
+    const int r = w - band * kBand * p.cols;
+    const int high = min(kBand, p.rows - band * kBand);
+    x.col = r / high;
+    x.row = band * kBand + r - x.col * high;
+    x.nk = p.nk;
+  } else if (w < p.dh_items) {
+    const int per = p.dh_rows * p.dim_tiles;
+    x.slice = w / per;
+    const int r = w - x.slice * per;
+    x.row = r / p.dim_tiles;
+    x.col = r - x.row * p.dim_tiles;
+    x.k0 = x.slice * p.slice_nk;
+    x.nk = min(p.slice_nk, p.dh_nk - x.k0);
+  } else {
+    const int r = w - p.dh_items;
+    x.kind = 1;
+    x.row = r / p.dim_tiles;
+    x.col = r - x.row * p.dim_tiles;
+    x.nk = p.nk;
+  }
+  return x;
+}
+
+// ------------------------------------------------------------------ what the loss wants of a row
+// The wanted entries of one token inside its 128 columns, in ascending order: next() is the id of the
+// next one, or INT_MAX.
+struct Cursor {
+  const int32_t* ids;
+  const float* q;
+  int pos, n, id;
+  __device__ __forceinline__ void start(const Wanted& w, int64_t t, bool in, int first) {
+    pos = n = 0;
+    id = INT_MAX;
+    if (!in) return;
+    if (w.targets != nullptr) {
+      const int64_t y = w.targets[t];
+      if (y >= first && y < w.vocab) id = static_cast<int>(y);
+      return;
+    }
+    ids = w.ids + t * w.top;
+    q = w.q + t * w.top;
+    n = w.count[t];
+    int lo = 0, hi = n;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (ids[mid] < first) lo = mid + 1;
+      else hi = mid;
+    }
+    pos = lo;
+    if (pos < n) id = ids[pos];
+  }
+  __device__ __forceinline__ float share(const Wanted& w) const { return w.targets != nullptr ? 1.f : q[pos]; }
+  __device__ __forceinline__ void next(const Wanted& w) {
+    ++pos;
+    id = w.targets == nullptr && pos < n ? ids[pos] : INT_MAX;
+  }
+};
+
+// One warp's part of a logits tile: 32 tokens, 128 entries from j0. `wait` returns false when the CTA gave up.
+template <class Wait>
+__device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, int j0, uint32_t tbase, Wait&& wait) {
+  const bool in = t < p.tokens;
+  Cursor c;
+  c.start(p.want, t, in, j0);
+  if (!wait()) return false;
+  ptx::tc_fence_after();
+  float peak = -INFINITY, sum = 0.f;
+  float last = 0.f;
+  int last_id = -1;
+#pragma unroll 1
+  for (int ch = 0; ch < 4; ++ch) {
+    const int jc = j0 + ch * 32;
+    if (jc >= p.vocab) break;
+    float v[32];
+    ptx::tmem_ld_32x32b_x32(tbase + ch * 32, v);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] *= p.scale;
+    if (jc + 32 > p.vocab) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (jc + k >= p.vocab) v[k] = -INFINITY;
+    }
+    while (__any_sync(0xffffffffu, c.id < jc + 32)) {
+      if (c.id < jc + 32) {
+        const int at = c.id - jc;
+        if (c.id != last_id) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (k == at) {
+              last = v[k];
+              v[k] = -INFINITY;
+            }
+          last_id = c.id;
+        }
+        p.picked[t * p.want.top + c.pos] = last;
+        c.next(p.want);
+      }
+    }
+    float top = v[0];
+#pragma unroll
+    for (int k = 1; k < 32; ++k) top = fmaxf(top, v[k]);
+    top = fmaxf(peak, top);
+    const float from = top == -INFINITY ? 0.f : top;  // nothing yet: every exponential is 0
+    float s[4] = {};
+#pragma unroll
+    for (int k = 0; k < 32; ++k) s[k & 3] += ex2((v[k] - from) * kLog2e);
+    sum = sum * ex2((peak - from) * kLog2e) + ((s[0] + s[1]) + (s[2] + s[3]));
+    peak = top;
+  }
+  if (in && j0 < p.vocab) p.parts[int64_t(j0 / kGroup) * p.tokens + t] = Part{peak, sum};
+  return true;
+}
+
+// One warp's part of a dz tile. Row t's gradient relative to the largest: g (p - wanted), rounded to bf16
+// as the operand of the gradients' products (the only rounding of dz).
+template <class Wait>
+__device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t, int64_t t0, int j0, uint32_t tbase,
+                                         int lane, uint8_t* stg, uint32_t& nbox, Wait&& wait) {
+  const LogitParams& p = P.l;
+  const bool in = t < p.tokens;
+  Cursor c;
+  c.start(p.want, t, in, j0);
+  float g = 0.f, lse = 0.f;
+  if (in) {
+    const bool counts = p.want.targets != nullptr ? p.want.targets[t] >= 0 && p.want.targets[t] < p.vocab
+                                                  : p.want.count[t] > 0;
+    lse = p.lse[t];
+    g = counts ? p.grad[t] / gmax : 0.f;
+  }
+  if (!wait()) return false;
+  ptx::tc_fence_after();
+#pragma unroll 1
+  for (int ch = 0; ch < 4; ++ch) {
+    const int jc = j0 + ch * 32;
+    float v[32];
+    ptx::tmem_ld_32x32b_x32(tbase + ch * 32, v);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      // a row that does not count, and entries past the vocabulary, give exact zeros whatever z is
+      const float e = g * ex2_full((v[k] * p.scale - lse) * kLog2e);
+      v[k] = g == 0.f || jc + k >= p.vocab ? 0.f : e;
+    }
+    while (__any_sync(0xffffffffu, c.id < jc + 32)) {
+      if (c.id < jc + 32) {
+        const int at = c.id - jc;
+        const float off = g * c.share(p.want);
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (k == at) v[k] -= off;
+        c.next(p.want);
+      }
+    }
+    uint8_t* box = stg + (nbox & 1u) * kBox;
+    if (lane == 0) ptx::bulk_wait_read<1>();  // the store that last read this box is done with it
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint4 u;
+      __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(v[q * 8 + 2 * e], v[q * 8 + 2 * e + 1]);
+      *piece(box, lane, q) = u;
+    }
+    ptx::fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      if (t0 < p.tokens) ptx::tma_store_2d(&P.out[0], box, jc - p.v0, static_cast<int>(t0));
+      ptx::bulk_commit();
+    }
+    ++nbox;
+  }
+  return true;
+}
+
+// One warp's part of a gradient tile: 32 rows from r0, 128 columns from d0.
+template <class Wait>
+__device__ __forceinline__ bool drain_grads(const Params& P, const Where& x, int64_t r0, int64_t r_lim, int d0,
+                                            uint32_t tbase, int lane, uint8_t* stg, uint32_t& nbox, Wait&& wait) {
+  const bool sums = x.kind == 0 && !P.dh_direct;
+  const float scale = sums ? 1.f : *P.gmax * P.gscale;
+  if (!wait()) return false;
+  ptx::tc_fence_after();
+#pragma unroll 1
+  for (int ch = 0; ch < 4; ++ch) {
+    const int dc = d0 + ch * 32;
+    float v[32];
+    ptx::tmem_ld_32x32b_x32(tbase + ch * 32, v);
+    const bool in = r0 < r_lim && dc < P.l.dim;
+    if (sums) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint8_t* box = stg + (nbox & 1u) * kBox;
+        if (lane == 0) ptx::bulk_wait_read<1>();
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int k = h * 16 + q * 4;
+          *reinterpret_cast<float4*>(piece(box, lane, q)) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+        }
+        ptx::fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          const int d = dc + h * 16;
+          if (in && d < P.l.dim) {
+            if (P.first) ptx::tma_store_3d(&P.out[0], box, d, static_cast<int>(r0), x.slice);
+            else tma_add_3d(&P.out[0], box, d, static_cast<int>(r0), x.slice);
+          }
+          ptx::bulk_commit();
+        }
+        ++nbox;
+      }
+    } else {
+      uint8_t* box = stg + (nbox & 1u) * kBox;
+      if (lane == 0) ptx::bulk_wait_read<1>();
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint4 u;
+        __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          h[e] = __floats2bfloat162_rn(v[q * 8 + 2 * e] * scale, v[q * 8 + 2 * e + 1] * scale);
+        *piece(box, lane, q) = u;
+      }
+      ptx::fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        if (in) ptx::tma_store_2d(&P.out[x.kind], box, dc, static_cast<int>(r0));
+        ptx::bulk_commit();
+      }
+      ++nbox;
+    }
+  }
+  return true;
+}
+
+// ------------------------------------------------------------------ the kernel
+__device__ __forceinline__ bool take(Shared* sh, uint32_t j, int& w, uint32_t lead_empty, volatile int* abortf,
+                                     const Params& p) {
+  const uint32_t slot = j % kRing;
+  if (!ptx::mbar_wait_cluster(&sh->ring_full[slot], (j / kRing) & 1u, abortf, p.status, kWaitNs)) return false;
+  w = *reinterpret_cast<volatile int*>(&sh->ring[slot]);
+  ptx::mbar_arrive_cluster(lead_empty + slot * static_cast<uint32_t>(sizeof(uint64_t)));
+  return true;
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = base;
+  uint8_t* sB = base + kStages * kHalf;
+  Shared* sh = reinterpret_cast<Shared*>(sB + kStages * kHalf);
+  uint8_t* boxes = sB + kStages * kHalf + 1024;
+  const int rank = static_cast<int>(ptx::cluster_ctarank());
+  const bool leader = rank == 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abortf = &sh->abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&sh->full[s], 1);
+      ptx::mbar_init(&sh->empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(&sh->tfull[a], 1);
+      ptx::mbar_init(&sh->tempty[a], 2 * kEpiWarps);
+    }
+    ptx::mbar_init(&sh->mma_done, 1);
+    for (int k = 0; k < kRing; ++k) {
+      ptx::mbar_init(&sh->ring_full[k], 1);
+      ptx::mbar_init(&sh->ring_empty[k], kRingReaders);
+    }
+    sh->abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(&sh->tmem, kTmemCols);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sh->tmem;
+  const uint32_t lead_empty = ptx::mapa_shared(ptx::smem_u32(&sh->ring_empty[0]), 0);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- loads
+      const uint32_t lead_full = ptx::mapa_shared(ptx::smem_u32(&sh->full[0]), 0);
+      uint32_t stage = 0, phase = 0, fills = 0;
+      auto load_tile = [&](int w) -> bool {
+        const Where x = where_is<MODE>(p, w);
+        const int row = x.row * kTile + rank * 128, col = x.col * kTile + rank * 128;
+        for (int kb = 0; kb < x.nk; ++kb) {
+          if (!ptx::mbar_wait_cluster(&sh->empty[stage], phase ^ 1u, abortf, p.status, kWaitNs)) return false;
+          if (leader) ptx::mbar_arrive_expect_tx(&sh->full[stage], 4 * kHalf);
+          const uint32_t fb = lead_full + stage * static_cast<uint32_t>(sizeof(uint64_t));
+          uint8_t *a = sA + stage * kHalf, *b = sB + stage * kHalf;
+          const int k = (x.k0 + kb) * kStep;
+          if (MODE != kGrads) {  // both K-major: 128 rows of 64
+            tma_load_2d_pair(a, &p.a[0], fb, k, row);
+            tma_load_2d_pair(b, &p.b[0], fb, k, (MODE == kDz ? p.l.v0 : 0) + col);
+          } else {
+            if (x.kind == 0) tma_load_2d_pair(a, &p.a[0], fb, k, row);           // dz, K-major
+            else ptx::tma_load_3d_pair(a, &p.a[1], fb, 0, k, row / 64);          // dz, two blocks of 64 columns
+            const CUtensorMap* mb = &p.b[x.kind];                                // W or H, MN-major
+            const int kr = k + (x.kind == 0 ? p.l.v0 : 0);
+            if (p.chunked) {
+              ptx::tma_load_3d_pair(b, mb, fb, 0, kr, col / 64);
+            } else {
+              tma_load_2d_pair(b, mb, fb, col, kr);
+              tma_load_2d_pair(b + kHalf / 2, mb, fb, col + 64, kr);
+            }
+          }
+          ++fills;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        return true;
+      };
+      if (leader) {
+        const uint32_t peer_ring = ptx::mapa_shared(ptx::smem_u32(&sh->ring[0]), 1);
+        const uint32_t peer_full = ptx::mapa_shared(ptx::smem_u32(&sh->ring_full[0]), 1);
+        auto claim = [&]() -> int {
+          const unsigned w = atomicAdd(p.sched, 1u);
+          return w < static_cast<unsigned>(p.items) ? static_cast<int>(w) : -1;
+        };
+        int w = claim();
+        for (uint32_t j = 0;; ++j) {
+          const uint32_t slot = j % kRing;
+          if (!ptx::mbar_wait_cluster(&sh->ring_empty[slot], ((j / kRing) & 1u) ^ 1u, abortf, p.status, kWaitNs)) break;
+          sh->ring[slot] = w;
+          ptx::st_shared_cluster_s32(peer_ring + slot * 4u, w);
+          ptx::mbar_arrive(&sh->ring_full[slot]);
+          ptx::mbar_arrive_cluster(peer_full + slot * static_cast<uint32_t>(sizeof(uint64_t)));
+          if (w < 0) break;
+          const int next = claim();  // its latency hides under this tile's loads
+          if (!load_tile(w)) break;
+          w = next;
+        }
+        // the leader's full barriers count both CTAs' bytes: nothing is in flight once they complete
+        for (uint32_t s = 0; s < kStages; ++s) {
+          if (fills > s) {
+            const uint32_t n = (fills - 1u - s) / kStages + 1u;
+            int zero = 0;
+            ptx::mbar_wait_cluster(&sh->full[s], (n - 1u) & 1u, &zero, p.status, kWaitNs);
+          }
+        }
+      } else {
+        for (uint32_t j = 0;; ++j) {
+          int w;
+          if (!take(sh, j, w, lead_empty, abortf, p) || w < 0) break;
+          if (!load_tile(w)) break;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ---------------------------------------------------------- products
+      uint32_t stage = 0, phase = 0, local = 0;
+      bool ok = true;
+      for (int w; ok && take(sh, local, w, lead_empty, abortf, p) && w >= 0; ++local) {
+        const Where x = where_is<MODE>(p, w);
+        const bool a_mn = MODE == kGrads && x.kind == 1;
+        constexpr bool b_mn = MODE == kGrads;
+        const uint32_t id = a_mn ? idesc(true, b_mn) : idesc(false, b_mn);
+        const uint32_t acc = local & 1u;
+        if (!ptx::mbar_wait_cluster(&sh->tempty[acc], ((local >> 1) & 1u) ^ 1u, abortf, p.status, kWaitNs)) break;
+        ptx::tc_fence_after();
+        const uint32_t d = tmem + acc * kTile;
+        for (int kb = 0; kb < x.nk; ++kb) {
+          if (!ptx::mbar_wait_cluster(&sh->full[stage], phase, abortf, p.status, kWaitNs)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t a0 = ptx::smem_u32(sA + stage * kHalf), b0 = ptx::smem_u32(sB + stage * kHalf);
+#pragma unroll
+          for (int kk = 0; kk < kStep / 16; ++kk) {
+            // K-major: 16 columns further in the swizzled rows; MN-major: 16 rows of 128 bytes further, the
+            // operand's second 64-element block kHalf / 2 on
+            const uint64_t ad = a_mn ? ptx::sw128_desc(a0 + kk * 2048, kHalf / 2, 1024)
+                                     : ptx::sw128_desc(a0 + kk * 32, 16, 1024);
+            const uint64_t bd = b_mn ? ptx::sw128_desc(b0 + kk * 2048, kHalf / 2, 1024)
+                                     : ptx::sw128_desc(b0 + kk * 32, 16, 1024);
+            ptx::umma_f16_pair(d, ad, bd, id, (kb | kk) != 0 ? 1u : 0u);
+          }
+          ptx::umma_commit_pair(&sh->empty[stage], 0x3);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        ptx::umma_commit_pair(&sh->tfull[acc], 0x3);
+      }
+      ptx::umma_commit_pair(&sh->mma_done, 0x1);
+      int zero = 0;
+      ptx::mbar_wait(&sh->mma_done, 0, &zero, p.status, kWaitNs);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t lead_tempty = ptx::mapa_shared(ptx::smem_u32(&sh->tempty[0]), 0);
+    uint8_t* stg = boxes + (warp - 2) * (2 * kBox);
+    float gmax = 1.f;
+    if (MODE == kDz) {  // under the first tile's products
+      float m = 0.f;
+      for (int64_t t = threadIdx.x - 64; t < p.l.tokens; t += kEpiWarps * 32) m = fmaxf(m, fabsf(p.l.grad[t]));
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      if (lane == 0) sh->red[warp - 2] = m;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      for (int k = 0; k < kEpiWarps; ++k) gmax = k == 0 ? sh->red[0] : fmaxf(gmax, sh->red[k]);
+      if (gmax == 0.f) gmax = 1.f;
+      if (blockIdx.x == 0 && threadIdx.x == 64) *p.gmax = gmax;
+    }
+    uint32_t nbox = 0;
+    for (uint32_t local = 0;; ++local) {
+      int w = -2;
+      if (lane == 0 && !take(sh, local, w, lead_empty, abortf, p)) w = -2;
+      w = __shfl_sync(0xffffffffu, w, 0);
+      if (w < 0) break;
+      const Where x = where_is<MODE>(p, w);
+      const uint32_t acc = local & 1u;
+      const int64_t r0 = int64_t(x.row) * kTile + rank * 128 + q * 32;
+      const int c0 = x.col * kTile + half * 128;
+      const uint32_t tbase = tmem + acc * kTile + half * 128 + (static_cast<uint32_t>(q * 32) << 16);
+      auto wait = [&]() {
+        return ptx::mbar_wait_cluster(&sh->tfull[acc], (local >> 1) & 1u, abortf, p.status, kWaitNs);
+      };
+      bool ok;
+      if (MODE == kLogits) {
+        ok = drain_logits(p.l, r0 + lane, c0, tbase, wait);
+      } else if (MODE == kDz) {
+        ok = drain_dz(p, gmax, r0 + lane, r0, p.l.v0 + c0, tbase, lane, stg, nbox, wait);
+      } else {
+        const int64_t row = r0 + (x.kind == 1 ? p.l.v0 : 0);
+        ok = drain_grads(p, x, row, x.kind == 1 ? p.l.vocab : p.l.tokens, c0, tbase, lane, stg, nbox, wait);
+      }
+      if (!ok) break;
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(lead_tempty + acc * static_cast<uint32_t>(sizeof(uint64_t)));
+    }
+    ptx::bulk_wait_all();
+  }
+
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    // every claim precedes its CTA's arrival here; the last CTA leaves both words zero for the next launch
+    __threadfence();
+    if (atomicAdd(p.sched + 1, 1u) == gridDim.x - 1) {
+      p.sched[0] = 0u;
+      p.sched[1] = 0u;
+    }
+  }
+  ptx::cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ host
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+cudaError_t encode(CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank, const cuuint64_t* dims,
+                   const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swz) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  const cuuint32_t one[3] = {1, 1, 1};
+  const CUresult r = fn(m, type, rank, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Row-major bf16 rows x cols in boxes of box_rows x box_cols. Reads past either edge give zeros.
+cudaError_t map_rows(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_cols,
+                     int box_rows, CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 2, dims, strides, box, swz);
+}
+
+// The same matrix as [block of 64 columns][row][64 columns], so that one box brings 64 rows of two blocks,
+// each a block of 128-byte rows as the MN-major operand wants them. cols must be a multiple of 64.
+cudaError_t map_blocks(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld) {
+  const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)cols / 64};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, 128};
+  const cuuint32_t box[3] = {64, 64, 2};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+cudaError_t map_operand_mn(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld) {
+  return cols % 64 == 0 ? map_blocks(m, base, cols, rows, ld) : map_rows(m, base, cols, rows, ld, 64, 64);
+}
+
+int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+template <int MODE>
+cudaError_t launch_pairs(const Params& p, int pairs, cudaStream_t s) {
+  const size_t smem = 1024 + kStages * 2 * kHalf + 1024 + kEpiWarps * 2 * kBox;
+  cudaError_t e = cudaFuncSetAttribute(head_pair_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * std::min(pairs, p.items));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, head_pair_kernel<MODE>, p);
+}
+
+cudaError_t logit_maps(Params& P, const LogitParams& p) {
+  cudaError_t e = map_rows(&P.a[0], p.hidden, p.dim, p.tokens, p.ld_hidden, kStep, 128);
+  if (e == cudaSuccess) e = map_rows(&P.b[0], p.weight, p.dim, p.vocab, p.ld_weight, kStep, 128);
+  return e;
+}
+
+Params logit_tiles(const LogitParams& p, const Pipe& pipe, int64_t entries) {
+  Params P;
+  std::memset(&P, 0, sizeof(P));
+  P.l = p;
+  P.rows = cdiv(p.tokens, kTile);
+  P.cols = cdiv(entries, kTile);
+  P.items = P.rows * P.cols;
+  P.nk = cdiv(p.dim, kStep);
+  P.sched = pipe.sched;
+  P.status = pipe.status;
+  P.gmax = pipe.gmax;
+  return P;
+}
+
+}  // namespace
+
+cudaError_t launch_logits(const LogitParams& p, const Pipe& pipe, cudaStream_t s) {
+  Params P = logit_tiles(p, pipe, p.vocab);
+  const cudaError_t e = logit_maps(P, p);
+  return e != cudaSuccess ? e : launch_pairs<kLogits>(P, pipe.pairs, s);
+}
+
+cudaError_t launch_dz(const LogitParams& p, const Pipe& pipe, cudaStream_t s) {
+  Params P = logit_tiles(p, pipe, p.width);
+  cudaError_t e = logit_maps(P, p);
+  if (e == cudaSuccess)
+    e = map_rows(&P.out[0], p.dz, p.ld_dz, p.tokens, p.ld_dz, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  return e != cudaSuccess ? e : launch_pairs<kDz>(P, pipe.pairs, s);
+}
+
+// K is cut where whole dH tiles would keep a few pairs busy after all others are done: until a slice's K
+// is no longer than the launch's work per pair. Each slice has sums of its own, joined by the rounding
+// kernel in a fixed order.
+Slices dh_slices(int64_t tokens, int64_t dim, int64_t width, bool dweight, int pairs) {
+  const int64_t tiles = int64_t(cdiv(tokens, kTile)) * cdiv(dim, kTile);
+  const int64_t nk = cdiv(width, kStep);
+  const int64_t dw = dweight ? int64_t(cdiv(width, kTile)) * cdiv(dim, kTile) * cdiv(tokens, kStep) : 0;
+  const int64_t fair = std::max<int64_t>(16, cdiv(tiles * nk + dw, pairs));
+  Slices x;
+  x.nk = static_cast<int32_t>(nk <= fair ? nk : cdiv(nk, cdiv(nk, fair)));
+  x.count = cdiv(nk, x.nk);
+  return x;
+}
+
+cudaError_t launch_grads(const GradParams& p, const Pipe& pipe, cudaStream_t s) {
+  Params P;
+  std::memset(&P, 0, sizeof(P));
+  P.l.tokens = p.tokens;
+  P.l.vocab = p.v0 + p.width;
+  P.l.dim = p.dim;
+  P.l.v0 = p.v0;
+  P.dim_tiles = cdiv(p.dim, kTile);
+  P.chunked = p.dim % 64 == 0;
+  P.gscale = p.gscale;
+  P.gmax = pipe.gmax;
+  P.sched = pipe.sched;
+  P.status = pipe.status;
+  cudaError_t e = cudaSuccess;
+  const int64_t acc_ld = acc_pitch(p.dim);
+  if (p.dhidden != nullptr || p.dh_acc != nullptr) {
+    P.dh_rows = cdiv(p.tokens, kTile);
+    P.dh_nk = cdiv(p.width, kStep);
+    P.slice_nk = p.slices.nk;
+    P.slices = cdiv(P.dh_nk, P.slice_nk);
+    P.dh_items = P.dh_rows * P.dim_tiles * P.slices;
+    P.dh_direct = p.dhidden != nullptr;
+    P.first = p.first;
+    e = map_rows(&P.a[0], p.dz, p.ld_dz, p.tokens, p.ld_dz, kStep, 128);
+    if (e == cudaSuccess) e = map_operand_mn(&P.b[0], p.weight, p.dim, p.vocab, p.ld_weight);
+    if (e == cudaSuccess && P.dh_direct) {
+      e = map_rows(&P.out[0], p.dhidden, p.dim, p.tokens, p.ld_dhidden, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    } else if (e == cudaSuccess) {
+      const cuuint64_t dims[3] = {(cuuint64_t)p.dim, (cuuint64_t)p.tokens, (cuuint64_t)p.slices.count};
+      const cuuint64_t strides[2] = {(cuuint64_t)acc_ld * 4, (cuuint64_t)acc_ld * 4 * p.tokens};
+      const cuuint32_t box[3] = {16, 32, 1};
+      e = encode(&P.out[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.dh_acc, 3, dims, strides, box,
+                 CU_TENSOR_MAP_SWIZZLE_64B);
+    }
+  }
+  if (e != cudaSuccess) return e;
+  P.items = P.dh_items;
+  if (p.dweight != nullptr) {
+    P.items += cdiv(p.width, kTile) * P.dim_tiles;
+    P.nk = cdiv(p.tokens, kStep);
+    e = map_blocks(&P.a[1], p.dz, p.ld_dz, p.tokens, p.ld_dz);
+    if (e == cudaSuccess) e = map_operand_mn(&P.b[1], p.hidden, p.dim, p.tokens, p.ld_hidden);
+    if (e == cudaSuccess)
+      e = map_rows(&P.out[1], p.dweight, p.dim, p.vocab, p.ld_dweight, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pairs<kGrads>(P, pipe.pairs, s);
+}
+
+}  // namespace head
+}  // namespace dmuon
