@@ -116,13 +116,20 @@ dmuon_status check_loss(dmuon_head_t H, const Loss& L, int64_t tokens, bool dist
   return DMUON_OK;
 }
 
-// What the kernels are told of the loss; for distillation the lists are sorted into the workspace first.
-dmuon_status prepare_wanted(dmuon_head_t H, const Loss& L, int64_t tokens, head::Wanted* w, cudaStream_t s) {
+// What the kernels are told of the loss; for distillation the lists are sorted into the workspace first. The
+// logits of the likeliest entries go to the picked ones (a forward cross entropy forms them in its last kernel).
+dmuon_status prepare_wanted(dmuon_head_t H, const Loss& L, int64_t tokens, const head::DotParams& dot, bool backward,
+                            head::Wanted* w, cudaStream_t s) {
   *w = head::Wanted{};
   w->vocab = static_cast<int32_t>(H->vocab);
+  float* picked = reinterpret_cast<float*>(H->ws + H->off_picked);
   if (L.targets != nullptr) {
     w->targets = L.targets;
     w->top = 1;
+    if (backward) {
+      const cudaError_t e = head::launch_targets(dot, L.targets, tokens, w->vocab, picked, s);
+      if (e != cudaSuccess) return cuda_refuse(e, "target kernel");
+    }
     return DMUON_OK;
   }
   head::TeacherParams p{};
@@ -136,6 +143,8 @@ dmuon_status prepare_wanted(dmuon_head_t H, const Loss& L, int64_t tokens, head:
   p.out_q = reinterpret_cast<float*>(H->ws + H->off_q);
   p.out_count = reinterpret_cast<int32_t*>(H->ws + H->off_count);
   p.out_entropy = reinterpret_cast<float*>(H->ws + H->off_entropy);
+  p.dot = dot;
+  p.picked = picked;
   cudaError_t e = head::launch_teacher(p, s);
   if (e != cudaSuccess) return cuda_refuse(e, "teacher kernel");
   w->ids = p.out_ids;
@@ -160,6 +169,12 @@ head::LogitParams logit_params(dmuon_head_t H, const void* hidden, int64_t ld_hi
   return p;
 }
 
+head::DotParams dot_params(dmuon_head_t H, const void* hidden, int64_t ld_hidden, const void* weight,
+                           int64_t ld_weight, const Loss& L) {
+  return {static_cast<const head::bf16*>(hidden), static_cast<const head::bf16*>(weight), ld_hidden, ld_weight,
+          static_cast<int32_t>(H->dim), 1.f / L.temperature};
+}
+
 dmuon_status forward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, const void* weight, int64_t ld_weight,
                      const Loss& L, bool distill, int64_t tokens, float* loss, float* lse, void* stream) {
   dmuon_status st = check_call(H, hidden, ld_hidden, weight, ld_weight, tokens);
@@ -170,7 +185,8 @@ dmuon_status forward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, cons
     return refuse(DMUON_ERR_INVALID_ARG, "loss or lse is NULL or not 4-byte aligned");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   head::Wanted w;
-  if ((st = prepare_wanted(H, L, tokens, &w, s)) != DMUON_OK) return st;
+  const head::DotParams dot = dot_params(H, hidden, ld_hidden, weight, ld_weight, L);
+  if ((st = prepare_wanted(H, L, tokens, dot, false, &w, s)) != DMUON_OK) return st;
   head::LogitParams p = logit_params(H, hidden, ld_hidden, weight, ld_weight, tokens, L, w);
   p.parts = reinterpret_cast<head::Part*>(H->ws + H->off_parts);
   p.picked = reinterpret_cast<float*>(H->ws + H->off_picked);
@@ -180,6 +196,7 @@ dmuon_status forward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, cons
   r.tokens = tokens;
   r.vocab = p.vocab;
   r.want = w;
+  r.dot = dot;
   r.parts = p.parts;
   r.groups = static_cast<int32_t>(cdiv(H->vocab, head::kGroup));
   r.picked = p.picked;
@@ -211,8 +228,11 @@ dmuon_status backward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, con
     return refuse(DMUON_ERR_INVALID_ARG, "lse or grad_loss is NULL or not 4-byte aligned");
   if (dhidden == nullptr && dweight == nullptr) return ok();
   head::Wanted w;
-  if ((st = prepare_wanted(H, L, tokens, &w, s)) != DMUON_OK) return st;
+  if ((st = prepare_wanted(H, L, tokens, dot_params(H, hidden, ld_hidden, weight, ld_weight, L), true, &w, s)) !=
+      DMUON_OK)
+    return st;
   head::LogitParams p = logit_params(H, hidden, ld_hidden, weight, ld_weight, tokens, L, w);
+  p.picked = reinterpret_cast<float*>(H->ws + H->off_picked);
   p.lse = lse;
   p.grad = grad_loss;
   p.dz = reinterpret_cast<head::bf16*>(H->ws + H->off_dz);

@@ -29,6 +29,14 @@ struct Wanted {
   int32_t vocab;
 };
 
+// Tensor cores truncate what they accumulate: a logit z of theirs is off by about 1.0e-9 * dim * z, always
+// towards zero (measured: -6.6e-5 at z = 16, dim = 4096, where fp32 FMAs are off by 8e-7). Sums over the
+// vocabulary average that out, but the loss of a token predicted with near certainty is 1 - p of its
+// target, and its relative error the absolute one of the target's logit. So the logits of wanted entries
+// with at least this probability (at most 8 per token, for cross entropy the target) are formed apart,
+// in fp32 FMAs, in both passes.
+constexpr float kSure = 0.125f;
+
 // One group's share of a token's softmax sum: sum of exp(z - peak), over the entries that are not wanted.
 struct alignas(8) Part {
   float peak;
@@ -45,7 +53,7 @@ struct LogitParams {
   Wanted want;
   // forward
   Part* parts;             // [groups][tokens]
-  float* picked;           // [tokens][want.top]: scaled logits of the wanted entries
+  float* picked;           // [tokens][want.top]: scaled logits of the wanted entries (below kSure: written here)
   // backward: entries v0 .. v0 + width - 1
   int32_t v0, width;
   const float* lse;
@@ -89,9 +97,19 @@ struct GradParams {
 
 inline int64_t acc_pitch(int64_t dim) { return (dim + 7) / 8 * 8; }
 
+// Logits formed in fp32 FMAs.
+struct DotParams {
+  const bf16* hidden;
+  const bf16* weight;
+  int64_t ld_hidden, ld_weight;
+  int32_t dim;
+  float scale;
+};
+
 struct RowParams {
   int64_t tokens;
   int32_t vocab;
+  DotParams dot;           // cross entropy: the target's logit
   Wanted want;
   const Part* parts;
   int32_t groups;
@@ -112,6 +130,8 @@ struct TeacherParams {
   float* out_q;
   int32_t* out_count;
   float* out_entropy;
+  DotParams dot;
+  float* picked;           // entries of at least kSure
 };
 
 cudaError_t launch_logits(const LogitParams& p, const Pipe& pipe, cudaStream_t s);
@@ -119,6 +139,9 @@ cudaError_t launch_dz(const LogitParams& p, const Pipe& pipe, cudaStream_t s);
 Slices dh_slices(int64_t tokens, int64_t dim, int64_t width, bool dweight, int pairs);
 cudaError_t launch_grads(const GradParams& p, const Pipe& pipe, cudaStream_t s);
 cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t s);
+// picked[t] = the logit of targets[t] (where it is in the vocabulary)
+cudaError_t launch_targets(const DotParams& d, const int64_t* targets, int64_t tokens, int32_t vocab, float* picked,
+                           cudaStream_t s);
 cudaError_t launch_rows(const RowParams& p, cudaStream_t s);
 // out = bf16(gscale * *gmax * the sum of the slices of acc)
 cudaError_t launch_round(const float* acc, int slices, int64_t tokens, int32_t dim, float gscale, const float* gmax,

@@ -234,7 +234,7 @@ __device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, in
             }
           last_id = c.id;
         }
-        p.picked[t * p.want.top + c.pos] = last;
+        if (c.share(p.want) < kSure) p.picked[t * p.want.top + c.pos] = last;
         c.next(p.want);
       }
     }
@@ -268,7 +268,9 @@ __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t,
                                                   : p.want.count[t] > 0;
     lse = p.lse[t];
     g = counts ? p.grad[t] / gmax : 0.f;
+    if (g == 0.f) c.id = INT_MAX;  // zeros, whatever z is
   }
+  int last_id = -1;
   if (!wait()) return false;
   ptx::tc_fence_after();
 #pragma unroll 1
@@ -285,10 +287,13 @@ __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t,
     while (__any_sync(0xffffffffu, c.id < jc + 32)) {
       if (c.id < jc + 32) {
         const int at = c.id - jc;
-        const float off = g * c.share(p.want);
+        const float share = c.share(p.want);
+        const bool sure = share >= kSure && c.id != last_id;
+        const float e = sure ? ex2_full((p.picked[t * p.want.top + c.pos] - lse) * kLog2e) : 0.f;
+        last_id = c.id;
 #pragma unroll
         for (int k = 0; k < 32; ++k)
-          if (k == at) v[k] -= off;
+          if (k == at) v[k] = sure ? g * (e - share) : v[k] - g * share;
         c.next(p.want);
       }
     }

@@ -12,6 +12,43 @@ namespace {
 
 constexpr float kNegInf = -INFINITY;
 
+// One thread's part (thread `at` of `of`) of the logit of (t, v): 8 elements at a time, the last few one by one.
+__device__ __forceinline__ float dot_part(const DotParams& d, int64_t t, int64_t v, int at, int of) {
+  const bf16* h = d.hidden + t * d.ld_hidden;
+  const bf16* w = d.weight + v * d.ld_weight;
+  const int whole = d.dim / 8;
+  float s = 0.f;
+  for (int c = at; c < whole; c += of) {
+    const uint4 a = *reinterpret_cast<const uint4*>(h + 8 * c), b = *reinterpret_cast<const uint4*>(w + 8 * c);
+    const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&a);
+    const __nv_bfloat162* y = reinterpret_cast<const __nv_bfloat162*>(&b);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = __bfloat1622float2(x[k]), g = __bfloat1622float2(y[k]);
+      s = fmaf(f.x, g.x, s);
+      s = fmaf(f.y, g.y, s);
+    }
+  }
+  for (int k = 8 * whole + at; k < d.dim; k += of) s = fmaf(__bfloat162float(h[k]), __bfloat162float(w[k]), s);
+  return s;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// One warp per token.
+__global__ void __launch_bounds__(256) targets_kernel(const __grid_constant__ DotParams d, const int64_t* targets,
+                                                      int64_t tokens, int32_t vocab, float* picked) {
+  const int64_t t = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (t >= tokens) return;
+  const int64_t y = targets[t];
+  if (y < 0 || y >= vocab) return;
+  const float z = warp_sum(dot_part(d, t, y, threadIdx.x & 31, 32)) * d.scale;
+  if ((threadIdx.x & 31) == 0) picked[t] = z;
+}
+
 // ------------------------------------------------------------------ teacher
 // One block per token, one thread per entry of a list padded to a power of two
 // (at most 256): a bitonic sort by id in shared memory, then the softmax over
@@ -87,6 +124,16 @@ __global__ void teacher_kernel(const __grid_constant__ TeacherParams p) {
     p.out_count[t] = static_cast<int>(count);
     p.out_entropy[t] = ent;
   }
+  // the logits of the likeliest entries, a warp for each
+  lg[k] = q;
+  __syncthreads();
+  int seen = 0;
+  for (int e = 0; e < static_cast<int>(count); ++e) {
+    if (!(lg[e] >= kSure)) continue;
+    if (seen++ % warps != warp) continue;
+    const float z = warp_sum(dot_part(p.dot, t, id[e], lane, 32)) * p.dot.scale;
+    if (lane == 0) p.picked[t * p.top + e] = z;
+  }
 }
 
 // ------------------------------------------------------------------ rows
@@ -103,7 +150,7 @@ __device__ __forceinline__ void join(float& peak, float& sum, float peak2, float
 }
 
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ RowParams p) {
-  __shared__ float s_peak[kRowThreads / 32], s_sum[kRowThreads / 32];
+  __shared__ float s_peak[kRowThreads / 32], s_sum[kRowThreads / 32], s_dot[kRowThreads / 32];
   const int64_t t = blockIdx.x;
   float peak = kNegInf, sum = 0.f;
   for (int g = threadIdx.x; g < p.groups; g += kRowThreads) {
@@ -118,31 +165,42 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     s_peak[threadIdx.x >> 5] = peak;
     s_sum[threadIdx.x >> 5] = sum;
   }
+  float z = 0.f;
+  int64_t y = -1;
+  if (p.want.targets != nullptr) {
+    y = p.want.targets[t];
+    if (y >= p.vocab) y = -1;
+    if (y >= 0) z = warp_sum(dot_part(p.dot, t, y, threadIdx.x, kRowThreads));
+    if ((threadIdx.x & 31) == 0) s_dot[threadIdx.x >> 5] = z;
+  }
   __syncthreads();
-  if (threadIdx.x != 0) return;
+  if (threadIdx.x >= 32) return;
   for (int w = 1; w < kRowThreads / 32; ++w) join(peak, sum, s_peak[w], s_sum[w]);
-  // peak, sum: the others. Now the wanted entries.
+  // peak, sum: the others (warp 0 has them in every lane). Now the wanted entries.
   float hit_peak = kNegInf, hit = 0.f, dot = 0.f;
-  const float* z = p.picked + t * p.want.top;
   int n;
   if (p.want.targets != nullptr) {
-    const int64_t y = p.want.targets[t];
-    n = y >= 0 && y < p.vocab;
-    if (n) {
-      hit_peak = z[0];
-      hit = 1.f;
-      dot = z[0];
-    }
+    n = y >= 0;
+    z = s_dot[0];
+    for (int w = 1; w < kRowThreads / 32; ++w) z += s_dot[w];
+    hit_peak = z * p.dot.scale;
+    hit = 1.f;
   } else {
     n = p.want.count[t];
+    const float* zs = p.picked + t * p.want.top;
     const int32_t* id = p.want.ids + t * p.want.top;
     const float* q = p.want.q + t * p.want.top;
-    for (int k = 0; k < n; ++k) hit_peak = fmaxf(hit_peak, z[k]);
-    for (int k = 0; k < n; ++k) {
-      if (k == 0 || id[k] != id[k - 1]) hit += expf(z[k] - hit_peak);
-      dot = fmaf(q[k], z[k] - hit_peak, dot);
+    const int lane = threadIdx.x;
+    for (int k = lane; k < n; k += 32) hit_peak = fmaxf(hit_peak, zs[k]);
+    for (int d = 16; d > 0; d >>= 1) hit_peak = fmaxf(hit_peak, __shfl_xor_sync(0xffffffffu, hit_peak, d));
+    for (int k = lane; k < n; k += 32) {
+      if (k == 0 || id[k] != id[k - 1]) hit += expf(zs[k] - hit_peak);
+      dot = fmaf(q[k], zs[k] - hit_peak, dot);
     }
+    hit = warp_sum(hit);
+    dot = warp_sum(dot);
   }
+  if (threadIdx.x != 0) return;
   if (n == 0) {
     p.lse[t] = peak + logf(sum);
     p.loss[t] = 0.f;
@@ -201,6 +259,12 @@ cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t s) {
   int n = 32;
   while (n < p.top) n <<= 1;
   teacher_kernel<<<static_cast<unsigned>(p.tokens), n, 8 * n, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_targets(const DotParams& d, const int64_t* targets, int64_t tokens, int32_t vocab, float* picked,
+                           cudaStream_t s) {
+  targets_kernel<<<static_cast<unsigned>((tokens + 7) / 8), 256, 0, s>>>(d, targets, tokens, vocab, picked);
   return cudaGetLastError();
 }
 
