@@ -24,6 +24,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "follow.cuh"
 #include "head.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -430,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem = sh->tmem;
+  follow();
   const uint32_t lead_empty = ptx::mapa_shared(ptx::smem_u32(&sh->ring_empty[0]), 0);
 
   if (warp == 0) {
@@ -666,19 +668,7 @@ cudaError_t launch_pairs(const Params& p, int pairs, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(head_pair_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * std::min(pairs, p.items));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, head_pair_kernel<MODE>, p);
+  return launch_follow(head_pair_kernel<MODE>, dim3(2 * std::min(pairs, p.items)), kThreads, smem, s, 2, p);
 }
 
 cudaError_t logit_maps(Params& P, const LogitParams& p) {

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "follow.cuh"
 #include "head.h"
 
 namespace dmuon {
@@ -41,6 +42,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 // One warp per token.
 __global__ void __launch_bounds__(256) targets_kernel(const __grid_constant__ DotParams d, const int64_t* targets,
                                                       int64_t tokens, int32_t vocab, float* picked) {
+  follow();
   const int64_t t = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (t >= tokens) return;
   const int64_t y = targets[t];
@@ -59,6 +61,7 @@ __global__ void teacher_kernel(const __grid_constant__ TeacherParams p) {
   int* id = reinterpret_cast<int*>(raw);
   float* lg = reinterpret_cast<float*>(id + n);
   __shared__ float red[8];
+  follow();
   const int64_t t = blockIdx.x;
   const int k = threadIdx.x;
   int my = p.vocab;
@@ -151,6 +154,7 @@ __device__ __forceinline__ void join(float& peak, float& sum, float peak2, float
 
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ RowParams p) {
   __shared__ float s_peak[kRowThreads / 32], s_sum[kRowThreads / 32], s_dot[kRowThreads / 32];
+  follow();
   const int64_t t = blockIdx.x;
   float peak = kNegInf, sum = 0.f;
   for (int g = threadIdx.x; g < p.groups; g += kRowThreads) {
@@ -230,6 +234,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
 __global__ void __launch_bounds__(256) round_kernel(const float* acc, int slices, int64_t tokens, int32_t dim,
                                                     int64_t pitch, float gscale, const float* gmax, bf16* out,
                                                     int64_t ld) {
+  follow();
   const float scale = gscale * *gmax;
   const int64_t n = tokens * (pitch / 4), slice = tokens * pitch;
   for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
@@ -258,27 +263,25 @@ __global__ void __launch_bounds__(256) round_kernel(const float* acc, int slices
 cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t s) {
   int n = 32;
   while (n < p.top) n <<= 1;
-  teacher_kernel<<<static_cast<unsigned>(p.tokens), n, 8 * n, s>>>(p);
-  return cudaGetLastError();
+  return launch_follow(teacher_kernel, dim3(static_cast<unsigned>(p.tokens)), n, 8 * n, s, 1, p);
 }
 
 cudaError_t launch_targets(const DotParams& d, const int64_t* targets, int64_t tokens, int32_t vocab, float* picked,
                            cudaStream_t s) {
-  targets_kernel<<<static_cast<unsigned>((tokens + 7) / 8), 256, 0, s>>>(d, targets, tokens, vocab, picked);
-  return cudaGetLastError();
+  return launch_follow(targets_kernel, dim3(static_cast<unsigned>((tokens + 7) / 8)), 256, 0, s, 1, d, targets, tokens,
+                       vocab, picked);
 }
 
 cudaError_t launch_rows(const RowParams& p, cudaStream_t s) {
-  rows_kernel<<<static_cast<unsigned>(p.tokens), kRowThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_follow(rows_kernel, dim3(static_cast<unsigned>(p.tokens)), kRowThreads, 0, s, 1, p);
 }
 
 cudaError_t launch_round(const float* acc, int slices, int64_t tokens, int32_t dim, float gscale, const float* gmax,
                          bf16* out, int64_t ld_out, cudaStream_t s) {
   const int64_t pitch = acc_pitch(dim), n = tokens * (pitch / 4);
   const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 152 * 8));
-  round_kernel<<<blocks, 256, 0, s>>>(acc, slices, tokens, dim, pitch, gscale, gmax, out, ld_out);
-  return cudaGetLastError();
+  return launch_follow(round_kernel, dim3(blocks), 256, 0, s, 1, acc, slices, tokens, dim, pitch, gscale, gmax, out,
+                       ld_out);
 }
 
 }  // namespace head

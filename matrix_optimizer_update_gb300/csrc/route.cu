@@ -7,6 +7,7 @@
 #include <algorithm>
 
 #include "dmuon.h"
+#include "follow.cuh"
 #include "internal.h"
 
 namespace dmuon {
@@ -63,6 +64,7 @@ __device__ __forceinline__ void warp_counts(const SortParams& p, int* hist, int6
 
 __global__ void __launch_bounds__(kSortThreads) route_count_kernel(const __grid_constant__ SortParams p) {
   extern __shared__ int hist[];
+  follow();
   const int per_warp = p.run / kSortWarps;
   warp_counts(p, hist, int64_t(blockIdx.x) * p.run + int64_t(threadIdx.x >> 5) * per_warp, per_warp);
   for (int e = threadIdx.x; e < p.experts; e += kSortThreads) {
@@ -96,6 +98,7 @@ __device__ __forceinline__ int block_exclusive(int v, int* scratch, int* total) 
 // One block: the counts become each block's first row per expert, and offsets the experts' first rows.
 __global__ void __launch_bounds__(kSortThreads) route_scan_kernel(const __grid_constant__ SortParams p) {
   __shared__ int scratch[kSortWarps];
+  follow();
   int base = 0;
   for (int e0 = 0; e0 < p.experts; e0 += kSortThreads) {
     const int e = e0 + threadIdx.x;
@@ -123,6 +126,7 @@ template <bool ONE>
 __global__ void __launch_bounds__(kSortThreads) route_place_kernel(const __grid_constant__ SortParams p) {
   extern __shared__ int hist[];
   __shared__ int scratch[kSortWarps];
+  follow();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per_warp = p.run / kSortWarps;
   const int64_t first = int64_t(blockIdx.x) * p.run + int64_t(warp) * per_warp;
@@ -221,6 +225,7 @@ constexpr int kRowThreads = 256;
 template <typename T, int V>
 __global__ void __launch_bounds__(kRowThreads) route_dispatch_kernel(const __grid_constant__ RowParams p) {
   using P = Packed<T, V>;
+  follow();
   const int64_t t = blockIdx.x;
   const T* x = static_cast<const T*>(p.in) + t * p.ld;
   const int64_t dim = int64_t(p.pieces) * V;
@@ -243,6 +248,7 @@ __global__ void __launch_bounds__(kRowThreads) route_dispatch_kernel(const __gri
 template <typename T, int V>
 __global__ void __launch_bounds__(kRowThreads) route_combine_kernel(const __grid_constant__ RowParams p) {
   using P = Packed<T, V>;
+  follow();
   const int64_t t = blockIdx.x;
   T* y = static_cast<T*>(p.out) + t * p.ld;
   const int64_t dim = int64_t(p.pieces) * V;
@@ -270,6 +276,7 @@ __global__ void __launch_bounds__(kRowThreads) route_combine_kernel(const __grid
 template <typename T, int V>
 __global__ void __launch_bounds__(kRowThreads) route_combine_backward_kernel(const __grid_constant__ RowParams p) {
   using P = Packed<T, V>;
+  follow();
   const int lane = threadIdx.x & 31;
   const int64_t i = int64_t(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
   if (i >= p.tokens * p.top) return;
@@ -326,8 +333,7 @@ dmuon_status check_rows(int64_t tokens, int32_t top, int64_t dim, int32_t dtype,
   return DMUON_OK;
 }
 
-dmuon_status launched() {
-  const cudaError_t e = cudaGetLastError();
+dmuon_status done(cudaError_t e) {
   if (e != cudaSuccess) return set_last_error(DMUON_ERR_CUDA, cudaGetErrorString(e));
   return set_last_error(DMUON_OK, "");
 }
@@ -337,19 +343,16 @@ bool misaligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p
 enum RowOp { kDispatch, kCombine, kCombineBackward };
 
 template <typename T, int V>
-void launch_rows(RowOp op, RowParams& p, int64_t dim, cudaStream_t s) {
+cudaError_t launch_rows(RowOp op, RowParams& p, int64_t dim, cudaStream_t s) {
   p.pieces = static_cast<int32_t>(dim / V);
   if (op == kCombineBackward) {
     const int64_t blocks = (p.tokens * p.top + kRowThreads / 32 - 1) / (kRowThreads / 32);
-    route_combine_backward_kernel<T, V><<<static_cast<unsigned>(blocks), kRowThreads, 0, s>>>(p);
-    return;
+    return launch_follow(route_combine_backward_kernel<T, V>, dim3(static_cast<unsigned>(blocks)), kRowThreads, 0, s, 1,
+                         p);
   }
   const unsigned parts = static_cast<unsigned>(std::min<int64_t>((p.pieces + kRowThreads - 1) / kRowThreads, 65535));
-  const dim3 grid(static_cast<unsigned>(p.tokens), parts);
-  if (op == kDispatch)
-    route_dispatch_kernel<T, V><<<grid, kRowThreads, 0, s>>>(p);
-  else
-    route_combine_kernel<T, V><<<grid, kRowThreads, 0, s>>>(p);
+  return launch_follow(op == kDispatch ? route_dispatch_kernel<T, V> : route_combine_kernel<T, V>,
+                       dim3(static_cast<unsigned>(p.tokens), parts), kRowThreads, 0, s, 1, p);
 }
 
 dmuon_status run_rows(RowOp op, RowParams p, int64_t dim, int32_t dtype, void* stream) {
@@ -357,14 +360,8 @@ dmuon_status run_rows(RowOp op, RowParams p, int64_t dim, int32_t dtype, void* s
   const bool vec = (dim * es) % 16 == 0 && (p.ld * es) % 16 == 0 && !misaligned(p.in, 16) && !misaligned(p.out, 16) &&
                    !misaligned(p.dy, 16);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == DMUON_BF16) {
-    if (vec) launch_rows<bf16, 8>(op, p, dim, s);
-    else launch_rows<bf16, 1>(op, p, dim, s);
-  } else {
-    if (vec) launch_rows<float, 4>(op, p, dim, s);
-    else launch_rows<float, 1>(op, p, dim, s);
-  }
-  return launched();
+  if (dtype == DMUON_BF16) return done(vec ? launch_rows<bf16, 8>(op, p, dim, s) : launch_rows<bf16, 1>(op, p, dim, s));
+  return done(vec ? launch_rows<float, 4>(op, p, dim, s) : launch_rows<float, 1>(op, p, dim, s));
 }
 
 }  // namespace
@@ -415,13 +412,12 @@ extern "C" dmuon_status dmuon_route_sort(const int64_t* expert_ids, int64_t toke
     }
   }
   if (p.blocks == 1) {
-    route_place_kernel<true><<<1, kSortThreads, smem, s>>>(p);
-  } else {
-    route_count_kernel<<<p.blocks, kSortThreads, smem, s>>>(p);
-    route_scan_kernel<<<1, kSortThreads, 0, s>>>(p);
-    route_place_kernel<false><<<p.blocks, kSortThreads, smem, s>>>(p);
+    return done(launch_follow(route_place_kernel<true>, dim3(1), kSortThreads, smem, s, 1, p));
   }
-  return launched();
+  cudaError_t e = launch_follow(route_count_kernel, dim3(p.blocks), kSortThreads, smem, s, 1, p);
+  if (e == cudaSuccess) e = launch_follow(route_scan_kernel, dim3(1), kSortThreads, 0, s, 1, p);
+  if (e == cudaSuccess) e = launch_follow(route_place_kernel<false>, dim3(p.blocks), kSortThreads, smem, s, 1, p);
+  return done(e);
 }
 
 extern "C" dmuon_status dmuon_route_dispatch(const void* x, int64_t ld_x, const int32_t* dest, const int32_t* source,

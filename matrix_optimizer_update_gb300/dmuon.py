@@ -348,44 +348,59 @@ class Muon:
 # losses of the language-model head, and routing to experts
 # --------------------------------------------------------------------------
 
-def _want(ok: bool, msg: str):
-    if not ok:
-        raise DmuonError(ERR_INVALID_ARG, msg)
+_torch = None
+
+
+def _t():
+    """torch, imported by the first call that takes tensors."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _refuse(msg: str):
+    raise DmuonError(ERR_INVALID_ARG, msg)
 
 
 def _rows(t, dim, dtype, name, rows=None):
     """A CUDA matrix whose rows lie contiguous (any row pitch); returns that pitch."""
-    _want(t.is_cuda and t.dtype == dtype and t.dim() == 2 and t.shape[1] == dim and
-          (rows is None or t.shape[0] == rows) and (t.shape[1] <= 1 or t.stride(1) == 1),
-          f"{name} must be a CUDA {dtype} tensor of shape [{'rows' if rows is None else rows}, {dim}] "
-          "with contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], -(-t.shape[1] // 8) * 8)
+    shape = t.shape
+    if not (t.is_cuda and t.dtype == dtype and len(shape) == 2 and shape[1] == dim and
+            (rows is None or shape[0] == rows) and (dim <= 1 or t.stride(1) == 1)):
+        _refuse(f"{name} must be a CUDA {dtype} tensor of shape [{'rows' if rows is None else rows}, {dim}] "
+                "with contiguous rows")
+    return t.stride(0) if shape[0] > 1 else -(-dim // 8) * 8
 
 
 def _flat(t, shape, dtype, name):
-    _want(t.is_cuda and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
-          f"{name} must be a contiguous CUDA {dtype} tensor of shape {list(shape)}")
+    if not (t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
+        _refuse(f"{name} must be a contiguous CUDA {dtype} tensor of shape {list(shape)}")
+    return t.data_ptr()
 
 
 class _on:
-    """Run a call on ``stream``: what it allocates belongs to that stream, and what it is given stays
-    alive until the stream is done with it."""
+    """Run a call on ``stream`` (None: the current one of ``like``'s device): what it allocates belongs to
+    that stream, and what it is given stays alive until the stream is done with it."""
 
-    def __init__(self, stream, *tensors):
-        import torch
-        here = torch.cuda.current_stream()
-        self.stream = here if stream is None else stream
+    __slots__ = ("handle", "other")
+
+    def __init__(self, stream, like, *tensors):
+        # the raw handle: the object torch.cuda.current_stream() makes costs more than a small call
+        self.handle = _t()._C._cuda_getCurrentRawStream(like.device.index)
         self.other = None
-        if self.stream != here:
-            self.other = torch.cuda.stream(self.stream)
-            for t in tensors:
-                if t is not None and t.is_cuda:
-                    t.record_stream(self.stream)
+        if stream is not None and stream.cuda_stream != self.handle:
+            self.handle = stream.cuda_stream
+            self.other = _t().cuda.stream(stream)
+            for t in (like, *tensors):
+                if t is not None:
+                    t.record_stream(stream)
 
     def __enter__(self):
         if self.other is not None:
             self.other.__enter__()
-        return self.stream.cuda_stream
+        return self.handle
 
     def __exit__(self, *exc):
         if self.other is not None:
@@ -409,13 +424,12 @@ class Head:
 
     @classmethod
     def create(cls, max_tokens, vocab, dim, *, max_top=0, device=None, stream=None):
-        import torch
         h = ctypes.c_void_p()
         _check(lib().dmuon_head_create(int(max_tokens), int(vocab), int(dim), int(max_top), ctypes.byref(h)))
         self = cls(h, int(max_tokens), int(vocab), int(dim), int(max_top))
         nbytes = self.workspace_bytes()
-        with _on(stream) as s:
-            ws = torch.empty(nbytes + 1024, dtype=torch.uint8, device=device or "cuda")
+        ws = _t().empty(nbytes + 1024, dtype=_t().uint8, device=device or "cuda")
+        with _on(stream, ws) as s:
             self.bind((ws.data_ptr() + 1023) // 1024 * 1024, nbytes, s)
         self.workspace = ws
         return self
@@ -429,50 +443,45 @@ class Head:
         _check(lib().dmuon_head_bind(self._h, ctypes.c_void_p(d_workspace), nbytes, ctypes.c_void_p(stream)))
 
     def _inputs(self, hidden, weight):
-        import torch
-        lh = _rows(hidden, self.dim, torch.bfloat16, "hidden")
-        lw = _rows(weight, self.dim, torch.bfloat16, "weight", self.vocab)
+        lh = _rows(hidden, self.dim, _t().bfloat16, "hidden")
+        lw = _rows(weight, self.dim, _t().bfloat16, "weight", self.vocab)
         return hidden.data_ptr(), lh, weight.data_ptr(), lw
 
     def _teacher(self, top_ids, top_logits, tokens):
-        import torch
-        _want(top_ids.dim() == 2, "top_ids must be [tokens, top]")
-        _flat(top_ids, (tokens, top_ids.shape[1]), torch.int64, "top_ids")
-        _flat(top_logits, top_ids.shape, torch.float32, "top_logits")
-        return top_ids.data_ptr(), top_logits.data_ptr(), top_ids.shape[1]
+        top = top_ids.shape[-1]
+        ids = _flat(top_ids, (tokens, top), _t().int64, "top_ids")
+        return ids, _flat(top_logits, (tokens, top), _t().float32, "top_logits"), top
 
     def _grads(self, hidden, weight, dhidden, dweight):
         """Gradient tensors (made where True, left out where False or None) with addresses and pitches."""
-        import torch
         out = []
         for want, like, name in ((dhidden, hidden, "dhidden"), (dweight, weight, "dweight")):
             if want is True:
-                want = torch.empty(like.shape[0], -(-self.dim // 8) * 8, dtype=like.dtype,
+                want = _t().empty(like.shape[0], -(-self.dim // 8) * 8, dtype=like.dtype,
                                    device=like.device)[:, :self.dim]
             elif want is False:
                 want = None
-            ld = 0 if want is None else _rows(want, self.dim, torch.bfloat16, name, like.shape[0])
+            ld = 0 if want is None else _rows(want, self.dim, _t().bfloat16, name, like.shape[0])
             out += [want, None if want is None else want.data_ptr(), ld]
         return out
 
     def xent(self, hidden, weight, targets, *, stream=None):
         """(loss, lse) per token; targets int64, one outside the vocabulary does not count."""
-        import torch
         n = hidden.shape[0]
-        _flat(targets, (n,), torch.int64, "targets")
+        _flat(targets, (n,), _t().int64, "targets")
         args = self._inputs(hidden, weight)
         with _on(stream, hidden, weight, targets, self.workspace) as s:
-            loss, lse = (torch.empty(n, dtype=torch.float32, device=hidden.device) for _ in range(2))
+            loss = _t().empty(n, dtype=_t().float32, device=hidden.device)
+            lse = _t().empty(n, dtype=_t().float32, device=hidden.device)
             _check(lib().dmuon_head_xent(self._h, *args, targets.data_ptr(), n, loss.data_ptr(), lse.data_ptr(), s))
         return loss, lse
 
     def xent_backward(self, hidden, weight, targets, lse, grad_loss, *, dhidden=True, dweight=True, stream=None):
         """(dhidden, dweight) of sum(grad_loss * loss). Either may be a tensor to write into, or False."""
-        import torch
         n = hidden.shape[0]
-        _flat(targets, (n,), torch.int64, "targets")
-        _flat(lse, (n,), torch.float32, "lse")
-        _flat(grad_loss, (n,), torch.float32, "grad_loss")
+        _flat(targets, (n,), _t().int64, "targets")
+        _flat(lse, (n,), _t().float32, "lse")
+        _flat(grad_loss, (n,), _t().float32, "grad_loss")
         args = self._inputs(hidden, weight)
         with _on(stream, hidden, weight, targets, lse, grad_loss, self.workspace) as s:
             dh, ph, lh, dw, pw, lw = self._grads(hidden, weight, dhidden, dweight)
@@ -482,12 +491,12 @@ class Head:
 
     def distill(self, hidden, weight, top_ids, top_logits, temperature=1.0, *, stream=None):
         """(loss, lse) per token against a teacher's top logits; ids int64 and logits fp32, both [tokens, top]."""
-        import torch
         n = hidden.shape[0]
         ids, lg, k = self._teacher(top_ids, top_logits, n)
         args = self._inputs(hidden, weight)
         with _on(stream, hidden, weight, top_ids, top_logits, self.workspace) as s:
-            loss, lse = (torch.empty(n, dtype=torch.float32, device=hidden.device) for _ in range(2))
+            loss = _t().empty(n, dtype=_t().float32, device=hidden.device)
+            lse = _t().empty(n, dtype=_t().float32, device=hidden.device)
             _check(lib().dmuon_head_distill(self._h, *args, ids, lg, k, float(temperature), n, loss.data_ptr(),
                                             lse.data_ptr(), s))
         return loss, lse
@@ -495,11 +504,10 @@ class Head:
     def distill_backward(self, hidden, weight, top_ids, top_logits, temperature, lse, grad_loss, *, dhidden=True,
                          dweight=True, stream=None):
         """(dhidden, dweight) of sum(grad_loss * loss), as xent_backward."""
-        import torch
         n = hidden.shape[0]
         ids, lg, k = self._teacher(top_ids, top_logits, n)
-        _flat(lse, (n,), torch.float32, "lse")
-        _flat(grad_loss, (n,), torch.float32, "grad_loss")
+        _flat(lse, (n,), _t().float32, "lse")
+        _flat(grad_loss, (n,), _t().float32, "grad_loss")
         args = self._inputs(hidden, weight)
         with _on(stream, hidden, weight, top_ids, top_logits, lse, grad_loss, self.workspace) as s:
             dh, ph, lh, dw, pw, lw = self._grads(hidden, weight, dhidden, dweight)
@@ -545,80 +553,73 @@ class Router:
 
     @classmethod
     def create(cls, max_tokens, top, experts, *, device=None):
-        import torch
         n = ctypes.c_size_t()
         _check(lib().dmuon_route_workspace_bytes(int(max_tokens), int(top), int(experts), ctypes.byref(n)))
         return cls(int(max_tokens), int(top), int(experts),
-                   torch.empty(n.value, dtype=torch.uint8, device=device or "cuda"))
+                   _t().empty(n.value, dtype=_t().uint8, device=device or "cuda"))
 
     def sort(self, expert_ids, *, stream=None) -> Route:
         """Order the assignments by expert; expert_ids int64 [tokens, top], one outside 0..experts-1 is dropped."""
-        import torch
-        _want(expert_ids.dim() == 2 and expert_ids.shape[0] <= self.max_tokens,
-              f"expert_ids must be [tokens <= {self.max_tokens}, {self.top}]")
         t = expert_ids.shape[0]
-        _flat(expert_ids, (t, self.top), torch.int64, "expert_ids")
+        if t > self.max_tokens:
+            _refuse(f"expert_ids has {t} tokens, more than max_tokens ({self.max_tokens})")
+        _flat(expert_ids, (t, self.top), _t().int64, "expert_ids")
         with _on(stream, expert_ids, self.workspace) as s:
             dev = expert_ids.device
-            dest = torch.empty(t, self.top, dtype=torch.int32, device=dev)
-            source = torch.empty(t * self.top, dtype=torch.int32, device=dev)
-            offsets = torch.empty(self.experts + 1, dtype=torch.int32, device=dev)
+            dest = _t().empty(t, self.top, dtype=_t().int32, device=dev)
+            source = _t().empty(t * self.top, dtype=_t().int32, device=dev)
+            offsets = _t().empty(self.experts + 1, dtype=_t().int32, device=dev)
             _check(lib().dmuon_route_sort(expert_ids.data_ptr(), t, self.top, self.experts, dest.data_ptr(),
                                           source.data_ptr(), offsets.data_ptr(), self.workspace.data_ptr(),
                                           self.workspace.numel(), s))
         return Route(dest, source, offsets)
 
     def _row_type(self, t, name):
-        import torch
-        kinds = {torch.bfloat16: BF16, torch.float32: F32}
-        _want(t.dtype in kinds and t.dim() == 2, f"{name} must be a bf16 or fp32 matrix")
-        return kinds[t.dtype]
+        if t.dim() != 2 or t.dtype not in (_t().bfloat16, _t().float32):
+            _refuse(f"{name} must be a bf16 or fp32 matrix")
+        return BF16 if t.dtype == _t().bfloat16 else F32
 
     def _route(self, route, tokens):
-        import torch
-        _flat(route.dest, (tokens, self.top), torch.int32, "route.dest")
-        _flat(route.source, (tokens * self.top,), torch.int32, "route.source")
+        _flat(route.dest, (tokens, self.top), _t().int32, "route.dest")
+        _flat(route.source, (tokens * self.top,), _t().int32, "route.source")
 
     def dispatch(self, x, route, *, stream=None):
         """xs [tokens * top, dim]: x's rows in expert order, zeros in rows not in use."""
-        import torch
         kind = self._row_type(x, "x")
         t, dim = x.shape
         ld = _rows(x, dim, x.dtype, "x")
         self._route(route, t)
         with _on(stream, x, route.dest, route.source) as s:
-            xs = torch.empty(t * self.top, dim, dtype=x.dtype, device=x.device)
+            xs = _t().empty(t * self.top, dim, dtype=x.dtype, device=x.device)
             _check(lib().dmuon_route_dispatch(x.data_ptr(), ld, route.dest.data_ptr(), route.source.data_ptr(), t,
                                               self.top, dim, kind, xs.data_ptr(), s))
         return xs
 
     def combine(self, ys, weights, route, *, stream=None):
         """y [tokens, dim]: the sum of each token's expert rows, times weights (fp32 [tokens, top], or None: 1)."""
-        import torch
         kind = self._row_type(ys, "ys")
         t, dim = route.dest.shape[0], ys.shape[1]
         self._route(route, t)
         _flat(ys, (t * self.top, dim), ys.dtype, "ys")
         if weights is not None:
-            _flat(weights, (t, self.top), torch.float32, "weights")
+            _flat(weights, (t, self.top), _t().float32, "weights")
         with _on(stream, ys, weights, route.dest) as s:
-            y = torch.empty(t, dim, dtype=ys.dtype, device=ys.device)
+            y = _t().empty(t, dim, dtype=ys.dtype, device=ys.device)
             _check(lib().dmuon_route_combine(ys.data_ptr(), None if weights is None else weights.data_ptr(),
                                              route.dest.data_ptr(), t, self.top, dim, kind, y.data_ptr(), dim, s))
         return y
 
     def combine_backward(self, dy, ys, weights, route, *, stream=None):
         """(dys, dweights) of combine."""
-        import torch
         kind = self._row_type(ys, "ys")
         t, dim = route.dest.shape[0], ys.shape[1]
         self._route(route, t)
         _flat(ys, (t * self.top, dim), ys.dtype, "ys")
-        _flat(weights, (t, self.top), torch.float32, "weights")
+        _flat(weights, (t, self.top), _t().float32, "weights")
         ld = _rows(dy, dim, ys.dtype, "dy", t)
         with _on(stream, dy, ys, weights, route.dest, route.source) as s:
-            dys = torch.empty_like(ys)
-            dw = torch.empty_like(weights)
+            dys = _t().empty_like(ys)
+            dw = _t().empty_like(weights)
             _check(lib().dmuon_route_combine_backward(dy.data_ptr(), ld, ys.data_ptr(), weights.data_ptr(),
                                                       route.dest.data_ptr(), route.source.data_ptr(), t, self.top,
                                                       dim, kind, dys.data_ptr(), dw.data_ptr(), s))
