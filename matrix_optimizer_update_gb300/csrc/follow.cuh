@@ -10,9 +10,9 @@
 
 namespace dmuon {
 
-__device__ __forceinline__ void follow() {
+__device__ __forceinline__ void follow(bool lead = true) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (lead) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // cluster > 1: thread-block clusters of that many CTAs along x.

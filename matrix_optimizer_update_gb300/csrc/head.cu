@@ -21,6 +21,8 @@ constexpr size_t kAlign = 1024;
 // dz exists for one piece of the vocabulary at a time: as many entries as keep it within these bytes.
 constexpr int64_t kPieceBytes = int64_t(512) << 20;
 constexpr int64_t kPieceStep = 256;
+constexpr int64_t kMaxPairs = 128;
+constexpr int64_t kFewTokens = 128;
 constexpr int64_t kMaxSlices = 152;
 constexpr int64_t kSliceBytes = 2 * kMaxSlices * 256 * 256 * 4;
 
@@ -166,6 +168,7 @@ head::LogitParams logit_params(dmuon_head_t H, const void* hidden, int64_t ld_hi
   p.dim = static_cast<int32_t>(H->dim);
   p.scale = 1.f / L.temperature;
   p.want = w;
+  p.width = p.vocab;
   return p;
 }
 
@@ -198,7 +201,7 @@ dmuon_status forward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, cons
   r.want = w;
   r.dot = dot;
   r.parts = p.parts;
-  r.groups = static_cast<int32_t>(cdiv(H->vocab, head::kGroup));
+  r.groups = head::logit_groups(tokens, H->vocab, H->pairs);
   r.picked = p.picked;
   r.entropy = reinterpret_cast<const float*>(H->ws + H->off_entropy);
   r.temperature = L.temperature;
@@ -249,7 +252,7 @@ dmuon_status backward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, con
   g.ld_dz = p.ld_dz;
   g.gscale = L.temperature;
   g.slices = head::dh_slices(tokens, H->dim, std::min(H->piece, H->vocab), dweight != nullptr, H->pairs);
-  const bool direct = H->vocab <= H->piece && g.slices.count == 1;
+  const bool direct = H->vocab <= H->piece && g.slices.count == 1 && !head::thin_tokens(tokens);
   if (dhidden != nullptr && direct) {
     g.dhidden = static_cast<head::bf16*>(dhidden);
     g.ld_dhidden = ld_dhidden;
@@ -297,7 +300,10 @@ extern "C" dmuon_status dmuon_head_create(int64_t max_tokens, int64_t vocab, int
     return o;
   };
   H->off_status = take(256);
-  H->off_parts = take(sizeof(head::Part) * cdiv(vocab, head::kGroup) * max_tokens);
+  // a call with few tokens has up to 8 groups for each 256 entries and for each pair of SMs
+  H->off_parts = take(sizeof(head::Part) * std::max(cdiv(vocab, head::kGroup) * max_tokens,
+                                                    (cdiv(vocab, 32) + 8 * kMaxPairs) *
+                                                        std::min<int64_t>(max_tokens, kFewTokens)));
   H->off_picked = take(4 * max_tokens * std::max(1, max_top));
   H->off_ids = take(4 * max_tokens * max_top);
   H->off_q = take(4 * max_tokens * max_top);
@@ -343,7 +349,7 @@ extern "C" dmuon_status dmuon_head_bind(dmuon_head_t H, void* d_workspace, size_
     return cuda_refuse(e, "clearing the status word");
   H->ws = static_cast<char*>(d_workspace);
   H->device = device;
-  H->pairs = sms / 2;
+  H->pairs = std::min<int>(sms / 2, kMaxPairs);
   return ok();
 }
 

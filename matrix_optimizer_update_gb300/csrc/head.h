@@ -14,7 +14,8 @@ namespace head {
 
 using bf16 = __nv_bfloat16;
 
-// The forward pass reduces each token's logits over groups of 128 vocabulary entries.
+// The forward pass reduces each token's logits over groups of 128 vocabulary entries (of up to 32 when the
+// tokens are few: logit_groups).
 constexpr int kGroup = 128;
 constexpr int kMaxTop = 256;
 
@@ -54,8 +55,8 @@ struct LogitParams {
   // forward
   Part* parts;             // [groups][tokens]
   float* picked;           // [tokens][want.top]: scaled logits of the wanted entries (below kSure: written here)
-  // backward: entries v0 .. v0 + width - 1
-  int32_t v0, width;
+  int32_t v0, width;       // entries v0 .. v0 + width - 1 (forward: all)
+  // backward
   const float* lse;
   const float* grad;
   bf16* dz;                // [tokens][ld_dz]
@@ -133,6 +134,14 @@ struct TeacherParams {
   DotParams dot;
   float* picked;           // entries of at least kSure
 };
+
+// Tiles of a launch over so many vocabulary entries when the tokens are few.
+struct Thin {
+  int32_t height, tiles;
+};
+bool thin_tokens(int64_t tokens);
+Thin thin_tiles(int64_t entries, int pairs);
+int logit_groups(int64_t tokens, int64_t vocab, int pairs);
 
 cudaError_t launch_logits(const LogitParams& p, const Pipe& pipe, cudaStream_t s);
 cudaError_t launch_dz(const LogitParams& p, const Pipe& pipe, cudaStream_t s);

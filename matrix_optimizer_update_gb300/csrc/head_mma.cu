@@ -36,7 +36,9 @@ namespace {
 constexpr int kTile = 256;                     // rows and columns of a pair's tile
 constexpr int kStep = 64;                      // K per stage
 constexpr uint32_t kHalf = 128 * kStep * 2;    // a CTA's 128 rows (or columns) of an operand, one stage
-constexpr int kStages = 6;
+constexpr int kRingBytes = 6 * 2 * kHalf;      // operand stages: 6 of 32 KB, or more of fewer rows
+constexpr int kMaxStages = 16;
+constexpr int kThin = 128;                     // up to so many tokens, they are the N side of the products
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
 constexpr int kBox = 32 * 64;                  // staging box of a TMA store: 32 rows of 64 bytes
@@ -46,7 +48,10 @@ constexpr uint32_t kTmemCols = 2 * kTile;
 constexpr int64_t kWaitNs = 2000000000LL;
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum Mode { kLogits, kDz, kGrads };
+// The thin forms of logits and dz turn the product round: vocabulary entries are the M side and the tokens
+// the N side, padded to 32. With 77 tokens the M = 256 side of the other form is two thirds empty, and the
+// launch is bound by products of zeros; turned round it is bound by reading W.
+enum Mode { kLogits, kDz, kGrads, kThinLogits, kThinDz, kThinGrads };
 
 struct Params {
   CUtensorMap a[2], b[2];  // [1]: the second kind of tile of a grads launch (dW)
@@ -58,9 +63,14 @@ struct Params {
   // grads: dH tiles come first (the longer ones), `slices` parts of K each, then dW tiles
   int32_t dh_items, dh_rows, dh_nk, slices, slice_nk;
   int32_t dim_tiles;
+  int32_t thin_n;          // tokens padded to 32 when they are the N side, else 0
+  int32_t thin_h;          // thin logits, dz: vocabulary entries per tile
+  int32_t stages, stage_bytes, a_bytes;  // thin logits, dz: a stage holds a_bytes of A, then B
   int32_t chunked;         // dim is a multiple of 64: one copy brings two 64-column blocks
   int32_t dh_direct;       // dH is complete: store bf16; else add into fp32 sums
   int32_t first;           // ... of which this is the first piece (store, not add)
+  float* dh_acc;           // thin: the fp32 sums, pitch acc_ld
+  int64_t acc_ld;
   float gscale;            // factor of the gradients beside *gmax
   float* gmax;             // largest |grad|: dz holds gradients relative to it
   LogitParams l;
@@ -69,8 +79,8 @@ struct Params {
 };
 
 struct Shared {
-  uint64_t full[kStages];
-  uint64_t empty[kStages];
+  uint64_t full[kMaxStages];
+  uint64_t empty[kMaxStages];
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t mma_done;
@@ -83,9 +93,17 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= 1024, "barriers must fit their 1 KB");
 
+// A thin launch's tokens, in shared memory (after the barriers, in front of the staging boxes' use).
+struct ThinTokens {
+  int target[kThin];   // cross entropy: the entry to take out, or -1
+  float g[kThin];      // dz: gradient relative to the largest, 0 for a token that does not count
+  float lse[kThin];
+  float hit[kThin];    // dz, cross entropy: the target's own dz
+};
+
 // Instruction descriptor as ptx::idesc_bf16, with A MN-major too (bit 15).
-__host__ __device__ constexpr uint32_t idesc(bool a_mn, bool b_mn) {
-  return ptx::idesc_bf16(kTile, kTile, b_mn) | (a_mn ? (1u << 15) : 0u);
+__device__ __forceinline__ uint32_t idesc(int n, bool a_mn, bool b_mn) {
+  return ptx::idesc_bf16(kTile, n, b_mn) | (a_mn ? (1u << 15) : 0u);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -139,7 +157,11 @@ __device__ __forceinline__ Where where_is(const Params& p, int w) {
   x.kind = 0;
   x.slice = 0;
   x.k0 = 0;
-  if (MODE != kGrads) {
+  if (MODE == kThinLogits || MODE == kThinDz) {
+    x.row = 0;
+    x.col = w;
+    x.nk = p.nk;
+  } else if (MODE == kLogits || MODE == kDz) {
     const int band = w / (kBand * p.cols);
     const int r = w - band * kBand * p.cols;
     const int high = min(kBand, p.rows - band * kBand);
@@ -150,7 +172,7 @@ __device__ __forceinline__ Where where_is(const Params& p, int w) {
     const int per = p.dh_rows * p.dim_tiles;
     x.slice = w / per;
     const int r = w - x.slice * per;
-    x.row = r / p.dim_tiles;
+    x.row = r / p.dim_tiles;             // thin: always 0
     x.col = r - x.row * p.dim_tiles;
     x.k0 = x.slice * p.slice_nk;
     x.nk = min(p.slice_nk, p.dh_nk - x.k0);
@@ -208,7 +230,6 @@ __device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, in
   if (!wait()) return false;
   ptx::tc_fence_after();
   float peak = -INFINITY, sum = 0.f;
-  float last = 0.f;
   int last_id = -1;
 #pragma unroll 1
   for (int ch = 0; ch < 4; ++ch) {
@@ -226,16 +247,17 @@ __device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, in
     while (__any_sync(0xffffffffu, c.id < jc + 32)) {
       if (c.id < jc + 32) {
         const int at = c.id - jc;
-        if (c.id != last_id) {
+        float z = 0.f;
+        if (c.id != last_id) {  // entries that share an id have one logit, with the first of them
 #pragma unroll
           for (int k = 0; k < 32; ++k)
             if (k == at) {
-              last = v[k];
+              z = v[k];
               v[k] = -INFINITY;
             }
-          last_id = c.id;
+          if (c.share(p.want) < kSure) p.picked[t * p.want.top + c.pos] = z;
         }
-        if (c.share(p.want) < kSure) p.picked[t * p.want.top + c.pos] = last;
+        last_id = c.id;
         c.next(p.want);
       }
     }
@@ -320,6 +342,178 @@ __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t,
   return true;
 }
 
+// ------------------------------------------------------------------ thin epilogues: lane = vocabulary entry, column = token
+// Reduces 32 columns over the 32 lanes by halving: lane j ends with column j's result, in 31 exchanges.
+template <class Op>
+__device__ __forceinline__ float columns(const float (&v)[32], int lane, Op op) {
+  float r[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const bool up = (lane & 16) != 0;
+    r[k] = op(up ? v[k + 16] : v[k], __shfl_xor_sync(0xffffffffu, up ? v[k] : v[k + 16], 16));
+  }
+#pragma unroll
+  for (int s = 8; s > 0; s >>= 1)
+#pragma unroll
+    for (int k = 0; k < s; ++k) {
+      const bool up = (lane & s) != 0;
+      r[k] = op(up ? r[k + s] : r[k], __shfl_xor_sync(0xffffffffu, up ? r[k] : r[k + s], s));
+    }
+  return r[0];
+}
+
+// The wanted entries of 32 tokens among 32 lanes' vocabulary entries [first, end): lane L's cursor belongs to
+// token t0 + L. take(k, id, q, pos, again) is called by the lane whose entry `id` is, for column k; `again`
+// when the token's previous entry had the same id.
+template <class Take>
+__device__ __forceinline__ void each_wanted(const Wanted& w, Cursor& c, int first, int end, int lane, Take&& take) {
+  int last = -1;
+  while (true) {
+    unsigned more = __ballot_sync(0xffffffffu, c.id < end);
+    if (more == 0u) return;
+    const float q = c.id < end ? c.share(w) : 0.f;
+    while (more != 0u) {
+      const int L = __ffs(more) - 1;
+      more &= more - 1u;
+      const int id = __shfl_sync(0xffffffffu, c.id, L), pos = __shfl_sync(0xffffffffu, c.pos, L);
+      const int before = __shfl_sync(0xffffffffu, last, L);
+      const float share = __shfl_sync(0xffffffffu, q, L);
+      if (id - first == lane) take(L, id, share, pos, id == before);
+    }
+    if (c.id < end) {
+      last = c.id;
+      c.next(w);
+    }
+  }
+}
+
+// One warp's part of a thin logits tile: 32 entries from `first` (those before `end` are this tile's), the
+// blocks of 32 tokens that are its half's.
+template <class Wait>
+__device__ __forceinline__ bool drain_thin_logits(const Params& P, const ThinTokens& tk, int first, int end, int group,
+                                                  int half, uint32_t tbase, int lane, Wait&& wait) {
+  const LogitParams& p = P.l;
+  const bool lists = p.want.targets == nullptr;
+  const int blocks = P.thin_n / 32;
+  Cursor c[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = (half + 2 * i) * 32 + lane;
+    c[i].id = INT_MAX;
+    if (lists) c[i].start(p.want, t, t < p.tokens && first < end, first);
+  }
+  if (!wait()) return false;
+  ptx::tc_fence_after();
+  const int v0 = first + lane;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int b = half + 2 * i;
+    if (b >= blocks) break;
+    float v[32];
+    ptx::tmem_ld_32x32b_x32(tbase + b * 32, v);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = v0 < end ? v[k] * p.scale : -INFINITY;
+    if (!lists) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (tk.target[b * 32 + k] == v0) v[k] = -INFINITY;
+    } else {
+      each_wanted(p.want, c[i], first, end, lane, [&](int k, int, float share, int pos, bool again) {
+        if (again) return;
+        float z = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j == k) {
+            z = v[j];
+            v[j] = -INFINITY;
+          }
+        if (share < kSure) p.picked[int64_t(b * 32 + k) * p.want.top + pos] = z;
+      });
+    }
+    const float peak = columns(v, lane, [](float x, float y) { return fmaxf(x, y); });
+    const float from = peak == -INFINITY ? 0.f : peak;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = ex2((v[k] - __shfl_sync(0xffffffffu, from, k)) * kLog2e);
+    const float sum = columns(v, lane, [](float x, float y) { return x + y; });
+    const int t = b * 32 + lane;
+    if (t < p.tokens) p.parts[int64_t(group) * p.tokens + t] = Part{peak, sum};
+  }
+  return true;
+}
+
+// One warp's part of a thin dz tile; dz[t][v - v0] as in the other form.
+template <class Wait>
+__device__ __forceinline__ bool drain_thin_dz(const Params& P, const ThinTokens& tk, int first, int end, int half,
+                                              uint32_t tbase, int lane, Wait&& wait) {
+  const LogitParams& p = P.l;
+  const bool lists = p.want.targets == nullptr;
+  const int blocks = P.thin_n / 32;
+  Cursor c[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = (half + 2 * i) * 32 + lane;
+    c[i].id = INT_MAX;
+    if (lists) c[i].start(p.want, t, t < p.tokens && first < end && tk.g[t & (kThin - 1)] != 0.f, first);
+  }
+  if (!wait()) return false;
+  ptx::tc_fence_after();
+  const int v0 = first + lane;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int b = half + 2 * i;
+    if (b >= blocks) break;
+    float v[32];
+    ptx::tmem_ld_32x32b_x32(tbase + b * 32, v);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float g = tk.g[b * 32 + k];
+      const float e = g * ex2_full((v[k] * p.scale - tk.lse[b * 32 + k]) * kLog2e);
+      v[k] = g == 0.f ? 0.f : !lists && tk.target[b * 32 + k] == v0 ? tk.hit[b * 32 + k] : e;
+    }
+    if (lists)
+      each_wanted(p.want, c[i], first, end, lane, [&](int k, int, float share, int pos, bool again) {
+        const int t = b * 32 + k;
+        const float g = tk.g[t];
+        const bool sure = share >= kSure && !again;
+        const float e =
+            sure ? ex2_full((p.picked[int64_t(t) * p.want.top + pos] - tk.lse[t]) * kLog2e) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j == k) v[j] = sure ? g * (e - share) : v[j] - g * share;
+      });
+    if (v0 < end) {
+      bf16* row = p.dz + (v0 - p.v0);
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (b * 32 + k < p.tokens) row[(b * 32 + k) * p.ld_dz] = __float2bfloat16_rn(v[k]);
+    }
+  }
+  return true;
+}
+
+// One warp's part of a thin dH tile: 32 columns of dH (lane) by the tokens, into the slice's fp32 sums.
+template <class Wait>
+__device__ __forceinline__ bool drain_thin_dh(const Params& P, const Where& x, int d0, int half, uint32_t tbase,
+                                              int lane, Wait&& wait) {
+  if (!wait()) return false;
+  ptx::tc_fence_after();
+  const int d = d0 + lane;
+  float* acc = P.dh_acc + int64_t(x.slice) * P.l.tokens * P.acc_ld + d;
+  for (int b = half; b < P.thin_n / 32; b += 2) {
+    float v[32];
+    ptx::tmem_ld_32x32b_x32(tbase + b * 32, v);
+    if (d < P.l.dim) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (b * 32 + k < P.l.tokens) {
+          float* o = acc + int64_t(b * 32 + k) * P.acc_ld;
+          *o = P.first ? v[k] : *o + v[k];
+        }
+    }
+  }
+  return true;
+}
+
 // One warp's part of a gradient tile: 32 rows from r0, 128 columns from d0.
 template <class Wait>
 __device__ __forceinline__ bool drain_grads(const Params& P, const Where& x, int64_t r0, int64_t r_lim, int d0,
@@ -396,17 +590,22 @@ template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sA = base;
-  uint8_t* sB = base + kStages * kHalf;
-  Shared* sh = reinterpret_cast<Shared*>(sB + kStages * kHalf);
-  uint8_t* boxes = sB + kStages * kHalf + 1024;
+  constexpr bool thin = MODE == kThinLogits || MODE == kThinDz;
+  constexpr bool grads = MODE == kGrads || MODE == kThinGrads;
+  Shared* sh = reinterpret_cast<Shared*>(base + kRingBytes);
+  uint8_t* boxes = base + kRingBytes + 1024;
+  ThinTokens& tk = *reinterpret_cast<ThinTokens*>(boxes);  // thin launches stage no boxes
+  // operand ring: fixed at compile time but for the thin logits and dz, whose stages hold fewer rows
+  const uint32_t stages = thin ? p.stages : kRingBytes / (2 * kHalf);
+  const uint32_t stage_bytes = thin ? p.stage_bytes : 2 * kHalf;
+  const uint32_t a_bytes = thin ? p.a_bytes : kHalf;
   const int rank = static_cast<int>(ptx::cluster_ctarank());
   const bool leader = rank == 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abortf = &sh->abort_flag;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       ptx::mbar_init(&sh->full[s], 1);
       ptx::mbar_init(&sh->empty[s], 1);
     }
@@ -431,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem = sh->tmem;
-  follow();
+  follow(MODE != kLogits && MODE != kThinLogits);
   const uint32_t lead_empty = ptx::mapa_shared(ptx::smem_u32(&sh->ring_empty[0]), 0);
 
   if (warp == 0) {
@@ -441,30 +640,38 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
       uint32_t stage = 0, phase = 0, fills = 0;
       auto load_tile = [&](int w) -> bool {
         const Where x = where_is<MODE>(p, w);
+        const bool turned = MODE == kThinGrads && x.kind == 0;  // dH^T = W^T dz^T
         const int row = x.row * kTile + rank * 128, col = x.col * kTile + rank * 128;
+        const uint32_t bytes = thin ? stage_bytes : turned ? kHalf + p.thin_n * 64 : 2 * kHalf;
         for (int kb = 0; kb < x.nk; ++kb) {
           if (!ptx::mbar_wait_cluster(&sh->empty[stage], phase ^ 1u, abortf, p.status, kWaitNs)) return false;
-          if (leader) ptx::mbar_arrive_expect_tx(&sh->full[stage], 4 * kHalf);
+          if (leader) ptx::mbar_arrive_expect_tx(&sh->full[stage], 2 * bytes);
           const uint32_t fb = lead_full + stage * static_cast<uint32_t>(sizeof(uint64_t));
-          uint8_t *a = sA + stage * kHalf, *b = sB + stage * kHalf;
+          uint8_t* a = base + stage * stage_bytes;
+          uint8_t* b = a + a_bytes;
           const int k = (x.k0 + kb) * kStep;
-          if (MODE != kGrads) {  // both K-major: 128 rows of 64
+          if (thin) {  // W and H, K-major: thin_h / 2 and thin_n / 2 rows of 64
+            tma_load_2d_pair(a, &p.b[0], fb, k, p.l.v0 + x.col * p.thin_h + rank * (p.thin_h / 2));
+            tma_load_2d_pair(b, &p.a[0], fb, k, rank * (p.thin_n / 2));
+          } else if (!grads) {  // both K-major: 128 rows of 64
             tma_load_2d_pair(a, &p.a[0], fb, k, row);
-            tma_load_2d_pair(b, &p.b[0], fb, k, (MODE == kDz ? p.l.v0 : 0) + col);
+            tma_load_2d_pair(b, &p.b[0], fb, k, p.l.v0 + col);
           } else {
-            if (x.kind == 0) tma_load_2d_pair(a, &p.a[0], fb, k, row);           // dz, K-major
-            else ptx::tma_load_3d_pair(a, &p.a[1], fb, 0, k, row / 64);          // dz, two blocks of 64 columns
-            const CUtensorMap* mb = &p.b[x.kind];                                // W or H, MN-major
+            uint8_t* wide = turned ? a : b;                                     // W or H, MN-major
+            const CUtensorMap* mw = &p.b[x.kind];
             const int kr = k + (x.kind == 0 ? p.l.v0 : 0);
+            if (turned) tma_load_2d_pair(b, &p.a[0], fb, k, rank * (p.thin_n / 2));  // dz, K-major
+            else if (x.kind == 0) tma_load_2d_pair(a, &p.a[0], fb, k, row);          // dz, K-major
+            else ptx::tma_load_3d_pair(a, &p.a[1], fb, 0, k, row / 64);              // dz, two blocks of 64 columns
             if (p.chunked) {
-              ptx::tma_load_3d_pair(b, mb, fb, 0, kr, col / 64);
+              ptx::tma_load_3d_pair(wide, mw, fb, 0, kr, col / 64);
             } else {
-              tma_load_2d_pair(b, mb, fb, col, kr);
-              tma_load_2d_pair(b + kHalf / 2, mb, fb, col + 64, kr);
+              tma_load_2d_pair(wide, mw, fb, col, kr);
+              tma_load_2d_pair(wide + kHalf / 2, mw, fb, col + 64, kr);
             }
           }
           ++fills;
-          if (++stage == kStages) {
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -492,9 +699,9 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
           w = next;
         }
         // the leader's full barriers count both CTAs' bytes: nothing is in flight once they complete
-        for (uint32_t s = 0; s < kStages; ++s) {
+        for (uint32_t s = 0; s < stages; ++s) {
           if (fills > s) {
-            const uint32_t n = (fills - 1u - s) / kStages + 1u;
+            const uint32_t n = (fills - 1u - s) / stages + 1u;
             int zero = 0;
             ptx::mbar_wait_cluster(&sh->full[s], (n - 1u) & 1u, &zero, p.status, kWaitNs);
           }
@@ -514,9 +721,10 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
       bool ok = true;
       for (int w; ok && take(sh, local, w, lead_empty, abortf, p) && w >= 0; ++local) {
         const Where x = where_is<MODE>(p, w);
-        const bool a_mn = MODE == kGrads && x.kind == 1;
-        constexpr bool b_mn = MODE == kGrads;
-        const uint32_t id = a_mn ? idesc(true, b_mn) : idesc(false, b_mn);
+        const bool turned = MODE == kThinGrads && x.kind == 0;
+        const bool a_mn = MODE == kThinGrads || (MODE == kGrads && x.kind == 1);
+        const bool b_mn = grads && !turned;
+        const uint32_t id = idesc(thin || turned ? p.thin_n : kTile, a_mn, b_mn);
         const uint32_t acc = local & 1u;
         if (!ptx::mbar_wait_cluster(&sh->tempty[acc], ((local >> 1) & 1u) ^ 1u, abortf, p.status, kWaitNs)) break;
         ptx::tc_fence_after();
@@ -527,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t a0 = ptx::smem_u32(sA + stage * kHalf), b0 = ptx::smem_u32(sB + stage * kHalf);
+          const uint32_t a0 = ptx::smem_u32(base) + stage * stage_bytes, b0 = a0 + a_bytes;
 #pragma unroll
           for (int kk = 0; kk < kStep / 16; ++kk) {
             // K-major: 16 columns further in the swizzled rows; MN-major: 16 rows of 128 bytes further, the
@@ -539,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
             ptx::umma_f16_pair(d, ad, bd, id, (kb | kk) != 0 ? 1u : 0u);
           }
           ptx::umma_commit_pair(&sh->empty[stage], 0x3);
-          if (++stage == kStages) {
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -557,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
     const uint32_t lead_tempty = ptx::mapa_shared(ptx::smem_u32(&sh->tempty[0]), 0);
     uint8_t* stg = boxes + (warp - 2) * (2 * kBox);
     float gmax = 1.f;
-    if (MODE == kDz) {  // under the first tile's products
+    if (MODE == kDz || MODE == kThinDz) {  // under the first tile's products
       float m = 0.f;
       for (int64_t t = threadIdx.x - 64; t < p.l.tokens; t += kEpiWarps * 32) m = fmaxf(m, fabsf(p.l.grad[t]));
       for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -566,6 +774,33 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
       for (int k = 0; k < kEpiWarps; ++k) gmax = k == 0 ? sh->red[0] : fmaxf(gmax, sh->red[k]);
       if (gmax == 0.f) gmax = 1.f;
       if (blockIdx.x == 0 && threadIdx.x == 64) *p.gmax = gmax;
+    }
+    if (thin) {
+      const int t = threadIdx.x - 64;
+      if (t < kThin) {
+        int y = -1;
+        float g = 0.f, lse = 0.f, hit = 0.f;
+        if (t < p.l.tokens) {
+          bool counts;
+          if (p.l.want.targets != nullptr) {
+            const int64_t id = p.l.want.targets[t];
+            counts = id >= 0 && id < p.l.vocab;
+            if (counts) y = static_cast<int>(id);
+          } else {
+            counts = p.l.want.count[t] > 0;
+          }
+          if (MODE == kThinDz) {
+            lse = p.l.lse[t];
+            g = counts ? p.l.grad[t] / gmax : 0.f;
+            if (y >= 0) hit = g * (ex2_full((p.l.picked[t] - lse) * kLog2e) - 1.f);
+          }
+        }
+        tk.target[t] = y;
+        tk.g[t] = g;
+        tk.lse[t] = lse;
+        tk.hit[t] = hit;
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
     }
     uint32_t nbox = 0;
     for (uint32_t local = 0;; ++local) {
@@ -582,7 +817,18 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
         return ptx::mbar_wait_cluster(&sh->tfull[acc], (local >> 1) & 1u, abortf, p.status, kWaitNs);
       };
       bool ok;
-      if (MODE == kLogits) {
+      if (thin) {
+        const int base_v = p.l.v0 + x.col * p.thin_h + rank * (p.thin_h / 2);
+        const int last = min(min(base_v + p.thin_h / 2, p.l.v0 + p.l.width), base_v + q * 32 + 32);
+        const uint32_t rows = tmem + acc * kTile + (static_cast<uint32_t>(q * 32) << 16);
+        if (MODE == kThinLogits)
+          ok = drain_thin_logits(p, tk, base_v + q * 32, last, (x.col * 2 + rank) * 4 + q, half, rows, lane, wait);
+        else
+          ok = drain_thin_dz(p, tk, base_v + q * 32, last, half, rows, lane, wait);
+      } else if (MODE == kThinGrads && x.kind == 0) {
+        const uint32_t rows = tmem + acc * kTile + (static_cast<uint32_t>(q * 32) << 16);
+        ok = drain_thin_dh(p, x, x.col * kTile + rank * 128 + q * 32, half, rows, lane, wait);
+      } else if (MODE == kLogits) {
         ok = drain_logits(p.l, r0 + lane, c0, tbase, wait);
       } else if (MODE == kDz) {
         ok = drain_dz(p, gmax, r0 + lane, r0, p.l.v0 + c0, tbase, lane, stg, nbox, wait);
@@ -664,56 +910,87 @@ int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
 template <int MODE>
 cudaError_t launch_pairs(const Params& p, int pairs, cudaStream_t s) {
-  const size_t smem = 1024 + kStages * 2 * kHalf + 1024 + kEpiWarps * 2 * kBox;
+  const size_t smem = 1024 + kRingBytes + 1024 + kEpiWarps * 2 * kBox;
   cudaError_t e = cudaFuncSetAttribute(head_pair_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   return launch_follow(head_pair_kernel<MODE>, dim3(2 * std::min(pairs, p.items)), kThreads, smem, s, 2, p);
 }
 
-cudaError_t logit_maps(Params& P, const LogitParams& p) {
-  cudaError_t e = map_rows(&P.a[0], p.hidden, p.dim, p.tokens, p.ld_hidden, kStep, 128);
-  if (e == cudaSuccess) e = map_rows(&P.b[0], p.weight, p.dim, p.vocab, p.ld_weight, kStep, 128);
-  return e;
-}
-
-Params logit_tiles(const LogitParams& p, const Pipe& pipe, int64_t entries) {
-  Params P;
+// A launch over `entries` of the vocabulary (from p.v0): tiles, operand maps and words of the workspace.
+cudaError_t logit_launch(Params& P, const LogitParams& p, const Pipe& pipe) {
   std::memset(&P, 0, sizeof(P));
   P.l = p;
-  P.rows = cdiv(p.tokens, kTile);
-  P.cols = cdiv(entries, kTile);
-  P.items = P.rows * P.cols;
   P.nk = cdiv(p.dim, kStep);
   P.sched = pipe.sched;
   P.status = pipe.status;
   P.gmax = pipe.gmax;
-  return P;
+  int w_rows = 128, h_rows = 128;
+  if (thin_tokens(p.tokens)) {
+    const Thin x = thin_tiles(p.width, pipe.pairs);
+    P.thin_n = cdiv(p.tokens, 32) * 32;
+    P.thin_h = x.height;
+    P.rows = 1;
+    P.cols = P.items = x.tiles;
+    w_rows = P.thin_h / 2;
+    h_rows = P.thin_n / 2;
+    P.a_bytes = w_rows * kStep * 2;
+    P.stage_bytes = P.a_bytes + h_rows * kStep * 2;
+    P.stages = std::min(kMaxStages, kRingBytes / P.stage_bytes);
+  } else {
+    P.rows = cdiv(p.tokens, kTile);
+    P.cols = cdiv(p.width, kTile);
+    P.items = P.rows * P.cols;
+  }
+  cudaError_t e = map_rows(&P.a[0], p.hidden, p.dim, p.tokens, p.ld_hidden, kStep, h_rows);
+  if (e == cudaSuccess) e = map_rows(&P.b[0], p.weight, p.dim, p.vocab, p.ld_weight, kStep, w_rows);
+  return e;
 }
 
 }  // namespace
 
+bool thin_tokens(int64_t tokens) { return tokens <= kThin; }
+
+// Heights of at most 256 that spread the entries evenly over whole rounds of the pairs: 32000 entries on 76
+// pairs make two rounds of 216 rather than 125 tiles of 256, of which the second round has 49.
+Thin thin_tiles(int64_t entries, int pairs) {
+  const int rounds = cdiv(entries, int64_t(kTile) * pairs);
+  Thin x;
+  x.height = std::max(16, cdiv(cdiv(entries, int64_t(rounds) * pairs), 16) * 16);
+  x.tiles = cdiv(entries, x.height);
+  return x;
+}
+
+int logit_groups(int64_t tokens, int64_t vocab, int pairs) {
+  return thin_tokens(tokens) ? thin_tiles(vocab, pairs).tiles * 8 : cdiv(vocab, kGroup);
+}
+
 cudaError_t launch_logits(const LogitParams& p, const Pipe& pipe, cudaStream_t s) {
-  Params P = logit_tiles(p, pipe, p.vocab);
-  const cudaError_t e = logit_maps(P, p);
-  return e != cudaSuccess ? e : launch_pairs<kLogits>(P, pipe.pairs, s);
+  Params P;
+  const cudaError_t e = logit_launch(P, p, pipe);
+  if (e != cudaSuccess) return e;
+  return P.thin_n != 0 ? launch_pairs<kThinLogits>(P, pipe.pairs, s) : launch_pairs<kLogits>(P, pipe.pairs, s);
 }
 
 cudaError_t launch_dz(const LogitParams& p, const Pipe& pipe, cudaStream_t s) {
-  Params P = logit_tiles(p, pipe, p.width);
-  cudaError_t e = logit_maps(P, p);
-  if (e == cudaSuccess)
+  Params P;
+  cudaError_t e = logit_launch(P, p, pipe);
+  if (e == cudaSuccess && P.thin_n == 0)
     e = map_rows(&P.out[0], p.dz, p.ld_dz, p.tokens, p.ld_dz, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
-  return e != cudaSuccess ? e : launch_pairs<kDz>(P, pipe.pairs, s);
+  if (e != cudaSuccess) return e;
+  return P.thin_n != 0 ? launch_pairs<kThinDz>(P, pipe.pairs, s) : launch_pairs<kDz>(P, pipe.pairs, s);
 }
 
 // K is cut where whole dH tiles would keep a few pairs busy after all others are done: until a slice's K
 // is no longer than the launch's work per pair. Each slice has sums of its own, joined by the rounding
 // kernel in a fixed order.
 Slices dh_slices(int64_t tokens, int64_t dim, int64_t width, bool dweight, int pairs) {
+  // (a thin tile of dH reads as much of W as a full one, and less of everything else)
   const int64_t tiles = int64_t(cdiv(tokens, kTile)) * cdiv(dim, kTile);
   const int64_t nk = cdiv(width, kStep);
-  const int64_t dw = dweight ? int64_t(cdiv(width, kTile)) * cdiv(dim, kTile) * cdiv(tokens, kStep) : 0;
+  // a tile of dW takes the time of 4 stages at least: it writes 128 KB
+  const int64_t dw =
+      dweight ? int64_t(cdiv(width, kTile)) * cdiv(dim, kTile) * std::max(4, cdiv(tokens, kStep)) : 0;
   const int64_t fair = std::max<int64_t>(16, cdiv(tiles * nk + dw, pairs));
   Slices x;
   x.nk = static_cast<int32_t>(nk <= fair ? nk : cdiv(nk, cdiv(nk, fair)));
@@ -729,6 +1006,7 @@ cudaError_t launch_grads(const GradParams& p, const Pipe& pipe, cudaStream_t s) 
   P.l.dim = p.dim;
   P.l.v0 = p.v0;
   P.dim_tiles = cdiv(p.dim, kTile);
+  P.thin_n = thin_tokens(p.tokens) ? cdiv(p.tokens, 32) * 32 : 0;
   P.chunked = p.dim % 64 == 0;
   P.gscale = p.gscale;
   P.gmax = pipe.gmax;
@@ -744,11 +1022,13 @@ cudaError_t launch_grads(const GradParams& p, const Pipe& pipe, cudaStream_t s) 
     P.dh_items = P.dh_rows * P.dim_tiles * P.slices;
     P.dh_direct = p.dhidden != nullptr;
     P.first = p.first;
-    e = map_rows(&P.a[0], p.dz, p.ld_dz, p.tokens, p.ld_dz, kStep, 128);
+    P.dh_acc = p.dh_acc;
+    P.acc_ld = acc_ld;
+    e = map_rows(&P.a[0], p.dz, p.width, p.tokens, p.ld_dz, kStep, P.thin_n != 0 ? P.thin_n / 2 : 128);
     if (e == cudaSuccess) e = map_operand_mn(&P.b[0], p.weight, p.dim, p.vocab, p.ld_weight);
     if (e == cudaSuccess && P.dh_direct) {
       e = map_rows(&P.out[0], p.dhidden, p.dim, p.tokens, p.ld_dhidden, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
-    } else if (e == cudaSuccess) {
+    } else if (e == cudaSuccess && P.thin_n == 0) {
       const cuuint64_t dims[3] = {(cuuint64_t)p.dim, (cuuint64_t)p.tokens, (cuuint64_t)p.slices.count};
       const cuuint64_t strides[2] = {(cuuint64_t)acc_ld * 4, (cuuint64_t)acc_ld * 4 * p.tokens};
       const cuuint32_t box[3] = {16, 32, 1};
@@ -767,7 +1047,7 @@ cudaError_t launch_grads(const GradParams& p, const Pipe& pipe, cudaStream_t s) 
       e = map_rows(&P.out[1], p.dweight, p.dim, p.vocab, p.ld_dweight, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
     if (e != cudaSuccess) return e;
   }
-  return launch_pairs<kGrads>(P, pipe.pairs, s);
+  return P.thin_n != 0 ? launch_pairs<kThinGrads>(P, pipe.pairs, s) : launch_pairs<kGrads>(P, pipe.pairs, s);
 }
 
 }  // namespace head

@@ -195,11 +195,18 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     const int32_t* id = p.want.ids + t * p.want.top;
     const float* q = p.want.q + t * p.want.top;
     const int lane = threadIdx.x;
-    for (int k = lane; k < n; k += 32) hit_peak = fmaxf(hit_peak, zs[k]);
+    // entries that share an id: the first of them has the logit, and counts once
+    auto first_of = [&](int k) {
+      while (k > 0 && id[k - 1] == id[k]) --k;
+      return k;
+    };
+    for (int k = lane; k < n; k += 32) hit_peak = fmaxf(hit_peak, zs[first_of(k)]);
     for (int d = 16; d > 0; d >>= 1) hit_peak = fmaxf(hit_peak, __shfl_xor_sync(0xffffffffu, hit_peak, d));
     for (int k = lane; k < n; k += 32) {
-      if (k == 0 || id[k] != id[k - 1]) hit += expf(zs[k] - hit_peak);
-      dot = fmaf(q[k], zs[k] - hit_peak, dot);
+      const int f = first_of(k);
+      const float above = zs[f] - hit_peak;
+      if (f == k) hit += expf(above);
+      dot = fmaf(q[k], above, dot);
     }
     hit = warp_sum(hit);
     dot = warp_sum(dot);
