@@ -23,8 +23,8 @@ constexpr int64_t kPieceBytes = int64_t(512) << 20;
 constexpr int64_t kPieceStep = 256;
 constexpr int64_t kMaxPairs = 128;
 constexpr int64_t kFewTokens = 128;
-constexpr int64_t kMaxSlices = 152;
-constexpr int64_t kSliceBytes = 2 * kMaxSlices * 256 * 256 * 4;
+constexpr int64_t kMaxSlices = 2 * kMaxPairs + 256;  // few tokens: 2 per pair, and one more per column of tiles
+constexpr int64_t kSliceBytes = int64_t(kMaxSlices) * 256 * kFewTokens * 4;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -202,6 +202,8 @@ dmuon_status forward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, cons
   r.dot = dot;
   r.parts = p.parts;
   r.groups = head::logit_groups(tokens, H->vocab, H->pairs);
+  r.token_step = head::thin_tokens(tokens) ? r.groups : 1;
+  r.group_step = head::thin_tokens(tokens) ? 1 : tokens;
   r.picked = p.picked;
   r.entropy = reinterpret_cast<const float*>(H->ws + H->off_entropy);
   r.temperature = L.temperature;
@@ -310,7 +312,8 @@ extern "C" dmuon_status dmuon_head_create(int64_t max_tokens, int64_t vocab, int
   H->off_count = take(max_top > 0 ? 4 * max_tokens : 0);
   H->off_entropy = take(max_top > 0 ? 4 * max_tokens : 0);
   H->off_dz = take(2 * max_tokens * H->piece);
-  // dH's sums: one set where tokens are many; up to 2 x 76 tiles of 256 x 256 where K is cut into slices
+  // dH's sums: one set where tokens are many; where K is cut into slices, up to 2 tiles of 256 x 256 per pair,
+  // or 3 of 256 x 128 with few tokens
   const int64_t row = 4 * head::acc_pitch(dim);
   H->off_acc = take(std::max(row * max_tokens, std::min(row * max_tokens * kMaxSlices, kSliceBytes)));
   H->bytes = at;

@@ -53,7 +53,7 @@ struct LogitParams {
   float scale;             // 1 / temperature
   Wanted want;
   // forward
-  Part* parts;             // [groups][tokens]
+  Part* parts;             // [groups][tokens]; few tokens: [tokens][groups]
   float* picked;           // [tokens][want.top]: scaled logits of the wanted entries (below kSure: written here)
   int32_t v0, width;       // entries v0 .. v0 + width - 1 (forward: all)
   // backward
@@ -112,7 +112,8 @@ struct RowParams {
   int32_t vocab;
   DotParams dot;           // cross entropy: the target's logit
   Wanted want;
-  const Part* parts;
+  const Part* parts;       // of token t and group g at t * token_step + g * group_step
+  int64_t token_step, group_step;
   int32_t groups;
   const float* picked;
   const float* entropy;    // [tokens]: sum_k q log q (distillation)

@@ -37,11 +37,13 @@ constexpr int kTile = 256;                     // rows and columns of a pair's t
 constexpr int kStep = 64;                      // K per stage
 constexpr uint32_t kHalf = 128 * kStep * 2;    // a CTA's 128 rows (or columns) of an operand, one stage
 constexpr int kRingBytes = 6 * 2 * kHalf;      // operand stages: 6 of 32 KB, or more of fewer rows
+constexpr int kThinGradStages = 5;             // gradients of few tokens: 5, and wide boxes in the sixth's place
 constexpr int kMaxStages = 16;
 constexpr int kThin = 128;                     // up to so many tokens, they are the N side of the products
 constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
 constexpr int kBox = 32 * 64;                  // staging box of a TMA store: 32 rows of 64 bytes
+constexpr int kWideBox = 32 * 128;             // ... of 128 bytes (gradients of few tokens)
 constexpr int kRing = 8;
 constexpr uint32_t kRingReaders = 2 + 2 * kEpiWarps;
 constexpr uint32_t kTmemCols = 2 * kTile;
@@ -60,7 +62,9 @@ struct Params {
   int32_t items;
   int32_t rows, cols;      // logits, dz: tiles along the tokens and the vocabulary
   int32_t nk;              // K stages per tile
-  // grads: dH tiles come first (the longer ones), `slices` parts of K each, then dW tiles
+  // grads: tiles of dH (`slices` parts of K each) and of dW. The longer dH tiles come first; when the tokens
+  // are few they are dealt over the first `spread` places of the list (see where_is).
+  int32_t spread;
   int32_t dh_items, dh_rows, dh_nk, slices, slice_nk;
   int32_t dim_tiles;
   int32_t thin_n;          // tokens padded to 32 when they are the N side, else 0
@@ -127,6 +131,13 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, uin
       : "memory");
 }
 
+// Arrive on an mbarrier of either CTA of the pair (cluster address). What it orders are this thread's own
+// reads (a ring slot, TMEM) before the arrival, for which the scope of the CTA is enough; with the scope of the
+// cluster the arrival waits for every store in flight, which took 2300 of the 5900 cycles of a dW tile.
+__device__ __forceinline__ void arrive_pair(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // Adds a staged fp32 box to global memory, element by element.
 __device__ __forceinline__ void tma_add_3d(const void* map, const void* src, int x, int y, int z) {
   asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
@@ -140,6 +151,20 @@ __device__ __forceinline__ uint4* piece(uint8_t* box, int r, int c) {
   return reinterpret_cast<uint4*>(box + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
+// Boxes with 128-byte rows: piece c of row r at piece c ^ (r & 7) (128-byte swizzle).
+__device__ __forceinline__ uint4* wide_piece(uint8_t* box, int r, int c) {
+  return reinterpret_cast<uint4*>(box + r * 128 + ((c ^ (r & 7)) << 4));
+}
+
+// 8 consecutive values, scaled, as bf16.
+__device__ __forceinline__ uint4 rounded(const float (&v)[32], int at, float scale) {
+  uint4 u;
+  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(v[at + 2 * e] * scale, v[at + 2 * e + 1] * scale);
+  return u;
+}
+
 struct Where {
   int kind;        // grads: 0 = dH, 1 = dW
   int row, col;    // tile coordinates
@@ -151,9 +176,20 @@ struct Where {
 // work share the band's H (8 x 256 rows) and about ten blocks of W.
 constexpr int kBand = 8;
 
+// Gradients of few tokens: dH reads W and dW writes as much, so their tiles alternate, reads under writes
+// (writes alone go at about 3.6 TB/s, a mix at 6.6). 64 tokens x 128000 x 4096: 450 us with dH first.
 template <int MODE>
 __device__ __forceinline__ Where where_is(const Params& p, int w) {
   Where x;
+  if (MODE == kThinGrads) {
+    int before = p.dh_items;  // dH tiles among places 0 .. w - 1
+    bool dh = false;
+    if (w < p.spread) {
+      before = static_cast<int>(int64_t(w) * p.dh_items / p.spread);
+      dh = static_cast<int>((int64_t(w) + 1) * p.dh_items / p.spread) > before;
+    }
+    w = dh ? before : p.dh_items + (w - before);
+  }
   x.kind = 0;
   x.slice = 0;
   x.k0 = 0;
@@ -222,8 +258,8 @@ struct Cursor {
 };
 
 // One warp's part of a logits tile: 32 tokens, 128 entries from j0. `wait` returns false when the CTA gave up.
-template <class Wait>
-__device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, int j0, uint32_t tbase, Wait&& wait) {
+template <class Wait, class Free>
+__device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, int j0, uint32_t tbase, Wait&& wait, Free&& free) {
   const bool in = t < p.tokens;
   Cursor c;
   c.start(p.want, t, in, j0);
@@ -234,9 +270,10 @@ __device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, in
 #pragma unroll 1
   for (int ch = 0; ch < 4; ++ch) {
     const int jc = j0 + ch * 32;
-    if (jc >= p.vocab) break;
     float v[32];
     ptx::tmem_ld_32x32b_x32(tbase + ch * 32, v);
+    if (ch == 3) free();
+    if (jc >= p.vocab) continue;
 #pragma unroll
     for (int k = 0; k < 32; ++k) v[k] *= p.scale;
     if (jc + 32 > p.vocab) {
@@ -278,9 +315,9 @@ __device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, in
 
 // One warp's part of a dz tile. Row t's gradient relative to the largest: g (p - wanted), rounded to bf16
 // as the operand of the gradients' products (the only rounding of dz).
-template <class Wait>
+template <class Wait, class Free>
 __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t, int64_t t0, int j0, uint32_t tbase,
-                                         int lane, uint8_t* stg, uint32_t& nbox, Wait&& wait) {
+                                         int lane, uint8_t* stg, uint32_t& nbox, Wait&& wait, Free&& free) {
   const LogitParams& p = P.l;
   const bool in = t < p.tokens;
   Cursor c;
@@ -301,6 +338,7 @@ __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t,
     const int jc = j0 + ch * 32;
     float v[32];
     ptx::tmem_ld_32x32b_x32(tbase + ch * 32, v);
+    if (ch == 3) free();
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
       // a row that does not count, and entries past the vocabulary, give exact zeros whatever z is
@@ -324,13 +362,7 @@ __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t,
     if (lane == 0) ptx::bulk_wait_read<1>();  // the store that last read this box is done with it
     __syncwarp();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint4 u;
-      __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(v[q * 8 + 2 * e], v[q * 8 + 2 * e + 1]);
-      *piece(box, lane, q) = u;
-    }
+    for (int q = 0; q < 4; ++q) *piece(box, lane, q) = rounded(v, q * 8, 1.f);
     ptx::fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) {
@@ -389,9 +421,9 @@ __device__ __forceinline__ void each_wanted(const Wanted& w, Cursor& c, int firs
 
 // One warp's part of a thin logits tile: 32 entries from `first` (those before `end` are this tile's), the
 // blocks of 32 tokens that are its half's.
-template <class Wait>
+template <class Wait, class Free>
 __device__ __forceinline__ bool drain_thin_logits(const Params& P, const ThinTokens& tk, int first, int end, int group,
-                                                  int half, uint32_t tbase, int lane, Wait&& wait) {
+                                                  int half, uint32_t tbase, int lane, Wait&& wait, Free&& free) {
   const LogitParams& p = P.l;
   const bool lists = p.want.targets == nullptr;
   const int blocks = P.thin_n / 32;
@@ -408,9 +440,13 @@ __device__ __forceinline__ bool drain_thin_logits(const Params& P, const ThinTok
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int b = half + 2 * i;
-    if (b >= blocks) break;
+    if (b >= blocks) {
+      if (b < 2) free();  // this half has no tokens
+      break;
+    }
     float v[32];
     ptx::tmem_ld_32x32b_x32(tbase + b * 32, v);
+    if (b + 2 >= blocks) free();
 #pragma unroll
     for (int k = 0; k < 32; ++k) v[k] = v0 < end ? v[k] * p.scale : -INFINITY;
     if (!lists) {
@@ -436,15 +472,15 @@ __device__ __forceinline__ bool drain_thin_logits(const Params& P, const ThinTok
     for (int k = 0; k < 32; ++k) v[k] = ex2((v[k] - __shfl_sync(0xffffffffu, from, k)) * kLog2e);
     const float sum = columns(v, lane, [](float x, float y) { return x + y; });
     const int t = b * 32 + lane;
-    if (t < p.tokens) p.parts[int64_t(group) * p.tokens + t] = Part{peak, sum};
+    if (t < p.tokens) p.parts[int64_t(t) * (P.items * 8) + group] = Part{peak, sum};
   }
   return true;
 }
 
 // One warp's part of a thin dz tile; dz[t][v - v0] as in the other form.
-template <class Wait>
+template <class Wait, class Free>
 __device__ __forceinline__ bool drain_thin_dz(const Params& P, const ThinTokens& tk, int first, int end, int half,
-                                              uint32_t tbase, int lane, Wait&& wait) {
+                                              uint32_t tbase, int lane, Wait&& wait, Free&& free) {
   const LogitParams& p = P.l;
   const bool lists = p.want.targets == nullptr;
   const int blocks = P.thin_n / 32;
@@ -461,9 +497,13 @@ __device__ __forceinline__ bool drain_thin_dz(const Params& P, const ThinTokens&
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int b = half + 2 * i;
-    if (b >= blocks) break;
+    if (b >= blocks) {
+      if (b < 2) free();  // this half has no tokens
+      break;
+    }
     float v[32];
     ptx::tmem_ld_32x32b_x32(tbase + b * 32, v);
+    if (b + 2 >= blocks) free();
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
       const float g = tk.g[b * 32 + k];
@@ -492,16 +532,18 @@ __device__ __forceinline__ bool drain_thin_dz(const Params& P, const ThinTokens&
 }
 
 // One warp's part of a thin dH tile: 32 columns of dH (lane) by the tokens, into the slice's fp32 sums.
-template <class Wait>
+template <class Wait, class Free>
 __device__ __forceinline__ bool drain_thin_dh(const Params& P, const Where& x, int d0, int half, uint32_t tbase,
-                                              int lane, Wait&& wait) {
+                                              int lane, Wait&& wait, Free&& free) {
   if (!wait()) return false;
   ptx::tc_fence_after();
   const int d = d0 + lane;
   float* acc = P.dh_acc + int64_t(x.slice) * P.l.tokens * P.acc_ld + d;
+  if (half >= P.thin_n / 32) free();  // this half has no tokens
   for (int b = half; b < P.thin_n / 32; b += 2) {
     float v[32];
     ptx::tmem_ld_32x32b_x32(tbase + b * 32, v);
+    if (b + 2 >= P.thin_n / 32) free();
     if (d < P.l.dim) {
 #pragma unroll
       for (int k = 0; k < 32; ++k)
@@ -515,9 +557,9 @@ __device__ __forceinline__ bool drain_thin_dh(const Params& P, const Where& x, i
 }
 
 // One warp's part of a gradient tile: 32 rows from r0, 128 columns from d0.
-template <class Wait>
+template <class Wait, class Free>
 __device__ __forceinline__ bool drain_grads(const Params& P, const Where& x, int64_t r0, int64_t r_lim, int d0,
-                                            uint32_t tbase, int lane, uint8_t* stg, uint32_t& nbox, Wait&& wait) {
+                                            uint32_t tbase, int lane, uint8_t* stg, uint32_t& nbox, Wait&& wait, Free&& free) {
   const bool sums = x.kind == 0 && !P.dh_direct;
   const float scale = sums ? 1.f : *P.gmax * P.gscale;
   if (!wait()) return false;
@@ -527,6 +569,7 @@ __device__ __forceinline__ bool drain_grads(const Params& P, const Where& x, int
     const int dc = d0 + ch * 32;
     float v[32];
     ptx::tmem_ld_32x32b_x32(tbase + ch * 32, v);
+    if (ch == 3) free();
     const bool in = r0 < r_lim && dc < P.l.dim;
     if (sums) {
 #pragma unroll
@@ -556,14 +599,7 @@ __device__ __forceinline__ bool drain_grads(const Params& P, const Where& x, int
       if (lane == 0) ptx::bulk_wait_read<1>();
       __syncwarp();
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint4 u;
-        __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          h[e] = __floats2bfloat162_rn(v[q * 8 + 2 * e] * scale, v[q * 8 + 2 * e + 1] * scale);
-        *piece(box, lane, q) = u;
-      }
+      for (int q = 0; q < 4; ++q) *piece(box, lane, q) = rounded(v, q * 8, scale);
       ptx::fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) {
@@ -576,13 +612,42 @@ __device__ __forceinline__ bool drain_grads(const Params& P, const Where& x, int
   return true;
 }
 
+// The same for dW of few tokens, whose product is one or two K stages, so that the epilogue sets the pace: all
+// 128 columns are staged before one fence and two stores of 64 columns. v0: first row, below v_lim if any is.
+template <class Wait, class Free>
+__device__ __forceinline__ bool drain_thin_dw(const Params& P, int v0, int v_lim, int d0, uint32_t tbase, int lane,
+                                              uint8_t* stg, Wait&& wait, Free&& free) {
+  const float scale = *P.gmax * P.gscale;
+  if (lane == 0) ptx::bulk_wait_read<0>();  // the last tile's stores are done with the boxes
+  __syncwarp();
+  if (!wait()) return false;
+  ptx::tc_fence_after();
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch) {
+    float v[32];
+    ptx::tmem_ld_32x32b_x32(tbase + ch * 32, v);
+    if (ch == 3) free();
+    uint8_t* box = stg + (ch >> 1) * kWideBox;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *wide_piece(box, lane, (ch & 1) * 4 + q) = rounded(v, q * 8, scale);
+  }
+  ptx::fence_proxy_async_shared();
+  __syncwarp();
+  if (lane == 0) {
+    if (v0 < v_lim && d0 < P.l.dim) ptx::tma_store_2d(&P.out[1], stg, d0, v0);
+    if (v0 < v_lim && d0 + 64 < P.l.dim) ptx::tma_store_2d(&P.out[1], stg + kWideBox, d0 + 64, v0);
+    ptx::bulk_commit();
+  }
+  return true;
+}
+
 // ------------------------------------------------------------------ the kernel
 __device__ __forceinline__ bool take(Shared* sh, uint32_t j, int& w, uint32_t lead_empty, volatile int* abortf,
                                      const Params& p) {
   const uint32_t slot = j % kRing;
   if (!ptx::mbar_wait_cluster(&sh->ring_full[slot], (j / kRing) & 1u, abortf, p.status, kWaitNs)) return false;
   w = *reinterpret_cast<volatile int*>(&sh->ring[slot]);
-  ptx::mbar_arrive_cluster(lead_empty + slot * static_cast<uint32_t>(sizeof(uint64_t)));
+  arrive_pair(lead_empty + slot * static_cast<uint32_t>(sizeof(uint64_t)));
   return true;
 }
 
@@ -592,11 +657,13 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr bool thin = MODE == kThinLogits || MODE == kThinDz;
   constexpr bool grads = MODE == kGrads || MODE == kThinGrads;
-  Shared* sh = reinterpret_cast<Shared*>(base + kRingBytes);
-  uint8_t* boxes = base + kRingBytes + 1024;
+  constexpr int ring_bytes = MODE == kThinGrads ? kThinGradStages * 2 * kHalf : kRingBytes;
+  constexpr int box_bytes = MODE == kThinGrads ? kWideBox : kBox;
+  Shared* sh = reinterpret_cast<Shared*>(base + ring_bytes);
+  uint8_t* boxes = base + ring_bytes + 1024;
   ThinTokens& tk = *reinterpret_cast<ThinTokens*>(boxes);  // thin launches stage no boxes
   // operand ring: fixed at compile time but for the thin logits and dz, whose stages hold fewer rows
-  const uint32_t stages = thin ? p.stages : kRingBytes / (2 * kHalf);
+  const uint32_t stages = thin ? p.stages : ring_bytes / (2 * kHalf);
   const uint32_t stage_bytes = thin ? p.stage_bytes : 2 * kHalf;
   const uint32_t a_bytes = thin ? p.a_bytes : kHalf;
   const int rank = static_cast<int>(ptx::cluster_ctarank());
@@ -763,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lead_tempty = ptx::mapa_shared(ptx::smem_u32(&sh->tempty[0]), 0);
-    uint8_t* stg = boxes + (warp - 2) * (2 * kBox);
+    uint8_t* stg = boxes + (warp - 2) * (2 * box_bytes);
     float gmax = 1.f;
     if (MODE == kDz || MODE == kThinDz) {  // under the first tile's products
       float m = 0.f;
@@ -816,30 +883,34 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
       auto wait = [&]() {
         return ptx::mbar_wait_cluster(&sh->tfull[acc], (local >> 1) & 1u, abortf, p.status, kWaitNs);
       };
+      auto free = [&]() {  // the accumulator has been read
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_pair(lead_tempty + acc * static_cast<uint32_t>(sizeof(uint64_t)));
+      };
       bool ok;
       if (thin) {
         const int base_v = p.l.v0 + x.col * p.thin_h + rank * (p.thin_h / 2);
         const int last = min(min(base_v + p.thin_h / 2, p.l.v0 + p.l.width), base_v + q * 32 + 32);
         const uint32_t rows = tmem + acc * kTile + (static_cast<uint32_t>(q * 32) << 16);
         if (MODE == kThinLogits)
-          ok = drain_thin_logits(p, tk, base_v + q * 32, last, (x.col * 2 + rank) * 4 + q, half, rows, lane, wait);
+          ok = drain_thin_logits(p, tk, base_v + q * 32, last, (x.col * 2 + rank) * 4 + q, half, rows, lane, wait, free);
         else
-          ok = drain_thin_dz(p, tk, base_v + q * 32, last, half, rows, lane, wait);
+          ok = drain_thin_dz(p, tk, base_v + q * 32, last, half, rows, lane, wait, free);
       } else if (MODE == kThinGrads && x.kind == 0) {
         const uint32_t rows = tmem + acc * kTile + (static_cast<uint32_t>(q * 32) << 16);
-        ok = drain_thin_dh(p, x, x.col * kTile + rank * 128 + q * 32, half, rows, lane, wait);
+        ok = drain_thin_dh(p, x, x.col * kTile + rank * 128 + q * 32, half, rows, lane, wait, free);
       } else if (MODE == kLogits) {
-        ok = drain_logits(p.l, r0 + lane, c0, tbase, wait);
+        ok = drain_logits(p.l, r0 + lane, c0, tbase, wait, free);
       } else if (MODE == kDz) {
-        ok = drain_dz(p, gmax, r0 + lane, r0, p.l.v0 + c0, tbase, lane, stg, nbox, wait);
+        ok = drain_dz(p, gmax, r0 + lane, r0, p.l.v0 + c0, tbase, lane, stg, nbox, wait, free);
+      } else if (MODE == kThinGrads) {
+        ok = drain_thin_dw(p, p.l.v0 + static_cast<int>(r0), p.l.vocab, c0, tbase, lane, stg, wait, free);
       } else {
         const int64_t row = r0 + (x.kind == 1 ? p.l.v0 : 0);
-        ok = drain_grads(p, x, row, x.kind == 1 ? p.l.vocab : p.l.tokens, c0, tbase, lane, stg, nbox, wait);
+        ok = drain_grads(p, x, row, x.kind == 1 ? p.l.vocab : p.l.tokens, c0, tbase, lane, stg, nbox, wait, free);
       }
       if (!ok) break;
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(lead_tempty + acc * static_cast<uint32_t>(sizeof(uint64_t)));
     }
     ptx::bulk_wait_all();
   }
@@ -910,6 +981,8 @@ int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
 template <int MODE>
 cudaError_t launch_pairs(const Params& p, int pairs, cudaStream_t s) {
+  // (gradients of few tokens: one stage less and boxes twice as large, the same total)
+  static_assert(2 * kHalf == kEpiWarps * 2 * (kWideBox - kBox), "both layouts fill the same shared memory");
   const size_t smem = 1024 + kRingBytes + 1024 + kEpiWarps * 2 * kBox;
   cudaError_t e = cudaFuncSetAttribute(head_pair_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
@@ -991,7 +1064,9 @@ Slices dh_slices(int64_t tokens, int64_t dim, int64_t width, bool dweight, int p
   // a tile of dW takes the time of 4 stages at least: it writes 128 KB
   const int64_t dw =
       dweight ? int64_t(cdiv(width, kTile)) * cdiv(dim, kTile) * std::max(4, cdiv(tokens, kStep)) : 0;
-  const int64_t fair = std::max<int64_t>(16, cdiv(tiles * nk + dw, pairs));
+  // (few tokens: twice as many, as their sums are small and a tile that starts late should end early)
+  const int64_t share = thin_tokens(tokens) ? 2 * pairs : pairs;
+  const int64_t fair = std::max<int64_t>(16, cdiv(tiles * nk + dw, share));
   Slices x;
   x.nk = static_cast<int32_t>(nk <= fair ? nk : cdiv(nk, cdiv(nk, fair)));
   x.count = cdiv(nk, x.nk);
@@ -1044,9 +1119,12 @@ cudaError_t launch_grads(const GradParams& p, const Pipe& pipe, cudaStream_t s) 
     e = map_blocks(&P.a[1], p.dz, p.ld_dz, p.tokens, p.ld_dz);
     if (e == cudaSuccess) e = map_operand_mn(&P.b[1], p.hidden, p.dim, p.tokens, p.ld_hidden);
     if (e == cudaSuccess)
-      e = map_rows(&P.out[1], p.dweight, p.dim, p.vocab, p.ld_dweight, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+      e = P.thin_n != 0 ? map_rows(&P.out[1], p.dweight, p.dim, p.vocab, p.ld_dweight, 64, 32)
+                        : map_rows(&P.out[1], p.dweight, p.dim, p.vocab, p.ld_dweight, 32, 32,
+                                   CU_TENSOR_MAP_SWIZZLE_64B);
     if (e != cudaSuccess) return e;
   }
+  P.spread = std::max(P.dh_items, P.items / 2);
   return P.thin_n != 0 ? launch_pairs<kThinGrads>(P, pipe.pairs, s) : launch_pairs<kGrads>(P, pipe.pairs, s);
 }
 

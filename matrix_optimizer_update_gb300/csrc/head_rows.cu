@@ -52,18 +52,20 @@ __global__ void __launch_bounds__(256) targets_kernel(const __grid_constant__ Do
 }
 
 // ------------------------------------------------------------------ teacher
-// One block per token, one thread per entry of a list padded to a power of two
-// (at most 256): a bitonic sort by id in shared memory, then the softmax over
-// the entries that count. Entries that do not count sort last, with id vocab.
-__global__ void teacher_kernel(const __grid_constant__ TeacherParams p) {
-  extern __shared__ unsigned char raw[];
-  const int n = blockDim.x;
-  int* id = reinterpret_cast<int*>(raw);
-  float* lg = reinterpret_cast<float*>(id + n);
-  __shared__ float red[8];
+// One block per token, a thread per entry and at least 4 warps. Each entry of the list finds its place in the order by id by counting the
+// entries before it (no sorting network: with 128 entries 128 compares and one barrier against 28 barriers),
+// then a softmax over the entries that count, and the logits of the likeliest ones, a warp for each. Entries
+// that do not count come last, with id vocab.
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) teacher_kernel(const __grid_constant__ TeacherParams p) {
+  __shared__ uint64_t key[kThreads];
+  __shared__ int id[kThreads];
+  __shared__ float lg[kThreads];
+  __shared__ float red[3][kThreads / 32];
   follow();
   const int64_t t = blockIdx.x;
-  const int k = threadIdx.x;
+  const int k = threadIdx.x, lane = k & 31, warp = k >> 5;
+  constexpr int warps = kThreads / 32;
   int my = p.vocab;
   float l = kNegInf;
   if (k < p.top) {
@@ -74,76 +76,70 @@ __global__ void teacher_kernel(const __grid_constant__ TeacherParams p) {
       l = x;
     }
   }
-  id[k] = my;
-  lg[k] = l;
+  // by id, and entries of equal id by their logits' bits, so that the result does not depend on the order
+  // they came in
+  const uint64_t mine = (static_cast<uint64_t>(my) << 32) | __float_as_uint(l);
+  key[k] = mine;
   __syncthreads();
-  for (int size = 2; size <= n; size <<= 1) {
-    for (int d = size >> 1; d > 0; d >>= 1) {
-      const int o = k ^ d;
-      if (o > k) {
-        const bool up = (k & size) == 0;
-        const int a = id[k], b = id[o];
-        // entries of equal id keep an order of their own (by logit), so that the result does not
-        // depend on the order they came in
-        const bool swap = up ? (a > b || (a == b && lg[k] > lg[o])) : (a < b || (a == b && lg[k] < lg[o]));
-        if (swap) {
-          id[k] = b;
-          id[o] = a;
-          const float x = lg[k];
-          lg[k] = lg[o];
-          lg[o] = x;
-        }
-      }
-      __syncthreads();
-    }
+  if (k < p.top) {
+    int place = 0;
+#pragma unroll 8
+    for (int j = 0; j < p.top; ++j) place += key[j] < mine || (key[j] == mine && j < k);
+    id[place] = my;
+    lg[place] = l;
   }
-  const int lane = k & 31, warp = k >> 5, warps = (n + 31) >> 5;
-  auto reduce = [&](float v, bool max) {
+  __syncthreads();
+  const bool on = k < p.top && id[k] < p.vocab;
+  l = on ? lg[k] : kNegInf;
+  auto block = [&](float v, int slot, bool max) {
     for (int d = 16; d > 0; d >>= 1) {
       const float o = __shfl_xor_sync(0xffffffffu, v, d);
       v = max ? fmaxf(v, o) : v + o;
     }
-    if (lane == 0) red[warp] = v;
+    if (lane == 0) red[slot][warp] = v;
     __syncthreads();
-    v = red[0];
-    for (int w = 1; w < warps; ++w) v = max ? fmaxf(v, red[w]) : v + red[w];
-    __syncthreads();
+    v = red[slot][0];
+    for (int w = 1; w < warps; ++w) v = max ? fmaxf(v, red[slot][w]) : v + red[slot][w];
     return v;
   };
-  const bool on = id[k] < p.vocab;
-  l = lg[k];
   // a NaN logit makes its whole row NaN through the sum
-  const float best = reduce(on ? l : kNegInf, true);
+  const float best = block(l, 0, true);
   const float e = on ? expf((l - best) * p.scale) : 0.f;
-  const float sum = reduce(e, false);
+  const float sum = block(e, 1, false);
   const float q = on ? e / sum : 0.f;
-  const float ent = reduce(q > 0.f ? q * logf(q) : q, false);
-  const float count = reduce(on ? 1.f : 0.f, false);
+  if (k < p.top) lg[k] = q;
+  const float ent = block(q > 0.f ? q * logf(q) : q, 2, false);
+  const int count = __syncthreads_count(on);
   if (k < p.top) {
     p.out_ids[t * p.top + k] = id[k];
     p.out_q[t * p.top + k] = q;
   }
   if (k == 0) {
-    p.out_count[t] = static_cast<int>(count);
+    p.out_count[t] = count;
     p.out_entropy[t] = ent;
   }
-  // the logits of the likeliest entries, a warp for each
-  lg[k] = q;
-  __syncthreads();
+  // lane j looks at entries j, j + 32, ...; warp w takes the w-th, w + 8-th ... of the likely ones
   int seen = 0;
-  for (int e = 0; e < static_cast<int>(count); ++e) {
-    if (!(lg[e] >= kSure)) continue;
-    if (seen++ % warps != warp) continue;
-    const float z = warp_sum(dot_part(p.dot, t, id[e], lane, 32)) * p.dot.scale;
-    if (lane == 0) p.picked[t * p.top + e] = z;
+  for (int e0 = 0; e0 < count; e0 += 32) {
+    unsigned likely = __ballot_sync(0xffffffffu, e0 + lane < count && lg[e0 + lane] >= kSure);
+    while (likely != 0u) {
+      const int at = e0 + __ffs(likely) - 1;
+      likely &= likely - 1u;
+      if (seen++ % warps != warp) continue;
+      const float z = warp_sum(dot_part(p.dot, t, id[at], lane, 32)) * p.dot.scale;
+      if (lane == 0) p.picked[t * p.top + at] = z;
+    }
   }
 }
 
 // ------------------------------------------------------------------ rows
-// One block per token. The sum over the vocabulary is kept in two shares, of
-// the wanted entries and of all others, so that a loss that is small beside
-// the logits is formed from their ratio (log1p) and not as a difference.
-constexpr int kRowThreads = 128;
+// The sum over the vocabulary is kept in two shares, of the wanted entries and of all others, so that a loss
+// that is small beside the logits is formed from their ratio (log1p) and not as a difference.
+//
+// A block takes kTokens tokens: 8 where the groups' sums lie token by token (8 threads read a 64-byte piece
+// of each group), 1 where the tokens are few and each has its groups' sums in a row. Four sums are joined at
+// a time, so that their loads are in flight together.
+constexpr int kRowThreads = 256;
 
 __device__ __forceinline__ void join(float& peak, float& sum, float peak2, float sum2) {
   const float m = fmaxf(peak, peak2);
@@ -152,41 +148,67 @@ __device__ __forceinline__ void join(float& peak, float& sum, float peak2, float
   peak = m;
 }
 
+template <int kTokens>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ RowParams p) {
-  __shared__ float s_peak[kRowThreads / 32], s_sum[kRowThreads / 32], s_dot[kRowThreads / 32];
+  constexpr int kLanes = kRowThreads / kTokens;  // threads that share a token's groups
+  constexpr int kWarps = kRowThreads / 32;
+  __shared__ float s_peak[kWarps][kTokens], s_sum[kWarps][kTokens], s_dot[kWarps];
   follow();
-  const int64_t t = blockIdx.x;
-  float peak = kNegInf, sum = 0.f;
-  for (int g = threadIdx.x; g < p.groups; g += kRowThreads) {
-    const Part q = p.parts[int64_t(g) * p.tokens + t];
-    join(peak, sum, q.peak, q.sum);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  {
+    const int64_t t = int64_t(blockIdx.x) * kTokens + threadIdx.x % kTokens;
+    float peak = kNegInf, sum = 0.f;
+    if (t < p.tokens) {
+      const Part* parts = p.parts + t * p.token_step;
+      for (int g = threadIdx.x / kTokens; g < p.groups; g += 4 * kLanes) {
+        Part q[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          q[u] = g + u * kLanes < p.groups ? parts[(g + u * kLanes) * p.group_step] : Part{kNegInf, 0.f};
+        const float m = fmaxf(fmaxf(q[0].peak, q[1].peak), fmaxf(q[2].peak, q[3].peak));
+        if (m == kNegInf) {
+          sum += q[0].sum + q[1].sum + q[2].sum + q[3].sum;  // zeros, or NaN to pass on
+          continue;
+        }
+        float s = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s += q[u].sum * expf(q[u].peak - m);
+        join(peak, sum, m, s);
+      }
+    }
+    for (int d = 16; d >= kTokens; d >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, peak, d), s2 = __shfl_xor_sync(0xffffffffu, sum, d);
+      join(peak, sum, m2, s2);
+    }
+    if (lane < kTokens) {
+      s_peak[warp][lane] = peak;
+      s_sum[warp][lane] = sum;
+    }
   }
-  for (int d = 16; d > 0; d >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, peak, d), s2 = __shfl_xor_sync(0xffffffffu, sum, d);
-    join(peak, sum, m2, s2);
-  }
-  if ((threadIdx.x & 31) == 0) {
-    s_peak[threadIdx.x >> 5] = peak;
-    s_sum[threadIdx.x >> 5] = sum;
-  }
+  // from here a warp per token
+  const int64_t t = int64_t(blockIdx.x) * kTokens + (kTokens == 1 ? 0 : warp);
+  const bool xent = p.want.targets != nullptr;
   float z = 0.f;
   int64_t y = -1;
-  if (p.want.targets != nullptr) {
+  if (xent && t < p.tokens) {
     y = p.want.targets[t];
     if (y >= p.vocab) y = -1;
-    if (y >= 0) z = warp_sum(dot_part(p.dot, t, y, threadIdx.x, kRowThreads));
-    if ((threadIdx.x & 31) == 0) s_dot[threadIdx.x >> 5] = z;
+    if (y >= 0)
+      z = warp_sum(kTokens == 1 ? dot_part(p.dot, t, y, threadIdx.x, kRowThreads) : dot_part(p.dot, t, y, lane, 32));
   }
+  if (lane == 0) s_dot[warp] = z;
   __syncthreads();
-  if (threadIdx.x >= 32) return;
-  for (int w = 1; w < kRowThreads / 32; ++w) join(peak, sum, s_peak[w], s_sum[w]);
-  // peak, sum: the others (warp 0 has them in every lane). Now the wanted entries.
+  const int mine = kTokens == 1 ? 0 : warp;
+  if (warp >= kTokens || t >= p.tokens) return;
+  float peak = s_peak[0][mine], sum = s_sum[0][mine];
+  for (int w = 1; w < kWarps; ++w) join(peak, sum, s_peak[w][mine], s_sum[w][mine]);
+  // peak, sum: the others. Now the wanted entries.
   float hit_peak = kNegInf, hit = 0.f, dot = 0.f;
   int n;
-  if (p.want.targets != nullptr) {
+  if (xent) {
     n = y >= 0;
-    z = s_dot[0];
-    for (int w = 1; w < kRowThreads / 32; ++w) z += s_dot[w];
+    if (kTokens == 1)
+      for (int w = 1; w < kWarps; ++w) z += s_dot[w];
     hit_peak = z * p.dot.scale;
     hit = 1.f;
   } else {
@@ -194,7 +216,6 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     const float* zs = p.picked + t * p.want.top;
     const int32_t* id = p.want.ids + t * p.want.top;
     const float* q = p.want.q + t * p.want.top;
-    const int lane = threadIdx.x;
     // entries that share an id: the first of them has the logit, and counts once
     auto first_of = [&](int k) {
       while (k > 0 && id[k - 1] == id[k]) --k;
@@ -211,7 +232,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     hit = warp_sum(hit);
     dot = warp_sum(dot);
   }
-  if (threadIdx.x != 0) return;
+  if (lane != 0) return;
   if (n == 0) {
     p.lse[t] = peak + logf(sum);
     p.loss[t] = 0.f;
@@ -228,7 +249,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     rest = lse - lse_hit;
   }
   p.lse[t] = lse;
-  if (p.want.targets != nullptr) {
+  if (xent) {
     p.loss[t] = rest;
   } else {
     // sum_k q log q - q (z - hit_peak) + log(hit): the divergence within the list; rest: of the list's share
@@ -268,9 +289,10 @@ __global__ void __launch_bounds__(256) round_kernel(const float* acc, int slices
 }  // namespace
 
 cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t s) {
-  int n = 32;
-  while (n < p.top) n <<= 1;
-  return launch_follow(teacher_kernel, dim3(static_cast<unsigned>(p.tokens)), n, 8 * n, s, 1, p);
+  const dim3 grid(static_cast<unsigned>(p.tokens));
+  if (p.top <= 128) return launch_follow(teacher_kernel<128>, grid, 128, 0, s, 1, p);
+  static_assert(kMaxTop <= 256, "a thread per entry");
+  return launch_follow(teacher_kernel<256>, grid, 256, 0, s, 1, p);
 }
 
 cudaError_t launch_targets(const DotParams& d, const int64_t* targets, int64_t tokens, int32_t vocab, float* picked,
@@ -280,7 +302,9 @@ cudaError_t launch_targets(const DotParams& d, const int64_t* targets, int64_t t
 }
 
 cudaError_t launch_rows(const RowParams& p, cudaStream_t s) {
-  return launch_follow(rows_kernel, dim3(static_cast<unsigned>(p.tokens)), kRowThreads, 0, s, 1, p);
+  if (p.group_step == 1)
+    return launch_follow(rows_kernel<1>, dim3(static_cast<unsigned>(p.tokens)), kRowThreads, 0, s, 1, p);
+  return launch_follow(rows_kernel<8>, dim3(static_cast<unsigned>((p.tokens + 7) / 8)), kRowThreads, 0, s, 1, p);
 }
 
 cudaError_t launch_round(const float* acc, int slices, int64_t tokens, int32_t dim, float gscale, const float* gmax,
