@@ -23,8 +23,8 @@ constexpr int64_t kPieceBytes = int64_t(512) << 20;
 constexpr int64_t kPieceStep = 256;
 constexpr int64_t kMaxPairs = 128;
 constexpr int64_t kFewTokens = 128;
-constexpr int64_t kMaxSlices = 2 * kMaxPairs + 256;  // few tokens: 2 per pair, and one more per column of tiles
-constexpr int64_t kSliceBytes = int64_t(kMaxSlices) * 256 * kFewTokens * 4;
+constexpr int64_t kMaxSlices = 2 * kMaxPairs;
+constexpr int64_t kSliceBytes = kMaxSlices * 256 * 256 * 4;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -118,20 +118,14 @@ dmuon_status check_loss(dmuon_head_t H, const Loss& L, int64_t tokens, bool dist
   return DMUON_OK;
 }
 
-// What the kernels are told of the loss; for distillation the lists are sorted into the workspace first. The
-// logits of the likeliest entries go to the picked ones (a forward cross entropy forms them in its last kernel).
-dmuon_status prepare_wanted(dmuon_head_t H, const Loss& L, int64_t tokens, const head::DotParams& dot, bool backward,
+// What the kernels are told of the loss; for distillation the lists are sorted into the workspace first.
+dmuon_status prepare_wanted(dmuon_head_t H, const Loss& L, int64_t tokens, const head::DotParams& in,
                             head::Wanted* w, cudaStream_t s) {
   *w = head::Wanted{};
   w->vocab = static_cast<int32_t>(H->vocab);
-  float* picked = reinterpret_cast<float*>(H->ws + H->off_picked);
   if (L.targets != nullptr) {
     w->targets = L.targets;
     w->top = 1;
-    if (backward) {
-      const cudaError_t e = head::launch_targets(dot, L.targets, tokens, w->vocab, picked, s);
-      if (e != cudaSuccess) return cuda_refuse(e, "target kernel");
-    }
     return DMUON_OK;
   }
   head::TeacherParams p{};
@@ -145,8 +139,8 @@ dmuon_status prepare_wanted(dmuon_head_t H, const Loss& L, int64_t tokens, const
   p.out_q = reinterpret_cast<float*>(H->ws + H->off_q);
   p.out_count = reinterpret_cast<int32_t*>(H->ws + H->off_count);
   p.out_entropy = reinterpret_cast<float*>(H->ws + H->off_entropy);
-  p.dot = dot;
-  p.picked = picked;
+  p.dot = in;
+  p.picked = reinterpret_cast<float*>(H->ws + H->off_picked);
   cudaError_t e = head::launch_teacher(p, s);
   if (e != cudaSuccess) return cuda_refuse(e, "teacher kernel");
   w->ids = p.out_ids;
@@ -157,25 +151,15 @@ dmuon_status prepare_wanted(dmuon_head_t H, const Loss& L, int64_t tokens, const
 }
 
 head::LogitParams logit_params(dmuon_head_t H, const void* hidden, int64_t ld_hidden, const void* weight,
-                               int64_t ld_weight, int64_t tokens, const Loss& L, const head::Wanted& w) {
+                               int64_t ld_weight, int64_t tokens, const Loss& L) {
   head::LogitParams p{};
-  p.hidden = static_cast<const head::bf16*>(hidden);
-  p.weight = static_cast<const head::bf16*>(weight);
-  p.ld_hidden = ld_hidden;
-  p.ld_weight = ld_weight;
+  p.in = {static_cast<const head::bf16*>(hidden), static_cast<const head::bf16*>(weight), ld_hidden, ld_weight,
+          static_cast<int32_t>(H->dim), 1.f / L.temperature};
   p.tokens = tokens;
   p.vocab = static_cast<int32_t>(H->vocab);
-  p.dim = static_cast<int32_t>(H->dim);
-  p.scale = 1.f / L.temperature;
-  p.want = w;
   p.width = p.vocab;
+  p.picked = reinterpret_cast<float*>(H->ws + H->off_picked);
   return p;
-}
-
-head::DotParams dot_params(dmuon_head_t H, const void* hidden, int64_t ld_hidden, const void* weight,
-                           int64_t ld_weight, const Loss& L) {
-  return {static_cast<const head::bf16*>(hidden), static_cast<const head::bf16*>(weight), ld_hidden, ld_weight,
-          static_cast<int32_t>(H->dim), 1.f / L.temperature};
 }
 
 dmuon_status forward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, const void* weight, int64_t ld_weight,
@@ -187,19 +171,16 @@ dmuon_status forward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, cons
   if (loss == nullptr || lse == nullptr || misaligned(loss, 4) || misaligned(lse, 4))
     return refuse(DMUON_ERR_INVALID_ARG, "loss or lse is NULL or not 4-byte aligned");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  head::Wanted w;
-  const head::DotParams dot = dot_params(H, hidden, ld_hidden, weight, ld_weight, L);
-  if ((st = prepare_wanted(H, L, tokens, dot, false, &w, s)) != DMUON_OK) return st;
-  head::LogitParams p = logit_params(H, hidden, ld_hidden, weight, ld_weight, tokens, L, w);
+  head::LogitParams p = logit_params(H, hidden, ld_hidden, weight, ld_weight, tokens, L);
+  if ((st = prepare_wanted(H, L, tokens, p.in, &p.want, s)) != DMUON_OK) return st;
   p.parts = reinterpret_cast<head::Part*>(H->ws + H->off_parts);
-  p.picked = reinterpret_cast<float*>(H->ws + H->off_picked);
   cudaError_t e = head::launch_logits(p, H->pipe(), s);
   if (e != cudaSuccess) return cuda_refuse(e, "logits kernel");
   head::RowParams r{};
   r.tokens = tokens;
   r.vocab = p.vocab;
-  r.want = w;
-  r.dot = dot;
+  r.want = p.want;
+  r.dot = p.in;
   r.parts = p.parts;
   r.groups = head::logit_groups(tokens, H->vocab, H->pairs);
   r.token_step = head::thin_tokens(tokens) ? r.groups : 1;
@@ -232,24 +213,20 @@ dmuon_status backward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, con
   if (lse == nullptr || grad_loss == nullptr || misaligned(lse, 4) || misaligned(grad_loss, 4))
     return refuse(DMUON_ERR_INVALID_ARG, "lse or grad_loss is NULL or not 4-byte aligned");
   if (dhidden == nullptr && dweight == nullptr) return ok();
-  head::Wanted w;
-  if ((st = prepare_wanted(H, L, tokens, dot_params(H, hidden, ld_hidden, weight, ld_weight, L), true, &w, s)) !=
-      DMUON_OK)
-    return st;
-  head::LogitParams p = logit_params(H, hidden, ld_hidden, weight, ld_weight, tokens, L, w);
-  p.picked = reinterpret_cast<float*>(H->ws + H->off_picked);
+  head::LogitParams p = logit_params(H, hidden, ld_hidden, weight, ld_weight, tokens, L);
+  if ((st = prepare_wanted(H, L, tokens, p.in, &p.want, s)) != DMUON_OK) return st;
   p.lse = lse;
   p.grad = grad_loss;
   p.dz = reinterpret_cast<head::bf16*>(H->ws + H->off_dz);
   p.ld_dz = H->piece;
   head::GradParams g{};
-  g.hidden = p.hidden;
-  g.weight = p.weight;
+  g.hidden = p.in.hidden;
+  g.weight = p.in.weight;
   g.ld_hidden = ld_hidden;
   g.ld_weight = ld_weight;
   g.tokens = tokens;
   g.vocab = p.vocab;
-  g.dim = p.dim;
+  g.dim = p.in.dim;
   g.dz = p.dz;
   g.ld_dz = p.ld_dz;
   g.gscale = L.temperature;
@@ -312,8 +289,7 @@ extern "C" dmuon_status dmuon_head_create(int64_t max_tokens, int64_t vocab, int
   H->off_count = take(max_top > 0 ? 4 * max_tokens : 0);
   H->off_entropy = take(max_top > 0 ? 4 * max_tokens : 0);
   H->off_dz = take(2 * max_tokens * H->piece);
-  // dH's sums: one set where tokens are many; where K is cut into slices, up to 2 tiles of 256 x 256 per pair,
-  // or 3 of 256 x 128 with few tokens
+  // dH's sums: one set where tokens are many; where K is cut into slices, up to 2 tiles of 256 x 256 per pair
   const int64_t row = 4 * head::acc_pitch(dim);
   H->off_acc = take(std::max(row * max_tokens, std::min(row * max_tokens * kMaxSlices, kSliceBytes)));
   H->bytes = at;

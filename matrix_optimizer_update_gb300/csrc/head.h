@@ -30,6 +30,15 @@ struct Wanted {
   int32_t vocab;
 };
 
+// Logits formed in fp32 FMAs.
+struct DotParams {
+  const bf16* hidden;
+  const bf16* weight;
+  int64_t ld_hidden, ld_weight;
+  int32_t dim;
+  float scale;
+};
+
 // Tensor cores truncate what they accumulate: a logit z of theirs is off by about 1.0e-9 * dim * z, always
 // towards zero (measured: -6.6e-5 at z = 16, dim = 4096, where fp32 FMAs are off by 8e-7). Sums over the
 // vocabulary average that out, but the loss of a token predicted with near certainty is 1 - p of its
@@ -45,16 +54,13 @@ struct alignas(8) Part {
 };
 
 struct LogitParams {
-  const bf16* hidden;
-  const bf16* weight;
-  int64_t ld_hidden, ld_weight;
+  DotParams in;            // H, W and their pitches, dim, 1 / temperature
   int64_t tokens;
-  int32_t vocab, dim;
-  float scale;             // 1 / temperature
+  int32_t vocab;
   Wanted want;
   // forward
   Part* parts;             // [groups][tokens]; few tokens: [tokens][groups]
-  float* picked;           // [tokens][want.top]: scaled logits of the wanted entries (below kSure: written here)
+  float* picked;           // [tokens][want.top]: scaled logits of the wanted entries
   int32_t v0, width;       // entries v0 .. v0 + width - 1 (forward: all)
   // backward
   const float* lse;
@@ -98,15 +104,6 @@ struct GradParams {
 
 inline int64_t acc_pitch(int64_t dim) { return (dim + 7) / 8 * 8; }
 
-// Logits formed in fp32 FMAs.
-struct DotParams {
-  const bf16* hidden;
-  const bf16* weight;
-  int64_t ld_hidden, ld_weight;
-  int32_t dim;
-  float scale;
-};
-
 struct RowParams {
   int64_t tokens;
   int32_t vocab;
@@ -133,7 +130,7 @@ struct TeacherParams {
   int32_t* out_count;
   float* out_entropy;
   DotParams dot;
-  float* picked;           // entries of at least kSure
+  float* picked;           // the logits of entries of at least kSure
 };
 
 // Tiles of a launch over so many vocabulary entries when the tokens are few.
@@ -149,9 +146,6 @@ cudaError_t launch_dz(const LogitParams& p, const Pipe& pipe, cudaStream_t s);
 Slices dh_slices(int64_t tokens, int64_t dim, int64_t width, bool dweight, int pairs);
 cudaError_t launch_grads(const GradParams& p, const Pipe& pipe, cudaStream_t s);
 cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t s);
-// picked[t] = the logit of targets[t] (where it is in the vocabulary)
-cudaError_t launch_targets(const DotParams& d, const int64_t* targets, int64_t tokens, int32_t vocab, float* picked,
-                           cudaStream_t s);
 cudaError_t launch_rows(const RowParams& p, cudaStream_t s);
 // out = bf16(gscale * *gmax * the sum of the slices of acc)
 cudaError_t launch_round(const float* acc, int slices, int64_t tokens, int32_t dim, float gscale, const float* gmax,

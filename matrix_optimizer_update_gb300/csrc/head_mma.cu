@@ -26,6 +26,7 @@
 
 #include "follow.cuh"
 #include "head.h"
+#include "head_dot.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -97,12 +98,10 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= 1024, "barriers must fit their 1 KB");
 
-// A thin launch's tokens, in shared memory (after the barriers, in front of the staging boxes' use).
+// What thin dz needs of its tokens, in shared memory (in the place of the staging boxes, which it has not).
 struct ThinTokens {
-  int target[kThin];   // cross entropy: the entry to take out, or -1
-  float g[kThin];      // dz: gradient relative to the largest, 0 for a token that does not count
+  float g[kThin];      // gradient relative to the largest, 0 for a token that does not count
   float lse[kThin];
-  float hit[kThin];    // dz, cross entropy: the target's own dz
 };
 
 // Instruction descriptor as ptx::idesc_bf16, with A MN-major too (bit 15).
@@ -116,12 +115,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Keeps results below 2^-126: gradients of entries far down the tail, which sums may still be made of.
-__device__ __forceinline__ float ex2_full(float x) {
-  float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+// exp(x) * 2^32, to be multiplied by kLow: the product may lie below 2^-126, where ex2 itself gives 0.
+// Gradients of entries far down the tail, which sums may still be made of.
+constexpr float kLow = 1.f / 4294967296.f;
+__device__ __forceinline__ float exp_high(float x) { return ex2(fmaf(x, kLog2e, 32.f)); }
 
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, uint32_t bar, int x, int y) {
   asm volatile(
@@ -176,20 +173,9 @@ struct Where {
 // work share the band's H (8 x 256 rows) and about ten blocks of W.
 constexpr int kBand = 8;
 
-// Gradients of few tokens: dH reads W and dW writes as much, so their tiles alternate, reads under writes
-// (writes alone go at about 3.6 TB/s, a mix at 6.6). 64 tokens x 128000 x 4096: 450 us with dH first.
 template <int MODE>
 __device__ __forceinline__ Where where_is(const Params& p, int w) {
   Where x;
-  if (MODE == kThinGrads) {
-    int before = p.dh_items;  // dH tiles among places 0 .. w - 1
-    bool dh = false;
-    if (w < p.spread) {
-      before = static_cast<int>(int64_t(w) * p.dh_items / p.spread);
-      dh = static_cast<int>((int64_t(w) + 1) * p.dh_items / p.spread) > before;
-    }
-    w = dh ? before : p.dh_items + (w - before);
-  }
   x.kind = 0;
   x.slice = 0;
   x.k0 = 0;
@@ -257,9 +243,33 @@ struct Cursor {
   }
 };
 
+// Whether a token has a loss at all.
+__device__ __forceinline__ bool counts(const Wanted& w, int64_t t) {
+  return w.targets != nullptr ? w.targets[t] >= 0 && w.targets[t] < w.vocab : w.count[t] > 0;
+}
+
+// Cross entropy's backward pass: the logits of this warp's targets (lane: token t, cursor c) before `end`, in
+// fp32 FMAs, to picked. By whole warps, before the wait for the tile's product: one target per token in the
+// whole vocabulary, so few to a tile, and a launch of its own costs more (77 tokens: 128 against 116 us).
+__device__ __forceinline__ void target_logits(const LogitParams& p, const Cursor& c, int64_t t, int end, int lane) {
+  if (p.want.targets == nullptr) return;  // a list's are formed where it is sorted
+  unsigned more = __ballot_sync(0xffffffffu, c.id < end);
+  if (more == 0u) return;
+  while (more != 0u) {
+    const int L = __ffs(more) - 1;
+    more &= more - 1u;
+    float z[1];
+    dot_parts<1>(p.in, {__shfl_sync(0xffffffffu, t, L)}, {__shfl_sync(0xffffffffu, c.id, L)}, lane, 32, z);
+    z[0] = warp_sum(z[0]) * p.in.scale;
+    if (lane == L) p.picked[t] = z[0];
+  }
+  __syncwarp();  // other lanes may read what was written
+}
+
 // One warp's part of a logits tile: 32 tokens, 128 entries from j0. `wait` returns false when the CTA gave up.
 template <class Wait, class Free>
-__device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, int j0, uint32_t tbase, Wait&& wait, Free&& free) {
+__device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, int j0, uint32_t tbase, Wait&& wait,
+                                             Free&& free) {
   const bool in = t < p.tokens;
   Cursor c;
   c.start(p.want, t, in, j0);
@@ -275,7 +285,7 @@ __device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, in
     if (ch == 3) free();
     if (jc >= p.vocab) continue;
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] *= p.scale;
+    for (int k = 0; k < 32; ++k) v[k] *= p.in.scale;
     if (jc + 32 > p.vocab) {
 #pragma unroll
       for (int k = 0; k < 32; ++k)
@@ -324,12 +334,12 @@ __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t,
   c.start(p.want, t, in, j0);
   float g = 0.f, lse = 0.f;
   if (in) {
-    const bool counts = p.want.targets != nullptr ? p.want.targets[t] >= 0 && p.want.targets[t] < p.vocab
-                                                  : p.want.count[t] > 0;
     lse = p.lse[t];
-    g = counts ? p.grad[t] / gmax : 0.f;
+    g = counts(p.want, t) ? p.grad[t] / gmax : 0.f;
     if (g == 0.f) c.id = INT_MAX;  // zeros, whatever z is
   }
+  target_logits(p, c, t, min(j0 + 128, p.vocab), lane);
+  const float g_low = g * kLow;
   int last_id = -1;
   if (!wait()) return false;
   ptx::tc_fence_after();
@@ -339,18 +349,23 @@ __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t,
     float v[32];
     ptx::tmem_ld_32x32b_x32(tbase + ch * 32, v);
     if (ch == 3) free();
+    // a row that does not count, and entries past the vocabulary, give exact zeros whatever z is
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
-      // a row that does not count, and entries past the vocabulary, give exact zeros whatever z is
-      const float e = g * ex2_full((v[k] * p.scale - lse) * kLog2e);
-      v[k] = g == 0.f || jc + k >= p.vocab ? 0.f : e;
+      const float e = g_low * exp_high(fmaf(v[k], p.in.scale, -lse));
+      v[k] = g == 0.f ? 0.f : e;
+    }
+    if (jc + 32 > p.vocab) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (jc + k >= p.vocab) v[k] = 0.f;
     }
     while (__any_sync(0xffffffffu, c.id < jc + 32)) {
       if (c.id < jc + 32) {
         const int at = c.id - jc;
         const float share = c.share(p.want);
         const bool sure = share >= kSure && c.id != last_id;
-        const float e = sure ? ex2_full((p.picked[t * p.want.top + c.pos] - lse) * kLog2e) : 0.f;
+        const float e = sure ? expf(p.picked[t * p.want.top + c.pos] - lse) : 0.f;
         last_id = c.id;
 #pragma unroll
         for (int k = 0; k < 32; ++k)
@@ -395,8 +410,8 @@ __device__ __forceinline__ float columns(const float (&v)[32], int lane, Op op) 
 }
 
 // The wanted entries of 32 tokens among 32 lanes' vocabulary entries [first, end): lane L's cursor belongs to
-// token t0 + L. take(k, id, q, pos, again) is called by the lane whose entry `id` is, for column k; `again`
-// when the token's previous entry had the same id.
+// token t0 + L. take(k, q, pos, again) is called by the lane whose entry it is, for column k and the pos-th of
+// the list; `again` when the token's entry before had the same id.
 template <class Take>
 __device__ __forceinline__ void each_wanted(const Wanted& w, Cursor& c, int first, int end, int lane, Take&& take) {
   int last = -1;
@@ -410,7 +425,7 @@ __device__ __forceinline__ void each_wanted(const Wanted& w, Cursor& c, int firs
       const int id = __shfl_sync(0xffffffffu, c.id, L), pos = __shfl_sync(0xffffffffu, c.pos, L);
       const int before = __shfl_sync(0xffffffffu, last, L);
       const float share = __shfl_sync(0xffffffffu, q, L);
-      if (id - first == lane) take(L, id, share, pos, id == before);
+      if (id - first == lane) take(L, share, pos, id == before);
     }
     if (c.id < end) {
       last = c.id;
@@ -422,17 +437,15 @@ __device__ __forceinline__ void each_wanted(const Wanted& w, Cursor& c, int firs
 // One warp's part of a thin logits tile: 32 entries from `first` (those before `end` are this tile's), the
 // blocks of 32 tokens that are its half's.
 template <class Wait, class Free>
-__device__ __forceinline__ bool drain_thin_logits(const Params& P, const ThinTokens& tk, int first, int end, int group,
+__device__ __forceinline__ bool drain_thin_logits(const Params& P, int first, int end, int group,
                                                   int half, uint32_t tbase, int lane, Wait&& wait, Free&& free) {
   const LogitParams& p = P.l;
-  const bool lists = p.want.targets == nullptr;
   const int blocks = P.thin_n / 32;
   Cursor c[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int t = (half + 2 * i) * 32 + lane;
-    c[i].id = INT_MAX;
-    if (lists) c[i].start(p.want, t, t < p.tokens && first < end, first);
+    c[i].start(p.want, t, t < p.tokens && first < end, first);
   }
   if (!wait()) return false;
   ptx::tc_fence_after();
@@ -448,24 +461,18 @@ __device__ __forceinline__ bool drain_thin_logits(const Params& P, const ThinTok
     ptx::tmem_ld_32x32b_x32(tbase + b * 32, v);
     if (b + 2 >= blocks) free();
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] = v0 < end ? v[k] * p.scale : -INFINITY;
-    if (!lists) {
+    for (int k = 0; k < 32; ++k) v[k] = v0 < end ? v[k] * p.in.scale : -INFINITY;
+    each_wanted(p.want, c[i], first, end, lane, [&](int k, float share, int pos, bool again) {
+      if (again) return;
+      float z = 0.f;
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (tk.target[b * 32 + k] == v0) v[k] = -INFINITY;
-    } else {
-      each_wanted(p.want, c[i], first, end, lane, [&](int k, int, float share, int pos, bool again) {
-        if (again) return;
-        float z = 0.f;
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j == k) {
-            z = v[j];
-            v[j] = -INFINITY;
-          }
-        if (share < kSure) p.picked[int64_t(b * 32 + k) * p.want.top + pos] = z;
-      });
-    }
+      for (int j = 0; j < 32; ++j)
+        if (j == k) {
+          z = v[j];
+          v[j] = -INFINITY;
+        }
+      if (share < kSure) p.picked[int64_t(b * 32 + k) * p.want.top + pos] = z;
+    });
     const float peak = columns(v, lane, [](float x, float y) { return fmaxf(x, y); });
     const float from = peak == -INFINITY ? 0.f : peak;
 #pragma unroll
@@ -482,14 +489,13 @@ template <class Wait, class Free>
 __device__ __forceinline__ bool drain_thin_dz(const Params& P, const ThinTokens& tk, int first, int end, int half,
                                               uint32_t tbase, int lane, Wait&& wait, Free&& free) {
   const LogitParams& p = P.l;
-  const bool lists = p.want.targets == nullptr;
   const int blocks = P.thin_n / 32;
   Cursor c[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int t = (half + 2 * i) * 32 + lane;
-    c[i].id = INT_MAX;
-    if (lists) c[i].start(p.want, t, t < p.tokens && first < end && tk.g[t & (kThin - 1)] != 0.f, first);
+    c[i].start(p.want, t, t < p.tokens && first < end && tk.g[t] != 0.f, first);
+    target_logits(p, c[i], t, end, lane);
   }
   if (!wait()) return false;
   ptx::tc_fence_after();
@@ -507,20 +513,20 @@ __device__ __forceinline__ bool drain_thin_dz(const Params& P, const ThinTokens&
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
       const float g = tk.g[b * 32 + k];
-      const float e = g * ex2_full((v[k] * p.scale - tk.lse[b * 32 + k]) * kLog2e);
-      v[k] = g == 0.f ? 0.f : !lists && tk.target[b * 32 + k] == v0 ? tk.hit[b * 32 + k] : e;
+      const float e = g * kLow * exp_high(fmaf(v[k], p.in.scale, -tk.lse[b * 32 + k]));
+      v[k] = g == 0.f ? 0.f : e;
     }
-    if (lists)
-      each_wanted(p.want, c[i], first, end, lane, [&](int k, int, float share, int pos, bool again) {
-        const int t = b * 32 + k;
-        const float g = tk.g[t];
-        const bool sure = share >= kSure && !again;
-        const float e =
-            sure ? ex2_full((p.picked[int64_t(t) * p.want.top + pos] - tk.lse[t]) * kLog2e) : 0.f;
+    each_wanted(p.want, c[i], first, end, lane, [&](int k, float share, int pos, bool again) {
+      const int t = b * 32 + k;
+      const float g = tk.g[t];
+      const bool sure = share >= kSure && !again;
+      // another lane of this warp wrote the logit, before the wait
+      const float z = sure ? __ldcg(&p.picked[int64_t(t) * p.want.top + pos]) : 0.f;
+      const float e = sure ? expf(z - tk.lse[t]) : 0.f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j == k) v[j] = sure ? g * (e - share) : v[j] - g * share;
-      });
+      for (int j = 0; j < 32; ++j)
+        if (j == k) v[j] = sure ? g * (e - share) : v[j] - g * share;
+    });
     if (v0 < end) {
       bf16* row = p.dz + (v0 - p.v0);
 #pragma unroll
@@ -544,7 +550,7 @@ __device__ __forceinline__ bool drain_thin_dh(const Params& P, const Where& x, i
     float v[32];
     ptx::tmem_ld_32x32b_x32(tbase + b * 32, v);
     if (b + 2 >= P.thin_n / 32) free();
-    if (d < P.l.dim) {
+    if (d < P.l.in.dim) {
 #pragma unroll
       for (int k = 0; k < 32; ++k)
         if (b * 32 + k < P.l.tokens) {
@@ -558,10 +564,9 @@ __device__ __forceinline__ bool drain_thin_dh(const Params& P, const Where& x, i
 
 // One warp's part of a gradient tile: 32 rows from r0, 128 columns from d0.
 template <class Wait, class Free>
-__device__ __forceinline__ bool drain_grads(const Params& P, const Where& x, int64_t r0, int64_t r_lim, int d0,
+__device__ __forceinline__ bool drain_grads(const Params& P, const Where& x, float scale, int64_t r0, int64_t r_lim, int d0,
                                             uint32_t tbase, int lane, uint8_t* stg, uint32_t& nbox, Wait&& wait, Free&& free) {
   const bool sums = x.kind == 0 && !P.dh_direct;
-  const float scale = sums ? 1.f : *P.gmax * P.gscale;
   if (!wait()) return false;
   ptx::tc_fence_after();
 #pragma unroll 1
@@ -570,7 +575,7 @@ __device__ __forceinline__ bool drain_grads(const Params& P, const Where& x, int
     float v[32];
     ptx::tmem_ld_32x32b_x32(tbase + ch * 32, v);
     if (ch == 3) free();
-    const bool in = r0 < r_lim && dc < P.l.dim;
+    const bool in = r0 < r_lim && dc < P.l.in.dim;
     if (sums) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -586,7 +591,7 @@ __device__ __forceinline__ bool drain_grads(const Params& P, const Where& x, int
         __syncwarp();
         if (lane == 0) {
           const int d = dc + h * 16;
-          if (in && d < P.l.dim) {
+          if (in && d < P.l.in.dim) {
             if (P.first) ptx::tma_store_3d(&P.out[0], box, d, static_cast<int>(r0), x.slice);
             else tma_add_3d(&P.out[0], box, d, static_cast<int>(r0), x.slice);
           }
@@ -615,9 +620,8 @@ __device__ __forceinline__ bool drain_grads(const Params& P, const Where& x, int
 // The same for dW of few tokens, whose product is one or two K stages, so that the epilogue sets the pace: all
 // 128 columns are staged before one fence and two stores of 64 columns. v0: first row, below v_lim if any is.
 template <class Wait, class Free>
-__device__ __forceinline__ bool drain_thin_dw(const Params& P, int v0, int v_lim, int d0, uint32_t tbase, int lane,
+__device__ __forceinline__ bool drain_thin_dw(const Params& P, float scale, int v0, int v_lim, int d0, uint32_t tbase, int lane,
                                               uint8_t* stg, Wait&& wait, Free&& free) {
-  const float scale = *P.gmax * P.gscale;
   if (lane == 0) ptx::bulk_wait_read<0>();  // the last tile's stores are done with the boxes
   __syncwarp();
   if (!wait()) return false;
@@ -634,8 +638,8 @@ __device__ __forceinline__ bool drain_thin_dw(const Params& P, int v0, int v_lim
   ptx::fence_proxy_async_shared();
   __syncwarp();
   if (lane == 0) {
-    if (v0 < v_lim && d0 < P.l.dim) ptx::tma_store_2d(&P.out[1], stg, d0, v0);
-    if (v0 < v_lim && d0 + 64 < P.l.dim) ptx::tma_store_2d(&P.out[1], stg + kWideBox, d0 + 64, v0);
+    if (v0 < v_lim && d0 < P.l.in.dim) ptx::tma_store_2d(&P.out[1], stg, d0, v0);
+    if (v0 < v_lim && d0 + 64 < P.l.in.dim) ptx::tma_store_2d(&P.out[1], stg + kWideBox, d0 + 64, v0);
     ptx::bulk_commit();
   }
   return true;
@@ -842,33 +846,20 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
       if (gmax == 0.f) gmax = 1.f;
       if (blockIdx.x == 0 && threadIdx.x == 64) *p.gmax = gmax;
     }
-    if (thin) {
+    if (MODE == kThinDz) {
       const int t = threadIdx.x - 64;
       if (t < kThin) {
-        int y = -1;
-        float g = 0.f, lse = 0.f, hit = 0.f;
+        float g = 0.f, lse = 0.f;
         if (t < p.l.tokens) {
-          bool counts;
-          if (p.l.want.targets != nullptr) {
-            const int64_t id = p.l.want.targets[t];
-            counts = id >= 0 && id < p.l.vocab;
-            if (counts) y = static_cast<int>(id);
-          } else {
-            counts = p.l.want.count[t] > 0;
-          }
-          if (MODE == kThinDz) {
-            lse = p.l.lse[t];
-            g = counts ? p.l.grad[t] / gmax : 0.f;
-            if (y >= 0) hit = g * (ex2_full((p.l.picked[t] - lse) * kLog2e) - 1.f);
-          }
+          lse = p.l.lse[t];
+          if (counts(p.l.want, t)) g = p.l.grad[t] / gmax;
         }
-        tk.target[t] = y;
         tk.g[t] = g;
         tk.lse[t] = lse;
-        tk.hit[t] = hit;
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
     }
+    const float scale = grads ? *p.gmax * p.gscale : 1.f;
     uint32_t nbox = 0;
     for (uint32_t local = 0;; ++local) {
       int w = -2;
@@ -894,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
         const int last = min(min(base_v + p.thin_h / 2, p.l.v0 + p.l.width), base_v + q * 32 + 32);
         const uint32_t rows = tmem + acc * kTile + (static_cast<uint32_t>(q * 32) << 16);
         if (MODE == kThinLogits)
-          ok = drain_thin_logits(p, tk, base_v + q * 32, last, (x.col * 2 + rank) * 4 + q, half, rows, lane, wait, free);
+          ok = drain_thin_logits(p, base_v + q * 32, last, (x.col * 2 + rank) * 4 + q, half, rows, lane, wait, free);
         else
           ok = drain_thin_dz(p, tk, base_v + q * 32, last, half, rows, lane, wait, free);
       } else if (MODE == kThinGrads && x.kind == 0) {
@@ -905,10 +896,10 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
       } else if (MODE == kDz) {
         ok = drain_dz(p, gmax, r0 + lane, r0, p.l.v0 + c0, tbase, lane, stg, nbox, wait, free);
       } else if (MODE == kThinGrads) {
-        ok = drain_thin_dw(p, p.l.v0 + static_cast<int>(r0), p.l.vocab, c0, tbase, lane, stg, wait, free);
+        ok = drain_thin_dw(p, scale, p.l.v0 + static_cast<int>(r0), p.l.vocab, c0, tbase, lane, stg, wait, free);
       } else {
         const int64_t row = r0 + (x.kind == 1 ? p.l.v0 : 0);
-        ok = drain_grads(p, x, row, x.kind == 1 ? p.l.vocab : p.l.tokens, c0, tbase, lane, stg, nbox, wait, free);
+        ok = drain_grads(p, x, scale, row, x.kind == 1 ? p.l.vocab : p.l.tokens, c0, tbase, lane, stg, nbox, wait, free);
       }
       if (!ok) break;
     }
@@ -994,7 +985,7 @@ cudaError_t launch_pairs(const Params& p, int pairs, cudaStream_t s) {
 cudaError_t logit_launch(Params& P, const LogitParams& p, const Pipe& pipe) {
   std::memset(&P, 0, sizeof(P));
   P.l = p;
-  P.nk = cdiv(p.dim, kStep);
+  P.nk = cdiv(p.in.dim, kStep);
   P.sched = pipe.sched;
   P.status = pipe.status;
   P.gmax = pipe.gmax;
@@ -1015,8 +1006,8 @@ cudaError_t logit_launch(Params& P, const LogitParams& p, const Pipe& pipe) {
     P.cols = cdiv(p.width, kTile);
     P.items = P.rows * P.cols;
   }
-  cudaError_t e = map_rows(&P.a[0], p.hidden, p.dim, p.tokens, p.ld_hidden, kStep, h_rows);
-  if (e == cudaSuccess) e = map_rows(&P.b[0], p.weight, p.dim, p.vocab, p.ld_weight, kStep, w_rows);
+  cudaError_t e = map_rows(&P.a[0], p.in.hidden, p.in.dim, p.tokens, p.in.ld_hidden, kStep, h_rows);
+  if (e == cudaSuccess) e = map_rows(&P.b[0], p.in.weight, p.in.dim, p.vocab, p.in.ld_weight, kStep, w_rows);
   return e;
 }
 
@@ -1058,17 +1049,16 @@ cudaError_t launch_dz(const LogitParams& p, const Pipe& pipe, cudaStream_t s) {
 // is no longer than the launch's work per pair. Each slice has sums of its own, joined by the rounding
 // kernel in a fixed order.
 Slices dh_slices(int64_t tokens, int64_t dim, int64_t width, bool dweight, int pairs) {
-  // (a thin tile of dH reads as much of W as a full one, and less of everything else)
   const int64_t tiles = int64_t(cdiv(tokens, kTile)) * cdiv(dim, kTile);
   const int64_t nk = cdiv(width, kStep);
   // a tile of dW takes the time of 4 stages at least: it writes 128 KB
   const int64_t dw =
       dweight ? int64_t(cdiv(width, kTile)) * cdiv(dim, kTile) * std::max(4, cdiv(tokens, kStep)) : 0;
-  // (few tokens: twice as many, as their sums are small and a tile that starts late should end early)
-  const int64_t share = thin_tokens(tokens) ? 2 * pairs : pairs;
-  const int64_t fair = std::max<int64_t>(16, cdiv(tiles * nk + dw, share));
+  const int64_t fair = std::max<int64_t>(16, cdiv(tiles * nk + dw, pairs));
+  int64_t count = cdiv(nk, fair);
+  if (!dweight && tiles < pairs) count = std::min<int64_t>(count, pairs / tiles);  // one round of the pairs
   Slices x;
-  x.nk = static_cast<int32_t>(nk <= fair ? nk : cdiv(nk, cdiv(nk, fair)));
+  x.nk = cdiv(nk, count);
   x.count = cdiv(nk, x.nk);
   return x;
 }
@@ -1078,7 +1068,7 @@ cudaError_t launch_grads(const GradParams& p, const Pipe& pipe, cudaStream_t s) 
   std::memset(&P, 0, sizeof(P));
   P.l.tokens = p.tokens;
   P.l.vocab = p.v0 + p.width;
-  P.l.dim = p.dim;
+  P.l.in.dim = p.dim;
   P.l.v0 = p.v0;
   P.dim_tiles = cdiv(p.dim, kTile);
   P.thin_n = thin_tokens(p.tokens) ? cdiv(p.tokens, 32) * 32 : 0;
@@ -1124,7 +1114,6 @@ cudaError_t launch_grads(const GradParams& p, const Pipe& pipe, cudaStream_t s) 
                                    CU_TENSOR_MAP_SWIZZLE_64B);
     if (e != cudaSuccess) return e;
   }
-  P.spread = std::max(P.dh_items, P.items / 2);
   return P.thin_n != 0 ? launch_pairs<kThinGrads>(P, pipe.pairs, s) : launch_pairs<kGrads>(P, pipe.pairs, s);
 }
 

@@ -6,6 +6,7 @@
 
 #include "follow.cuh"
 #include "head.h"
+#include "head_dot.cuh"
 
 namespace dmuon {
 namespace head {
@@ -13,49 +14,11 @@ namespace {
 
 constexpr float kNegInf = -INFINITY;
 
-// One thread's part (thread `at` of `of`) of the logit of (t, v): 8 elements at a time, the last few one by one.
-__device__ __forceinline__ float dot_part(const DotParams& d, int64_t t, int64_t v, int at, int of) {
-  const bf16* h = d.hidden + t * d.ld_hidden;
-  const bf16* w = d.weight + v * d.ld_weight;
-  const int whole = d.dim / 8;
-  float s = 0.f;
-  for (int c = at; c < whole; c += of) {
-    const uint4 a = *reinterpret_cast<const uint4*>(h + 8 * c), b = *reinterpret_cast<const uint4*>(w + 8 * c);
-    const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&a);
-    const __nv_bfloat162* y = reinterpret_cast<const __nv_bfloat162*>(&b);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = __bfloat1622float2(x[k]), g = __bfloat1622float2(y[k]);
-      s = fmaf(f.x, g.x, s);
-      s = fmaf(f.y, g.y, s);
-    }
-  }
-  for (int k = 8 * whole + at; k < d.dim; k += of) s = fmaf(__bfloat162float(h[k]), __bfloat162float(w[k]), s);
-  return s;
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  return v;
-}
-
-// One warp per token.
-__global__ void __launch_bounds__(256) targets_kernel(const __grid_constant__ DotParams d, const int64_t* targets,
-                                                      int64_t tokens, int32_t vocab, float* picked) {
-  follow();
-  const int64_t t = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (t >= tokens) return;
-  const int64_t y = targets[t];
-  if (y < 0 || y >= vocab) return;
-  const float z = warp_sum(dot_part(d, t, y, threadIdx.x & 31, 32)) * d.scale;
-  if ((threadIdx.x & 31) == 0) picked[t] = z;
-}
-
 // ------------------------------------------------------------------ teacher
-// One block per token, a thread per entry and at least 4 warps. Each entry of the list finds its place in the order by id by counting the
+// One block per token, a thread per entry. Each entry of the list finds its place in the order by id by counting the
 // entries before it (no sorting network: with 128 entries 128 compares and one barrier against 28 barriers),
-// then a softmax over the entries that count, and the logits of the likeliest ones, a warp for each. Entries
-// that do not count come last, with id vocab.
+// then a softmax over the entries that count, and the logits of the likeliest ones, two at a time to a warp.
+// Entries that do not count come last, with id vocab.
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) teacher_kernel(const __grid_constant__ TeacherParams p) {
   __shared__ uint64_t key[kThreads];
@@ -118,16 +81,24 @@ __global__ void __launch_bounds__(kThreads) teacher_kernel(const __grid_constant
     p.out_count[t] = count;
     p.out_entropy[t] = ent;
   }
-  // lane j looks at entries j, j + 32, ...; warp w takes the w-th, w + 8-th ... of the likely ones
+  // lane j looks at entries j, j + 32, ...; warp w takes the pairs w, w + warps, ... of the likely ones
   int seen = 0;
   for (int e0 = 0; e0 < count; e0 += 32) {
     unsigned likely = __ballot_sync(0xffffffffu, e0 + lane < count && lg[e0 + lane] >= kSure);
     while (likely != 0u) {
-      const int at = e0 + __ffs(likely) - 1;
+      const int a = e0 + __ffs(likely) - 1;
+      likely &= likely - 1u;
+      const int b = likely != 0u ? e0 + __ffs(likely) - 1 : a;
       likely &= likely - 1u;
       if (seen++ % warps != warp) continue;
-      const float z = warp_sum(dot_part(p.dot, t, id[at], lane, 32)) * p.dot.scale;
-      if (lane == 0) p.picked[t * p.top + at] = z;
+      float z[2];
+      dot_parts<2>(p.dot, {t, t}, {id[a], id[b]}, lane, 32, z);
+      z[0] = warp_sum(z[0]);
+      z[1] = warp_sum(z[1]);
+      if (lane == 0) {
+        p.picked[t * p.top + a] = z[0] * p.dot.scale;
+        p.picked[t * p.top + b] = z[1] * p.dot.scale;
+      }
     }
   }
 }
@@ -193,8 +164,11 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
   if (xent && t < p.tokens) {
     y = p.want.targets[t];
     if (y >= p.vocab) y = -1;
-    if (y >= 0)
-      z = warp_sum(kTokens == 1 ? dot_part(p.dot, t, y, threadIdx.x, kRowThreads) : dot_part(p.dot, t, y, lane, 32));
+    if (y >= 0) {
+      float part[1];
+      dot_parts<1>(p.dot, {t}, {y}, kTokens == 1 ? threadIdx.x : lane, kTokens == 1 ? kRowThreads : 32, part);
+      z = warp_sum(part[0]);
+    }
   }
   if (lane == 0) s_dot[warp] = z;
   __syncthreads();
@@ -293,12 +267,6 @@ cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t s) {
   if (p.top <= 128) return launch_follow(teacher_kernel<128>, grid, 128, 0, s, 1, p);
   static_assert(kMaxTop <= 256, "a thread per entry");
   return launch_follow(teacher_kernel<256>, grid, 256, 0, s, 1, p);
-}
-
-cudaError_t launch_targets(const DotParams& d, const int64_t* targets, int64_t tokens, int32_t vocab, float* picked,
-                           cudaStream_t s) {
-  return launch_follow(targets_kernel, dim3(static_cast<unsigned>((tokens + 7) / 8)), 256, 0, s, 1, d, targets, tokens,
-                       vocab, picked);
 }
 
 cudaError_t launch_rows(const RowParams& p, cudaStream_t s) {
