@@ -20,20 +20,24 @@ constexpr int kMaxExperts = 4096;
 constexpr int64_t kMaxAssignments = int64_t(1) << 30;
 
 // ------------------------------------------------------------------ sort
-// Stable counting sort. A block owns a contiguous run of assignments and each of
-// its 8 warps a contiguous part of it; a warp takes 32 assignments at a time and
-// finds those of equal expert with one match per round, so the order within an
-// expert is the order of the assignments whatever the blocks' timing.
-constexpr int kSortWarps = 8;
-constexpr int kSortThreads = 32 * kSortWarps;
-constexpr int kSortRun = 2048;      // assignments per block while there are few
+// Stable counting sort. A block owns a contiguous run of assignments and each of its warps a contiguous part of
+// it; a warp takes 32 assignments at a time and finds those of equal expert with one match per round, so the
+// order within an expert is the order of the assignments whatever the blocks' timing. A warp reads 256 ids
+// before it looks at the first and keeps what it found of them: the sort takes the latency of one round of
+// loads, eight dependent updates of the counts and the sums over the warps. Up to 8192 assignments go into
+// one block of as many warps as they fill, and one launch.
+constexpr int kSortBatch = 8;       // rounds of 32 a warp holds at a time
+constexpr int kSortHeld = 32 * kSortBatch;
 constexpr int kSortMaxBlocks = 1024;
+// Warps per block at most: 32, or 8 where 32 counts per expert would not fit in shared memory (128 KB either way).
+constexpr int kManyExperts = 1024;
+int sort_warps(int experts) { return experts <= kManyExperts ? 32 : 8; }
 
 struct SortParams {
   const int64_t* ids;
   int64_t n;
   int32_t experts;
-  int32_t run;        // assignments per block, a multiple of kSortThreads
+  int32_t per_warp;   // assignments per warp, a multiple of kSortHeld
   int32_t blocks;
   int32_t* dest;
   int32_t* source;
@@ -41,40 +45,57 @@ struct SortParams {
   int32_t* counts;    // [blocks][experts]: a block's assignments per expert, then its first rows
 };
 
-__device__ __forceinline__ int expert_of(const SortParams& p, int64_t i) {
-  if (i >= p.n) return -1;
-  const int64_t e = p.ids[i];
-  return (e >= 0 && e < p.experts) ? static_cast<int>(e) : -1;
-}
-
-// Each warp's assignments per expert into hist[warp][experts].
-__device__ __forceinline__ void warp_counts(const SortParams& p, int* hist, int64_t first, int per_warp) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < kSortWarps * p.experts; e += kSortThreads) hist[e] = 0;
-  __syncthreads();
-  int* mine = hist + warp * p.experts;
-  for (int r = 0; r < per_warp; r += 32) {
-    const int e = expert_of(p, first + r + lane);
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && (same & ((1u << lane) - 1u)) == 0u) mine[e] += __popc(same);
+// 256 assignments of a warp: their experts (-1: dropped), and each one's place among the warp's of its expert;
+// mine[expert] counts them.
+__device__ __forceinline__ void count_batch(const SortParams& p, int64_t first, int lane, int* mine,
+                                            int (&e)[kSortBatch], int (&place)[kSortBatch]) {
+  int64_t id[kSortBatch];
+#pragma unroll
+  for (int r = 0; r < kSortBatch; ++r) {
+    const int64_t i = first + r * 32 + lane;
+    id[r] = i < p.n ? p.ids[i] : -1;
+  }
+  unsigned same[kSortBatch];
+#pragma unroll
+  for (int r = 0; r < kSortBatch; ++r) {
+    e[r] = id[r] >= 0 && id[r] < p.experts ? static_cast<int>(id[r]) : -1;
+    same[r] = __match_any_sync(0xffffffffu, e[r]);
+  }
+#pragma unroll
+  for (int r = 0; r < kSortBatch; ++r) {
+    const int before = e[r] >= 0 ? mine[e[r]] : 0;
+    const int rank = __popc(same[r] & ((1u << lane) - 1u));
+    place[r] = before + rank;
+    __syncwarp();
+    if (e[r] >= 0 && rank == 0) mine[e[r]] = before + __popc(same[r]);
     __syncwarp();
   }
+}
+
+// Each warp's assignments per expert into hist[warp][experts]; e and place hold the last batch's.
+__device__ __forceinline__ void warp_counts(const SortParams& p, int* hist, int64_t first, int (&e)[kSortBatch],
+                                            int (&place)[kSortBatch]) {
+  for (int j = threadIdx.x; j < int(blockDim.x >> 5) * p.experts; j += blockDim.x) hist[j] = 0;
+  __syncthreads();
+  for (int at = 0; at < p.per_warp; at += kSortHeld)
+    count_batch(p, first + at, threadIdx.x & 31, hist + (threadIdx.x >> 5) * p.experts, e, place);
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(kSortThreads) route_count_kernel(const __grid_constant__ SortParams p) {
+__global__ void __launch_bounds__(1024) route_count_kernel(const __grid_constant__ SortParams p) {
   extern __shared__ int hist[];
   follow();
-  const int per_warp = p.run / kSortWarps;
-  warp_counts(p, hist, int64_t(blockIdx.x) * p.run + int64_t(threadIdx.x >> 5) * per_warp, per_warp);
-  for (int e = threadIdx.x; e < p.experts; e += kSortThreads) {
+  const int warps = blockDim.x >> 5;
+  int e[kSortBatch], place[kSortBatch];
+  warp_counts(p, hist, (int64_t(blockIdx.x) * warps + (threadIdx.x >> 5)) * p.per_warp, e, place);
+  for (int j = threadIdx.x; j < p.experts; j += blockDim.x) {
     int c = 0;
-    for (int w = 0; w < kSortWarps; ++w) c += hist[w * p.experts + e];
-    p.counts[int64_t(blockIdx.x) * p.experts + e] = c;
+    for (int w = 0; w < warps; ++w) c += hist[w * p.experts + j];
+    p.counts[int64_t(blockIdx.x) * p.experts + j] = c;
   }
 }
 
-// Exclusive sum over the block's threads (kSortThreads of them); *total receives the sum of all.
+// Exclusive sum over the block's threads; *total receives the sum of all.
 __device__ __forceinline__ int block_exclusive(int v, int* scratch, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int s = v;
@@ -85,7 +106,7 @@ __device__ __forceinline__ int block_exclusive(int v, int* scratch, int* total) 
   if (lane == 31) scratch[warp] = s;
   __syncthreads();
   int before = 0, all = 0;
-  for (int w = 0; w < kSortWarps; ++w) {
+  for (int w = 0; w < int(blockDim.x >> 5); ++w) {
     const int c = scratch[w];
     before += w < warp ? c : 0;
     all += c;
@@ -96,11 +117,12 @@ __device__ __forceinline__ int block_exclusive(int v, int* scratch, int* total) 
 }
 
 // One block: the counts become each block's first row per expert, and offsets the experts' first rows.
-__global__ void __launch_bounds__(kSortThreads) route_scan_kernel(const __grid_constant__ SortParams p) {
-  __shared__ int scratch[kSortWarps];
+constexpr int kScanThreads = 256;
+__global__ void __launch_bounds__(kScanThreads) route_scan_kernel(const __grid_constant__ SortParams p) {
+  __shared__ int scratch[32];
   follow();
   int base = 0;
-  for (int e0 = 0; e0 < p.experts; e0 += kSortThreads) {
+  for (int e0 = 0; e0 < p.experts; e0 += kScanThreads) {
     const int e = e0 + threadIdx.x;
     int mine = 0;
     if (e < p.experts)
@@ -123,57 +145,48 @@ __global__ void __launch_bounds__(kSortThreads) route_scan_kernel(const __grid_c
 
 // Rows of the block's assignments. ONE: a single block has all of them and makes the offsets itself.
 template <bool ONE>
-__global__ void __launch_bounds__(kSortThreads) route_place_kernel(const __grid_constant__ SortParams p) {
+__global__ void __launch_bounds__(1024) route_place_kernel(const __grid_constant__ SortParams p) {
   extern __shared__ int hist[];
-  __shared__ int scratch[kSortWarps];
+  __shared__ int scratch[32];
   follow();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per_warp = p.run / kSortWarps;
-  const int64_t first = int64_t(blockIdx.x) * p.run + int64_t(warp) * per_warp;
-  warp_counts(p, hist, first, per_warp);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int64_t first = (int64_t(blockIdx.x) * warps + warp) * p.per_warp;
+  int e[kSortBatch], place[kSortBatch];
+  warp_counts(p, hist, first, e, place);
   int rows = 0;  // rows in use
-  if (ONE) {
-    for (int e0 = 0; e0 < p.experts; e0 += kSortThreads) {
-      const int e = e0 + threadIdx.x;
-      int mine = 0;
-      if (e < p.experts)
-        for (int w = 0; w < kSortWarps; ++w) mine += hist[w * p.experts + e];
-      int total;
-      int at = rows + block_exclusive(mine, scratch, &total);
-      if (e < p.experts) {
-        p.offsets[e] = at;
-        for (int w = 0; w < kSortWarps; ++w) {
-          const int k = hist[w * p.experts + e];
-          hist[w * p.experts + e] = at;
-          at += k;
-        }
-      }
+  for (int e0 = 0; e0 < p.experts; e0 += blockDim.x) {
+    const int x = e0 + threadIdx.x;
+    int at = 0;
+    if (ONE) {
+      int mine = 0, total;
+      if (x < p.experts)
+        for (int w = 0; w < warps; ++w) mine += hist[w * p.experts + x];
+      at = rows + block_exclusive(mine, scratch, &total);
+      if (x < p.experts) p.offsets[x] = at;
       rows += total;
+    } else if (x < p.experts) {
+      at = p.counts[int64_t(blockIdx.x) * p.experts + x];
     }
-    if (threadIdx.x == 0) p.offsets[p.experts] = rows;
-  } else {
-    for (int e = threadIdx.x; e < p.experts; e += kSortThreads) {
-      int at = p.counts[int64_t(blockIdx.x) * p.experts + e];
-      for (int w = 0; w < kSortWarps; ++w) {
-        const int k = hist[w * p.experts + e];
-        hist[w * p.experts + e] = at;
+    if (x < p.experts) {
+      for (int w = 0; w < warps; ++w) {  // the warps' first rows
+        const int k = hist[w * p.experts + x];
+        hist[w * p.experts + x] = at;
         at += k;
       }
     }
-    rows = p.offsets[p.experts];
   }
+  if (!ONE) rows = p.offsets[p.experts];
+  else if (threadIdx.x == 0) p.offsets[p.experts] = rows;
   __syncthreads();
   int* mine = hist + warp * p.experts;
-  for (int r = 0; r < per_warp; r += 32) {
-    const int64_t i = first + r + lane;
-    const int e = expert_of(p, i);
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    const int row = e >= 0 ? mine[e] + rank : -1;
-    __syncwarp();
-    if (e >= 0 && rank == 0) mine[e] += __popc(same);
-    __syncwarp();
-    if (i < p.n) {
+  const bool held = p.per_warp == kSortHeld;  // else the batches are gone through again, the rows in place of counts
+  for (int a = 0; a < p.per_warp; a += kSortHeld) {
+    if (!held) count_batch(p, first + a, lane, mine, e, place);
+#pragma unroll
+    for (int r = 0; r < kSortBatch; ++r) {
+      const int64_t i = first + a + r * 32 + lane;
+      if (i >= p.n) break;
+      const int row = e[r] < 0 ? -1 : held ? mine[e[r]] + place[r] : place[r];
       p.dest[i] = row;
       if (row >= 0) p.source[row] = static_cast<int32_t>(i);
       if (i >= rows) p.source[i] = -1;
@@ -181,8 +194,30 @@ __global__ void __launch_bounds__(kSortThreads) route_place_kernel(const __grid_
   }
 }
 
-int64_t sort_blocks(int64_t n) {
-  return std::max<int64_t>(1, std::min<int64_t>((n + kSortRun - 1) / kSortRun, kSortMaxBlocks));
+int64_t sort_blocks(int64_t n, int experts) {
+  const int64_t run = int64_t(sort_warps(experts)) * kSortHeld;
+  return std::max<int64_t>(1, std::min<int64_t>((n + run - 1) / run, kSortMaxBlocks));
+}
+
+cudaError_t launch_sort(SortParams& p, cudaStream_t s) {
+  // a single block has no more warps than its assignments fill
+  const int warps = p.blocks > 1 ? sort_warps(p.experts)
+                                 : static_cast<int>(std::max<int64_t>(1, (p.n + kSortHeld - 1) / kSortHeld));
+  const int64_t all = int64_t(p.blocks) * warps, per = (p.n + all - 1) / all;
+  p.per_warp = static_cast<int32_t>(std::max<int64_t>(1, (per + kSortHeld - 1) / kSortHeld) * kSortHeld);
+  const size_t smem = sizeof(int) * warps * p.experts;
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024) {  // beside the static arrays, within the 48 KB a launch has without asking
+    for (auto* k : {route_count_kernel, route_place_kernel<true>, route_place_kernel<false>})
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  if (p.blocks == 1) return launch_follow(route_place_kernel<true>, dim3(1), warps * 32, smem, s, 1, p);
+  e = launch_follow(route_count_kernel, dim3(p.blocks), warps * 32, smem, s, 1, p);
+  if (e == cudaSuccess) e = launch_follow(route_scan_kernel, dim3(1), kScanThreads, 0, s, 1, p);
+  if (e == cudaSuccess) e = launch_follow(route_place_kernel<false>, dim3(p.blocks), warps * 32, smem, s, 1, p);
+  return e;
 }
 
 // ------------------------------------------------------------------ rows
@@ -374,7 +409,7 @@ extern "C" dmuon_status dmuon_route_workspace_bytes(int64_t tokens, int32_t top,
   dmuon_status st = check_sizes(tokens, top);
   if (st != DMUON_OK) return st;
   if (experts < 1 || experts > kMaxExperts) return refuse("experts must be between 1 and 4096");
-  *bytes = static_cast<size_t>(sort_blocks(tokens * top) * experts) * sizeof(int32_t);
+  *bytes = static_cast<size_t>(sort_blocks(tokens * top, experts) * experts) * sizeof(int32_t);
   return set_last_error(DMUON_OK, "");
 }
 
@@ -396,28 +431,12 @@ extern "C" dmuon_status dmuon_route_sort(const int64_t* expert_ids, int64_t toke
   p.ids = expert_ids;
   p.n = n;
   p.experts = experts;
-  p.blocks = static_cast<int32_t>(sort_blocks(n));
-  const int64_t per = (n + p.blocks - 1) / p.blocks;
-  p.run = static_cast<int32_t>(std::max<int64_t>(1, (per + kSortThreads - 1) / kSortThreads) * kSortThreads);
+  p.blocks = static_cast<int32_t>(sort_blocks(n, experts));
   p.dest = dest;
   p.source = source;
   p.offsets = offsets;
   p.counts = static_cast<int32_t*>(d_workspace);
-  const size_t smem = sizeof(int) * kSortWarps * experts;
-  if (smem > 48 * 1024) {
-    for (auto* k : {route_count_kernel, route_place_kernel<true>, route_place_kernel<false>}) {
-      const cudaError_t e =
-          cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-      if (e != cudaSuccess) return set_last_error(DMUON_ERR_CUDA, cudaGetErrorString(e));
-    }
-  }
-  if (p.blocks == 1) {
-    return done(launch_follow(route_place_kernel<true>, dim3(1), kSortThreads, smem, s, 1, p));
-  }
-  cudaError_t e = launch_follow(route_count_kernel, dim3(p.blocks), kSortThreads, smem, s, 1, p);
-  if (e == cudaSuccess) e = launch_follow(route_scan_kernel, dim3(1), kSortThreads, 0, s, 1, p);
-  if (e == cudaSuccess) e = launch_follow(route_place_kernel<false>, dim3(p.blocks), kSortThreads, smem, s, 1, p);
-  return done(e);
+  return done(launch_sort(p, s));
 }
 
 extern "C" dmuon_status dmuon_route_dispatch(const void* x, int64_t ld_x, const int32_t* dest, const int32_t* source,

@@ -380,31 +380,22 @@ def _flat(t, shape, dtype, name):
     return t.data_ptr()
 
 
-class _on:
-    """Run a call on ``stream`` (None: the current one of ``like``'s device): what it allocates belongs to
-    that stream, and what it is given stays alive until the stream is done with it."""
+def _here(t) -> int:
+    """The raw handle of the current stream of t's device (the object torch.cuda.current_stream() makes costs
+    more than a small call)."""
+    return _t()._C._cuda_getCurrentRawStream(t.get_device())
 
-    __slots__ = ("handle", "other")
 
-    def __init__(self, stream, like, *tensors):
-        # the raw handle: the object torch.cuda.current_stream() makes costs more than a small call
-        self.handle = _t()._C._cuda_getCurrentRawStream(like.device.index)
-        self.other = None
-        if stream is not None and stream.cuda_stream != self.handle:
-            self.handle = stream.cuda_stream
-            self.other = _t().cuda.stream(stream)
-            for t in (like, *tensors):
-                if t is not None:
-                    t.record_stream(stream)
-
-    def __enter__(self):
-        if self.other is not None:
-            self.other.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.other is not None:
-            self.other.__exit__(*exc)
+def _on(stream, call, *tensors):
+    """Run ``call(handle)`` on ``stream``: what it allocates belongs to that stream, and what it is given stays
+    alive until the stream is done with it."""
+    if stream.cuda_stream == _here(tensors[0]):
+        return call(stream.cuda_stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    with _t().cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 class Head:
@@ -429,8 +420,10 @@ class Head:
         self = cls(h, int(max_tokens), int(vocab), int(dim), int(max_top))
         nbytes = self.workspace_bytes()
         ws = _t().empty(nbytes + 1024, dtype=_t().uint8, device=device or "cuda")
-        with _on(stream, ws) as s:
-            self.bind((ws.data_ptr() + 1023) // 1024 * 1024, nbytes, s)
+        s = _here(ws) if stream is None else stream.cuda_stream
+        if s != _here(ws):
+            ws.record_stream(stream)
+        self.bind((ws.data_ptr() + 1023) // 1024 * 1024, nbytes, s)
         self.workspace = ws
         return self
 
@@ -443,8 +436,9 @@ class Head:
         _check(lib().dmuon_head_bind(self._h, ctypes.c_void_p(d_workspace), nbytes, ctypes.c_void_p(stream)))
 
     def _inputs(self, hidden, weight):
-        lh = _rows(hidden, self.dim, _t().bfloat16, "hidden")
-        lw = _rows(weight, self.dim, _t().bfloat16, "weight", self.vocab)
+        bf16 = _t().bfloat16
+        lh = _rows(hidden, self.dim, bf16, "hidden")
+        lw = _rows(weight, self.dim, bf16, "weight", self.vocab)
         return hidden.data_ptr(), lh, weight.data_ptr(), lw
 
     def _teacher(self, top_ids, top_logits, tokens):
@@ -452,68 +446,72 @@ class Head:
         ids = _flat(top_ids, (tokens, top), _t().int64, "top_ids")
         return ids, _flat(top_logits, (tokens, top), _t().float32, "top_logits"), top
 
-    def _grads(self, hidden, weight, dhidden, dweight):
-        """Gradient tensors (made where True, left out where False or None) with addresses and pitches."""
-        out = []
-        for want, like, name in ((dhidden, hidden, "dhidden"), (dweight, weight, "dweight")):
-            if want is True:
-                want = _t().empty(like.shape[0], -(-self.dim // 8) * 8, dtype=like.dtype,
-                                   device=like.device)[:, :self.dim]
-            elif want is False:
-                want = None
-            ld = 0 if want is None else _rows(want, self.dim, _t().bfloat16, name, like.shape[0])
-            out += [want, None if want is None else want.data_ptr(), ld]
-        return out
+    def _forward(self, fn, hidden, args, stream, *tensors):
+        n = hidden.shape[0]
+
+        def call(s):
+            empty, f32 = _t().empty, _t().float32
+            loss = empty(n, dtype=f32, device=hidden.device)
+            lse = empty(n, dtype=f32, device=hidden.device)
+            _check(fn(self._h, *args, n, loss.data_ptr(), lse.data_ptr(), s))
+            return loss, lse
+
+        if stream is None:
+            return call(_here(hidden))
+        return _on(stream, call, hidden, *tensors, self.workspace)
+
+    def _backward(self, fn, hidden, weight, args, lse, grad_loss, dhidden, dweight, stream, *tensors):
+        n = hidden.shape[0]
+        f32 = _t().float32
+        args += (n, _flat(lse, (n,), f32, "lse"), _flat(grad_loss, (n,), f32, "grad_loss"))
+
+        def call(s):
+            dh, ph, lh = self._grad(hidden, dhidden, "dhidden")
+            dw, pw, lw = self._grad(weight, dweight, "dweight")
+            _check(fn(self._h, *args, ph, lh, pw, lw, s))
+            return dh, dw
+
+        if stream is None:
+            return call(_here(hidden))
+        return _on(stream, call, hidden, weight, lse, grad_loss, *tensors, self.workspace)
+
+    def _grad(self, like, want, name):
+        """The gradient of ``like`` (made where True, left out where False or None), its address and pitch."""
+        if want is False or want is None:
+            return None, None, 0
+        rows, dim = like.shape[0], self.dim
+        if want is True:
+            if dim % 8 == 0:
+                want = _t().empty(rows, dim, dtype=like.dtype, device=like.device)
+                return want, want.data_ptr(), dim
+            want = _t().empty(rows, -(-dim // 8) * 8, dtype=like.dtype, device=like.device)[:, :dim]
+        return want, want.data_ptr(), _rows(want, dim, _t().bfloat16, name, rows)
 
     def xent(self, hidden, weight, targets, *, stream=None):
         """(loss, lse) per token; targets int64, one outside the vocabulary does not count."""
-        n = hidden.shape[0]
-        _flat(targets, (n,), _t().int64, "targets")
-        args = self._inputs(hidden, weight)
-        with _on(stream, hidden, weight, targets, self.workspace) as s:
-            loss = _t().empty(n, dtype=_t().float32, device=hidden.device)
-            lse = _t().empty(n, dtype=_t().float32, device=hidden.device)
-            _check(lib().dmuon_head_xent(self._h, *args, targets.data_ptr(), n, loss.data_ptr(), lse.data_ptr(), s))
-        return loss, lse
+        y = _flat(targets, hidden.shape[:1], _t().int64, "targets")
+        return self._forward(lib().dmuon_head_xent, hidden, (*self._inputs(hidden, weight), y), stream, weight, targets)
 
     def xent_backward(self, hidden, weight, targets, lse, grad_loss, *, dhidden=True, dweight=True, stream=None):
         """(dhidden, dweight) of sum(grad_loss * loss). Either may be a tensor to write into, or False."""
-        n = hidden.shape[0]
-        _flat(targets, (n,), _t().int64, "targets")
-        _flat(lse, (n,), _t().float32, "lse")
-        _flat(grad_loss, (n,), _t().float32, "grad_loss")
-        args = self._inputs(hidden, weight)
-        with _on(stream, hidden, weight, targets, lse, grad_loss, self.workspace) as s:
-            dh, ph, lh, dw, pw, lw = self._grads(hidden, weight, dhidden, dweight)
-            _check(lib().dmuon_head_xent_backward(self._h, *args, targets.data_ptr(), n, lse.data_ptr(),
-                                                  grad_loss.data_ptr(), ph, lh, pw, lw, s))
-        return dh, dw
+        y = _flat(targets, hidden.shape[:1], _t().int64, "targets")
+        return self._backward(lib().dmuon_head_xent_backward, hidden, weight, (*self._inputs(hidden, weight), y), lse,
+                              grad_loss, dhidden, dweight, stream, targets)
 
     def distill(self, hidden, weight, top_ids, top_logits, temperature=1.0, *, stream=None):
         """(loss, lse) per token against a teacher's top logits; ids int64 and logits fp32, both [tokens, top]."""
-        n = hidden.shape[0]
-        ids, lg, k = self._teacher(top_ids, top_logits, n)
-        args = self._inputs(hidden, weight)
-        with _on(stream, hidden, weight, top_ids, top_logits, self.workspace) as s:
-            loss = _t().empty(n, dtype=_t().float32, device=hidden.device)
-            lse = _t().empty(n, dtype=_t().float32, device=hidden.device)
-            _check(lib().dmuon_head_distill(self._h, *args, ids, lg, k, float(temperature), n, loss.data_ptr(),
-                                            lse.data_ptr(), s))
-        return loss, lse
+        lists = self._teacher(top_ids, top_logits, hidden.shape[0])
+        return self._forward(lib().dmuon_head_distill, hidden,
+                             (*self._inputs(hidden, weight), *lists, float(temperature)), stream, weight, top_ids,
+                             top_logits)
 
     def distill_backward(self, hidden, weight, top_ids, top_logits, temperature, lse, grad_loss, *, dhidden=True,
                          dweight=True, stream=None):
         """(dhidden, dweight) of sum(grad_loss * loss), as xent_backward."""
-        n = hidden.shape[0]
-        ids, lg, k = self._teacher(top_ids, top_logits, n)
-        _flat(lse, (n,), _t().float32, "lse")
-        _flat(grad_loss, (n,), _t().float32, "grad_loss")
-        args = self._inputs(hidden, weight)
-        with _on(stream, hidden, weight, top_ids, top_logits, lse, grad_loss, self.workspace) as s:
-            dh, ph, lh, dw, pw, lw = self._grads(hidden, weight, dhidden, dweight)
-            _check(lib().dmuon_head_distill_backward(self._h, *args, ids, lg, k, float(temperature), n,
-                                                     lse.data_ptr(), grad_loss.data_ptr(), ph, lh, pw, lw, s))
-        return dh, dw
+        lists = self._teacher(top_ids, top_logits, hidden.shape[0])
+        return self._backward(lib().dmuon_head_distill_backward, hidden, weight,
+                              (*self._inputs(hidden, weight), *lists, float(temperature)), lse, grad_loss, dhidden,
+                              dweight, stream, top_ids, top_logits)
 
     def read_device_status(self, stream: int = 0) -> int:
         b = ctypes.c_uint32()
@@ -560,70 +558,90 @@ class Router:
 
     def sort(self, expert_ids, *, stream=None) -> Route:
         """Order the assignments by expert; expert_ids int64 [tokens, top], one outside 0..experts-1 is dropped."""
-        t = expert_ids.shape[0]
+        t, top = expert_ids.shape[0], self.top
         if t > self.max_tokens:
             _refuse(f"expert_ids has {t} tokens, more than max_tokens ({self.max_tokens})")
-        _flat(expert_ids, (t, self.top), _t().int64, "expert_ids")
-        with _on(stream, expert_ids, self.workspace) as s:
-            dev = expert_ids.device
-            dest = _t().empty(t, self.top, dtype=_t().int32, device=dev)
-            source = _t().empty(t * self.top, dtype=_t().int32, device=dev)
-            offsets = _t().empty(self.experts + 1, dtype=_t().int32, device=dev)
-            _check(lib().dmuon_route_sort(expert_ids.data_ptr(), t, self.top, self.experts, dest.data_ptr(),
-                                          source.data_ptr(), offsets.data_ptr(), self.workspace.data_ptr(),
-                                          self.workspace.numel(), s))
-        return Route(dest, source, offsets)
+        ids = _flat(expert_ids, (t, top), _t().int64, "expert_ids")
 
-    def _row_type(self, t, name):
-        if t.dim() != 2 or t.dtype not in (_t().bfloat16, _t().float32):
-            _refuse(f"{name} must be a bf16 or fp32 matrix")
-        return BF16 if t.dtype == _t().bfloat16 else F32
+        def call(s):
+            empty, i32, dev = _t().empty, _t().int32, expert_ids.device
+            dest = empty((t, top), dtype=i32, device=dev)
+            source = empty(t * top, dtype=i32, device=dev)
+            offsets = empty(self.experts + 1, dtype=i32, device=dev)
+            ws = self.workspace
+            _check(lib().dmuon_route_sort(ids, t, top, self.experts, dest.data_ptr(), source.data_ptr(),
+                                          offsets.data_ptr(), ws.data_ptr(), ws.numel(), s))
+            return Route(dest, source, offsets)
+
+        if stream is None:
+            return call(_here(expert_ids))
+        return _on(stream, call, expert_ids, self.workspace)
+
+    def _kind(self, t, name):
+        if t.dim() == 2:
+            if t.dtype == _t().bfloat16:
+                return BF16
+            if t.dtype == _t().float32:
+                return F32
+        _refuse(f"{name} must be a bf16 or fp32 matrix")
 
     def _route(self, route, tokens):
-        _flat(route.dest, (tokens, self.top), _t().int32, "route.dest")
-        _flat(route.source, (tokens * self.top,), _t().int32, "route.source")
+        i32 = _t().int32
+        return (_flat(route.dest, (tokens, self.top), i32, "route.dest"),
+                _flat(route.source, (tokens * self.top,), i32, "route.source"))
 
     def dispatch(self, x, route, *, stream=None):
         """xs [tokens * top, dim]: x's rows in expert order, zeros in rows not in use."""
-        kind = self._row_type(x, "x")
+        kind = self._kind(x, "x")
         t, dim = x.shape
         ld = _rows(x, dim, x.dtype, "x")
-        self._route(route, t)
-        with _on(stream, x, route.dest, route.source) as s:
-            xs = _t().empty(t * self.top, dim, dtype=x.dtype, device=x.device)
-            _check(lib().dmuon_route_dispatch(x.data_ptr(), ld, route.dest.data_ptr(), route.source.data_ptr(), t,
-                                              self.top, dim, kind, xs.data_ptr(), s))
-        return xs
+        dest, source = self._route(route, t)
+
+        def call(s):
+            xs = _t().empty((t * self.top, dim), dtype=x.dtype, device=x.device)
+            _check(lib().dmuon_route_dispatch(x.data_ptr(), ld, dest, source, t, self.top, dim, kind, xs.data_ptr(), s))
+            return xs
+
+        if stream is None:
+            return call(_here(x))
+        return _on(stream, call, x, route.dest, route.source)
 
     def combine(self, ys, weights, route, *, stream=None):
         """y [tokens, dim]: the sum of each token's expert rows, times weights (fp32 [tokens, top], or None: 1)."""
-        kind = self._row_type(ys, "ys")
+        kind = self._kind(ys, "ys")
         t, dim = route.dest.shape[0], ys.shape[1]
-        self._route(route, t)
-        _flat(ys, (t * self.top, dim), ys.dtype, "ys")
-        if weights is not None:
-            _flat(weights, (t, self.top), _t().float32, "weights")
-        with _on(stream, ys, weights, route.dest) as s:
-            y = _t().empty(t, dim, dtype=ys.dtype, device=ys.device)
-            _check(lib().dmuon_route_combine(ys.data_ptr(), None if weights is None else weights.data_ptr(),
-                                             route.dest.data_ptr(), t, self.top, dim, kind, y.data_ptr(), dim, s))
-        return y
+        dest, _ = self._route(route, t)
+        rows = _flat(ys, (t * self.top, dim), ys.dtype, "ys")
+        w = None if weights is None else _flat(weights, (t, self.top), _t().float32, "weights")
+
+        def call(s):
+            y = _t().empty((t, dim), dtype=ys.dtype, device=ys.device)
+            _check(lib().dmuon_route_combine(rows, w, dest, t, self.top, dim, kind, y.data_ptr(), dim, s))
+            return y
+
+        if stream is None:
+            return call(_here(ys))
+        return _on(stream, call, ys, weights, route.dest)
 
     def combine_backward(self, dy, ys, weights, route, *, stream=None):
         """(dys, dweights) of combine."""
-        kind = self._row_type(ys, "ys")
+        kind = self._kind(ys, "ys")
         t, dim = route.dest.shape[0], ys.shape[1]
-        self._route(route, t)
-        _flat(ys, (t * self.top, dim), ys.dtype, "ys")
-        _flat(weights, (t, self.top), _t().float32, "weights")
+        dest, source = self._route(route, t)
+        rows = _flat(ys, (t * self.top, dim), ys.dtype, "ys")
+        w = _flat(weights, (t, self.top), _t().float32, "weights")
         ld = _rows(dy, dim, ys.dtype, "dy", t)
-        with _on(stream, dy, ys, weights, route.dest, route.source) as s:
+
+        def call(s):
             dys = _t().empty_like(ys)
             dw = _t().empty_like(weights)
-            _check(lib().dmuon_route_combine_backward(dy.data_ptr(), ld, ys.data_ptr(), weights.data_ptr(),
-                                                      route.dest.data_ptr(), route.source.data_ptr(), t, self.top,
-                                                      dim, kind, dys.data_ptr(), dw.data_ptr(), s))
-        return dys, dw
+            _check(lib().dmuon_route_combine_backward(dy.data_ptr(), ld, rows, w, dest, source, t, self.top, dim, kind,
+                                                      dys.data_ptr(), dw.data_ptr(), s))
+            return dys, dw
+
+        if stream is None:
+            return call(_here(ys))
+        return _on(stream, call, dy, ys, weights, route.dest, route.source)
 
     def dispatch_backward(self, dxs, route, *, stream=None):
         """dx [tokens, dim]: the gradient of dispatch, the sum of each token's rows of dxs."""
