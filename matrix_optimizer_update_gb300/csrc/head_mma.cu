@@ -63,9 +63,7 @@ struct Params {
   int32_t items;
   int32_t rows, cols;      // logits, dz: tiles along the tokens and the vocabulary
   int32_t nk;              // K stages per tile
-  // grads: tiles of dH (`slices` parts of K each) and of dW. The longer dH tiles come first; when the tokens
-  // are few they are dealt over the first `spread` places of the list (see where_is).
-  int32_t spread;
+  // grads: dH tiles come first (the longer ones), `slices` parts of K each, then dW tiles
   int32_t dh_items, dh_rows, dh_nk, slices, slice_nk;
   int32_t dim_tiles;
   int32_t thin_n;          // tokens padded to 32 when they are the N side, else 0
@@ -676,6 +674,10 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
   volatile int* abortf = &sh->abort_flag;
 
   if (threadIdx.x == 0) {
+    for (int i = 0; i < (grads ? 2 : 1); ++i) {
+      ptx::prefetch_tmap(&p.a[i]);
+      ptx::prefetch_tmap(&p.b[i]);
+    }
     for (int s = 0; s < kMaxStages; ++s) {
       ptx::mbar_init(&sh->full[s], 1);
       ptx::mbar_init(&sh->empty[s], 1);
@@ -752,11 +754,12 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
       if (leader) {
         const uint32_t peer_ring = ptx::mapa_shared(ptx::smem_u32(&sh->ring[0]), 1);
         const uint32_t peer_full = ptx::mapa_shared(ptx::smem_u32(&sh->ring_full[0]), 1);
+        // the first tile is the pair's own number, the others are claimed in the order of the list
         auto claim = [&]() -> int {
-          const unsigned w = atomicAdd(p.sched, 1u);
+          const unsigned w = (gridDim.x >> 1) + atomicAdd(p.sched, 1u);
           return w < static_cast<unsigned>(p.items) ? static_cast<int>(w) : -1;
         };
-        int w = claim();
+        int w = static_cast<int>(blockIdx.x >> 1);
         for (uint32_t j = 0;; ++j) {
           const uint32_t slot = j % kRing;
           if (!ptx::mbar_wait_cluster(&sh->ring_empty[slot], ((j / kRing) & 1u) ^ 1u, abortf, p.status, kWaitNs)) break;
