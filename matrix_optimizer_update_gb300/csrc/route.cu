@@ -24,12 +24,16 @@ constexpr int64_t kMaxAssignments = int64_t(1) << 30;
 // it; a warp takes 32 assignments at a time and finds those of equal expert with one match per round, so the
 // order within an expert is the order of the assignments whatever the blocks' timing. A warp reads 256 ids
 // before it looks at the first and keeps what it found of them: the sort takes the latency of one round of
-// loads, eight dependent updates of the counts and the sums over the warps. Up to 8192 assignments go into
-// one block of as many warps as they fill, and one launch.
+// loads, eight dependent updates of the counts and the sums over the warps.
+//
+// Up to 65536 assignments are one launch: a block of as many warps as they fill, or a cluster of up to 8
+// blocks that read each other's counts from shared memory. More take three: counts, sums over the blocks, rows.
+// (32768 assignments to 64 experts: 16 us against 28 in three launches; 131072 to 128: 39 against 31.)
 constexpr int kSortBatch = 8;       // rounds of 32 a warp holds at a time
 constexpr int kSortHeld = 32 * kSortBatch;
 constexpr int kSortMaxBlocks = 1024;
-// Warps per block at most: 32, or 8 where 32 counts per expert would not fit in shared memory (128 KB either way).
+constexpr int kSortCluster = 8;     // blocks of a cluster
+// Warps per block at most: 32, or 8 where 32 counts per expert would not fit in shared memory (132 or 144 KB).
 constexpr int kManyExperts = 1024;
 int sort_warps(int experts) { return experts <= kManyExperts ? 32 : 8; }
 
@@ -143,40 +147,74 @@ __global__ void __launch_bounds__(kScanThreads) route_scan_kernel(const __grid_c
   if (threadIdx.x == 0) p.offsets[p.experts] = base;
 }
 
-// Rows of the block's assignments. ONE: a single block has all of them and makes the offsets itself.
-template <bool ONE>
+__device__ __forceinline__ int cluster_load(const int* mine, unsigned rank) {
+  uint32_t a;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(a)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(mine))), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Rows of the block's assignments. ALL: the launch is one cluster (of gridDim.x blocks) that has all of them and
+// makes the offsets itself; else the blocks' first rows are in p.counts.
+template <bool ALL>
 __global__ void __launch_bounds__(1024) route_place_kernel(const __grid_constant__ SortParams p) {
-  extern __shared__ int hist[];
+  extern __shared__ int hist[];  // [warps][experts], then (ALL) the block's own counts [experts]
   __shared__ int scratch[32];
   follow();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int64_t first = (int64_t(blockIdx.x) * warps + warp) * p.per_warp;
   int e[kSortBatch], place[kSortBatch];
   warp_counts(p, hist, first, e, place);
+  int* own = hist + warps * p.experts;
+  if (ALL) {
+    for (int x = threadIdx.x; x < p.experts; x += blockDim.x) {
+      int mine = 0;
+      for (int w = 0; w < warps; ++w) mine += hist[w * p.experts + x];
+      own[x] = mine;
+    }
+    if (gridDim.x > 1) cluster_barrier();
+    else __syncthreads();
+  }
   int rows = 0;  // rows in use
   for (int e0 = 0; e0 < p.experts; e0 += blockDim.x) {
     const int x = e0 + threadIdx.x;
     int at = 0;
-    if (ONE) {
-      int mine = 0, total;
+    if (ALL) {
+      int before = 0, mine = 0, total;  // of the blocks before this one, of all
       if (x < p.experts)
-        for (int w = 0; w < warps; ++w) mine += hist[w * p.experts + x];
-      at = rows + block_exclusive(mine, scratch, &total);
-      if (x < p.experts) p.offsets[x] = at;
+        for (unsigned b = 0; b < gridDim.x; ++b) {
+          const int c = gridDim.x > 1 ? cluster_load(&own[x], b) : own[x];
+          before += b < blockIdx.x ? c : 0;
+          mine += c;
+        }
+      const int start = rows + block_exclusive(mine, scratch, &total);
+      if (x < p.experts && blockIdx.x == 0) p.offsets[x] = start;
+      at = start + before;
       rows += total;
     } else if (x < p.experts) {
       at = p.counts[int64_t(blockIdx.x) * p.experts + x];
     }
     if (x < p.experts) {
-      for (int w = 0; w < warps; ++w) {  // the warps' first rows
-        const int k = hist[w * p.experts + x];
-        hist[w * p.experts + x] = at;
-        at += k;
+      for (int w0 = 0; w0 < warps; w0 += 8) {  // the warps' first rows; 8 reads in flight, then 8 writes
+        int k[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) k[u] = w0 + u < warps ? hist[(w0 + u) * p.experts + x] : 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (w0 + u < warps) hist[(w0 + u) * p.experts + x] = at;
+          at += k[u];
+        }
       }
     }
   }
-  if (!ONE) rows = p.offsets[p.experts];
-  else if (threadIdx.x == 0) p.offsets[p.experts] = rows;
+  if (!ALL) rows = p.offsets[p.experts];
+  else if (threadIdx.x == 0 && blockIdx.x == 0) p.offsets[p.experts] = rows;
   __syncthreads();
   int* mine = hist + warp * p.experts;
   const bool held = p.per_warp == kSortHeld;  // else the batches are gone through again, the rows in place of counts
@@ -192,6 +230,7 @@ __global__ void __launch_bounds__(1024) route_place_kernel(const __grid_constant
       if (i >= rows) p.source[i] = -1;
     }
   }
+  if (ALL && gridDim.x > 1) cluster_barrier();  // no block leaves while others read its counts
 }
 
 int64_t sort_blocks(int64_t n, int experts) {
@@ -200,12 +239,17 @@ int64_t sort_blocks(int64_t n, int experts) {
 }
 
 cudaError_t launch_sort(SortParams& p, cudaStream_t s) {
-  // a single block has no more warps than its assignments fill
-  const int warps = p.blocks > 1 ? sort_warps(p.experts)
-                                 : static_cast<int>(std::max<int64_t>(1, (p.n + kSortHeld - 1) / kSortHeld));
-  const int64_t all = int64_t(p.blocks) * warps, per = (p.n + all - 1) / all;
-  p.per_warp = static_cast<int32_t>(std::max<int64_t>(1, (per + kSortHeld - 1) / kSortHeld) * kSortHeld);
-  const size_t smem = sizeof(int) * warps * p.experts;
+  const int most = sort_warps(p.experts);
+  const int64_t held = (p.n + kSortHeld - 1) / kSortHeld;  // batches of 256
+  const bool all = held <= int64_t(kSortCluster) * most;
+  int warps = most;
+  if (all) {
+    p.blocks = static_cast<int32_t>(std::min<int64_t>(kSortCluster, std::max<int64_t>(1, (held + most - 1) / most)));
+    if (p.blocks == 1) warps = static_cast<int>(std::max<int64_t>(1, held));
+  }
+  const int64_t total = int64_t(p.blocks) * warps;
+  p.per_warp = static_cast<int32_t>(std::max<int64_t>(1, (held + total - 1) / total) * kSortHeld);
+  const size_t smem = sizeof(int) * (warps + 1) * p.experts;
   cudaError_t e = cudaSuccess;
   if (smem > 40 * 1024) {  // beside the static arrays, within the 48 KB a launch has without asking
     for (auto* k : {route_count_kernel, route_place_kernel<true>, route_place_kernel<false>})
@@ -213,7 +257,7 @@ cudaError_t launch_sort(SortParams& p, cudaStream_t s) {
         e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  if (p.blocks == 1) return launch_follow(route_place_kernel<true>, dim3(1), warps * 32, smem, s, 1, p);
+  if (all) return launch_follow(route_place_kernel<true>, dim3(p.blocks), warps * 32, smem, s, p.blocks, p);
   e = launch_follow(route_count_kernel, dim3(p.blocks), warps * 32, smem, s, 1, p);
   if (e == cudaSuccess) e = launch_follow(route_scan_kernel, dim3(1), kScanThreads, 0, s, 1, p);
   if (e == cudaSuccess) e = launch_follow(route_place_kernel<false>, dim3(p.blocks), warps * 32, smem, s, 1, p);
@@ -257,6 +301,9 @@ struct RowParams {
 
 constexpr int kRowThreads = 256;
 
+// Assignments whose rows a thread reads at a time: their loads are in flight together.
+constexpr int kAtOnce = 4;
+
 template <typename T, int V>
 __global__ void __launch_bounds__(kRowThreads) route_dispatch_kernel(const __grid_constant__ RowParams p) {
   using P = Packed<T, V>;
@@ -264,17 +311,26 @@ __global__ void __launch_bounds__(kRowThreads) route_dispatch_kernel(const __gri
   const int64_t t = blockIdx.x;
   const T* x = static_cast<const T*>(p.in) + t * p.ld;
   const int64_t dim = int64_t(p.pieces) * V;
-  for (int c = blockIdx.y * kRowThreads + threadIdx.x; c < p.pieces; c += gridDim.y * kRowThreads) {
-    const P v = *reinterpret_cast<const P*>(x + int64_t(c) * V);
-    for (int k = 0; k < p.top; ++k) {
-      const int64_t i = t * p.top + k;
-      const int row = p.dest[i];
-      if (row >= 0) *reinterpret_cast<P*>(static_cast<T*>(p.out) + row * dim + int64_t(c) * V) = v;
-      if (p.source[i] < 0) {
-        P zero;
+  T* xs = static_cast<T*>(p.out);
+  P zero;
 #pragma unroll
-        for (int j = 0; j < V; ++j) zero.v[j] = from_f<T>(0.f);
-        *reinterpret_cast<P*>(static_cast<T*>(p.out) + i * dim + int64_t(c) * V) = zero;
+  for (int j = 0; j < V; ++j) zero.v[j] = from_f<T>(0.f);
+  for (int c = blockIdx.y * kRowThreads + threadIdx.x; c < p.pieces; c += gridDim.y * kRowThreads) {
+    const int64_t at = int64_t(c) * V;
+    const P v = *reinterpret_cast<const P*>(x + at);
+    for (int k0 = 0; k0 < p.top; k0 += kAtOnce) {
+      int row[kAtOnce];
+      bool unused[kAtOnce];  // row i of xs is not in use
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int64_t i = t * p.top + k0 + u;
+        row[u] = k0 + u < p.top ? p.dest[i] : -1;
+        unused[u] = k0 + u < p.top && p.source[i] < 0;
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (row[u] >= 0) *reinterpret_cast<P*>(xs + row[u] * dim + at) = v;
+        if (unused[u]) *reinterpret_cast<P*>(xs + (t * p.top + k0 + u) * dim + at) = zero;
       }
     }
   }
@@ -288,17 +344,29 @@ __global__ void __launch_bounds__(kRowThreads) route_combine_kernel(const __grid
   T* y = static_cast<T*>(p.out) + t * p.ld;
   const int64_t dim = int64_t(p.pieces) * V;
   for (int c = blockIdx.y * kRowThreads + threadIdx.x; c < p.pieces; c += gridDim.y * kRowThreads) {
+    const T* ys = static_cast<const T*>(p.in) + int64_t(c) * V;
     float sum[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) sum[j] = 0.f;
-    for (int k = 0; k < p.top; ++k) {
-      const int64_t i = t * p.top + k;
-      const int row = p.dest[i];
-      if (row < 0) continue;
-      const float w = p.weights != nullptr ? p.weights[i] : 1.f;
-      const P v = *reinterpret_cast<const P*>(static_cast<const T*>(p.in) + row * dim + int64_t(c) * V);
+    for (int k0 = 0; k0 < p.top; k0 += kAtOnce) {
+      int row[kAtOnce];
+      float w[kAtOnce];
+      P v[kAtOnce];
 #pragma unroll
-      for (int j = 0; j < V; ++j) sum[j] = fmaf(w, to_f(v.v[j]), sum[j]);
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int64_t i = t * p.top + k0 + u;
+        row[u] = k0 + u < p.top ? p.dest[i] : -1;
+        w[u] = p.weights != nullptr && k0 + u < p.top ? p.weights[i] : 1.f;
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+        if (row[u] >= 0) v[u] = *reinterpret_cast<const P*>(ys + row[u] * dim);
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (row[u] < 0) continue;
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum[j] = fmaf(w[u], to_f(v[u].v[j]), sum[j]);
+      }
     }
     P o;
 #pragma unroll

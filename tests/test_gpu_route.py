@@ -146,3 +146,21 @@ def test_bad_tensors_are_refused():
         with pytest.raises(dm.DmuonError) as e:
             call()
         assert e.value.status == dm.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("n,experts", [(255, 7), (257, 1), (8192, 64), (8193, 64), (40000, 1024), (65536, 1024), (65537, 1025),
+                                       (131072, 130), (131073, 3), (33000, 4096), (1100000, 300)])
+def test_sort_of_every_launch_shape(n, experts):
+    # one block, clusters of 2 to 8, and three launches
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n)
+    ids = (torch.rand(n, 1, generator=g, device="cuda") ** 3 * experts).long()
+    ids[torch.rand(n, 1, generator=g, device="cuda") < 0.03] = -5
+    route = dm.Router.create(n, 1, experts).sort(ids)
+    key = torch.where(ids[:, 0] < 0, experts, ids[:, 0])
+    order = torch.argsort(key, stable=True)
+    used = int((key < experts).sum())
+    assert route.offsets.tolist() == [0] + torch.bincount(key, minlength=experts + 1)[:experts].cumsum(0).tolist()
+    assert torch.equal(route.source[:used].long(), order[:used]) and (route.source[used:] == -1).all()
+    assert torch.equal(route.dest[order[:used], 0].long(), torch.arange(used, device="cuda"))
+    assert (route.dest[order[used:], 0] == -1).all()
