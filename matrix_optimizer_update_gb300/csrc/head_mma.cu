@@ -803,23 +803,25 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
         if (!ptx::mbar_wait_cluster(&sh->tempty[acc], ((local >> 1) & 1u) ^ 1u, abortf, p.status, kWaitNs)) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem + acc * kTile;
+        // Descriptors of stage 0; a stage or 16 columns of K further is an addition to the address field (in 16
+        // bytes). K-major: 16 columns further in the swizzled rows; MN-major: 16 rows of 128 bytes further, the
+        // operand's second 64-element block kHalf / 2 on. One thread issues everything, so what it computes per
+        // MMA counts: built anew each time, the four descriptors of a stage took 285 of its 512 cycles.
+        const uint32_t s0 = ptx::smem_u32(base);
+        const uint64_t a_desc = a_mn ? ptx::sw128_desc(s0, kHalf / 2, 1024) : ptx::sw128_desc(s0, 16, 1024);
+        const uint64_t b_desc =
+            b_mn ? ptx::sw128_desc(s0 + a_bytes, kHalf / 2, 1024) : ptx::sw128_desc(s0 + a_bytes, 16, 1024);
+        const uint32_t a_step = a_mn ? 2048 / 16 : 32 / 16, b_step = b_mn ? 2048 / 16 : 32 / 16;
         for (int kb = 0; kb < x.nk; ++kb) {
           if (!ptx::mbar_wait_cluster(&sh->full[stage], phase, abortf, p.status, kWaitNs)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t a0 = ptx::smem_u32(base) + stage * stage_bytes, b0 = a0 + a_bytes;
+          const uint64_t a0 = a_desc + stage * (stage_bytes / 16), b0 = b_desc + stage * (stage_bytes / 16);
 #pragma unroll
-          for (int kk = 0; kk < kStep / 16; ++kk) {
-            // K-major: 16 columns further in the swizzled rows; MN-major: 16 rows of 128 bytes further, the
-            // operand's second 64-element block kHalf / 2 on
-            const uint64_t ad = a_mn ? ptx::sw128_desc(a0 + kk * 2048, kHalf / 2, 1024)
-                                     : ptx::sw128_desc(a0 + kk * 32, 16, 1024);
-            const uint64_t bd = b_mn ? ptx::sw128_desc(b0 + kk * 2048, kHalf / 2, 1024)
-                                     : ptx::sw128_desc(b0 + kk * 32, 16, 1024);
-            ptx::umma_f16_pair(d, ad, bd, id, (kb | kk) != 0 ? 1u : 0u);
-          }
+          for (uint32_t kk = 0; kk < kStep / 16; ++kk)
+            ptx::umma_f16_pair(d, a0 + kk * a_step, b0 + kk * b_step, id, (kb | kk) != 0 ? 1u : 0u);
           ptx::umma_commit_pair(&sh->empty[stage], 0x3);
           if (++stage == stages) {
             stage = 0;
