@@ -174,6 +174,7 @@ dmuon_status forward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, cons
   head::LogitParams p = logit_params(H, hidden, ld_hidden, weight, ld_weight, tokens, L);
   if ((st = prepare_wanted(H, L, tokens, p.in, &p.want, s)) != DMUON_OK) return st;
   p.parts = reinterpret_cast<head::Part*>(H->ws + H->off_parts);
+  p.after_lists = distill;
   cudaError_t e = head::launch_logits(p, H->pipe(), s);
   if (e != cudaSuccess) return cuda_refuse(e, "logits kernel");
   head::RowParams r{};
@@ -244,6 +245,7 @@ dmuon_status backward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, con
     p.v0 = g.v0 = static_cast<int32_t>(v0);
     p.width = g.width = static_cast<int32_t>(std::min(H->piece, H->vocab - v0));
     g.first = v0 == 0;
+    p.after_lists = distill && v0 == 0;  // a later piece's dz has to wait for the one before to be read
     if ((e = head::launch_dz(p, H->pipe(), s)) != cudaSuccess) return cuda_refuse(e, "dz kernel");
     if ((e = head::launch_grads(g, H->pipe(), s)) != cudaSuccess) return cuda_refuse(e, "gradient kernel");
   }

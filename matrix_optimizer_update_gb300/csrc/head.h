@@ -60,6 +60,7 @@ struct LogitParams {
   Wanted want;
   // forward
   Part* parts;             // [groups][tokens]; few tokens: [tokens][groups]
+  int32_t after_lists;     // the launch before this one on the stream is launch_teacher's
   float* picked;           // [tokens][want.top]: scaled logits of the wanted entries
   int32_t v0, width;       // entries v0 .. v0 + width - 1 (forward: all)
   // backward

@@ -703,7 +703,9 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem = sh->tmem;
-  follow(MODE != kLogits && MODE != kThinLogits);
+  // After the kernel that sorts the lists, which lets this one start once everything before it is done, only the
+  // epilogue has to wait for it: loads and products of the first tile run beside it.
+  if (!p.l.after_lists || warp >= 2) follow(MODE != kLogits && MODE != kThinLogits);
   const uint32_t lead_empty = ptx::mapa_shared(ptx::smem_u32(&sh->ring_empty[0]), 0);
 
   if (warp == 0) {
