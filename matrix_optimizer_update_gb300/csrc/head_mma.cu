@@ -133,6 +133,14 @@ __device__ __forceinline__ void arrive_pair(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// A 32-bit store to the peer's shared memory that counts its 4 bytes on a barrier there. (A plain store and an
+// arrival that releases it at cluster scope wait for everything the thread has in flight.)
+__device__ __forceinline__ void store_async_peer(uint32_t addr, int v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(v),
+               "r"(bar)
+               : "memory");
+}
+
 // Adds a staged fp32 box to global memory, element by element.
 __device__ __forceinline__ void tma_add_3d(const void* map, const void* src, int x, int y, int z) {
   asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
@@ -645,10 +653,11 @@ __device__ __forceinline__ bool drain_thin_dw(const Params& P, float scale, int 
 
 // ------------------------------------------------------------------ the kernel
 __device__ __forceinline__ bool take(Shared* sh, uint32_t j, int& w, uint32_t lead_empty, volatile int* abortf,
-                                     const Params& p) {
+                                     const Params& p, bool arm = false) {
   const uint32_t slot = j % kRing;
   if (!ptx::mbar_wait_cluster(&sh->ring_full[slot], (j / kRing) & 1u, abortf, p.status, kWaitNs)) return false;
   w = *reinterpret_cast<volatile int*>(&sh->ring[slot]);
+  if (arm) ptx::mbar_arrive_expect_tx(&sh->ring_full[slot], 4);
   arrive_pair(lead_empty + slot * static_cast<uint32_t>(sizeof(uint64_t)));
   return true;
 }
@@ -756,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
       if (leader) {
         const uint32_t peer_ring = ptx::mapa_shared(ptx::smem_u32(&sh->ring[0]), 1);
         const uint32_t peer_full = ptx::mapa_shared(ptx::smem_u32(&sh->ring_full[0]), 1);
-        // the first tile is the pair's own number, the others are claimed in the order of the list
+        // The first tile is the pair's own number, the others are claimed in the order of the list.
         auto claim = [&]() -> int {
           const unsigned w = (gridDim.x >> 1) + atomicAdd(p.sched, 1u);
           return w < static_cast<unsigned>(p.items) ? static_cast<int>(w) : -1;
@@ -766,9 +775,8 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
           const uint32_t slot = j % kRing;
           if (!ptx::mbar_wait_cluster(&sh->ring_empty[slot], ((j / kRing) & 1u) ^ 1u, abortf, p.status, kWaitNs)) break;
           sh->ring[slot] = w;
-          ptx::st_shared_cluster_s32(peer_ring + slot * 4u, w);
+          store_async_peer(peer_ring + slot * 4u, w, peer_full + slot * static_cast<uint32_t>(sizeof(uint64_t)));
           ptx::mbar_arrive(&sh->ring_full[slot]);
-          ptx::mbar_arrive_cluster(peer_full + slot * static_cast<uint32_t>(sizeof(uint64_t)));
           if (w < 0) break;
           const int next = claim();  // its latency hides under this tile's loads
           if (!load_tile(w)) break;
@@ -783,9 +791,12 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
           }
         }
       } else {
+        // the ring's barriers here complete on the leader's 4 bytes: this thread arms each for its next use before
+        // it hands the slot back
+        for (int k = 0; k < kRing; ++k) ptx::mbar_arrive_expect_tx(&sh->ring_full[k], 4);
         for (uint32_t j = 0;; ++j) {
           int w;
-          if (!take(sh, j, w, lead_empty, abortf, p) || w < 0) break;
+          if (!take(sh, j, w, lead_empty, abortf, p, true) || w < 0) break;
           if (!load_tile(w)) break;
         }
       }
