@@ -623,30 +623,32 @@ __device__ __forceinline__ bool drain_grads(const Params& P, const Where& x, flo
   return true;
 }
 
-// The same for dW of few tokens, whose product is one or two K stages, so that the epilogue sets the pace: all
-// 128 columns are staged before one fence and two stores of 64 columns. v0: first row, below v_lim if any is.
+// The same for dW of few tokens, whose product is one or two K stages, so that the epilogue sets the pace: two
+// stores of 64 columns, from a box each, which the next tile finds free again. v0: first row; v_lim: past the last.
 template <class Wait, class Free>
 __device__ __forceinline__ bool drain_thin_dw(const Params& P, float scale, int v0, int v_lim, int d0, uint32_t tbase, int lane,
                                               uint8_t* stg, Wait&& wait, Free&& free) {
-  if (lane == 0) ptx::bulk_wait_read<0>();  // the last tile's stores are done with the boxes
-  __syncwarp();
   if (!wait()) return false;
   ptx::tc_fence_after();
 #pragma unroll
-  for (int ch = 0; ch < 4; ++ch) {
-    float v[32];
-    ptx::tmem_ld_32x32b_x32(tbase + ch * 32, v);
-    if (ch == 3) free();
-    uint8_t* box = stg + (ch >> 1) * kWideBox;
+  for (int h = 0; h < 2; ++h) {
+    uint8_t* box = stg + h * kWideBox;
+    if (lane == 0) ptx::bulk_wait_read<1>();  // the last tile's store from this box is done with it
+    __syncwarp();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) *wide_piece(box, lane, (ch & 1) * 4 + q) = rounded(v, q * 8, scale);
-  }
-  ptx::fence_proxy_async_shared();
-  __syncwarp();
-  if (lane == 0) {
-    if (v0 < v_lim && d0 < P.l.in.dim) ptx::tma_store_2d(&P.out[1], stg, d0, v0);
-    if (v0 < v_lim && d0 + 64 < P.l.in.dim) ptx::tma_store_2d(&P.out[1], stg + kWideBox, d0 + 64, v0);
-    ptx::bulk_commit();
+    for (int ch = 0; ch < 2; ++ch) {
+      float v[32];
+      ptx::tmem_ld_32x32b_x32(tbase + (2 * h + ch) * 32, v);
+      if (h == 1 && ch == 1) free();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) *wide_piece(box, lane, ch * 4 + q) = rounded(v, q * 8, scale);
+    }
+    ptx::fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      if (v0 < v_lim && d0 + 64 * h < P.l.in.dim) ptx::tma_store_2d(&P.out[1], box, d0 + 64 * h, v0);
+      ptx::bulk_commit();
+    }
   }
   return true;
 }
