@@ -482,7 +482,9 @@ dmuon_status dmuon_head_bind(dmuon_head_t head, void* d_workspace, size_t bytes,
  *   loss[t] = lse[t] - z[t][targets[t]]
  *
  *  targets   device, tokens int64. A target outside 0..vocab-1 (-100, say)
- *            marks a token that does not count: its loss is 0.
+ *            marks a token that does not count: its loss is 0, and its rows of
+ *            dz and dH are exact zeros whatever its logits are. (Its row of H
+ *            has to be finite all the same: dW sums 0 * H.)
  *  tokens    0..max_tokens; 0 is a no-op.
  *  loss, lse device, tokens floats each.
  *

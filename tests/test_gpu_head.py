@@ -303,3 +303,59 @@ def test_bad_tensors_are_refused():
         with pytest.raises(dm.DmuonError) as e:
             call()
         assert e.value.status == dm.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("tokens,vocab,dim", [(1, 100, 40), (77, 1003, 72), (128, 5000, 64), (300, 1500, 136)])
+def test_nothing_is_read_from_a_workspace_that_was_not_written(tokens, vocab, dim):
+    # NaN everywhere before the bind, and again, past the status and counters, before each call
+    h, w, y, g = inputs(tokens, vocab, dim, 16)
+    ids, lg = teacher(tokens, vocab, 9, 17)
+    head = dm.Head.create(tokens, vocab, dim, max_top=9)
+    clean = head.xent(h, w, y)
+    clean += head.xent_backward(h, w, y, clean[1], g)
+    soft = head.distill(h, w, ids, lg, 2.0)
+    soft += head.distill_backward(h, w, ids, lg, 2.0, soft[1], g)
+    ws = head.workspace
+    at = -ws.data_ptr() % 1024
+    ws.fill_(255)
+    head.bind(ws.data_ptr() + at, head.workspace_bytes(), torch.cuda.current_stream().cuda_stream)
+
+    def poisoned(call):
+        ws[at + 1024:].fill_(255)
+        return call()
+
+    again = poisoned(lambda: head.xent(h, w, y))
+    again += poisoned(lambda: head.xent_backward(h, w, y, again[1], g))
+    soft2 = poisoned(lambda: head.distill(h, w, ids, lg, 2.0))
+    soft2 += poisoned(lambda: head.distill_backward(h, w, ids, lg, 2.0, soft2[1], g))
+    assert all(torch.equal(a, b) for a, b in zip(clean + soft, again + soft2))
+    assert head.read_device_status(torch.cuda.current_stream().cuda_stream) == 0
+
+
+@pytest.mark.parametrize("tokens", [3, 200])
+def test_a_weight_of_more_than_2_to_the_31_elements(tokens):
+    vocab, dim = 540_000, 4096
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    w = torch.empty(vocab, dim, device="cuda", dtype=torch.bfloat16)
+    for a in range(0, vocab, 60_000):
+        w[a:a + 60_000].normal_(0, 0.02, generator=g)
+    h = torch.randn(tokens, dim, generator=g, device="cuda").to(torch.bfloat16)
+    y = vocab - 1 - torch.arange(tokens, device="cuda") * 7
+    head = dm.Head.create(tokens, vocab, dim)
+    loss, lse = head.xent(h, w, y)
+    grad = torch.full((tokens,), 1.0 / tokens, device="cuda")
+    dh, dw = head.xent_backward(h, w, y, lse, grad)
+    hd = h.double()
+    z = torch.cat([hd @ w[a:a + 30_000].double().T for a in range(0, vocab, 30_000)], 1)
+    want = torch.logsumexp(z, 1)
+    # |z| <= 8 and A <= 4096 * 0.02 * 3: the bound of test_xent with those, in round figures
+    assert (lse - want).abs().max() < 4104 * 2 * E * 250 * 2
+    assert (loss - (want - z[torch.arange(tokens), y])).abs().max() < 4104 * 2 * E * 250 * 2
+    dz = torch.exp(z - want[:, None])
+    dz[torch.arange(tokens), y] -= 1
+    dz /= tokens
+    for rows in (slice(0, 300), slice(524_200, 524_400), slice(vocab - 300, vocab)):  # 2^31 elements is row 524288
+        assert torch.linalg.norm(dw[rows].double() - dz[:, rows].T @ hd) < 2 * U * torch.linalg.norm(dz[:, rows].T @ hd)
+    want_h = sum(dz[:, a:a + 30_000] @ w[a:a + 30_000].double() for a in range(0, vocab, 30_000))
+    assert torch.linalg.norm(dh.double() - want_h) < 2 * U * torch.linalg.norm(want_h)

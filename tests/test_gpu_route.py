@@ -164,3 +164,23 @@ def test_sort_of_every_launch_shape(n, experts):
     assert torch.equal(route.source[:used].long(), order[:used]) and (route.source[used:] == -1).all()
     assert torch.equal(route.dest[order[:used], 0].long(), torch.arange(used, device="cuda"))
     assert (route.dest[order[used:], 0] == -1).all()
+
+
+def test_rows_of_more_than_2_to_the_31_elements():
+    tokens, top, experts, dim = 70_000, 8, 16, 4096  # 2.3e9 elements of expert rows
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    ids = torch.randint(0, experts, (tokens, top), generator=g, device="cuda")
+    x = torch.randn(tokens, dim, generator=g, device="cuda").to(torch.bfloat16)
+    router = dm.Router.create(tokens, top, experts)
+    route = router.sort(ids)
+    xs = router.dispatch(x, route)
+    src = route.source.long() // top
+    for a in range(0, tokens * top, 56_000):
+        assert torch.equal(xs[a:a + 56_000], x[src[a:a + 56_000]])
+    wts = torch.full((tokens, top), 0.125, device="cuda")
+    assert torch.equal(router.combine(xs, wts, route), x)  # eight eighths, exact
+    dys, dw = router.combine_backward(x, xs, wts, route)
+    assert torch.equal(dys[-1], xs[-1] * 0.125) and torch.equal(dys[-40_000], xs[-40_000] * 0.125)
+    norm = x.double().square().sum(1)
+    assert ((dw.double() - norm[:, None]).abs() <= dim * E * norm[:, None]).all()
