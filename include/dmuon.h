@@ -454,7 +454,7 @@ dmuon_status dmuon_adamw_flat(void* param, const void* grad, float* exp_avg, flo
  * is kept from one call for the next except the status word.
  *
  * H, W and their gradients start on 16 bytes, and their row pitches are
- * multiples of 8 elements and at least dim.
+ * multiples of 8 elements and at least dim. Outputs must not overlap inputs.
  */
 typedef struct dmuon_head_s* dmuon_head_t;
 
@@ -503,7 +503,8 @@ dmuon_status dmuon_head_xent(dmuon_head_t head, const void* hidden, int64_t ld_h
  *   dH = dz W,  dW = dz^T H
  *
  *  lse        device, tokens floats, as dmuon_head_xent wrote them.
- *  grad_loss  device, tokens floats (1/n for a mean over n tokens).
+ *  grad_loss  device, tokens floats (1/n for a mean over n tokens); not used
+ *             of tokens that do not count.
  *  dhidden    device, tokens x dim bf16, pitch ld_dhidden, or NULL: not wanted.
  *  dweight    device, vocab x dim bf16, pitch ld_dweight, or NULL: not wanted
  *             (a frozen head). Overwritten, also when tokens is 0.
@@ -573,7 +574,7 @@ void dmuon_head_destroy(dmuon_head_t head);
  *   source[r]   the assignment of row r, -1 past the last row in use
  *
  * Asynchronous on stream, no allocation, deterministic (no atomics whose order
- * could show).
+ * could show). Outputs must not overlap inputs.
  */
 
 /* Bytes of scratch dmuon_route_sort needs for up to these sizes (host only):

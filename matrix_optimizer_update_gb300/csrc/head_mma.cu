@@ -311,7 +311,7 @@ __device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, in
               z = v[k];
               v[k] = -INFINITY;
             }
-          if (c.share(p.want) < kSure) p.picked[t * p.want.top + c.pos] = z;
+          if (!(c.share(p.want) >= kSure)) p.picked[t * p.want.top + c.pos] = z;
         }
         last_id = c.id;
         c.next(p.want);
@@ -480,7 +480,7 @@ __device__ __forceinline__ bool drain_thin_logits(const Params& P, int first, in
           z = v[j];
           v[j] = -INFINITY;
         }
-      if (share < kSure) p.picked[int64_t(b * 32 + k) * p.want.top + pos] = z;
+      if (!(share >= kSure)) p.picked[int64_t(b * 32 + k) * p.want.top + pos] = z;
     });
     const float peak = columns(v, lane, [](float x, float y) { return fmaxf(x, y); });
     const float from = peak == -INFINITY ? 0.f : peak;
@@ -861,7 +861,8 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
     float gmax = 1.f;
     if (MODE == kDz || MODE == kThinDz) {  // under the first tile's products
       float m = 0.f;
-      for (int64_t t = threadIdx.x - 64; t < p.l.tokens; t += kEpiWarps * 32) m = fmaxf(m, fabsf(p.l.grad[t]));
+      for (int64_t t = threadIdx.x - 64; t < p.l.tokens; t += kEpiWarps * 32)
+        if (counts(p.l.want, t)) m = fmaxf(m, fabsf(p.l.grad[t]));
       for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
       if (lane == 0) sh->red[warp - 2] = m;
       asm volatile("bar.sync 1, 256;" ::: "memory");

@@ -359,3 +359,36 @@ def test_a_weight_of_more_than_2_to_the_31_elements(tokens):
         assert torch.linalg.norm(dw[rows].double() - dz[:, rows].T @ hd) < 2 * U * torch.linalg.norm(dz[:, rows].T @ hd)
     want_h = sum(dz[:, a:a + 30_000] @ w[a:a + 30_000].double() for a in range(0, vocab, 30_000))
     assert torch.linalg.norm(dh.double() - want_h) < 2 * U * torch.linalg.norm(want_h)
+
+
+@pytest.mark.parametrize("tokens", [20, 200])
+def test_gradients_of_tokens_that_do_not_count_may_hold_anything(tokens):
+    h, w, y, g = inputs(tokens, 300, 64, 18)
+    y[3], y[11] = -100, 300
+    head = dm.Head.create(tokens, 300, 64, max_top=3)
+    loss, lse = head.xent(h, w, y)
+    g[3] = g[11] = 0.0
+    want = head.xent_backward(h, w, y, lse, g)
+    g[3], g[11] = float("inf"), float("nan")
+    assert all(torch.equal(a, b) for a, b in zip(want, head.xent_backward(h, w, y, lse, g)))
+    ids, lg = teacher(tokens, 300, 3, 19)
+    lg[3], ids[11] = -torch.inf, -1
+    loss, lse = head.distill(h, w, ids, lg, 1.5)
+    g[3] = g[11] = 0.0
+    want = head.distill_backward(h, w, ids, lg, 1.5, lse, g)
+    g[3], g[11] = float("inf"), float("nan")
+    assert all(torch.equal(a, b) for a, b in zip(want, head.distill_backward(h, w, ids, lg, 1.5, lse, g)))
+
+
+@pytest.mark.parametrize("tokens", [20, 200])
+def test_a_nan_in_a_list_stays_in_its_row(tokens):
+    h, w, _, _ = inputs(tokens, 300, 64, 20, sure=False)
+    ids, lg = teacher(tokens, 300, 5, 21)
+    head = dm.Head.create(tokens, 300, 64, max_top=5)
+    clean, lse = head.distill(h, w, ids, lg, 2.0)
+    lg[4, 2] = float("nan")
+    loss, lse2 = head.distill(h, w, ids, lg, 2.0)
+    keep = torch.arange(tokens, device="cuda") != 4
+    assert torch.isnan(loss[4]) and torch.equal(loss[keep], clean[keep])
+    # the student's sum is the teacher's business in no row: equal up to where its logits were formed
+    assert torch.equal(lse2[keep], lse[keep]) and (lse2[4] - lse[4]).abs() < 1e-4
