@@ -83,7 +83,8 @@ def check_grads(dh, dw, r, h, w, g, er):
 
 
 SIZES = [(1, 1, 8), (1, 2, 1), (1, 300, 64), (3, 17, 24), (2, 128, 64), (64, 129, 72), (127, 255, 40), (129, 257, 264),
-         (256, 512, 128), (257, 1000, 512), (300, 5003, 136), (40, 20000, 256), (1025, 640, 96), (1, 33000, 1024)]
+         (256, 512, 128), (257, 1000, 512), (300, 5003, 136), (40, 20000, 256), (1025, 640, 96), (1, 33000, 1024),
+         (4, 300, 65536), (20000, 50, 16), (129, 1, 8), (1000, 3, 1), (128, 70000, 24), (513, 257, 200)]
 
 
 @pytest.mark.parametrize("tokens,vocab,dim", SIZES)
