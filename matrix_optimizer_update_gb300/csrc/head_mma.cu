@@ -129,6 +129,13 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, uin
       : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_2d(const void* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
 // Arrive on an mbarrier of either CTA of the pair (cluster address). What it orders are this thread's own
 // reads (a ring slot, TMEM) before the arrival, for which the scope of the CTA is enough; with the scope of the
 // cluster the arrival waits for every store in flight, which took 2300 of the 5900 cycles of a dW tile.
@@ -717,6 +724,12 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem = sh->tmem;
+  // Set up while the kernel before still runs: the first stages of W on their way to L2 (a hint: nothing is read
+  // before that kernel is done, and what it may write to W passes through L2). 1 to 2 % of a call with few tokens.
+  if ((MODE == kThinLogits || MODE == kThinDz) && threadIdx.x == 0) {
+    const int row = p.l.v0 + static_cast<int>(blockIdx.x >> 1) * p.thin_h + rank * (p.thin_h / 2);
+    for (int kb = 0; kb < min(p.nk, 16); ++kb) tma_prefetch_2d(&p.b[0], kb * kStep, row);
+  }
   // After the kernel that sorts the lists, which lets this one start once everything before it is done, only the
   // epilogue has to wait for it: loads and products of the first tile run beside it.
   if (!p.l.after_lists || warp >= 2) follow(MODE != kLogits && MODE != kThinLogits);
