@@ -99,7 +99,7 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= 1024, "barriers must fit their 1 KB");
 
-// What thin dz needs of its tokens, in shared memory (in the place of the staging boxes, which it has not).
+// What thin dz needs of its tokens, in shared memory.
 struct ThinTokens {
   float g[kThin];      // gradient relative to the largest, 0 for a token that does not count
   float lse[kThin];
@@ -279,20 +279,48 @@ __device__ __forceinline__ void target_logits(const LogitParams& p, const Cursor
     z[0] = warp_sum(z[0]) * p.in.scale;
     if (lane == L) p.picked[t] = z[0];
   }
-  __syncwarp();  // other lanes may read what was written
+}
+
+// 32 x 32 values in shared memory, rows turned so that neither rows nor columns conflict.
+__device__ __forceinline__ float& cell(float* sm, int row, int col) { return sm[row * 32 + (col ^ row)]; }
+
+// Visits the entries of this lane's cursor before `end`, whose values are row `lane` of sm (column: id - first):
+// visit(value, share, pos, again), `again` when the entry before had the same id. A lane's entries may be many:
+// frequent words lie together in many vocabularies. (With the values left in registers, where an entry takes a
+// compare for each of 32, and one after another over a warp's tokens, 48 lists of 68 entries against 9328 x 1616
+// made a call of 304 us; this way 87.)
+template <class Visit>
+__device__ __forceinline__ void walk(const Wanted& w, Cursor& c, int first, int end, float* sm, int lane,
+                                     Visit&& visit) {
+  int last = -1;
+  while (c.id < end) {
+    visit(cell(sm, lane, c.id - first), c.share(w), c.pos, c.id == last);
+    last = c.id;
+    c.next(w);
+  }
+}
+
+// The wanted entries of this lane's token among its 32 values v (entries from `first`).
+template <class Visit>
+__device__ __forceinline__ void wanted_of_row(const Wanted& w, Cursor& c, int first, float (&v)[32], float* sm,
+                                              int lane, Visit&& visit) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) cell(sm, lane, k) = v[k];
+  walk(w, c, first, first + 32, sm, lane, visit);
+#pragma unroll
+  for (int k = 0; k < 32; ++k) v[k] = cell(sm, lane, k);
 }
 
 // One warp's part of a logits tile: 32 tokens, 128 entries from j0. `wait` returns false when the CTA gave up.
 template <class Wait, class Free>
-__device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, int j0, uint32_t tbase, Wait&& wait,
-                                             Free&& free) {
+__device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, int j0, uint32_t tbase, int lane,
+                                             float* sm, Wait&& wait, Free&& free) {
   const bool in = t < p.tokens;
   Cursor c;
   c.start(p.want, t, in, j0);
   if (!wait()) return false;
   ptx::tc_fence_after();
   float peak = -INFINITY, sum = 0.f;
-  int last_id = -1;
 #pragma unroll 1
   for (int ch = 0; ch < 4; ++ch) {
     const int jc = j0 + ch * 32;
@@ -307,23 +335,12 @@ __device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, in
       for (int k = 0; k < 32; ++k)
         if (jc + k >= p.vocab) v[k] = -INFINITY;
     }
-    while (__any_sync(0xffffffffu, c.id < jc + 32)) {
-      if (c.id < jc + 32) {
-        const int at = c.id - jc;
-        float z = 0.f;
-        if (c.id != last_id) {  // entries that share an id have one logit, with the first of them
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (k == at) {
-              z = v[k];
-              v[k] = -INFINITY;
-            }
-          if (!(c.share(p.want) >= kSure)) p.picked[t * p.want.top + c.pos] = z;
-        }
-        last_id = c.id;
-        c.next(p.want);
-      }
-    }
+    if (__any_sync(0xffffffffu, c.id < jc + 32))
+      wanted_of_row(p.want, c, jc, v, sm, lane, [&](float& x, float share, int pos, bool again) {
+        if (again) return;  // entries that share an id have one logit, with the first of them
+        if (!(share >= kSure)) p.picked[t * p.want.top + pos] = x;
+        x = -INFINITY;
+      });
     float top = v[0];
 #pragma unroll
     for (int k = 1; k < 32; ++k) top = fmaxf(top, v[k]);
@@ -356,7 +373,6 @@ __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t,
   }
   target_logits(p, c, t, min(j0 + 128, p.vocab), lane);
   const float g_low = g * kLow;
-  int last_id = -1;
   if (!wait()) return false;
   ptx::tc_fence_after();
 #pragma unroll 1
@@ -376,18 +392,15 @@ __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t,
       for (int k = 0; k < 32; ++k)
         if (jc + k >= p.vocab) v[k] = 0.f;
     }
-    while (__any_sync(0xffffffffu, c.id < jc + 32)) {
-      if (c.id < jc + 32) {
-        const int at = c.id - jc;
-        const float share = c.share(p.want);
-        const bool sure = share >= kSure && c.id != last_id;
-        const float e = sure ? expf(p.picked[t * p.want.top + c.pos] - lse) : 0.f;
-        last_id = c.id;
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if (k == at) v[k] = sure ? g * (e - share) : v[k] - g * share;
-        c.next(p.want);
-      }
+    if (__any_sync(0xffffffffu, c.id < jc + 32)) {
+      if (lane == 0) ptx::bulk_wait_read<0>();  // both boxes' place
+      __syncwarp();
+      wanted_of_row(p.want, c, jc, v, reinterpret_cast<float*>(stg), lane,
+                    [&](float& x, float share, int pos, bool again) {
+                      const bool sure = share >= kSure && !again;
+                      const float e = sure ? expf(p.picked[t * p.want.top + pos] - lse) : 0.f;
+                      x = sure ? g * (e - share) : x - g * share;
+                    });
     }
     uint8_t* box = stg + (nbox & 1u) * kBox;
     if (lane == 0) ptx::bulk_wait_read<1>();  // the store that last read this box is done with it
@@ -425,36 +438,27 @@ __device__ __forceinline__ float columns(const float (&v)[32], int lane, Op op) 
   return r[0];
 }
 
-// The wanted entries of 32 tokens among 32 lanes' vocabulary entries [first, end): lane L's cursor belongs to
-// token t0 + L. take(k, q, pos, again) is called by the lane whose entry it is, for column k and the pos-th of
-// the list; `again` when the token's entry before had the same id.
-template <class Take>
-__device__ __forceinline__ void each_wanted(const Wanted& w, Cursor& c, int first, int end, int lane, Take&& take) {
-  int last = -1;
-  while (true) {
-    unsigned more = __ballot_sync(0xffffffffu, c.id < end);
-    if (more == 0u) return;
-    const float q = c.id < end ? c.share(w) : 0.f;
-    while (more != 0u) {
-      const int L = __ffs(more) - 1;
-      more &= more - 1u;
-      const int id = __shfl_sync(0xffffffffu, c.id, L), pos = __shfl_sync(0xffffffffu, c.pos, L);
-      const int before = __shfl_sync(0xffffffffu, last, L);
-      const float share = __shfl_sync(0xffffffffu, q, L);
-      if (id - first == lane) take(L, share, pos, id == before);
-    }
-    if (c.id < end) {
-      last = c.id;
-      c.next(w);
-    }
-  }
+// The wanted entries of 32 tokens (lane: token, cursor c) among the warp's vocabulary entries [first, end): the
+// lanes' columns go through shared memory, where each lane walks its own token's row.
+template <class Visit>
+__device__ __forceinline__ void wanted_of_tokens(const Wanted& w, Cursor& c, int first, int end, float (&v)[32],
+                                                 float* sm, int lane, Visit&& visit) {
+  if (!__any_sync(0xffffffffu, c.id < end)) return;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) cell(sm, k, lane) = v[k];
+  __syncwarp();
+  walk(w, c, first, end, sm, lane, visit);
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 32; ++k) v[k] = cell(sm, k, lane);
+  __syncwarp();  // before the next block's values
 }
 
 // One warp's part of a thin logits tile: 32 entries from `first` (those before `end` are this tile's), the
 // blocks of 32 tokens that are its half's.
 template <class Wait, class Free>
-__device__ __forceinline__ bool drain_thin_logits(const Params& P, int first, int end, int group,
-                                                  int half, uint32_t tbase, int lane, Wait&& wait, Free&& free) {
+__device__ __forceinline__ bool drain_thin_logits(const Params& P, int first, int end, int group, int half,
+                                                  uint32_t tbase, int lane, float* sm, Wait&& wait, Free&& free) {
   const LogitParams& p = P.l;
   const int blocks = P.thin_n / 32;
   Cursor c[2];
@@ -478,16 +482,10 @@ __device__ __forceinline__ bool drain_thin_logits(const Params& P, int first, in
     if (b + 2 >= blocks) free();
 #pragma unroll
     for (int k = 0; k < 32; ++k) v[k] = v0 < end ? v[k] * p.in.scale : -INFINITY;
-    each_wanted(p.want, c[i], first, end, lane, [&](int k, float share, int pos, bool again) {
+    wanted_of_tokens(p.want, c[i], first, end, v, sm, lane, [&](float& x, float share, int pos, bool again) {
       if (again) return;
-      float z = 0.f;
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j == k) {
-          z = v[j];
-          v[j] = -INFINITY;
-        }
-      if (!(share >= kSure)) p.picked[int64_t(b * 32 + k) * p.want.top + pos] = z;
+      if (!(share >= kSure)) p.picked[int64_t(b * 32 + lane) * p.want.top + pos] = x;
+      x = -INFINITY;
     });
     const float peak = columns(v, lane, [](float x, float y) { return fmaxf(x, y); });
     const float from = peak == -INFINITY ? 0.f : peak;
@@ -503,7 +501,7 @@ __device__ __forceinline__ bool drain_thin_logits(const Params& P, int first, in
 // One warp's part of a thin dz tile; dz[t][v - v0] as in the other form.
 template <class Wait, class Free>
 __device__ __forceinline__ bool drain_thin_dz(const Params& P, const ThinTokens& tk, int first, int end, int half,
-                                              uint32_t tbase, int lane, Wait&& wait, Free&& free) {
+                                              uint32_t tbase, int lane, float* sm, Wait&& wait, Free&& free) {
   const LogitParams& p = P.l;
   const int blocks = P.thin_n / 32;
   Cursor c[2];
@@ -532,16 +530,12 @@ __device__ __forceinline__ bool drain_thin_dz(const Params& P, const ThinTokens&
       const float e = g * kLow * exp_high(fmaf(v[k], p.in.scale, -tk.lse[b * 32 + k]));
       v[k] = g == 0.f ? 0.f : e;
     }
-    each_wanted(p.want, c[i], first, end, lane, [&](int k, float share, int pos, bool again) {
-      const int t = b * 32 + k;
+    wanted_of_tokens(p.want, c[i], first, end, v, sm, lane, [&](float& x, float share, int pos, bool again) {
+      const int t = b * 32 + lane;
       const float g = tk.g[t];
       const bool sure = share >= kSure && !again;
-      // another lane of this warp wrote the logit, before the wait
-      const float z = sure ? __ldcg(&p.picked[int64_t(t) * p.want.top + pos]) : 0.f;
-      const float e = sure ? expf(z - tk.lse[t]) : 0.f;
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j == k) v[j] = sure ? g * (e - share) : v[j] - g * share;
+      const float e = sure ? expf(p.picked[int64_t(t) * p.want.top + pos] - tk.lse[t]) : 0.f;
+      x = sure ? g * (e - share) : x - g * share;
     });
     if (v0 < end) {
       bf16* row = p.dz + (v0 - p.v0);
@@ -684,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
   constexpr int box_bytes = MODE == kThinGrads ? kWideBox : kBox;
   Shared* sh = reinterpret_cast<Shared*>(base + ring_bytes);
   uint8_t* boxes = base + ring_bytes + 1024;
-  ThinTokens& tk = *reinterpret_cast<ThinTokens*>(boxes);  // thin launches stage no boxes
+  ThinTokens& tk = *reinterpret_cast<ThinTokens*>(boxes + kEpiWarps * 2 * kBox);  // thin dz only
   // operand ring: fixed at compile time but for the thin logits and dz, whose stages hold fewer rows
   const uint32_t stages = thin ? p.stages : ring_bytes / (2 * kHalf);
   const uint32_t stage_bytes = thin ? p.stage_bytes : 2 * kHalf;
@@ -871,6 +865,8 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lead_tempty = ptx::mapa_shared(ptx::smem_u32(&sh->tempty[0]), 0);
     uint8_t* stg = boxes + (warp - 2) * (2 * box_bytes);
+    float* sm = reinterpret_cast<float*>(stg);  // logits and thin dz: 32 x 32 values in the place of boxes
+    static_assert(2 * kBox == 32 * 32 * 4, "a warp's two boxes");
     float gmax = 1.f;
     if (MODE == kDz || MODE == kThinDz) {  // under the first tile's products
       float m = 0.f;
@@ -922,14 +918,15 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
         const int last = min(min(base_v + p.thin_h / 2, p.l.v0 + p.l.width), base_v + q * 32 + 32);
         const uint32_t rows = tmem + acc * kTile + (static_cast<uint32_t>(q * 32) << 16);
         if (MODE == kThinLogits)
-          ok = drain_thin_logits(p, base_v + q * 32, last, (x.col * 2 + rank) * 4 + q, half, rows, lane, wait, free);
+          ok = drain_thin_logits(p, base_v + q * 32, last, (x.col * 2 + rank) * 4 + q, half, rows, lane, sm, wait,
+                                 free);
         else
-          ok = drain_thin_dz(p, tk, base_v + q * 32, last, half, rows, lane, wait, free);
+          ok = drain_thin_dz(p, tk, base_v + q * 32, last, half, rows, lane, sm, wait, free);
       } else if (MODE == kThinGrads && x.kind == 0) {
         const uint32_t rows = tmem + acc * kTile + (static_cast<uint32_t>(q * 32) << 16);
         ok = drain_thin_dh(p, x, x.col * kTile + rank * 128 + q * 32, half, rows, lane, wait, free);
       } else if (MODE == kLogits) {
-        ok = drain_logits(p.l, r0 + lane, c0, tbase, wait, free);
+        ok = drain_logits(p.l, r0 + lane, c0, tbase, lane, sm, wait, free);
       } else if (MODE == kDz) {
         ok = drain_dz(p, gmax, r0 + lane, r0, p.l.v0 + c0, tbase, lane, stg, nbox, wait, free);
       } else if (MODE == kThinGrads) {
@@ -1011,7 +1008,8 @@ template <int MODE>
 cudaError_t launch_pairs(const Params& p, int pairs, cudaStream_t s) {
   // (gradients of few tokens: one stage less and boxes twice as large, the same total)
   static_assert(2 * kHalf == kEpiWarps * 2 * (kWideBox - kBox), "both layouts fill the same shared memory");
-  const size_t smem = 1024 + kRingBytes + 1024 + kEpiWarps * 2 * kBox;
+  const size_t smem =
+      1024 + kRingBytes + 1024 + kEpiWarps * 2 * kBox + (MODE == kThinDz ? sizeof(ThinTokens) : 0);
   cudaError_t e = cudaFuncSetAttribute(head_pair_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;

@@ -163,6 +163,23 @@ def test_distill_order_does_not_matter_and_equal_ids_add_up():
     check_distill(h, w, ids, lg, 2.0, g, head)
 
 
+@pytest.mark.parametrize("tokens", [33, 200])
+@pytest.mark.parametrize("places", ["first", "last", "ends"])
+def test_lists_that_lie_together(tokens, places):
+    # every entry of every list in the same 32 of the vocabulary, or at the ends of neighbouring 32s
+    vocab, dim, top = 1000, 72, 30
+    h, w, _, g = inputs(tokens, vocab, dim, 11, sure=False)
+    ids, lg = teacher(tokens, vocab, top, 12)
+    near = {"first": torch.arange(32), "last": torch.arange(968, 1000),
+            "ends": torch.cat([torch.arange(31, 993, 32), torch.arange(32, 993, 32)])}[places].to(ids.dtype).cuda()
+    order = torch.Generator(device="cuda")
+    order.manual_seed(13)
+    for t in range(tokens):
+        ids[t] = near[torch.randperm(near.numel(), generator=order, device="cuda")[:top]]
+    ids[3] = near[0]  # one id for the whole list
+    check_distill(h, w, ids, lg, 2.0, g, dm.Head.create(tokens, vocab, dim, max_top=top))
+
+
 def test_pieces_of_the_vocabulary():
     # room for 2^20 tokens leaves pieces of 256 entries: 1000 entries make 4 of them, the last ragged
     h, w, y, g = inputs(200, 1000, 64, 5)
