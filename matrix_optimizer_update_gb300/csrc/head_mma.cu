@@ -252,11 +252,6 @@ struct Cursor {
     pos = lo;
     if (pos < n) id = ids[pos];
   }
-  __device__ __forceinline__ float share(const Wanted& w) const { return w.targets != nullptr ? 1.f : q[pos]; }
-  __device__ __forceinline__ void next(const Wanted& w) {
-    ++pos;
-    id = w.targets == nullptr && pos < n ? ids[pos] : INT_MAX;
-  }
 };
 
 // Whether a token has a loss at all.
@@ -289,24 +284,45 @@ __device__ __forceinline__ float& cell(float* sm, int row, int col) { return sm[
 // frequent words lie together in many vocabularies. (With the values left in registers, where an entry takes a
 // compare for each of 32, and one after another over a warp's tokens, 48 lists of 68 entries against 9328 x 1616
 // made a call of 304 us; this way 87.)
-template <class Visit>
-__device__ __forceinline__ void walk(const Wanted& w, Cursor& c, int first, int end, float* sm, int lane,
-                                     Visit&& visit) {
+//
+// Four entries are loaded together: a load of one each is a chain of trips to the L2, for the shared memory that
+// the tiles take leaves an L1 too small for the warps' lists (242 lists of 39 against 9800 x 1056: 82 -> 67 us).
+template <bool WITH_LOGIT, class Visit>
+__device__ __forceinline__ void walk(const LogitParams& p, int64_t t, Cursor& c, int first, int end, float* sm,
+                                     int lane, Visit&& visit) {
+  const Wanted& w = p.want;
   int last = -1;
   while (c.id < end) {
-    visit(cell(sm, lane, c.id - first), c.share(w), c.pos, c.id == last);
-    last = c.id;
-    c.next(w);
+    int id[5];
+    float q[4], z[4];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) {
+      const bool in = c.pos + j < c.n;
+      id[j] = in ? c.ids[c.pos + j] : INT_MAX;
+      if (j < 4) q[j] = in ? c.q[c.pos + j] : 1.f;  // a target's share
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      z[j] = WITH_LOGIT && (j == 0 || c.pos + j < c.n) && q[j] >= kSure ? p.picked[t * w.top + c.pos + j] : 0.f;
+    const int pos = c.pos;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c.id < end) {
+        visit(cell(sm, lane, c.id - first), q[j], z[j], pos + j, c.id == last);
+        last = c.id;
+        c.id = id[j + 1];
+        ++c.pos;
+      }
   }
 }
 
 // The wanted entries of this lane's token among its 32 values v (entries from `first`).
-template <class Visit>
-__device__ __forceinline__ void wanted_of_row(const Wanted& w, Cursor& c, int first, float (&v)[32], float* sm,
-                                              int lane, Visit&& visit) {
+template <bool WITH_LOGIT, class Visit>
+__device__ __forceinline__ void wanted_of_row(const LogitParams& p, int64_t t, Cursor& c, int first, float (&v)[32],
+                                              float* sm, int lane, Visit&& visit) {
 #pragma unroll
   for (int k = 0; k < 32; ++k) cell(sm, lane, k) = v[k];
-  walk(w, c, first, first + 32, sm, lane, visit);
+  walk<WITH_LOGIT>(p, t, c, first, first + 32, sm, lane, visit);
 #pragma unroll
   for (int k = 0; k < 32; ++k) v[k] = cell(sm, lane, k);
 }
@@ -336,7 +352,7 @@ __device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, in
         if (jc + k >= p.vocab) v[k] = -INFINITY;
     }
     if (__any_sync(0xffffffffu, c.id < jc + 32))
-      wanted_of_row(p.want, c, jc, v, sm, lane, [&](float& x, float share, int pos, bool again) {
+      wanted_of_row<false>(p, t, c, jc, v, sm, lane, [&](float& x, float share, float, int pos, bool again) {
         if (again) return;  // entries that share an id have one logit, with the first of them
         if (!(share >= kSure)) p.picked[t * p.want.top + pos] = x;
         x = -INFINITY;
@@ -395,12 +411,10 @@ __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t,
     if (__any_sync(0xffffffffu, c.id < jc + 32)) {
       if (lane == 0) ptx::bulk_wait_read<0>();  // both boxes' place
       __syncwarp();
-      wanted_of_row(p.want, c, jc, v, reinterpret_cast<float*>(stg), lane,
-                    [&](float& x, float share, int pos, bool again) {
-                      const bool sure = share >= kSure && !again;
-                      const float e = sure ? expf(p.picked[t * p.want.top + pos] - lse) : 0.f;
-                      x = sure ? g * (e - share) : x - g * share;
-                    });
+      wanted_of_row<true>(p, t, c, jc, v, reinterpret_cast<float*>(stg), lane,
+                          [&](float& x, float share, float z, int, bool again) {
+                            x = share >= kSure && !again ? g * (expf(z - lse) - share) : x - g * share;
+                          });
     }
     uint8_t* box = stg + (nbox & 1u) * kBox;
     if (lane == 0) ptx::bulk_wait_read<1>();  // the store that last read this box is done with it
@@ -440,14 +454,14 @@ __device__ __forceinline__ float columns(const float (&v)[32], int lane, Op op) 
 
 // The wanted entries of 32 tokens (lane: token, cursor c) among the warp's vocabulary entries [first, end): the
 // lanes' columns go through shared memory, where each lane walks its own token's row.
-template <class Visit>
-__device__ __forceinline__ void wanted_of_tokens(const Wanted& w, Cursor& c, int first, int end, float (&v)[32],
-                                                 float* sm, int lane, Visit&& visit) {
+template <bool WITH_LOGIT, class Visit>
+__device__ __forceinline__ void wanted_of_tokens(const LogitParams& p, int64_t t, Cursor& c, int first, int end,
+                                                 float (&v)[32], float* sm, int lane, Visit&& visit) {
   if (!__any_sync(0xffffffffu, c.id < end)) return;
 #pragma unroll
   for (int k = 0; k < 32; ++k) cell(sm, k, lane) = v[k];
   __syncwarp();
-  walk(w, c, first, end, sm, lane, visit);
+  walk<WITH_LOGIT>(p, t, c, first, end, sm, lane, visit);
   __syncwarp();
 #pragma unroll
   for (int k = 0; k < 32; ++k) v[k] = cell(sm, k, lane);
@@ -482,18 +496,19 @@ __device__ __forceinline__ bool drain_thin_logits(const Params& P, int first, in
     if (b + 2 >= blocks) free();
 #pragma unroll
     for (int k = 0; k < 32; ++k) v[k] = v0 < end ? v[k] * p.in.scale : -INFINITY;
-    wanted_of_tokens(p.want, c[i], first, end, v, sm, lane, [&](float& x, float share, int pos, bool again) {
-      if (again) return;
-      if (!(share >= kSure)) p.picked[int64_t(b * 32 + lane) * p.want.top + pos] = x;
-      x = -INFINITY;
-    });
+    const int64_t t = b * 32 + lane;
+    wanted_of_tokens<false>(p, t, c[i], first, end, v, sm, lane,
+                            [&](float& x, float share, float, int pos, bool again) {
+                              if (again) return;
+                              if (!(share >= kSure)) p.picked[t * p.want.top + pos] = x;
+                              x = -INFINITY;
+                            });
     const float peak = columns(v, lane, [](float x, float y) { return fmaxf(x, y); });
     const float from = peak == -INFINITY ? 0.f : peak;
 #pragma unroll
     for (int k = 0; k < 32; ++k) v[k] = ex2((v[k] - __shfl_sync(0xffffffffu, from, k)) * kLog2e);
     const float sum = columns(v, lane, [](float x, float y) { return x + y; });
-    const int t = b * 32 + lane;
-    if (t < p.tokens) p.parts[int64_t(t) * (P.items * 8) + group] = Part{peak, sum};
+    if (t < p.tokens) p.parts[t * (P.items * 8) + group] = Part{peak, sum};
   }
   return true;
 }
@@ -530,13 +545,12 @@ __device__ __forceinline__ bool drain_thin_dz(const Params& P, const ThinTokens&
       const float e = g * kLow * exp_high(fmaf(v[k], p.in.scale, -tk.lse[b * 32 + k]));
       v[k] = g == 0.f ? 0.f : e;
     }
-    wanted_of_tokens(p.want, c[i], first, end, v, sm, lane, [&](float& x, float share, int pos, bool again) {
-      const int t = b * 32 + lane;
-      const float g = tk.g[t];
-      const bool sure = share >= kSure && !again;
-      const float e = sure ? expf(p.picked[int64_t(t) * p.want.top + pos] - tk.lse[t]) : 0.f;
-      x = sure ? g * (e - share) : x - g * share;
-    });
+    const int t = b * 32 + lane;
+    wanted_of_tokens<true>(p, t, c[i], first, end, v, sm, lane,
+                           [&](float& x, float share, float z, int, bool again) {
+                             const float g = tk.g[t];
+                             x = share >= kSure && !again ? g * (expf(z - tk.lse[t]) - share) : x - g * share;
+                           });
     if (v0 < end) {
       bf16* row = p.dz + (v0 - p.v0);
 #pragma unroll
