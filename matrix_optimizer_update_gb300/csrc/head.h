@@ -40,11 +40,16 @@ struct DotParams {
 };
 
 // Tensor cores truncate what they accumulate: a logit z of theirs is off by about 1.0e-9 * dim * z, always
-// towards zero (measured: -6.6e-5 at z = 16, dim = 4096, where fp32 FMAs are off by 8e-7). Sums over the
-// vocabulary average that out, but the loss of a token predicted with near certainty is 1 - p of its
-// target, and its relative error the absolute one of the target's logit. So the logits of wanted entries
-// with at least this probability (at most 8 per token, for cross entropy the target) are formed apart,
-// in fp32 FMAs, in both passes.
+// towards zero (measured: -6.6e-5 at z = 16, dim = 4096, where fp32 FMAs are off by 8e-7; the factor is 0.85e-9
+// to 1.15e-9 for normal, spiked and planted states and dims of 1024 to 8192, 0.5e-9 to 1.1e-9 at 256, and more
+// only where a common part of all logits far above 30 outweighs the rest). Their scale puts the mean of it back:
+// lse is off by 4e-8 in place of 4.1e-7 (3912 dims, normal states), 3.7e-7 in place of 3.8e-6 (one logit of 12).
+constexpr double kTruncated = 1.0e-9;
+
+// What remains is a few percent of it, in a loss still too much: that of a token predicted with near certainty is
+// 1 - p of its target, and its relative error the absolute one of the target's logit. So the logits of wanted
+// entries with at least this probability (at most 8 per token, for cross entropy the target) are formed apart, in
+// fp32 FMAs, in both passes.
 constexpr float kSure = 0.125f;
 
 // One group's share of a token's softmax sum: sum of exp(z - peak), over the entries that are not wanted.

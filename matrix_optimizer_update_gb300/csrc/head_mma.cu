@@ -78,6 +78,7 @@ struct Params {
   float* dh_acc;           // thin: the fp32 sums, pitch acc_ld
   int64_t acc_ld;
   float gscale;            // factor of the gradients beside *gmax
+  float zscale;            // of the logits: 1 / temperature and what truncation takes
   float* gmax;             // largest |grad|: dz holds gradients relative to it
   LogitParams l;
   unsigned* sched;         // [0] tiles claimed, [1] CTAs done; both zero between launches
@@ -329,8 +330,8 @@ __device__ __forceinline__ void wanted_of_row(const LogitParams& p, int64_t t, C
 
 // One warp's part of a logits tile: 32 tokens, 128 entries from j0. `wait` returns false when the CTA gave up.
 template <class Wait, class Free>
-__device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, int j0, uint32_t tbase, int lane,
-                                             float* sm, Wait&& wait, Free&& free) {
+__device__ __forceinline__ bool drain_logits(const LogitParams& p, float zscale, int64_t t, int j0, uint32_t tbase,
+                                             int lane, float* sm, Wait&& wait, Free&& free) {
   const bool in = t < p.tokens;
   Cursor c;
   c.start(p.want, t, in, j0);
@@ -345,7 +346,7 @@ __device__ __forceinline__ bool drain_logits(const LogitParams& p, int64_t t, in
     if (ch == 3) free();
     if (jc >= p.vocab) continue;
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] *= p.in.scale;
+    for (int k = 0; k < 32; ++k) v[k] *= zscale;
     if (jc + 32 > p.vocab) {
 #pragma unroll
       for (int k = 0; k < 32; ++k)
@@ -400,7 +401,7 @@ __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t,
     // a row that does not count, and entries past the vocabulary, give exact zeros whatever z is
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
-      const float e = g_low * exp_high(fmaf(v[k], p.in.scale, -lse));
+      const float e = g_low * exp_high(fmaf(v[k], P.zscale, -lse));
       v[k] = g == 0.f ? 0.f : e;
     }
     if (jc + 32 > p.vocab) {
@@ -495,7 +496,7 @@ __device__ __forceinline__ bool drain_thin_logits(const Params& P, int first, in
     ptx::tmem_ld_32x32b_x32(tbase + b * 32, v);
     if (b + 2 >= blocks) free();
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] = v0 < end ? v[k] * p.in.scale : -INFINITY;
+    for (int k = 0; k < 32; ++k) v[k] = v0 < end ? v[k] * P.zscale : -INFINITY;
     const int64_t t = b * 32 + lane;
     wanted_of_tokens<false>(p, t, c[i], first, end, v, sm, lane,
                             [&](float& x, float share, float, int pos, bool again) {
@@ -542,7 +543,7 @@ __device__ __forceinline__ bool drain_thin_dz(const Params& P, const ThinTokens&
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
       const float g = tk.g[b * 32 + k];
-      const float e = g * kLow * exp_high(fmaf(v[k], p.in.scale, -tk.lse[b * 32 + k]));
+      const float e = g * kLow * exp_high(fmaf(v[k], P.zscale, -tk.lse[b * 32 + k]));
       v[k] = g == 0.f ? 0.f : e;
     }
     const int t = b * 32 + lane;
@@ -940,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
         const uint32_t rows = tmem + acc * kTile + (static_cast<uint32_t>(q * 32) << 16);
         ok = drain_thin_dh(p, x, x.col * kTile + rank * 128 + q * 32, half, rows, lane, wait, free);
       } else if (MODE == kLogits) {
-        ok = drain_logits(p.l, r0 + lane, c0, tbase, lane, sm, wait, free);
+        ok = drain_logits(p.l, p.zscale, r0 + lane, c0, tbase, lane, sm, wait, free);
       } else if (MODE == kDz) {
         ok = drain_dz(p, gmax, r0 + lane, r0, p.l.v0 + c0, tbase, lane, stg, nbox, wait, free);
       } else if (MODE == kThinGrads) {
@@ -1034,6 +1035,7 @@ cudaError_t launch_pairs(const Params& p, int pairs, cudaStream_t s) {
 cudaError_t logit_launch(Params& P, const LogitParams& p, const Pipe& pipe) {
   std::memset(&P, 0, sizeof(P));
   P.l = p;
+  P.zscale = static_cast<float>(p.in.scale * (1.0 + kTruncated * p.in.dim));
   P.nk = cdiv(p.in.dim, kStep);
   P.sched = pipe.sched;
   P.status = pipe.status;
