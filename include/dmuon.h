@@ -509,9 +509,10 @@ dmuon_status dmuon_head_xent(dmuon_head_t head, const void* hidden, int64_t ld_h
  *  dweight    device, vocab x dim bf16, pitch ld_dweight, or NULL: not wanted
  *             (a frozen head). Overwritten, also when tokens is 0.
  *
- * z is formed again, piece by piece, and dz is rounded to bf16 once, as the
- * operand of two tensor-core products that accumulate in fp32 over the whole
- * vocabulary (dH) and all tokens (dW).
+ * z is formed again, piece by piece, and dz is rounded to bf16 once (of up to
+ * 64 tokens: to the sum of two bf16), as the operand of two tensor-core
+ * products that accumulate in fp32 over the whole vocabulary (dH) and all
+ * tokens (dW).
  */
 dmuon_status dmuon_head_xent_backward(dmuon_head_t head, const void* hidden, int64_t ld_hidden, const void* weight,
                                       int64_t ld_weight, const int64_t* targets, int64_t tokens, const float* lse,

@@ -290,7 +290,7 @@ extern "C" dmuon_status dmuon_head_create(int64_t max_tokens, int64_t vocab, int
   H->off_q = take(4 * max_tokens * max_top);
   H->off_count = take(max_top > 0 ? 4 * max_tokens : 0);
   H->off_entropy = take(max_top > 0 ? 4 * max_tokens : 0);
-  H->off_dz = take(2 * max_tokens * H->piece);
+  H->off_dz = take(2 * std::max(max_tokens, std::min<int64_t>(2 * max_tokens, 2 * head::kTwofold)) * H->piece);
   // dH's sums: one set where tokens are many; where K is cut into slices, up to 2 tiles of 256 x 256 per pair
   const int64_t row = 4 * head::acc_pitch(dim);
   H->off_acc = take(std::max(row * max_tokens, std::min(row * max_tokens * kMaxSlices, kSliceBytes)));

@@ -71,6 +71,8 @@ struct Params {
   int32_t dim_tiles;
   int32_t thin_n;          // tokens padded to 32 when they are the N side, else 0
   int32_t thin_h;          // thin logits, dz: vocabulary entries per tile
+  int32_t low;             // thin dz, grads: rows from dz's first parts to the second, 0: there are none
+  int32_t dw_rows;         // grads: tokens per stage of dW
   int32_t stages, stage_bytes, a_bytes;  // thin logits, dz: a stage holds a_bytes of A, then B
   int32_t chunked;         // dim is a multiple of 64: one copy brings two 64-column blocks
   int32_t dh_direct;       // dH is complete: store bf16; else add into fp32 sums
@@ -529,7 +531,6 @@ __device__ __forceinline__ bool drain_thin_dz(const Params& P, const ThinTokens&
   }
   if (!wait()) return false;
   ptx::tc_fence_after();
-  const int v0 = first + lane;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int b = half + 2 * i;
@@ -552,11 +553,32 @@ __device__ __forceinline__ bool drain_thin_dz(const Params& P, const ThinTokens&
                              const float g = tk.g[t];
                              x = share >= kSure && !again ? g * (expf(z - tk.lse[t]) - share) : x - g * share;
                            });
-    if (v0 < end) {
-      bf16* row = p.dz + (v0 - p.v0);
+    // By way of shared memory, so that a lane stores 16 bytes: with 2 bytes a lane the number of stores shows in the
+    // launch's time (both passes over 77 tokens x 50257 x 1024: 103 us, this way 99.7; with the tokens that there are not left
+    // out, 103 again). `first` and the tiles' ends
+    // are multiples of 8 from the piece's start; past its last entry lies room of dz that nothing reads.
+    bf16* at = reinterpret_cast<bf16*>(sm);
+    const int row = lane >> 2, col = (lane & 3) * 8;
+    auto store = [&](bf16* out) {
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = row + 8 * j;
+        if (b * 32 + k < p.tokens && first + col < end)
+          *reinterpret_cast<uint4*>(out + (b * 32 + k) * p.ld_dz + col) =
+              *reinterpret_cast<const uint4*>(at + k * 32 + col);
+      }
+      __syncwarp();
+    };
+    bf16* out = p.dz + (first - p.v0);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) at[k * 32 + lane] = __float2bfloat16_rn(v[k]);
+    store(out);
+    if (P.low != 0) {
 #pragma unroll
       for (int k = 0; k < 32; ++k)
-        if (b * 32 + k < p.tokens) row[(b * 32 + k) * p.ld_dz] = __float2bfloat16_rn(v[k]);
+        at[k * 32 + lane] = __float2bfloat16_rn(v[k] - __bfloat162float(__float2bfloat16_rn(v[k])));
+      store(out + P.low * p.ld_dz);
     }
   }
   return true;
@@ -574,6 +596,12 @@ __device__ __forceinline__ bool drain_thin_dh(const Params& P, const Where& x, i
   for (int b = half; b < P.thin_n / 32; b += 2) {
     float v[32];
     ptx::tmem_ld_32x32b_x32(tbase + b * 32, v);
+    if (P.low != 0) {  // the second parts' columns
+      float u[32];
+      ptx::tmem_ld_32x32b_x32(tbase + P.thin_n + b * 32, u);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] += u[k];
+    }
     if (b + 2 >= P.thin_n / 32) free();
     if (d < P.l.in.dim) {
 #pragma unroll
@@ -753,7 +781,13 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
         const Where x = where_is<MODE>(p, w);
         const bool turned = MODE == kThinGrads && x.kind == 0;  // dH^T = W^T dz^T
         const int row = x.row * kTile + rank * 128, col = x.col * kTile + rank * 128;
-        const uint32_t bytes = thin ? stage_bytes : turned ? kHalf + p.thin_n * 64 : 2 * kHalf;
+        // dH^T's N side: half of the tokens each, or rank 0 their dz's first parts and rank 1 the second
+        const bool twofold = MODE == kThinGrads && p.low != 0;
+        const uint32_t dw_block = MODE == kThinGrads ? p.dw_rows * 128 : kHalf / 2;  // 64 columns of a stage of dW
+        const uint32_t bytes = thin       ? stage_bytes
+                               : turned   ? kHalf + p.thin_n * (twofold ? 128 : 64)
+                               : x.kind == 1 ? 4 * dw_block
+                                             : 2 * kHalf;
         for (int kb = 0; kb < x.nk; ++kb) {
           if (!ptx::mbar_wait_cluster(&sh->empty[stage], phase ^ 1u, abortf, p.status, kWaitNs)) return false;
           if (leader) ptx::mbar_arrive_expect_tx(&sh->full[stage], 2 * bytes);
@@ -770,15 +804,18 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
           } else {
             uint8_t* wide = turned ? a : b;                                     // W or H, MN-major
             const CUtensorMap* mw = &p.b[x.kind];
-            const int kr = k + (x.kind == 0 ? p.l.v0 : 0);
-            if (turned) tma_load_2d_pair(b, &p.a[0], fb, k, rank * (p.thin_n / 2));  // dz, K-major
-            else if (x.kind == 0) tma_load_2d_pair(a, &p.a[0], fb, k, row);          // dz, K-major
-            else ptx::tma_load_3d_pair(a, &p.a[1], fb, 0, k, row / 64);              // dz, two blocks of 64 columns
+            // dW of twofold dz: K is the tokens twice, one stage each. (What the first stage's box has of the second
+            // parts meets rows of zeros: those of H past its last token.)
+            const int kr = x.kind == 0 ? k + p.l.v0 : twofold ? 0 : k;
+            const int kz = twofold ? kb * p.low : k;
+            if (turned) tma_load_2d_pair(b, &p.a[0], fb, k, rank * (twofold ? p.low : p.thin_n / 2));  // dz, K-major
+            else if (x.kind == 0) tma_load_2d_pair(a, &p.a[0], fb, k, row);  // dz, K-major
+            else ptx::tma_load_3d_pair(a, &p.a[1], fb, 0, kz, row / 64);     // dz, two blocks of 64 columns
             if (p.chunked) {
               ptx::tma_load_3d_pair(wide, mw, fb, 0, kr, col / 64);
             } else {
               tma_load_2d_pair(wide, mw, fb, col, kr);
-              tma_load_2d_pair(wide + kHalf / 2, mw, fb, col + 64, kr);
+              tma_load_2d_pair(wide + (x.kind == 1 ? dw_block : kHalf / 2), mw, fb, col + 64, kr);
             }
           }
           ++fills;
@@ -838,19 +875,21 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
         const bool turned = MODE == kThinGrads && x.kind == 0;
         const bool a_mn = MODE == kThinGrads || (MODE == kGrads && x.kind == 1);
         const bool b_mn = grads && !turned;
-        const uint32_t id = idesc(thin || turned ? p.thin_n : kTile, a_mn, b_mn);
+        const uint32_t id = idesc(thin ? p.thin_n : turned ? p.thin_n * (p.low != 0 ? 2 : 1) : kTile, a_mn, b_mn);
         const uint32_t acc = local & 1u;
         if (!ptx::mbar_wait_cluster(&sh->tempty[acc], ((local >> 1) & 1u) ^ 1u, abortf, p.status, kWaitNs)) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem + acc * kTile;
         // Descriptors of stage 0; a stage or 16 columns of K further is an addition to the address field (in 16
         // bytes). K-major: 16 columns further in the swizzled rows; MN-major: 16 rows of 128 bytes further, the
-        // operand's second 64-element block kHalf / 2 on. One thread issues everything, so what it computes per
+        // operand's second 64-element block `block` on. One thread issues everything, so what it computes per
         // MMA counts: built anew each time, the four descriptors of a stage took 285 of its 512 cycles.
+        const bool few = MODE == kThinGrads && x.kind == 1;  // a stage may have fewer than 64 of K
+        const uint32_t block = few ? p.dw_rows * 128 : kHalf / 2, steps = few ? p.dw_rows / 16 : kStep / 16;
         const uint32_t s0 = ptx::smem_u32(base);
-        const uint64_t a_desc = a_mn ? ptx::sw128_desc(s0, kHalf / 2, 1024) : ptx::sw128_desc(s0, 16, 1024);
+        const uint64_t a_desc = a_mn ? ptx::sw128_desc(s0, block, 1024) : ptx::sw128_desc(s0, 16, 1024);
         const uint64_t b_desc =
-            b_mn ? ptx::sw128_desc(s0 + a_bytes, kHalf / 2, 1024) : ptx::sw128_desc(s0 + a_bytes, 16, 1024);
+            b_mn ? ptx::sw128_desc(s0 + a_bytes, block, 1024) : ptx::sw128_desc(s0 + a_bytes, 16, 1024);
         const uint32_t a_step = a_mn ? 2048 / 16 : 32 / 16, b_step = b_mn ? 2048 / 16 : 32 / 16;
         for (int kb = 0; kb < x.nk; ++kb) {
           if (!ptx::mbar_wait_cluster(&sh->full[stage], phase, abortf, p.status, kWaitNs)) {
@@ -861,7 +900,8 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
           const uint64_t a0 = a_desc + stage * (stage_bytes / 16), b0 = b_desc + stage * (stage_bytes / 16);
 #pragma unroll
           for (uint32_t kk = 0; kk < kStep / 16; ++kk)
-            ptx::umma_f16_pair(d, a0 + kk * a_step, b0 + kk * b_step, id, (kb | kk) != 0 ? 1u : 0u);
+            if (kk < steps)
+              ptx::umma_f16_pair(d, a0 + kk * a_step, b0 + kk * b_step, id, (kb | kk) != 0 ? 1u : 0u);
           ptx::umma_commit_pair(&sh->empty[stage], 0x3);
           if (++stage == stages) {
             stage = 0;
@@ -1004,20 +1044,25 @@ cudaError_t map_rows(CUtensorMap* m, const void* base, int64_t cols, int64_t row
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 2, dims, strides, box, swz);
 }
 
-// The same matrix as [block of 64 columns][row][64 columns], so that one box brings 64 rows of two blocks,
+// The same matrix as [block of 64 columns][row][64 columns], so that one box brings box_rows rows of two blocks,
 // each a block of 128-byte rows as the MN-major operand wants them. cols must be a multiple of 64.
-cudaError_t map_blocks(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld) {
+cudaError_t map_blocks(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
   const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)cols / 64};
   const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, 128};
-  const cuuint32_t box[3] = {64, 64, 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 2};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-cudaError_t map_operand_mn(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld) {
-  return cols % 64 == 0 ? map_blocks(m, base, cols, rows, ld) : map_rows(m, base, cols, rows, ld, 64, 64);
+cudaError_t map_operand_mn(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld,
+                           int box_rows = kStep) {
+  return cols % 64 == 0 ? map_blocks(m, base, cols, rows, ld, box_rows)
+                        : map_rows(m, base, cols, rows, ld, 64, box_rows);
 }
 
 int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+static_assert(kTwofold <= kStep && kTwofold <= kThin && 2 * kTwofold <= kTile, "a stage of dW, the N side of dH^T");
+int32_t low_rows(int64_t tokens) { return tokens <= kTwofold ? static_cast<int32_t>(tokens) : 0; }
 
 template <int MODE>
 cudaError_t launch_pairs(const Params& p, int pairs, cudaStream_t s) {
@@ -1045,6 +1090,7 @@ cudaError_t logit_launch(Params& P, const LogitParams& p, const Pipe& pipe) {
     const Thin x = thin_tiles(p.width, pipe.pairs);
     P.thin_n = cdiv(p.tokens, 32) * 32;
     P.thin_h = x.height;
+    P.low = low_rows(p.tokens);
     P.rows = 1;
     P.cols = P.items = x.tiles;
     w_rows = P.thin_h / 2;
@@ -1123,6 +1169,8 @@ cudaError_t launch_grads(const GradParams& p, const Pipe& pipe, cudaStream_t s) 
   P.l.v0 = p.v0;
   P.dim_tiles = cdiv(p.dim, kTile);
   P.thin_n = thin_tokens(p.tokens) ? cdiv(p.tokens, 32) * 32 : 0;
+  P.low = low_rows(p.tokens);
+  const int64_t dz_rows = p.tokens + P.low;
   P.chunked = p.dim % 64 == 0;
   P.gscale = p.gscale;
   P.gmax = pipe.gmax;
@@ -1140,7 +1188,8 @@ cudaError_t launch_grads(const GradParams& p, const Pipe& pipe, cudaStream_t s) 
     P.first = p.first;
     P.dh_acc = p.dh_acc;
     P.acc_ld = acc_ld;
-    e = map_rows(&P.a[0], p.dz, p.width, p.tokens, p.ld_dz, kStep, P.thin_n != 0 ? P.thin_n / 2 : 128);
+    e = map_rows(&P.a[0], p.dz, p.width, dz_rows, p.ld_dz, kStep,
+                 P.low != 0 ? P.thin_n : P.thin_n != 0 ? P.thin_n / 2 : 128);
     if (e == cudaSuccess) e = map_operand_mn(&P.b[0], p.weight, p.dim, p.vocab, p.ld_weight);
     if (e == cudaSuccess && P.dh_direct) {
       e = map_rows(&P.out[0], p.dhidden, p.dim, p.tokens, p.ld_dhidden, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
@@ -1156,9 +1205,11 @@ cudaError_t launch_grads(const GradParams& p, const Pipe& pipe, cudaStream_t s) 
   P.items = P.dh_items;
   if (p.dweight != nullptr) {
     P.items += cdiv(p.width, kTile) * P.dim_tiles;
-    P.nk = cdiv(p.tokens, kStep);
-    e = map_blocks(&P.a[1], p.dz, p.ld_dz, p.tokens, p.ld_dz);
-    if (e == cudaSuccess) e = map_operand_mn(&P.b[1], p.hidden, p.dim, p.tokens, p.ld_hidden);
+    P.nk = P.low != 0 ? 2 : cdiv(p.tokens, kStep);
+    // no more zeros than the MMA's 16 of K asks for: they are written and read all the same
+    P.dw_rows = P.low != 0 ? cdiv(p.tokens, 16) * 16 : kStep;
+    e = map_blocks(&P.a[1], p.dz, p.ld_dz, dz_rows, p.ld_dz, P.dw_rows);
+    if (e == cudaSuccess) e = map_operand_mn(&P.b[1], p.hidden, p.dim, p.tokens, p.ld_hidden, P.dw_rows);
     if (e == cudaSuccess)
       e = P.thin_n != 0 ? map_rows(&P.out[1], p.dweight, p.dim, p.vocab, p.ld_dweight, 64, 32)
                         : map_rows(&P.out[1], p.dweight, p.dim, p.vocab, p.ld_dweight, 32, 32,

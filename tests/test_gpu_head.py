@@ -398,6 +398,29 @@ def test_gradients_of_tokens_that_do_not_count_may_hold_anything(tokens):
     assert all(torch.equal(a, b) for a, b in zip(want, head.distill_backward(h, w, ids, lg, 1.5, lse, g)))
 
 
+@pytest.mark.parametrize("tokens,vocab,dim", [(1, 3000, 264), (16, 3001, 256), (17, 5000, 72), (64, 2000, 200)])
+def test_gradients_of_few_tokens_are_as_exact_as_their_type(tokens, vocab, dim):
+    # The result's rounding is off by ulp / sqrt(12) in the root mean square, ulp = 2^-7 of the power of two below.
+    # What else there is adds squares: dz to 2^-17, logits to 4 sqrt(dim) 2^-24 of 16, some 6e-5 against 1.7e-3.
+    def near(got, want):
+        ulp = 2.0 ** (np.floor(np.log2(np.abs(want) + 2.0 ** -120)) - 7)
+        assert np.linalg.norm(f64(got) - want) <= 1.1 * np.linalg.norm(ulp) / np.sqrt(12)
+
+    h, w, y, g = inputs(tokens, vocab, dim, 21)
+    head = dm.Head.create(tokens, vocab, dim, max_top=12)
+    _, lse = head.xent(h, w, y)
+    dh, dw = head.xent_backward(h, w, y, lse, g)
+    r = ref.xent(f64(h), f64(w), y.cpu().numpy(), f64(g))
+    near(dh, r["dhidden"])
+    near(dw, r["dweight"])
+    ids, lg = teacher(tokens, vocab, 12, 22)
+    _, lse = head.distill(h, w, ids, lg, 2.0)
+    dh, dw = head.distill_backward(h, w, ids, lg, 2.0, lse, g)
+    r = ref.distill(f64(h), f64(w), ids.cpu().numpy(), f64(lg), 2.0, f64(g))
+    near(dh, r["dhidden"])
+    near(dw, r["dweight"])
+
+
 @pytest.mark.parametrize("tokens", [20, 200])
 def test_a_nan_in_a_list_stays_in_its_row(tokens):
     h, w, _, _ = inputs(tokens, 300, 64, 20, sure=False)
