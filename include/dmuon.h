@@ -575,7 +575,8 @@ void dmuon_head_destroy(dmuon_head_t head);
  *   source[r]   the assignment of row r, -1 past the last row in use
  *
  * Asynchronous on stream, no allocation, deterministic (no atomics whose order
- * could show). Outputs must not overlap inputs.
+ * could show). Outputs must not overlap inputs. Pointers and stream are of the
+ * current device; the calls hold no handle to compare it with.
  */
 
 /* Bytes of scratch dmuon_route_sort needs for up to these sizes (host only):

@@ -364,32 +364,53 @@ def _refuse(msg: str):
     raise DmuonError(ERR_INVALID_ARG, msg)
 
 
-def _rows(t, dim, dtype, name, rows=None):
+def _current_device() -> int:
+    return _t()._C._cuda_getDevice()
+
+
+def _at(t, device, name):
+    """Refuse a tensor of another device than the object's (None: not bound, which the library refuses)."""
+    if device is not None and t.get_device() != device:
+        _refuse(f"{name} is on cuda:{t.get_device()}, what takes it on cuda:{device}")
+
+
+def _rows(t, dim, dtype, name, device, rows=None):
     """A CUDA matrix whose rows lie contiguous (any row pitch); returns that pitch."""
     shape = t.shape
     if not (t.is_cuda and t.dtype == dtype and len(shape) == 2 and shape[1] == dim and
             (rows is None or shape[0] == rows) and (dim <= 1 or t.stride(1) == 1)):
         _refuse(f"{name} must be a CUDA {dtype} tensor of shape [{'rows' if rows is None else rows}, {dim}] "
                 "with contiguous rows")
+    _at(t, device, name)
     return t.stride(0) if shape[0] > 1 else -(-dim // 8) * 8
 
 
-def _flat(t, shape, dtype, name):
+def _flat(t, shape, dtype, name, device):
     if not (t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
         _refuse(f"{name} must be a contiguous CUDA {dtype} tensor of shape {list(shape)}")
+    _at(t, device, name)
     return t.data_ptr()
 
 
-def _here(t) -> int:
-    """The raw handle of the current stream of t's device (the object torch.cuda.current_stream() makes costs
-    more than a small call)."""
-    return _t()._C._cuda_getCurrentRawStream(t.get_device())
+def _here(device) -> int:
+    """The raw handle of a device's current stream (the object torch.cuda.current_stream() makes costs more than
+    a small call)."""
+    return _t()._C._cuda_getCurrentRawStream(device)
 
 
-def _on(stream, call, *tensors):
-    """Run ``call(handle)`` on ``stream``: what it allocates belongs to that stream, and what it is given stays
-    alive until the stream is done with it."""
-    if stream.cuda_stream == _here(tensors[0]):
+def _run(owner, call, stream, *tensors):
+    """Run ``call(handle)`` on the device of ``owner`` and on ``stream`` (None: the current one): what it allocates
+    belongs to that stream, and what it is given stays alive until the stream is done with it."""
+    device, current = owner.device, _current_device()
+    if device is None:
+        device = current
+    if stream is None:
+        if current != device:
+            _refuse(f"the operator is on cuda:{device}, the current device is cuda:{current}")
+        return call(_here(device))
+    if stream.device_index != device:
+        _refuse(f"the operator is on cuda:{device}, the stream on cuda:{stream.device_index}")
+    if current == device and stream.cuda_stream == _here(device):
         return call(stream.cuda_stream)
     for t in tensors:
         if t is not None:
@@ -404,14 +425,16 @@ class Head:
     One object per (max_tokens, vocab, dim, max_top), with its workspace from
     torch; one call uses it at a time. ``hidden`` is [tokens, dim] and
     ``weight`` [vocab, dim], both bf16 with rows that start on 16 bytes;
-    losses, log sums and their gradients are fp32 [tokens]. See
-    include/dmuon.h for the formulas.
+    losses, log sums and their gradients are fp32 [tokens]. All of them lie on
+    the device the head is bound on, which is the current one or the stream's.
+    See include/dmuon.h for the formulas.
     """
 
     def __init__(self, handle, max_tokens, vocab, dim, max_top):
         self._h = handle
         self.max_tokens, self.vocab, self.dim, self.max_top = max_tokens, vocab, dim, max_top
         self.workspace = None
+        self.device = None  # index of the device it is bound on
 
     @classmethod
     def create(cls, max_tokens, vocab, dim, *, max_top=0, device=None, stream=None):
@@ -420,8 +443,9 @@ class Head:
         self = cls(h, int(max_tokens), int(vocab), int(dim), int(max_top))
         nbytes = self.workspace_bytes()
         ws = _t().empty(nbytes + 1024, dtype=_t().uint8, device=device or "cuda")
-        s = _here(ws) if stream is None else stream.cuda_stream
-        if s != _here(ws):
+        here = _here(ws.get_device())
+        s = here if stream is None else stream.cuda_stream
+        if s != here:
             ws.record_stream(stream)
         self.bind((ws.data_ptr() + 1023) // 1024 * 1024, nbytes, s)
         self.workspace = ws
@@ -434,17 +458,18 @@ class Head:
 
     def bind(self, d_workspace: int, nbytes: int, stream: int = 0):
         _check(lib().dmuon_head_bind(self._h, ctypes.c_void_p(d_workspace), nbytes, ctypes.c_void_p(stream)))
+        self.device = _current_device()
 
     def _inputs(self, hidden, weight):
         bf16 = _t().bfloat16
-        lh = _rows(hidden, self.dim, bf16, "hidden")
-        lw = _rows(weight, self.dim, bf16, "weight", self.vocab)
+        lh = _rows(hidden, self.dim, bf16, "hidden", self.device)
+        lw = _rows(weight, self.dim, bf16, "weight", self.device, self.vocab)
         return hidden.data_ptr(), lh, weight.data_ptr(), lw
 
     def _teacher(self, top_ids, top_logits, tokens):
         top = top_ids.shape[-1]
-        ids = _flat(top_ids, (tokens, top), _t().int64, "top_ids")
-        return ids, _flat(top_logits, (tokens, top), _t().float32, "top_logits"), top
+        ids = _flat(top_ids, (tokens, top), _t().int64, "top_ids", self.device)
+        return ids, _flat(top_logits, (tokens, top), _t().float32, "top_logits", self.device), top
 
     def _forward(self, fn, hidden, args, stream, *tensors):
         n = hidden.shape[0]
@@ -456,14 +481,12 @@ class Head:
             _check(fn(self._h, *args, n, loss.data_ptr(), lse.data_ptr(), s))
             return loss, lse
 
-        if stream is None:
-            return call(_here(hidden))
-        return _on(stream, call, hidden, *tensors, self.workspace)
+        return _run(self, call, stream, hidden, *tensors, self.workspace)
 
     def _backward(self, fn, hidden, weight, args, lse, grad_loss, dhidden, dweight, stream, *tensors):
         n = hidden.shape[0]
-        f32 = _t().float32
-        args += (n, _flat(lse, (n,), f32, "lse"), _flat(grad_loss, (n,), f32, "grad_loss"))
+        f32, dev = _t().float32, self.device
+        args += (n, _flat(lse, (n,), f32, "lse", dev), _flat(grad_loss, (n,), f32, "grad_loss", dev))
 
         def call(s):
             dh, ph, lh = self._grad(hidden, dhidden, "dhidden")
@@ -471,9 +494,7 @@ class Head:
             _check(fn(self._h, *args, ph, lh, pw, lw, s))
             return dh, dw
 
-        if stream is None:
-            return call(_here(hidden))
-        return _on(stream, call, hidden, weight, lse, grad_loss, *tensors, self.workspace)
+        return _run(self, call, stream, hidden, weight, lse, grad_loss, *tensors, self.workspace)
 
     def _grad(self, like, want, name):
         """The gradient of ``like`` (made where True, left out where False or None), its address and pitch."""
@@ -485,16 +506,16 @@ class Head:
                 want = _t().empty(rows, dim, dtype=like.dtype, device=like.device)
                 return want, want.data_ptr(), dim
             want = _t().empty(rows, -(-dim // 8) * 8, dtype=like.dtype, device=like.device)[:, :dim]
-        return want, want.data_ptr(), _rows(want, dim, _t().bfloat16, name, rows)
+        return want, want.data_ptr(), _rows(want, dim, _t().bfloat16, name, self.device, rows)
 
     def xent(self, hidden, weight, targets, *, stream=None):
         """(loss, lse) per token; targets int64, one outside the vocabulary does not count."""
-        y = _flat(targets, hidden.shape[:1], _t().int64, "targets")
+        y = _flat(targets, hidden.shape[:1], _t().int64, "targets", self.device)
         return self._forward(lib().dmuon_head_xent, hidden, (*self._inputs(hidden, weight), y), stream, weight, targets)
 
     def xent_backward(self, hidden, weight, targets, lse, grad_loss, *, dhidden=True, dweight=True, stream=None):
         """(dhidden, dweight) of sum(grad_loss * loss). Either may be a tensor to write into, or False."""
-        y = _flat(targets, hidden.shape[:1], _t().int64, "targets")
+        y = _flat(targets, hidden.shape[:1], _t().int64, "targets", self.device)
         return self._backward(lib().dmuon_head_xent_backward, hidden, weight, (*self._inputs(hidden, weight), y), lse,
                               grad_loss, dhidden, dweight, stream, targets)
 
@@ -543,11 +564,13 @@ class Router:
     """Tokens to experts and back, for up to ``max_tokens`` tokens with ``top`` experts each.
 
     Holds the sort's scratch (torch-allocated; one sort uses it at a time).
-    Rows are bf16 or fp32, weights fp32 [tokens, top].
+    Rows are bf16 or fp32, weights fp32 [tokens, top]. All of them lie on the
+    scratch's device, which is the current one or the stream's.
     """
 
     def __init__(self, max_tokens, top, experts, workspace):
         self.max_tokens, self.top, self.experts, self.workspace = max_tokens, top, experts, workspace
+        self.device = workspace.get_device()
 
     @classmethod
     def create(cls, max_tokens, top, experts, *, device=None):
@@ -561,7 +584,7 @@ class Router:
         t, top = expert_ids.shape[0], self.top
         if t > self.max_tokens:
             _refuse(f"expert_ids has {t} tokens, more than max_tokens ({self.max_tokens})")
-        ids = _flat(expert_ids, (t, top), _t().int64, "expert_ids")
+        ids = _flat(expert_ids, (t, top), _t().int64, "expert_ids", self.device)
 
         def call(s):
             empty, i32, dev = _t().empty, _t().int32, expert_ids.device
@@ -573,9 +596,7 @@ class Router:
                                           offsets.data_ptr(), ws.data_ptr(), ws.numel(), s))
             return Route(dest, source, offsets)
 
-        if stream is None:
-            return call(_here(expert_ids))
-        return _on(stream, call, expert_ids, self.workspace)
+        return _run(self, call, stream, expert_ids, self.workspace)
 
     def _kind(self, t, name):
         if t.dim() == 2:
@@ -587,14 +608,14 @@ class Router:
 
     def _route(self, route, tokens):
         i32 = _t().int32
-        return (_flat(route.dest, (tokens, self.top), i32, "route.dest"),
-                _flat(route.source, (tokens * self.top,), i32, "route.source"))
+        return (_flat(route.dest, (tokens, self.top), i32, "route.dest", self.device),
+                _flat(route.source, (tokens * self.top,), i32, "route.source", self.device))
 
     def dispatch(self, x, route, *, stream=None):
         """xs [tokens * top, dim]: x's rows in expert order, zeros in rows not in use."""
         kind = self._kind(x, "x")
         t, dim = x.shape
-        ld = _rows(x, dim, x.dtype, "x")
+        ld = _rows(x, dim, x.dtype, "x", self.device)
         dest, source = self._route(route, t)
 
         def call(s):
@@ -602,35 +623,31 @@ class Router:
             _check(lib().dmuon_route_dispatch(x.data_ptr(), ld, dest, source, t, self.top, dim, kind, xs.data_ptr(), s))
             return xs
 
-        if stream is None:
-            return call(_here(x))
-        return _on(stream, call, x, route.dest, route.source)
+        return _run(self, call, stream, x, route.dest, route.source)
 
     def combine(self, ys, weights, route, *, stream=None):
         """y [tokens, dim]: the sum of each token's expert rows, times weights (fp32 [tokens, top], or None: 1)."""
         kind = self._kind(ys, "ys")
         t, dim = route.dest.shape[0], ys.shape[1]
         dest, _ = self._route(route, t)
-        rows = _flat(ys, (t * self.top, dim), ys.dtype, "ys")
-        w = None if weights is None else _flat(weights, (t, self.top), _t().float32, "weights")
+        rows = _flat(ys, (t * self.top, dim), ys.dtype, "ys", self.device)
+        w = None if weights is None else _flat(weights, (t, self.top), _t().float32, "weights", self.device)
 
         def call(s):
             y = _t().empty((t, dim), dtype=ys.dtype, device=ys.device)
             _check(lib().dmuon_route_combine(rows, w, dest, t, self.top, dim, kind, y.data_ptr(), dim, s))
             return y
 
-        if stream is None:
-            return call(_here(ys))
-        return _on(stream, call, ys, weights, route.dest)
+        return _run(self, call, stream, ys, weights, route.dest)
 
     def combine_backward(self, dy, ys, weights, route, *, stream=None):
         """(dys, dweights) of combine."""
         kind = self._kind(ys, "ys")
         t, dim = route.dest.shape[0], ys.shape[1]
         dest, source = self._route(route, t)
-        rows = _flat(ys, (t * self.top, dim), ys.dtype, "ys")
-        w = _flat(weights, (t, self.top), _t().float32, "weights")
-        ld = _rows(dy, dim, ys.dtype, "dy", t)
+        rows = _flat(ys, (t * self.top, dim), ys.dtype, "ys", self.device)
+        w = _flat(weights, (t, self.top), _t().float32, "weights", self.device)
+        ld = _rows(dy, dim, ys.dtype, "dy", self.device, t)
 
         def call(s):
             dys = _t().empty_like(ys)
@@ -639,9 +656,7 @@ class Router:
                                                       dys.data_ptr(), dw.data_ptr(), s))
             return dys, dw
 
-        if stream is None:
-            return call(_here(ys))
-        return _on(stream, call, dy, ys, weights, route.dest, route.source)
+        return _run(self, call, stream, dy, ys, weights, route.dest, route.source)
 
     def dispatch_backward(self, dxs, route, *, stream=None):
         """dx [tokens, dim]: the gradient of dispatch, the sum of each token's rows of dxs."""
