@@ -494,7 +494,8 @@ class Head:
             _check(fn(self._h, *args, ph, lh, pw, lw, s))
             return dh, dw
 
-        return _run(self, call, stream, hidden, weight, lse, grad_loss, *tensors, self.workspace)
+        given = [t for t in (dhidden, dweight) if not isinstance(t, bool)]
+        return _run(self, call, stream, hidden, weight, lse, grad_loss, *tensors, *given, self.workspace)
 
     def _grad(self, like, want, name):
         """The gradient of ``like`` (made where True, left out where False or None), its address and pitch."""

@@ -139,3 +139,18 @@ def test_another_current_device_and_streams_of_another_device_are_refused(world,
     assert not world.library.calls
     CALLS[call][1](world.objects(), tensors(), stream(7))  # a stream of the object's device brings its device
     assert len(world.library.calls) == 1 and world.device == 1
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_every_tensor_of_a_call_is_recorded_on_its_stream(world, call):
+    t, objects = tensors(), world.objects()
+    CALLS[call][1](objects, t, stream(7))
+    for name in CALLS[call][0]:
+        assert 7 in getattr(t[name], "seen", ()), name
+
+
+@pytest.mark.parametrize("want", [True, False, None])
+def test_gradients_that_are_not_given_are_nothing_to_record(world, want):
+    t, (head, _) = tensors(), world.objects()
+    head.xent_backward(t["h"], t["w"], t["y"], t["lse"], t["g"], dhidden=want, dweight=want, stream=stream(7))
+    assert len(world.library.calls) == 1
