@@ -398,23 +398,27 @@ def _here(device) -> int:
     return _t()._C._cuda_getCurrentRawStream(device)
 
 
-def _run(owner, call, stream, *tensors):
+def _run(owner, call, stream, *tensors, scratch=None):
     """Run ``call(handle)`` on the device of ``owner`` and on ``stream`` (None: the current one): what it allocates
-    belongs to that stream, and what it is given stays alive until the stream is done with it."""
+    belongs to that stream. ``scratch``, the owner's workspace, and what a call with a stream of its own is given
+    stay alive until the stream is done with them; other tensors on the current stream are the caller's to keep."""
     device, current = owner.device, _current_device()
     if device is None:
         device = current
     if stream is None:
         if current != device:
             _refuse(f"the operator is on cuda:{device}, the current device is cuda:{current}")
-        return call(_here(device))
+        handle = _here(device)
+        if scratch is not None and handle != owner.home:
+            scratch.record_stream(_t().cuda.current_stream(device))
+        return call(handle)
     if stream.device_index != device:
         _refuse(f"the operator is on cuda:{device}, the stream on cuda:{stream.device_index}")
-    if current == device and stream.cuda_stream == _here(device):
-        return call(stream.cuda_stream)
-    for t in tensors:
+    for t in (*tensors, scratch):
         if t is not None:
             t.record_stream(stream)
+    if current == device and stream.cuda_stream == _here(device):
+        return call(stream.cuda_stream)
     with _t().cuda.stream(stream):
         return call(stream.cuda_stream)
 
@@ -435,6 +439,7 @@ class Head:
         self.max_tokens, self.vocab, self.dim, self.max_top = max_tokens, vocab, dim, max_top
         self.workspace = None
         self.device = None  # index of the device it is bound on
+        self.home = 0       # raw handle of the stream the workspace was allocated on
 
     @classmethod
     def create(cls, max_tokens, vocab, dim, *, max_top=0, device=None, stream=None):
@@ -448,7 +453,7 @@ class Head:
         if s != here:
             ws.record_stream(stream)
         self.bind((ws.data_ptr() + 1023) // 1024 * 1024, nbytes, s)
-        self.workspace = ws
+        self.workspace, self.home = ws, here
         return self
 
     def workspace_bytes(self) -> int:
@@ -481,7 +486,7 @@ class Head:
             _check(fn(self._h, *args, n, loss.data_ptr(), lse.data_ptr(), s))
             return loss, lse
 
-        return _run(self, call, stream, hidden, *tensors, self.workspace)
+        return _run(self, call, stream, hidden, *tensors, scratch=self.workspace)
 
     def _backward(self, fn, hidden, weight, args, lse, grad_loss, dhidden, dweight, stream, *tensors):
         n = hidden.shape[0]
@@ -494,8 +499,12 @@ class Head:
             _check(fn(self._h, *args, ph, lh, pw, lw, s))
             return dh, dw
 
-        given = [t for t in (dhidden, dweight) if not isinstance(t, bool)]
-        return _run(self, call, stream, hidden, weight, lse, grad_loss, *tensors, *given, self.workspace)
+        given = []
+        for like, want, name in ((hidden, dhidden, "dhidden"), (weight, dweight, "dweight")):
+            if want is not None and not isinstance(want, bool):
+                _rows(want, self.dim, _t().bfloat16, name, self.device, like.shape[0])
+                given.append(want)
+        return _run(self, call, stream, hidden, weight, lse, grad_loss, *tensors, *given, scratch=self.workspace)
 
     def _grad(self, like, want, name):
         """The gradient of ``like`` (made where True, left out where False or None), its address and pitch."""
@@ -572,6 +581,7 @@ class Router:
     def __init__(self, max_tokens, top, experts, workspace):
         self.max_tokens, self.top, self.experts, self.workspace = max_tokens, top, experts, workspace
         self.device = workspace.get_device()
+        self.home = _here(self.device)  # raw handle of the stream the workspace was allocated on
 
     @classmethod
     def create(cls, max_tokens, top, experts, *, device=None):
@@ -597,7 +607,7 @@ class Router:
                                           offsets.data_ptr(), ws.data_ptr(), ws.numel(), s))
             return Route(dest, source, offsets)
 
-        return _run(self, call, stream, expert_ids, self.workspace)
+        return _run(self, call, stream, expert_ids, scratch=self.workspace)
 
     def _kind(self, t, name):
         if t.dim() == 2:

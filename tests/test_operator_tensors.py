@@ -154,3 +154,35 @@ def test_gradients_that_are_not_given_are_nothing_to_record(world, want):
     t, (head, _) = tensors(), world.objects()
     head.xent_backward(t["h"], t["w"], t["y"], t["lse"], t["g"], dhidden=want, dweight=want, stream=stream(7))
     assert len(world.library.calls) == 1
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_a_stream_that_is_current_is_recorded_all_the_same(world, call):
+    t, objects = tensors(), world.objects()
+    world.current = stream(7)
+    CALLS[call][1](objects, t, stream(7))
+    for name in CALLS[call][0]:
+        assert 7 in getattr(t[name], "seen", ()), name
+
+
+@pytest.mark.parametrize("call", ["xent", "xent_backward", "distill", "distill_backward", "sort"])
+@pytest.mark.parametrize("given", [None, stream(7)])
+def test_a_workspace_is_recorded_on_the_streams_that_use_it(world, call, given):
+    # allocated on stream 0, used while stream 7 is current: only the object can record it
+    objects = world.objects()
+    scratch = objects[call == "sort"].workspace
+    CALLS[call][1](objects, tensors(), None)
+    assert not hasattr(scratch, "seen")
+    world.current = stream(7)
+    CALLS[call][1](objects, tensors(), given)
+    assert 7 in scratch.seen
+
+
+@pytest.mark.parametrize("name", ["dh", "dw"])
+def test_given_gradients_are_looked_at_before_they_are_recorded(world, name):
+    t = tensors()
+    t[name] = torch.zeros(t[name].shape, dtype=torch.bfloat16)  # of the host
+    with pytest.raises(dm.DmuonError) as e:
+        CALLS["xent_backward"][1](world.objects(), t, stream(7))
+    assert e.value.status == dm.ERR_INVALID_ARG and not world.library.calls
+    assert not any(hasattr(x, "seen") for x in t.values())
