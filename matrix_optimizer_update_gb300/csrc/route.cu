@@ -35,8 +35,11 @@ constexpr int kSortHeld = 32 * kSortBatch;
 constexpr int kSortMaxBlocks = 1024;
 constexpr int kSortCluster = 8;     // blocks of a cluster
 // Warps per block at most: 32, or 8 where 32 counts per expert would not fit in shared memory (132 or 144 KB).
-constexpr int kManyExperts = 1024;
-int sort_warps(int experts) { return experts <= kManyExperts ? 32 : 8; }
+constexpr int kManyExperts = 1024, kMaxWarps = 32, kManyExpertsWarps = 8;
+int sort_warps(int experts) { return experts <= kManyExperts ? kMaxWarps : kManyExpertsWarps; }
+// The most shared memory a sort asks for: the counts of each warp and the block's own.
+constexpr size_t kSortSmem =
+    sizeof(int) * std::max((kMaxWarps + 1) * kManyExperts, (kManyExpertsWarps + 1) * kMaxExperts);
 
 struct SortParams {
   const int64_t* ids;
@@ -252,10 +255,12 @@ cudaError_t launch_sort(SortParams& p, cudaStream_t s) {
   p.per_warp = static_cast<int32_t>(std::max<int64_t>(1, (held + total - 1) / total) * kSortHeld);
   const size_t smem = sizeof(int) * (warps + 1) * p.experts;
   cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024) {  // beside the static arrays, within the 48 KB a launch has without asking
+  // Beside the static arrays, 40 KB are within the 48 KB that a launch has without asking. The limit is a property of
+  // the kernel, not of the launch: every call sets the same, for threads that sort at the same time.
+  if (smem > 40 * 1024) {
     for (auto* k : {route_count_kernel, route_place_kernel<true>, route_place_kernel<false>})
       if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSortSmem));
     if (e != cudaSuccess) return e;
   }
   if (all) return launch_follow(route_place_kernel<true>, dim3(p.blocks), warps * 32, smem, s, p.blocks, p);
