@@ -87,7 +87,7 @@ struct LogitParams {
 struct Pipe {
   unsigned* status;
   unsigned* sched;         // two words, zero between launches
-  float* gmax;             // the largest |grad| of a backward call; dz is relative to it
+  float* gmax;             // the largest finite |grad| of a backward call; dz is relative to it
   int pairs;
 };
 

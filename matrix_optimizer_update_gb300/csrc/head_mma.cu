@@ -81,7 +81,7 @@ struct Params {
   int64_t acc_ld;
   float gscale;            // factor of the gradients beside *gmax
   float zscale;            // of the logits: 1 / temperature and what truncation takes
-  float* gmax;             // largest |grad|: dz holds gradients relative to it
+  float* gmax;             // largest finite |grad|: dz holds gradients relative to it
   LogitParams l;
   unsigned* sched;         // [0] tiles claimed, [1] CTAs done; both zero between launches
   unsigned* status;
@@ -941,7 +941,10 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
     if (MODE == kDz || MODE == kThinDz) {  // under the first tile's products
       float m = 0.f;
       for (int64_t t = threadIdx.x - 64; t < p.l.tokens; t += kEpiWarps * 32)
-        if (counts(p.l.want, t)) m = fmaxf(m, fabsf(p.l.grad[t]));
+        if (counts(p.l.want, t)) {
+          const float g = fabsf(p.l.grad[t]);
+          if (g < INFINITY) m = fmaxf(m, g);  // the others' gradients are relative to it, and finite
+        }
       for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
       if (lane == 0) sh->red[warp - 2] = m;
       asm volatile("bar.sync 1, 256;" ::: "memory");
