@@ -116,7 +116,10 @@ constexpr int kRowThreads = 256;
 
 __device__ __forceinline__ void join(float& peak, float& sum, float peak2, float sum2) {
   const float m = fmaxf(peak, peak2);
-  if (m == kNegInf) return;  // neither has anything
+  if (!(m > kNegInf)) {  // neither has a number: zeros, or NaN to pass on
+    sum += sum2;
+    return;
+  }
   sum = sum * expf(peak - m) + sum2 * expf(peak2 - m);
   peak = m;
 }
@@ -139,8 +142,8 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         for (int u = 0; u < 4; ++u)
           q[u] = g + u * kLanes < p.groups ? parts[(g + u * kLanes) * p.group_step] : Part{kNegInf, 0.f};
         const float m = fmaxf(fmaxf(q[0].peak, q[1].peak), fmaxf(q[2].peak, q[3].peak));
-        if (m == kNegInf) {
-          sum += q[0].sum + q[1].sum + q[2].sum + q[3].sum;  // zeros, or NaN to pass on
+        if (!(m > kNegInf)) {  // (a group of nothing but NaN may have NaN for its peak)
+          sum += q[0].sum + q[1].sum + q[2].sum + q[3].sum;
           continue;
         }
         float s = 0.f;
