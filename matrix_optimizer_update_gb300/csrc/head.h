@@ -39,11 +39,15 @@ struct DotParams {
   float scale;
 };
 
-// Tensor cores truncate what they accumulate: a logit z of theirs is off by about 1.0e-9 * dim * z, always
-// towards zero (measured: -6.6e-5 at z = 16, dim = 4096, where fp32 FMAs are off by 8e-7; the factor is 0.85e-9
-// to 1.15e-9 for normal, spiked and planted states and dims of 1024 to 8192, 0.5e-9 to 1.1e-9 at 256, and more
-// only where a common part of all logits far above 30 outweighs the rest). Their scale puts the mean of it back:
-// lse is off by 4e-8 in place of 4.1e-7 (3912 dims, normal states), 3.7e-7 in place of 3.8e-6 (one logit of 12).
+// Tensor cores truncate what they accumulate, always towards zero: a logit z whose terms are spread evenly along the
+// sum is off by about 1.0e-9 * dim * z (-6.6e-5 at z = 16, dim = 4096, where fp32 FMAs are off by 8e-7). Measured at
+// 1024 to 65536 dims: 0.74e-9 to 1.05e-9 for normal and planted states, 1.25e-9 with one common state of 100, 1.8e-9
+// where a sixteenth of the terms at the start makes the logit, 0.05e-9 to 0.25e-9 where it lies at the end or nothing
+// comes after it (at 256 dims up to 2.2e-9 and down to 0.2e-9; more only where partial sums far above z cancel). Their
+// scale puts 1.0e-9 back, the middle of that range: log sums are off by 4e-8 in place of 4.1e-7 (3912 dims, normal
+// states), 3.7e-7 in place of 3.8e-6 (one logit of 12), and by up to 1.0e-9 * dim * z either way, where it was up to
+// twice that one way, for logits made at one end of the sum (3.5e-6 of lse at 4096 dims). Below about 60 dims the
+// scale rounds to 1 / temperature alone, and up to 180 by up to half a unit in the last place too much or too little.
 constexpr double kTruncated = 1.0e-9;
 
 // What remains is a few percent of it, in a loss still too much: that of a token predicted with near certainty is
