@@ -17,6 +17,7 @@ from __future__ import annotations
 import argparse
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import dmuon as dm
 
@@ -30,6 +31,7 @@ class Dispatch(torch.autograd.Function):
         return router.dispatch(x, route)
 
     @staticmethod
+    @once_differentiable  # the library has no second derivatives: asked for, they are an error
     def backward(ctx, dxs):
         return ctx.router.dispatch_backward(dxs.contiguous(), ctx.route), None, None
 
@@ -44,6 +46,7 @@ class Combine(torch.autograd.Function):
         return router.combine(ys, weights, route)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         dys, dw = ctx.router.combine_backward(dy.contiguous(), *ctx.saved_tensors, ctx.route)
         return dys, dw, None, None
@@ -60,6 +63,7 @@ class Xent(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         hidden, weight, targets, lse = ctx.saved_tensors
         return (*ctx.head.xent_backward(hidden, weight, targets, lse, grad.contiguous()), None, None)
@@ -76,6 +80,7 @@ class Distill(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         hidden, weight, ids, logits, lse = ctx.saved_tensors
         return (*ctx.head.distill_backward(hidden, weight, ids, logits, ctx.temperature, lse, grad.contiguous()), None,
