@@ -15,11 +15,25 @@ which the model has to learn by heart.
 from __future__ import annotations
 
 import argparse
+import functools
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import dmuon as dm
+
+
+def first_derivative(backward):
+    """A backward pass that is an error with create_graph=True: the library's calls leave no graph, so a second
+    derivative through them would silently be missing. (once_differentiable refuses only where the gradient that
+    comes in has a graph, not where saved tensors have one.)"""
+
+    @functools.wraps(backward)
+    def checked(ctx, grad):
+        if torch.is_grad_enabled():
+            raise RuntimeError("the library's operators have no second derivatives")
+        return backward(ctx, grad)
+
+    return checked
 
 
 class Dispatch(torch.autograd.Function):
@@ -31,7 +45,7 @@ class Dispatch(torch.autograd.Function):
         return router.dispatch(x, route)
 
     @staticmethod
-    @once_differentiable  # the library has no second derivatives: asked for, they are an error
+    @first_derivative
     def backward(ctx, dxs):
         return ctx.router.dispatch_backward(dxs.contiguous(), ctx.route), None, None
 
@@ -46,7 +60,7 @@ class Combine(torch.autograd.Function):
         return router.combine(ys, weights, route)
 
     @staticmethod
-    @once_differentiable
+    @first_derivative
     def backward(ctx, dy):
         dys, dw = ctx.router.combine_backward(dy.contiguous(), *ctx.saved_tensors, ctx.route)
         return dys, dw, None, None
@@ -63,7 +77,7 @@ class Xent(torch.autograd.Function):
         return loss
 
     @staticmethod
-    @once_differentiable
+    @first_derivative
     def backward(ctx, grad):
         hidden, weight, targets, lse = ctx.saved_tensors
         return (*ctx.head.xent_backward(hidden, weight, targets, lse, grad.contiguous()), None, None)
@@ -80,7 +94,7 @@ class Distill(torch.autograd.Function):
         return loss
 
     @staticmethod
-    @once_differentiable
+    @first_derivative
     def backward(ctx, grad):
         hidden, weight, ids, logits, lse = ctx.saved_tensors
         return (*ctx.head.distill_backward(hidden, weight, ids, logits, ctx.temperature, lse, grad.contiguous()), None,
