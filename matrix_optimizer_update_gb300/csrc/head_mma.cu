@@ -292,6 +292,10 @@ __device__ __forceinline__ void target_logits(const LogitParams& p, int id, int6
   }
 }
 
+// p of a wanted entry from its logit. lse is rounded (by up to 1e-6 at 16 to 32) and z is, so that of a token predicted
+// with near certainty the difference may lie above 0; the gradient of p - 1 would then push the target down.
+__device__ __forceinline__ float probability(float z, float lse) { return z > lse ? 1.f : expf(z - lse); }
+
 // 32 x 32 values in shared memory, rows turned so that neither rows nor columns conflict.
 __device__ __forceinline__ float& cell(float* sm, int row, int col) { return sm[row * 32 + (col ^ row)]; }
 
@@ -429,7 +433,7 @@ __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t,
       __syncwarp();
       wanted_of_row<true>(p, t, c, jc, v, reinterpret_cast<float*>(stg), lane,
                           [&](float& x, float share, float z, int, bool again) {
-                            x = share >= kSure && !again ? g * (expf(z - lse) - share) : x - g * share;
+                            x = share >= kSure && !again ? g * (probability(z, lse) - share) : x - g * share;
                           });
     }
     uint8_t* box = stg + (nbox & 1u) * kBox;
@@ -566,7 +570,7 @@ __device__ __forceinline__ bool drain_thin_dz(const Params& P, const ThinTokens&
     wanted_of_tokens<true>(p, t, c[i], first, end, v, sm, lane,
                            [&](float& x, float share, float z, int, bool again) {
                              const float g = tk.g[t];
-                             x = share >= kSure && !again ? g * (expf(z - tk.lse[t]) - share) : x - g * share;
+                             x = share >= kSure && !again ? g * (probability(z, tk.lse[t]) - share) : x - g * share;
                            });
     // By way of shared memory, so that a lane stores 16 bytes: with 2 bytes a lane the number of stores shows in the
     // launch's time (both passes over 77 tokens x 50257 x 1024: 103 us, this way 99.7; with the tokens that there are not left
