@@ -528,6 +528,22 @@ dmuon_status dmuon_head_xent_backward(dmuon_head_t head, const void* hidden, int
                                       int64_t ld_dweight, void* stream);
 
 /*
+ * dmuon_head_xent_backward_loss - the same, given the losses too:
+ *
+ *  loss       device, tokens floats, as dmuon_head_xent wrote them beside lse.
+ *
+ * dz of a target is then grad_loss * expm1(-loss), which has all the digits of
+ * the loss. From z and lse, both rounded to 1e-6 at 16 to 32, 1 - p of the
+ * target is off by about that much: 1 % of dz where the loss is 1e-4, all of it
+ * below 1e-6 (it never has the wrong sign). The other entries are the same.
+ */
+dmuon_status dmuon_head_xent_backward_loss(dmuon_head_t head, const void* hidden, int64_t ld_hidden,
+                                           const void* weight, int64_t ld_weight, const int64_t* targets,
+                                           int64_t tokens, const float* lse, const float* loss,
+                                           const float* grad_loss, void* dhidden, int64_t ld_dhidden, void* dweight,
+                                           int64_t ld_dweight, void* stream);
+
+/*
  * dmuon_head_distill - distillation from a teacher's top logits: the divergence
  * of the student's distribution over the whole vocabulary from the teacher's
  * over its list, both at a temperature:
@@ -554,7 +570,9 @@ dmuon_status dmuon_head_distill(dmuon_head_t head, const void* hidden, int64_t l
  *
  *   dz[t][v] = grad_loss[t] * temperature * (p[t][v] - q[t][v])   (0 for a row without entries)
  *
- * lse as dmuon_head_distill wrote it; the rest as dmuon_head_xent_backward.
+ * lse as dmuon_head_distill wrote it; the rest as dmuon_head_xent_backward. p of
+ * a listed entry is off by about 1e-6 of itself, which is most of p - q once
+ * the student agrees with the teacher that closely.
  */
 dmuon_status dmuon_head_distill_backward(dmuon_head_t head, const void* hidden, int64_t ld_hidden, const void* weight,
                                          int64_t ld_weight, const int64_t* top_ids, const float* top_logits,

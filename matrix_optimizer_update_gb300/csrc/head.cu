@@ -196,8 +196,9 @@ dmuon_status forward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, cons
 }
 
 dmuon_status backward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, const void* weight, int64_t ld_weight,
-                      const Loss& L, bool distill, int64_t tokens, const float* lse, const float* grad_loss,
-                      void* dhidden, int64_t ld_dhidden, void* dweight, int64_t ld_dweight, void* stream) {
+                      const Loss& L, bool distill, int64_t tokens, const float* lse, const float* losses,
+                      const float* grad_loss, void* dhidden, int64_t ld_dhidden, void* dweight, int64_t ld_dweight,
+                      void* stream) {
   dmuon_status st = check_call(H, hidden, ld_hidden, weight, ld_weight, tokens);
   if (st == DMUON_OK) st = check_loss(H, L, tokens, distill);
   if (st == DMUON_OK && dhidden != nullptr && tokens > 0) st = check_matrix(dhidden, ld_dhidden, H->dim, "dhidden");
@@ -217,6 +218,7 @@ dmuon_status backward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, con
   head::LogitParams p = logit_params(H, hidden, ld_hidden, weight, ld_weight, tokens, L);
   if ((st = prepare_wanted(H, L, tokens, p.in, &p.want, s)) != DMUON_OK) return st;
   p.lse = lse;
+  p.loss = losses;
   p.grad = grad_loss;
   p.dz = reinterpret_cast<head::bf16*>(H->ws + H->off_dz);
   p.ld_dz = H->piece;
@@ -349,7 +351,20 @@ extern "C" dmuon_status dmuon_head_xent_backward(dmuon_head_t H, const void* hid
                                                  void* stream) {
   Loss L;
   L.targets = targets;
-  return backward(H, hidden, ld_hidden, weight, ld_weight, L, false, tokens, lse, grad_loss, dhidden, ld_dhidden,
+  return backward(H, hidden, ld_hidden, weight, ld_weight, L, false, tokens, lse, nullptr, grad_loss, dhidden,
+                  ld_dhidden, dweight, ld_dweight, stream);
+}
+
+extern "C" dmuon_status dmuon_head_xent_backward_loss(dmuon_head_t H, const void* hidden, int64_t ld_hidden,
+                                                      const void* weight, int64_t ld_weight, const int64_t* targets,
+                                                      int64_t tokens, const float* lse, const float* loss,
+                                                      const float* grad_loss, void* dhidden, int64_t ld_dhidden,
+                                                      void* dweight, int64_t ld_dweight, void* stream) {
+  if (tokens > 0 && (loss == nullptr || misaligned(loss, 4)))
+    return refuse(DMUON_ERR_INVALID_ARG, "loss is NULL or not 4-byte aligned");
+  Loss L;
+  L.targets = targets;
+  return backward(H, hidden, ld_hidden, weight, ld_weight, L, false, tokens, lse, loss, grad_loss, dhidden, ld_dhidden,
                   dweight, ld_dweight, stream);
 }
 
@@ -376,8 +391,8 @@ extern "C" dmuon_status dmuon_head_distill_backward(dmuon_head_t H, const void* 
   L.top_logits = top_logits;
   L.top = top;
   L.temperature = temperature;
-  return backward(H, hidden, ld_hidden, weight, ld_weight, L, true, tokens, lse, grad_loss, dhidden, ld_dhidden,
-                  dweight, ld_dweight, stream);
+  return backward(H, hidden, ld_hidden, weight, ld_weight, L, true, tokens, lse, nullptr, grad_loss, dhidden,
+                  ld_dhidden, dweight, ld_dweight, stream);
 }
 
 extern "C" dmuon_status dmuon_head_read_device_status(dmuon_head_t H, void* stream, uint32_t* bits) {

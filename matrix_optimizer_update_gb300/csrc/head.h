@@ -83,6 +83,7 @@ struct LogitParams {
   // backward
   const float* lse;
   const float* grad;
+  const float* loss;       // cross entropy: the losses, or nullptr: the targets' logits are formed again
   bf16* dz;                // [tokens][ld_dz]; up to kTwofold tokens: [2][tokens][ld_dz]
   int64_t ld_dz;
 };

@@ -268,7 +268,7 @@ __device__ __forceinline__ bool counts(const Wanted& w, int64_t t) {
 // they lie together they go by fours, as a trip to memory takes longer than what is fetched (243 tokens x 15031 x
 // 3928, both passes: one by one 190 us, this way 166).
 __device__ __forceinline__ void target_logits(const LogitParams& p, int id, int64_t t, int end, int lane) {
-  if (p.want.targets == nullptr) return;  // a list's are formed where it is sorted
+  if (p.want.targets == nullptr || p.loss != nullptr) return;  // a list's are formed where it is sorted
   unsigned more = __ballot_sync(0xffffffffu, id < end);
   while (more != 0u) {
     int L = 0;
@@ -292,15 +292,20 @@ __device__ __forceinline__ void target_logits(const LogitParams& p, int id, int6
   }
 }
 
-// p of a wanted entry from its logit. lse is rounded (by up to 1e-6 at 16 to 32) and z is, so that of a token predicted
-// with near certainty the difference may lie above 0; the gradient of p - 1 would then push the target down.
-__device__ __forceinline__ float probability(float z, float lse) { return z > lse ? 1.f : expf(z - lse); }
+// p - share of a likely entry. From its logit: lse is rounded (by up to 1e-6 at 16 to 32) and z is, so that of a token
+// predicted with near certainty p keeps no digit of 1 - p, and must at least not be above 1, where the gradient would
+// push the target down. From the token's loss, which keeps them: p of the target is exp(-loss).
+__device__ __forceinline__ float above(const LogitParams& p, float known, float lse, float share) {
+  if (p.loss != nullptr) return expm1f(-known);
+  return (known > lse ? 1.f : expf(known - lse)) - share;
+}
 
 // 32 x 32 values in shared memory, rows turned so that neither rows nor columns conflict.
 __device__ __forceinline__ float& cell(float* sm, int row, int col) { return sm[row * 32 + (col ^ row)]; }
 
 // Visits the entries of this lane's cursor before `end`, whose values are row `lane` of sm (column: id - first):
-// visit(value, share, pos, again), `again` when the entry before had the same id. A lane's entries may be many:
+// visit(value, share, known, pos, again), `known` the logit of a likely entry (the token's loss, where the call has
+// those), `again` when the entry before had the same id. A lane's entries may be many:
 // frequent words lie together in many vocabularies. (With the values left in registers, where an entry takes a
 // compare for each of 32, and one after another over a warp's tokens, 48 lists of 68 entries against 9328 x 1616
 // made a call of 304 us; this way 87.)
@@ -311,6 +316,7 @@ template <bool WITH_LOGIT, class Visit>
 __device__ __forceinline__ void walk(const LogitParams& p, int64_t t, Cursor& c, int first, int end, float* sm,
                                      int lane, Visit&& visit) {
   const Wanted& w = p.want;
+  const float* known = p.loss != nullptr ? p.loss : p.picked;
   int last = -1;
   while (c.id < end) {
     int id[5];
@@ -323,7 +329,7 @@ __device__ __forceinline__ void walk(const LogitParams& p, int64_t t, Cursor& c,
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      z[j] = WITH_LOGIT && (j == 0 || c.pos + j < c.n) && q[j] >= kSure ? p.picked[t * w.top + c.pos + j] : 0.f;
+      z[j] = WITH_LOGIT && (j == 0 || c.pos + j < c.n) && q[j] >= kSure ? known[t * w.top + c.pos + j] : 0.f;
     const int pos = c.pos;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -433,7 +439,7 @@ __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t,
       __syncwarp();
       wanted_of_row<true>(p, t, c, jc, v, reinterpret_cast<float*>(stg), lane,
                           [&](float& x, float share, float z, int, bool again) {
-                            x = share >= kSure && !again ? g * (probability(z, lse) - share) : x - g * share;
+                            x = share >= kSure && !again ? g * above(p, z, lse, share) : x - g * share;
                           });
     }
     uint8_t* box = stg + (nbox & 1u) * kBox;
@@ -570,7 +576,7 @@ __device__ __forceinline__ bool drain_thin_dz(const Params& P, const ThinTokens&
     wanted_of_tokens<true>(p, t, c[i], first, end, v, sm, lane,
                            [&](float& x, float share, float z, int, bool again) {
                              const float g = tk.g[t];
-                             x = share >= kSure && !again ? g * (probability(z, tk.lse[t]) - share) : x - g * share;
+                             x = share >= kSure && !again ? g * above(p, z, tk.lse[t], share) : x - g * share;
                            });
     // By way of shared memory, so that a lane stores 16 bytes: with 2 bytes a lane the number of stores shows in the
     // launch's time (both passes over 77 tokens x 50257 x 1024: 103 us, this way 99.7; with the tokens that there are not left

@@ -52,7 +52,7 @@ EXPORTS = (
     "dmuon_plan_costs", "dmuon_launch_count",
     "dmuon_selftest_wait_timeout", "dmuon_momentum_norm_noalloc", "dmuon_assign_owners", "dmuon_adamw_flat",
     "dmuon_head_create", "dmuon_head_workspace_bytes", "dmuon_head_bind", "dmuon_head_xent",
-    "dmuon_head_xent_backward", "dmuon_head_distill", "dmuon_head_distill_backward",
+    "dmuon_head_xent_backward", "dmuon_head_xent_backward_loss", "dmuon_head_distill", "dmuon_head_distill_backward",
     "dmuon_head_read_device_status", "dmuon_head_destroy",
     "dmuon_route_workspace_bytes", "dmuon_route_sort", "dmuon_route_dispatch", "dmuon_route_combine",
     "dmuon_route_combine_backward",
@@ -115,6 +115,7 @@ def lib():
         "dmuon_head_bind": (i32, [vp, vp, sz, vp]),
         "dmuon_head_xent": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, vp, vp]),
         "dmuon_head_xent_backward": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp]),
+        "dmuon_head_xent_backward_loss": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp]),
         "dmuon_head_distill": (i32, [vp, vp, i64, vp, i64, vp, vp, i32, f32, i64, vp, vp, vp]),
         "dmuon_head_distill_backward": (i32, [vp, vp, i64, vp, i64, vp, vp, i32, f32, i64, vp, vp, vp, i64, vp, i64,
                                               vp]),
@@ -488,10 +489,14 @@ class Head:
 
         return _run(self, call, stream, hidden, *tensors, scratch=self.workspace)
 
-    def _backward(self, fn, hidden, weight, args, lse, grad_loss, dhidden, dweight, stream, *tensors):
+    def _backward(self, fn, hidden, weight, args, lse, grad_loss, dhidden, dweight, stream, *tensors, loss=None):
         n = hidden.shape[0]
         f32, dev = _t().float32, self.device
-        args += (n, _flat(lse, (n,), f32, "lse", dev), _flat(grad_loss, (n,), f32, "grad_loss", dev))
+        args += (n, _flat(lse, (n,), f32, "lse", dev))
+        if loss is not None:
+            args += (_flat(loss, (n,), f32, "loss", dev),)
+            tensors += (loss,)
+        args += (_flat(grad_loss, (n,), f32, "grad_loss", dev),)
 
         def call(s):
             dh, ph, lh = self._grad(hidden, dhidden, "dhidden")
@@ -523,11 +528,14 @@ class Head:
         y = _flat(targets, hidden.shape[:1], _t().int64, "targets", self.device)
         return self._forward(lib().dmuon_head_xent, hidden, (*self._inputs(hidden, weight), y), stream, weight, targets)
 
-    def xent_backward(self, hidden, weight, targets, lse, grad_loss, *, dhidden=True, dweight=True, stream=None):
-        """(dhidden, dweight) of sum(grad_loss * loss). Either may be a tensor to write into, or False."""
+    def xent_backward(self, hidden, weight, targets, lse, grad_loss, *, loss=None, dhidden=True, dweight=True,
+                      stream=None):
+        """(dhidden, dweight) of sum(grad_loss * loss). Either may be a tensor to write into, or False. With ``loss``
+        as xent returned it, the gradients of tokens predicted with near certainty are exact too."""
         y = _flat(targets, hidden.shape[:1], _t().int64, "targets", self.device)
-        return self._backward(lib().dmuon_head_xent_backward, hidden, weight, (*self._inputs(hidden, weight), y), lse,
-                              grad_loss, dhidden, dweight, stream, targets)
+        fn = lib().dmuon_head_xent_backward if loss is None else lib().dmuon_head_xent_backward_loss
+        return self._backward(fn, hidden, weight, (*self._inputs(hidden, weight), y), lse, grad_loss, dhidden, dweight,
+                              stream, targets, loss=loss)
 
     def distill(self, hidden, weight, top_ids, top_logits, temperature=1.0, *, stream=None):
         """(loss, lse) per token against a teacher's top logits; ids int64 and logits fp32, both [tokens, top]."""

@@ -73,14 +73,14 @@ class Xent(torch.autograd.Function):
     def forward(ctx, hidden, weight, head, targets):
         loss, lse = head.xent(hidden, weight, targets)
         ctx.head = head
-        ctx.save_for_backward(hidden, weight, targets, lse)
+        ctx.save_for_backward(hidden, weight, targets, lse, loss)
         return loss
 
     @staticmethod
     @first_derivative
     def backward(ctx, grad):
-        hidden, weight, targets, lse = ctx.saved_tensors
-        return (*ctx.head.xent_backward(hidden, weight, targets, lse, grad.contiguous()), None, None)
+        hidden, weight, targets, lse, loss = ctx.saved_tensors
+        return (*ctx.head.xent_backward(hidden, weight, targets, lse, grad.contiguous(), loss=loss), None, None)
 
 
 class Distill(torch.autograd.Function):

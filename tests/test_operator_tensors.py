@@ -79,7 +79,7 @@ def world(monkeypatch):
 def tensors():
     bf16, i64, i32 = torch.bfloat16, torch.int64, torch.int32
     return dict(h=stand(6, 16, dtype=bf16), w=stand(40, 16, dtype=bf16), y=stand(6, dtype=i64), lse=stand(6),
-                g=stand(6), ids=stand(6, 4, dtype=i64), lg=stand(6, 4), dh=stand(6, 16, dtype=bf16),
+                loss=stand(6), g=stand(6), ids=stand(6, 4, dtype=i64), lg=stand(6, 4), dh=stand(6, 16, dtype=bf16),
                 dw=stand(40, 16, dtype=bf16), experts=stand(6, 2, dtype=i64), x=stand(6, 16, dtype=bf16),
                 ys=stand(12, 16, dtype=bf16), wts=stand(6, 2), dest=stand(6, 2, dtype=i32),
                 source=stand(12, dtype=i32))
@@ -95,6 +95,9 @@ CALLS = {
     "xent_backward": (("h", "w", "y", "lse", "g", "dh", "dw"),
                       lambda o, t, s: o[0].xent_backward(t["h"], t["w"], t["y"], t["lse"], t["g"], dhidden=t["dh"],
                                                          dweight=t["dw"], stream=s)),
+    "xent_backward_loss": (("h", "w", "y", "lse", "g", "loss"),
+                           lambda o, t, s: o[0].xent_backward(t["h"], t["w"], t["y"], t["lse"], t["g"],
+                                                              loss=t["loss"], stream=s)),
     "distill": (("h", "w", "ids", "lg"), lambda o, t, s: o[0].distill(t["h"], t["w"], t["ids"], t["lg"], 2.0,
                                                                       stream=s)),
     "distill_backward": (("h", "w", "ids", "lg", "lse", "g", "dh", "dw"),
