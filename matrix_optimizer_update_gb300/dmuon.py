@@ -366,37 +366,40 @@ def _refuse(msg: str):
 
 
 def _current_device() -> int:
-    return _t()._C._cuda_getDevice()
-
-
-def _at(t, device, name):
-    """Refuse a tensor of another device than the object's (None: not bound, which the library refuses)."""
-    if device is not None and t.get_device() != device:
-        _refuse(f"{name} is on cuda:{t.get_device()}, what takes it on cuda:{device}")
-
-
-def _rows(t, dim, dtype, name, device, rows=None):
-    """A CUDA matrix whose rows lie contiguous (any row pitch); returns that pitch."""
-    shape = t.shape
-    if not (t.is_cuda and t.dtype == dtype and len(shape) == 2 and shape[1] == dim and
-            (rows is None or shape[0] == rows) and (dim <= 1 or t.stride(1) == 1)):
-        _refuse(f"{name} must be a CUDA {dtype} tensor of shape [{'rows' if rows is None else rows}, {dim}] "
-                "with contiguous rows")
-    _at(t, device, name)
-    return t.stride(0) if shape[0] > 1 else -(-dim // 8) * 8
-
-
-def _flat(t, shape, dtype, name, device):
-    if not (t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
-        _refuse(f"{name} must be a contiguous CUDA {dtype} tensor of shape {list(shape)}")
-    _at(t, device, name)
-    return t.data_ptr()
+    return _torch._C._cuda_getDevice()
 
 
 def _here(device) -> int:
     """The raw handle of a device's current stream (the object torch.cuda.current_stream() makes costs more than
     a small call)."""
-    return _t()._C._cuda_getCurrentRawStream(device)
+    return _torch._C._cuda_getCurrentRawStream(device)
+
+
+def _elsewhere(t, device, name):
+    """Refuse a tensor of another device than the object's, which a caller's check has found."""
+    if device is None:
+        raise DmuonError(ERR_NOT_BOUND, "head is not bound")
+    if t.is_cuda and t.get_device() != device:
+        _refuse(f"{name} is on cuda:{t.get_device()}, what takes it on cuda:{device}")
+
+
+def _rows(t, dim, dtype, name, device, rows=None):
+    """A matrix on the object's device whose rows lie contiguous (any row pitch); returns that pitch."""
+    shape = t.shape
+    if not (t.get_device() == device and t.dtype == dtype and len(shape) == 2 and shape[1] == dim and
+            (rows is None or shape[0] == rows) and (dim <= 1 or t.stride(1) == 1)):
+        _elsewhere(t, device, name)
+        _refuse(f"{name} must be a CUDA {dtype} tensor of shape [{'rows' if rows is None else rows}, {dim}] "
+                "with contiguous rows")
+    return t.stride(0) if shape[0] > 1 else -(-dim // 8) * 8
+
+
+def _flat(t, shape, dtype, name, device):
+    """The address of a contiguous tensor on the object's device."""
+    if not (t.get_device() == device and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
+        _elsewhere(t, device, name)
+        _refuse(f"{name} must be a contiguous CUDA {dtype} tensor of shape {list(shape)}")
+    return t.data_ptr()
 
 
 def _run(owner, call, stream, *tensors, scratch=None):
@@ -404,8 +407,6 @@ def _run(owner, call, stream, *tensors, scratch=None):
     belongs to that stream. ``scratch``, the owner's workspace, and what a call with a stream of its own is given
     stay alive until the stream is done with them; other tensors on the current stream are the caller's to keep."""
     device, current = owner.device, _current_device()
-    if device is None:
-        device = current
     if stream is None:
         if current != device:
             _refuse(f"the operator is on cuda:{device}, the current device is cuda:{current}")
@@ -464,6 +465,7 @@ class Head:
 
     def bind(self, d_workspace: int, nbytes: int, stream: int = 0):
         _check(lib().dmuon_head_bind(self._h, ctypes.c_void_p(d_workspace), nbytes, ctypes.c_void_p(stream)))
+        _t()
         self.device = _current_device()
 
     def _inputs(self, hidden, weight):
@@ -588,6 +590,7 @@ class Router:
 
     def __init__(self, max_tokens, top, experts, workspace):
         self.max_tokens, self.top, self.experts, self.workspace = max_tokens, top, experts, workspace
+        _t()
         self.device = workspace.get_device()
         self.home = _here(self.device)  # raw handle of the stream the workspace was allocated on
 

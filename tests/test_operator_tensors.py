@@ -189,3 +189,11 @@ def test_given_gradients_are_looked_at_before_they_are_recorded(world, name):
         CALLS["xent_backward"][1](world.objects(), t, stream(7))
     assert e.value.status == dm.ERR_INVALID_ARG and not world.library.calls
     assert not any(hasattr(x, "seen") for x in t.values())
+
+
+def test_calls_before_a_bind_are_refused(world):
+    head = dm.Head(None, 6, 40, 16, 4)
+    for name in ("xent", "xent_backward", "distill", "distill_backward"):
+        with pytest.raises(dm.DmuonError) as e:
+            CALLS[name][1]((head, None), tensors(), None)
+        assert e.value.status == dm.ERR_NOT_BOUND
