@@ -469,7 +469,10 @@ typedef struct dmuon_head_s* dmuon_head_t;
 /*
  * dmuon_head_create - host only. 1 <= max_tokens <= 2^20, 1 <= vocab <= 2^22,
  * 1 <= dim <= 2^16; max_top (0..256) is the longest teacher list a
- * distillation call may pass (0: none).
+ * distillation call may pass (0: none). The backward pass works through the
+ * vocabulary in pieces of about 2^28 / max_tokens entries (256 at least), two
+ * launches each, however few tokens a call has: a head made for the lengths it
+ * is called with is faster than one made for many more.
  */
 dmuon_status dmuon_head_create(int64_t max_tokens, int64_t vocab, int64_t dim, int32_t max_top, dmuon_head_t* out);
 

@@ -13,7 +13,7 @@
 //          dW = dz^T H (K = the tokens), one list of tiles.
 // With many tokens each is bound by the tensor cores (a pair's tile moves 32 KB of operands per SM for 4.2
 // MFLOP), and in long runs by the power limit. 2048 tokens x 32000 x 2048, alone: logits 145 us (1.85 PFLOP/s),
-// dz 152 us (1.77), grads 271 us (1.98).
+// dz 152 us (1.77), grads 271 to 278 us (1.93 to 1.98).
 // With up to 128 tokens each is bound by reading W or writing dW. 64 tokens x 128000 x 4096: logits 165 us
 // (6.35 TB/s), dz 170 us, dW alone 152 us, dH alone 168 us, both 345 us (6.1 TB/s).
 //
@@ -307,11 +307,11 @@ __device__ __forceinline__ float& cell(float* sm, int row, int col) { return sm[
 // visit(value, share, known, pos, again), `known` the logit of a likely entry (the token's loss, where the call has
 // those), `again` when the entry before had the same id. A lane's entries may be many:
 // frequent words lie together in many vocabularies. (With the values left in registers, where an entry takes a
-// compare for each of 32, and one after another over a warp's tokens, 48 lists of 68 entries against 9328 x 1616
-// made a call of 304 us; this way 87.)
+// compare for each of 32, and one after another over a warp's tokens, both passes over 48 lists of 68 entries against
+// 9328 x 1616 take 300 us; this way 81, and 74 with what follows.)
 //
 // Four entries are loaded together: a load of one each is a chain of trips to the L2, for the shared memory that
-// the tiles take leaves an L1 too small for the warps' lists (242 lists of 39 against 9800 x 1056: 82 -> 67 us).
+// the tiles take leaves an L1 too small for the warps' lists (242 lists of 39 against 9800 x 1056: 92 -> 77 us).
 template <bool WITH_LOGIT, class Visit>
 __device__ __forceinline__ void walk(const LogitParams& p, int64_t t, Cursor& c, int first, int end, float* sm,
                                      int lane, Visit&& visit) {
