@@ -523,7 +523,8 @@ dmuon_status dmuon_head_xent(dmuon_head_t head, const void* hidden, int64_t ld_h
  * z is formed again, piece by piece, and dz is rounded to bf16 once (of up to
  * 64 tokens: to the sum of two bf16), as the operand of two tensor-core
  * products that accumulate in fp32 over the whole vocabulary (dH) and all
- * tokens (dW).
+ * tokens (dW). (What truncation takes there, at most about 2e-9 for each term
+ * summed, is not put back: below the result's rounding up to a million terms.)
  */
 dmuon_status dmuon_head_xent_backward(dmuon_head_t head, const void* hidden, int64_t ld_hidden, const void* weight,
                                       int64_t ld_weight, const int64_t* targets, int64_t tokens, const float* lse,
