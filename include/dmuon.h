@@ -654,6 +654,98 @@ dmuon_status dmuon_route_combine_backward(const void* dy, int64_t ld_dy, const v
                                           const int32_t* dest, const int32_t* source, int64_t tokens, int32_t top,
                                           int64_t dim, int32_t dtype, void* dys, float* dweights, void* stream);
 
+/*
+ * ---- A mixture's experts for a few tokens
+ *
+ * What generating with a mixture-of-experts layer needs between its router and
+ * its output, in two launches and without the rows in expert order: for
+ * assignment i = t*top + k, which sends token t to expert e = expert_ids[i],
+ *
+ *   h[i] = silu(G_e x_t) * (U_e x_t)      without a gate: silu(U_e x_t)
+ *   y[t] = sum_k weights[i] * D_e h[i]    silu(v) = v / (1 + exp(-v))
+ *
+ * An id outside 0..experts-1 marks an assignment that adds nothing, whatever its
+ * weight; a token without others gets zeros. A token may name an expert more
+ * than once. Only the matrices of experts that are named are read, each once
+ * for up to 32 assignments. Sums are fp32; h is held as the sum of two bf16, so
+ * that y has the one rounding of its type.
+ *
+ * For tokens * top <= 4096, and made for far fewer: what it costs is the reading
+ * of the experts' matrices. With more tokens the experts' own products between
+ * dmuon_route_dispatch and dmuon_route_combine use the tensor cores better.
+ *
+ * Asynchronous on stream, no allocation, deterministic. Pointers and stream are
+ * of the current device; the calls hold no handle to compare it with.
+ */
+
+/* Bytes of scratch dmuon_experts_forward needs for up to these sizes (host only):
+ * 0 <= tokens, 1 <= top <= 64, tokens*top <= 4096, 1 <= experts <= 4096, 1 <= dim, inner <= 2^20. */
+dmuon_status dmuon_experts_workspace_bytes(int64_t tokens, int32_t top, int32_t experts, int64_t dim, int64_t inner,
+                                           size_t* bytes);
+
+/*
+ * dmuon_experts_forward
+ *  x           device, tokens x dim bf16, row pitch ld_x.
+ *  expert_ids  device, tokens x top int64, contiguous;  weights  the same, fp32.
+ *  up, gate    device, experts x inner x dim bf16, contiguous; gate may be NULL.
+ *  down        device, experts x dim x inner bf16, contiguous.
+ *  y           device, tokens x dim bf16, row pitch ld_y.
+ *  d_workspace device scratch, 256-byte aligned, its contents need not be
+ *              initialised; free again when the call's work is done.
+ * Any dim and inner: rows that start on 16 bytes and are whole 16-byte pieces
+ * are read 16 bytes at a time, others element by element. The output must not
+ * overlap an input.
+ */
+dmuon_status dmuon_experts_forward(const void* x, int64_t ld_x, const int64_t* expert_ids, const float* weights,
+                                   int64_t tokens, int32_t top, int32_t experts, int64_t dim, int64_t inner,
+                                   const void* up, const void* gate, const void* down, void* y, int64_t ld_y,
+                                   void* d_workspace, size_t bytes, void* stream);
+
+/*
+ * ---- The global gradient norm, and clipping
+ *
+ * Over all tensors of a call, as a training step takes it before its optimizers:
+ *
+ *   norm   = sqrt(sum over all elements of x^2)
+ *   out[i] = grads[i] * min(1, max_norm / norm)
+ *
+ * Squares are summed in fp32 per vector and unit and in 64 bits beyond; where
+ * they leave the range of fp32 (gradients of 1e-30 or 1e30), in 64 bits
+ * throughout. A norm that is infinite or NaN clips nothing: the gradients stay
+ * (out becomes a copy of them), and norm says so. Elements are multiplied in
+ * fp32 and rounded once.
+ *
+ *  grads    host array of n device pointers; each tensor is contiguous and
+ *           aligned to its elements, which is enough.
+ *  counts   host array of n: elements of each tensor (0: none, the pointer is
+ *           not looked at).
+ *  dtypes   host array of n: DMUON_F32 or DMUON_BF16.
+ *  n        0..2^20. (norm is 0 where there are no elements.)
+ *  norm     device, one float: the norm before clipping.
+ *  d_workspace  device scratch, 256-byte aligned, its contents need not be
+ *           initialised; free again when the call's work is done.
+ *
+ * The arrays are read before the call returns. Asynchronous on stream, no
+ * allocation, deterministic. Pointers and stream are of the current device.
+ */
+
+/* Bytes of scratch the two calls need, whatever the tensors (host only). */
+dmuon_status dmuon_clip_workspace_bytes(size_t* bytes);
+
+/* dmuon_grad_norm - the norm alone. A tensor that is named twice counts twice. */
+dmuon_status dmuon_grad_norm(const void* const* grads, const int64_t* counts, const int32_t* dtypes, int32_t n,
+                             float* norm, void* d_workspace, size_t bytes, void* stream);
+
+/*
+ * dmuon_grad_clip - the norm, and the clipped gradients.
+ *  out       host array of n device pointers of the gradients' types: out[i] may
+ *            be grads[i] (in place) and must not overlap any other tensor of
+ *            the call. In place nothing is written where nothing is clipped.
+ *  max_norm  >= 0; infinity clips nothing.
+ */
+dmuon_status dmuon_grad_clip(const void* const* grads, void* const* out, const int64_t* counts, const int32_t* dtypes,
+                             int32_t n, float max_norm, float* norm, void* d_workspace, size_t bytes, void* stream);
+
 /* Free the host-side plan (the workspace stays the caller's). NULL is a no-op. */
 void dmuon_plan_destroy(dmuon_plan_t plan);
 

@@ -56,6 +56,8 @@ EXPORTS = (
     "dmuon_head_read_device_status", "dmuon_head_destroy",
     "dmuon_route_workspace_bytes", "dmuon_route_sort", "dmuon_route_dispatch", "dmuon_route_combine",
     "dmuon_route_combine_backward",
+    "dmuon_experts_workspace_bytes", "dmuon_experts_forward",
+    "dmuon_clip_workspace_bytes", "dmuon_grad_norm", "dmuon_grad_clip",
     "dmuon_plan_destroy", "dmuon_last_error", "dmuon_version",
 )
 
@@ -126,6 +128,11 @@ def lib():
         "dmuon_route_dispatch": (i32, [vp, i64, vp, vp, i64, i32, i64, i32, vp, vp]),
         "dmuon_route_combine": (i32, [vp, vp, vp, i64, i32, i64, i32, vp, i64, vp]),
         "dmuon_route_combine_backward": (i32, [vp, i64, vp, vp, vp, vp, i64, i32, i64, i32, vp, vp, vp]),
+        "dmuon_experts_workspace_bytes": (i32, [i64, i32, i32, i64, i64, ctypes.POINTER(sz)]),
+        "dmuon_experts_forward": (i32, [vp, i64, vp, vp, i64, i32, i32, i64, i64, vp, vp, vp, vp, i64, vp, sz, vp]),
+        "dmuon_clip_workspace_bytes": (i32, [ctypes.POINTER(sz)]),
+        "dmuon_grad_norm": (i32, [vp, vp, vp, i32, vp, vp, sz, vp]),
+        "dmuon_grad_clip": (i32, [vp, vp, vp, vp, i32, f32, vp, vp, sz, vp]),
         "dmuon_plan_destroy": (None, [vp]),
         "dmuon_last_error": (ctypes.c_char_p, []),
         "dmuon_version": (i32, []),
@@ -683,3 +690,123 @@ class Router:
     def dispatch_backward(self, dxs, route, *, stream=None):
         """dx [tokens, dim]: the gradient of dispatch, the sum of each token's rows of dxs."""
         return self.combine(dxs, None, route, stream=stream)
+
+
+class Experts:
+    """A mixture's experts for a few tokens, from the router's ids and weights to the layer's output.
+
+    For up to ``max_tokens`` tokens with ``top`` experts each (together at most
+    4096 assignments), beside ``Router``, which serves many tokens and training.
+    Holds the scratch of a call (torch-allocated; one call uses it at a time).
+    All tensors lie on the scratch's device, which is the current one or the
+    stream's. See include/dmuon.h for the formulas.
+    """
+
+    def __init__(self, max_tokens, top, experts, dim, inner, workspace):
+        self.max_tokens, self.top, self.experts, self.dim, self.inner = max_tokens, top, experts, dim, inner
+        self.workspace = workspace
+        _t()
+        self.device = workspace.get_device()
+        self.home = _here(self.device)  # raw handle of the stream the workspace was allocated on
+
+    @classmethod
+    def create(cls, max_tokens, top, experts, dim, inner, *, device=None):
+        sizes = int(max_tokens), int(top), int(experts), int(dim), int(inner)
+        n = ctypes.c_size_t()
+        _check(lib().dmuon_experts_workspace_bytes(*sizes, ctypes.byref(n)))
+        return cls(*sizes, _t().empty(n.value, dtype=_t().uint8, device=device or "cuda"))
+
+    def forward(self, x, expert_ids, weights, up, down, *, gate=None, stream=None):
+        """y [tokens, dim] of x [tokens, dim]; expert_ids int64 and weights fp32 [tokens, top], an id outside
+        0..experts-1 adds nothing; up and gate bf16 [experts, inner, dim], down [experts, dim, inner]."""
+        bf16, dev, dim = _t().bfloat16, self.device, self.dim
+        t = x.shape[0]
+        if t > self.max_tokens:
+            _refuse(f"x has {t} tokens, more than max_tokens ({self.max_tokens})")
+        ld = _rows(x, dim, bf16, "x", dev)
+        ids = _flat(expert_ids, (t, self.top), _t().int64, "expert_ids", dev)
+        w = _flat(weights, (t, self.top), _t().float32, "weights", dev)
+        wide = (self.experts, self.inner, dim)
+        pu = _flat(up, wide, bf16, "up", dev)
+        pg = None if gate is None else _flat(gate, wide, bf16, "gate", dev)
+        pd = _flat(down, (self.experts, dim, self.inner), bf16, "down", dev)
+
+        def call(s):
+            y = _t().empty((t, dim), dtype=bf16, device=x.device)
+            ws = self.workspace
+            _check(lib().dmuon_experts_forward(x.data_ptr(), ld, ids, w, t, self.top, self.experts, dim, self.inner, pu,
+                                               pg, pd, y.data_ptr(), dim, ws.data_ptr(), ws.numel(), s))
+            return y
+
+        return _run(self, call, stream, x, expert_ids, weights, up, down, gate, scratch=self.workspace)
+
+
+class GradClip:
+    """The global norm of many gradient tensors, and their clipping.
+
+    Holds the sums' scratch (torch-allocated; one call uses it at a time).
+    Gradients are contiguous bf16 or fp32 tensors on the scratch's device, which
+    is the current one or the stream's. See include/dmuon.h.
+    """
+
+    def __init__(self, workspace):
+        self.workspace = workspace
+        _t()
+        self.device = workspace.get_device()
+        self.home = _here(self.device)  # raw handle of the stream the workspace was allocated on
+
+    @classmethod
+    def create(cls, *, device=None):
+        n = ctypes.c_size_t()
+        _check(lib().dmuon_clip_workspace_bytes(ctypes.byref(n)))
+        return cls(_t().empty(n.value, dtype=_t().uint8, device=device or "cuda"))
+
+    def _table(self, tensors, name):
+        """Arrays of the tensors' addresses, element counts and types."""
+        torch, device = _t(), self.device
+        kinds = {torch.bfloat16: BF16, torch.float32: F32}
+        n = len(tensors)
+        try:
+            types = (ctypes.c_int32 * n)(*[kinds[t.dtype] for t in tensors])
+        except KeyError:
+            _refuse(f"{name} must be bf16 or fp32 tensors")
+        for t in tensors:
+            if t.get_device() != device or not t.is_contiguous():
+                _elsewhere(t, device, name)
+                _refuse(f"{name} must be contiguous CUDA tensors")
+        return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]),
+                (ctypes.c_int64 * n)(*[t.numel() for t in tensors]), types)
+
+    def norm(self, grads, *, stream=None):
+        """The 2-norm over all elements of all tensors: an fp32 tensor without dimensions."""
+        grads = list(grads)
+        ptrs, counts, types = self._table(grads, "grads")
+
+        def call(s):
+            norm = _t().empty((), dtype=_t().float32, device=self.workspace.device)
+            ws = self.workspace
+            _check(lib().dmuon_grad_norm(ptrs, counts, types, len(grads), norm.data_ptr(), ws.data_ptr(), ws.numel(), s))
+            return norm
+
+        return _run(self, call, stream, *grads, scratch=self.workspace)
+
+    def clip(self, grads, max_norm, *, out=None, stream=None):
+        """Scale the gradients by min(1, max_norm / norm), in place or into the tensors ``out``; returns the norm
+        before that, as ``norm`` does. A norm that is not finite clips nothing."""
+        grads = list(grads)
+        ptrs, counts, types = self._table(grads, "grads")
+        to, results = ptrs, []
+        if out is not None:
+            results = list(out)
+            if [(t.shape, t.dtype) for t in results] != [(t.shape, t.dtype) for t in grads]:
+                _refuse("out must have the gradients' shapes and types")
+            to = self._table(results, "out")[0]
+
+        def call(s):
+            norm = _t().empty((), dtype=_t().float32, device=self.workspace.device)
+            ws = self.workspace
+            _check(lib().dmuon_grad_clip(ptrs, to, counts, types, len(grads), float(max_norm), norm.data_ptr(),
+                                         ws.data_ptr(), ws.numel(), s))
+            return norm
+
+        return _run(self, call, stream, *grads, *results, scratch=self.workspace)
