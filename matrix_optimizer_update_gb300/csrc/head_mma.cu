@@ -140,8 +140,9 @@ __device__ __forceinline__ void tma_prefetch_2d(const void* map, int x, int y) {
 }
 
 // Arrive on an mbarrier of either CTA of the pair (cluster address). What it orders are this thread's own
-// reads (a ring slot, TMEM) before the arrival, for which the scope of the CTA is enough; with the scope of the
-// cluster the arrival waits for every store in flight, which took 2300 of the 5900 cycles of a dW tile.
+// reads before the arrival, whose values it must hold by then (TMEM: wait::ld; a ring slot: see take()), as the scope
+// of the CTA orders nothing for the other CTA. With the scope of the cluster the arrival waits for every store in
+// flight, which took 2300 of the 5900 cycles of a dW tile.
 __device__ __forceinline__ void arrive_pair(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -732,7 +733,11 @@ __device__ __forceinline__ bool take(Shared* sh, uint32_t j, int& w, uint32_t le
   if (!ptx::mbar_wait_cluster(&sh->ring_full[slot], (j / kRing) & 1u, abortf, p.status, kWaitNs)) return false;
   w = *reinterpret_cast<volatile int*>(&sh->ring[slot]);
   if (arm) ptx::mbar_arrive_expect_tx(&sh->ring_full[slot], 4);
-  arrive_pair(lead_empty + slot * static_cast<uint32_t>(sizeof(uint64_t)));
+  // The slot's barrier is named by way of the value (never below -1), so that the arrival cannot leave before the value
+  // is here: else the leader may write the slot's next tile first, and a warp that reads the end of the list there
+  // leaves its pair's accumulator waiting. (Seen where tiles take one K stage and the epilogue is the slower part: 128
+  // tokens x 200000 x 16.)
+  arrive_pair(lead_empty + (w < -1 ? kRing : slot) * static_cast<uint32_t>(sizeof(uint64_t)));
   return true;
 }
 
