@@ -584,6 +584,62 @@ dmuon_status dmuon_head_distill_backward(dmuon_head_t head, const void* hidden, 
                                          const float* grad_loss, void* dhidden, int64_t ld_dhidden, void* dweight,
                                          int64_t ld_dweight, void* stream);
 
+/*
+ * dmuon_head_logprobs - the log probability of each token's target, the entropy of
+ * what the model expected, and its likeliest entries (what a server returns beside
+ * a generated token, and what a policy's gradient starts from), at a temperature:
+ *
+ *   zt[t][v]   = z[t][v] / temperature
+ *   lse[t]     = log sum_v exp(zt[t][v])
+ *   logp[t]    = zt[t][targets[t]] - lse[t]
+ *   entropy[t] = - sum_v p log p,  p[t][v] = exp(zt[t][v] - lse[t])
+ *   top_ids[t], top_logp[t]: the entries with the `top` largest z, largest first (of
+ *                equal ones the lowest id first), and their log probabilities
+ *
+ *  targets   device, tokens int64, or NULL: none is given. A target outside
+ *            0..vocab-1 has the log probability 0; the rest of its token's
+ *            results are the same.
+ *  top       0..32, and not above vocab. With 0 top_ids and top_logp are not used.
+ *  tokens    0..max_tokens; 0 is a no-op.
+ *  logp, entropy, lse  device, tokens floats each.
+ *  top_ids   device, tokens x top int64;  top_logp  the same, fp32.
+ *
+ * The target's share of the sum is kept apart from the others', as in
+ * dmuon_head_xent, so that the log probability and the entropy of a token
+ * predicted with near certainty keep their leading digits (other entries' log
+ * probabilities are off by about 1e-6 of their logit). Neighbours among the top
+ * entries that are too near to tell in fp32 are put in order by sums with twice its
+ * digits. A row whose logits are not finite has unspecified top entries (ids
+ * within the vocabulary or -1).
+ * Where alternatives are asked for, the logits of a piece of the vocabulary (512
+ * MB of them) lie in the workspace at a time.
+ * Asynchronous on stream, no allocation, deterministic.
+ */
+dmuon_status dmuon_head_logprobs(dmuon_head_t head, const void* hidden, int64_t ld_hidden, const void* weight,
+                                 int64_t ld_weight, const int64_t* targets, float temperature, int32_t top,
+                                 int64_t tokens, float* logp, float* entropy, float* lse, int64_t* top_ids,
+                                 float* top_logp, void* stream);
+
+/*
+ * dmuon_head_logprobs_backward - gradients of
+ * sum_t grad_logp[t] * logp[t] + grad_entropy[t] * entropy[t]:
+ *
+ *   dz[t][v] = (grad_logp[t] * ([v == targets[t]] - p[t][v])
+ *               - grad_entropy[t] * p[t][v] * (log p[t][v] + entropy[t])) / temperature
+ *
+ *  targets, temperature  as the forward call had them.
+ *  logp, entropy, lse    device, tokens floats, as dmuon_head_logprobs wrote
+ *             them (logp may be NULL where targets is).
+ *  grad_logp, grad_entropy  device, tokens floats, or NULL: zeros. grad_logp is
+ *             not used of tokens without a target.
+ * The rest as dmuon_head_xent_backward.
+ */
+dmuon_status dmuon_head_logprobs_backward(dmuon_head_t head, const void* hidden, int64_t ld_hidden, const void* weight,
+                                          int64_t ld_weight, const int64_t* targets, float temperature, int64_t tokens,
+                                          const float* logp, const float* entropy, const float* lse,
+                                          const float* grad_logp, const float* grad_entropy, void* dhidden,
+                                          int64_t ld_dhidden, void* dweight, int64_t ld_dweight, void* stream);
+
 /* As dmuon_read_device_status, for the head's status word (DMUON_DEV_WAIT_TIMEOUT). */
 dmuon_status dmuon_head_read_device_status(dmuon_head_t head, void* stream, uint32_t* bits);
 

@@ -52,7 +52,8 @@ struct dmuon_head_s {
   int32_t max_top = 0;
   int64_t piece = 0;   // vocabulary entries per piece of the backward pass, a multiple of kPieceStep
   size_t off_status = 0, off_parts = 0, off_picked = 0, off_ids = 0, off_q = 0, off_count = 0, off_entropy = 0,
-         off_dz = 0, off_acc = 0, bytes = 0;
+         off_dz = 0, off_acc = 0, off_folds = 0, off_list = 0, bytes = 0;
+  int64_t z_bytes = 0;  // at off_dz: dz of the backward pass, logits of a scoring call
   char* ws = nullptr;
   int device = -1, pairs = 0;
 
@@ -93,16 +94,32 @@ dmuon_status check_call(dmuon_head_t H, const void* hidden, int64_t ld_hidden, c
   return st;
 }
 
-// The loss of a call: targets (cross entropy) or a teacher's lists (distillation).
+// The loss of a call: targets (cross entropy), a teacher's lists (distillation), or what is sent back to the log
+// probabilities of targets and the entropies (policy; without targets, to the entropies alone).
 struct Loss {
   const int64_t* targets = nullptr;
   const int64_t* top_ids = nullptr;
   const float* top_logits = nullptr;
   int32_t top = 0;
   float temperature = 1.f;
+  bool policy = false;
+  const float* entropy = nullptr;
+  const float* grad_entropy = nullptr;
 };
 
+dmuon_status check_temperature(float temperature) {
+  if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature))
+    return refuse(DMUON_ERR_INVALID_ARG, "temperature must be positive and finite");
+  return DMUON_OK;
+}
+
 dmuon_status check_loss(dmuon_head_t H, const Loss& L, int64_t tokens, bool distill) {
+  if (L.policy) {
+    if (misaligned(L.targets, 8)) return refuse(DMUON_ERR_INVALID_ARG, "targets is not 8-byte aligned");
+    if (tokens > 0 && (L.entropy == nullptr || misaligned(L.entropy, 4) || misaligned(L.grad_entropy, 4)))
+      return refuse(DMUON_ERR_INVALID_ARG, "entropy is NULL, or it or grad_entropy is not 4-byte aligned");
+    return check_temperature(L.temperature);
+  }
   if (!distill) {
     if (tokens > 0 && (L.targets == nullptr || misaligned(L.targets, 8)))
       return refuse(DMUON_ERR_INVALID_ARG, "targets is NULL or not 8-byte aligned");
@@ -110,8 +127,8 @@ dmuon_status check_loss(dmuon_head_t H, const Loss& L, int64_t tokens, bool dist
   }
   if (L.top < 1 || L.top > H->max_top)
     return refuse(DMUON_ERR_INVALID_ARG, "top (%d) must be between 1 and max_top (%d)", L.top, H->max_top);
-  if (!(L.temperature > 0.f) || !std::isfinite(L.temperature) || !std::isfinite(1.f / L.temperature))
-    return refuse(DMUON_ERR_INVALID_ARG, "temperature must be positive and finite");
+  const dmuon_status st = check_temperature(L.temperature);
+  if (st != DMUON_OK) return st;
   if (tokens > 0 && (L.top_ids == nullptr || L.top_logits == nullptr || misaligned(L.top_ids, 8) ||
                      misaligned(L.top_logits, 4)))
     return refuse(DMUON_ERR_INVALID_ARG, "top_ids or top_logits is NULL or not aligned to its elements");
@@ -123,7 +140,7 @@ dmuon_status prepare_wanted(dmuon_head_t H, const Loss& L, int64_t tokens, const
                             head::Wanted* w, cudaStream_t s) {
   *w = head::Wanted{};
   w->vocab = static_cast<int32_t>(H->vocab);
-  if (L.targets != nullptr) {
+  if (L.targets != nullptr || L.policy) {
     w->targets = L.targets;
     w->top = 1;
     return DMUON_OK;
@@ -212,7 +229,7 @@ dmuon_status backward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, con
       return cuda_refuse(e, "clearing dweight");
     return ok();
   }
-  if (lse == nullptr || grad_loss == nullptr || misaligned(lse, 4) || misaligned(grad_loss, 4))
+  if (lse == nullptr || (grad_loss == nullptr && !L.policy) || misaligned(lse, 4) || misaligned(grad_loss, 4))
     return refuse(DMUON_ERR_INVALID_ARG, "lse or grad_loss is NULL or not 4-byte aligned");
   if (dhidden == nullptr && dweight == nullptr) return ok();
   head::LogitParams p = logit_params(H, hidden, ld_hidden, weight, ld_weight, tokens, L);
@@ -220,6 +237,8 @@ dmuon_status backward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, con
   p.lse = lse;
   p.loss = losses;
   p.grad = grad_loss;
+  p.entropy = L.entropy;
+  p.grad_entropy = L.grad_entropy;
   p.dz = reinterpret_cast<head::bf16*>(H->ws + H->off_dz);
   p.ld_dz = H->piece;
   head::GradParams g{};
@@ -232,7 +251,7 @@ dmuon_status backward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, con
   g.dim = p.in.dim;
   g.dz = p.dz;
   g.ld_dz = p.ld_dz;
-  g.gscale = L.temperature;
+  g.gscale = L.policy ? 1.f / L.temperature : L.temperature;  // of distillation, temperature^2 / temperature
   g.slices = head::dh_slices(tokens, H->dim, std::min(H->piece, H->vocab), dweight != nullptr, H->pairs);
   const bool direct = H->vocab <= H->piece && g.slices.count == 1 && !head::thin_tokens(tokens);
   if (dhidden != nullptr && direct) {
@@ -255,6 +274,94 @@ dmuon_status backward(dmuon_head_t H, const void* hidden, int64_t ld_hidden, con
       (e = head::launch_round(g.dh_acc, g.slices.count, tokens, g.dim, g.gscale, H->pipe().gmax,
                               static_cast<head::bf16*>(dhidden), ld_dhidden, s)) != cudaSuccess)
     return cuda_refuse(e, "rounding kernel");
+  return ok();
+}
+
+// Scores: log probabilities, entropies and log sums, and the largest logits. Where those are asked for, the logits
+// of as many entries as the workspace holds are written at a time, and the largest chosen from them.
+dmuon_status score(dmuon_head_t H, const void* hidden, int64_t ld_hidden, const void* weight, int64_t ld_weight,
+                   const int64_t* targets, float temperature, int32_t top, int64_t tokens, float* logp, float* entropy,
+                   float* lse, int64_t* top_ids, float* top_logp, void* stream) {
+  dmuon_status st = check_call(H, hidden, ld_hidden, weight, ld_weight, tokens);
+  if (st == DMUON_OK) st = check_temperature(temperature);
+  if (st != DMUON_OK) return st;
+  if (top < 0 || top > head::kMaxAlternatives || top > H->vocab)
+    return refuse(DMUON_ERR_INVALID_ARG, "top (%d) must be between 0 and %d and not above vocab", top,
+                  head::kMaxAlternatives);
+  if (misaligned(targets, 8)) return refuse(DMUON_ERR_INVALID_ARG, "targets is not 8-byte aligned");
+  if (tokens == 0) return ok();
+  if (logp == nullptr || entropy == nullptr || lse == nullptr || misaligned(logp, 4) || misaligned(entropy, 4) ||
+      misaligned(lse, 4))
+    return refuse(DMUON_ERR_INVALID_ARG, "logp, entropy or lse is NULL or not 4-byte aligned");
+  if (top > 0 && (top_ids == nullptr || top_logp == nullptr || misaligned(top_ids, 8) || misaligned(top_logp, 4)))
+    return refuse(DMUON_ERR_INVALID_ARG, "top_ids or top_logp is NULL or not aligned to its elements");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  Loss L;
+  L.temperature = temperature;
+  head::LogitParams p = logit_params(H, hidden, ld_hidden, weight, ld_weight, tokens, L);
+  p.want.targets = targets;
+  p.want.top = 1;
+  p.want.vocab = p.vocab;
+  head::Part* parts = reinterpret_cast<head::Part*>(H->ws + H->off_parts);
+  float* folds = reinterpret_cast<float*>(H->ws + H->off_folds);
+  p.parts = parts;
+  p.folds = folds;
+  const bool thin = head::thin_tokens(tokens);
+  int64_t piece = H->vocab;
+  if (top > 0) {
+    piece = std::min(cdiv(H->vocab, kPieceStep), H->z_bytes / (4 * tokens) / kPieceStep) * kPieceStep;
+    p.z = reinterpret_cast<float*>(H->ws + H->off_dz);
+    p.ld_z = piece;
+  }
+  head::ScoreParams r{};
+  r.tokens = tokens;
+  r.vocab = p.vocab;
+  r.dot = p.in;
+  r.targets = targets;
+  r.parts = parts;
+  r.folds = folds;
+  for (int64_t v0 = 0; v0 < H->vocab; v0 += piece)
+    r.groups += head::logit_groups(tokens, std::min(piece, H->vocab - v0), H->pairs);
+  r.token_step = thin ? r.groups : 1;
+  r.group_step = thin ? 1 : tokens;
+  r.picked = p.picked;
+  r.logp = logp;
+  r.entropy = entropy;
+  r.lse = lse;
+  head::TopParams q{};
+  q.tokens = tokens;
+  q.vocab = p.vocab;
+  q.token_step = r.token_step;
+  q.group_step = r.group_step;
+  q.z = p.z;
+  q.ld_z = p.ld_z;
+  q.top = top;
+  q.list_z = reinterpret_cast<float*>(H->ws + H->off_list);
+  q.list_id = reinterpret_cast<int32_t*>(q.list_z + head::kHeld * tokens);
+  q.targets = targets;
+  q.lse = lse;
+  q.logp = logp;
+  q.dot = p.in;
+  q.top_ids = top_ids;
+  q.top_logp = top_logp;
+  p.groups = r.groups;
+  cudaError_t e;
+  for (int64_t v0 = 0; v0 < H->vocab; v0 += piece) {
+    p.v0 = q.v0 = static_cast<int32_t>(v0);
+    p.width = q.width = static_cast<int32_t>(std::min(piece, H->vocab - v0));
+    q.last = v0 + piece >= H->vocab;
+    q.first = v0 == 0;
+    if ((e = head::launch_logits(p, H->pipe(), s)) != cudaSuccess) return cuda_refuse(e, "scores kernel");
+    if (q.last && (e = head::launch_score_rows(r, s)) != cudaSuccess) return cuda_refuse(e, "rows kernel");
+    const int groups = head::logit_groups(tokens, p.width, H->pairs);
+    if (top > 0) {
+      q.parts = parts + p.group0 * r.group_step;
+      q.groups = groups;
+      q.thin_h = thin ? head::thin_tiles(p.width, H->pairs).height : 0;
+      if ((e = head::launch_top(q, s)) != cudaSuccess) return cuda_refuse(e, "alternatives kernel");
+    }
+    p.group0 += groups;
+  }
   return ok();
 }
 
@@ -283,19 +390,30 @@ extern "C" dmuon_status dmuon_head_create(int64_t max_tokens, int64_t vocab, int
     return o;
   };
   H->off_status = take(256);
-  // a call with few tokens has up to 8 groups for each 256 entries and for each pair of SMs
-  H->off_parts = take(sizeof(head::Part) * std::max(cdiv(vocab, head::kGroup) * max_tokens,
-                                                    (cdiv(vocab, 32) + 8 * kMaxPairs) *
-                                                        std::min<int64_t>(max_tokens, kFewTokens)));
+  // a call with few tokens has up to 8 groups for each 256 entries and for each pair of SMs and piece, of which a
+  // scoring call has one for each 2^20 entries (its logits' 512 MB over 128 tokens)
+  const int64_t parts = std::max(cdiv(vocab, head::kGroup) * max_tokens,
+                                 (cdiv(vocab, 32) + 8 * kMaxPairs * cdiv(vocab, int64_t(1) << 20)) *
+                                     std::min<int64_t>(max_tokens, kFewTokens));
+  H->off_parts = take(sizeof(head::Part) * parts);
   H->off_picked = take(4 * max_tokens * std::max(1, max_top));
   H->off_ids = take(4 * max_tokens * max_top);
   H->off_q = take(4 * max_tokens * max_top);
   H->off_count = take(max_top > 0 ? 4 * max_tokens : 0);
   H->off_entropy = take(max_top > 0 ? 4 * max_tokens : 0);
-  H->off_dz = take(2 * std::max(max_tokens, std::min<int64_t>(2 * max_tokens, 2 * head::kTwofold)) * H->piece);
+  // logits of a scoring call: all where they take no more than 512 MB, else as many; at least one block of entries
+  const int64_t all = 4 * max_tokens * cdiv(vocab, kPieceStep) * kPieceStep;
+  H->z_bytes = std::max({2 * std::max(max_tokens, std::min<int64_t>(2 * max_tokens, 2 * head::kTwofold)) * H->piece,
+                         std::min(all, kPieceBytes), 4 * max_tokens * kPieceStep});
+  H->off_dz = take(H->z_bytes);
   // dH's sums: one set where tokens are many; where K is cut into slices, up to 2 tiles of 256 x 256 per pair
   const int64_t row = 4 * head::acc_pitch(dim);
-  H->off_acc = take(std::max(row * max_tokens, std::min(row * max_tokens * kMaxSlices, kSliceBytes)));
+  const int64_t folds = cdiv(sizeof(float) * parts, kAlign) * kAlign;
+  const int64_t list = all > H->z_bytes ? 8 * max_tokens * head::kHeld : 0;
+  H->off_acc = take(std::max({row * max_tokens, std::min(row * max_tokens * kMaxSlices, kSliceBytes), folds + list}));
+  // in the same place, a scoring call's sums of the entropy, and the alternatives from one piece to the next
+  H->off_folds = H->off_acc;
+  H->off_list = H->off_acc + folds;
   H->bytes = at;
   *out = H;
   return ok();
@@ -393,6 +511,32 @@ extern "C" dmuon_status dmuon_head_distill_backward(dmuon_head_t H, const void* 
   L.temperature = temperature;
   return backward(H, hidden, ld_hidden, weight, ld_weight, L, true, tokens, lse, nullptr, grad_loss, dhidden,
                   ld_dhidden, dweight, ld_dweight, stream);
+}
+
+extern "C" dmuon_status dmuon_head_logprobs(dmuon_head_t H, const void* hidden, int64_t ld_hidden, const void* weight,
+                                            int64_t ld_weight, const int64_t* targets, float temperature, int32_t top,
+                                            int64_t tokens, float* logp, float* entropy, float* lse, int64_t* top_ids,
+                                            float* top_logp, void* stream) {
+  return score(H, hidden, ld_hidden, weight, ld_weight, targets, temperature, top, tokens, logp, entropy, lse, top_ids,
+               top_logp, stream);
+}
+
+extern "C" dmuon_status dmuon_head_logprobs_backward(dmuon_head_t H, const void* hidden, int64_t ld_hidden,
+                                                     const void* weight, int64_t ld_weight, const int64_t* targets,
+                                                     float temperature, int64_t tokens, const float* logp,
+                                                     const float* entropy, const float* lse, const float* grad_logp,
+                                                     const float* grad_entropy, void* dhidden, int64_t ld_dhidden,
+                                                     void* dweight, int64_t ld_dweight, void* stream) {
+  if (tokens > 0 && targets != nullptr && (logp == nullptr || misaligned(logp, 4)))
+    return refuse(DMUON_ERR_INVALID_ARG, "logp is NULL or not 4-byte aligned");
+  Loss L;
+  L.policy = true;
+  L.targets = targets;
+  L.temperature = temperature;
+  L.entropy = entropy;
+  L.grad_entropy = grad_entropy;
+  return backward(H, hidden, ld_hidden, weight, ld_weight, L, false, tokens, lse, logp, grad_logp, dhidden, ld_dhidden,
+                  dweight, ld_dweight, stream);
 }
 
 extern "C" dmuon_status dmuon_head_read_device_status(dmuon_head_t H, void* stream, uint32_t* bits) {

@@ -79,11 +79,19 @@ struct LogitParams {
   Part* parts;             // [groups][tokens]; few tokens: [tokens][groups]
   int32_t after_lists;     // the launch before this one on the stream is launch_teacher's
   float* picked;           // [tokens][want.top]: scaled logits of the wanted entries
-  int32_t v0, width;       // entries v0 .. v0 + width - 1 (forward: all)
+  int32_t v0, width;       // entries v0 .. v0 + width - 1 (forward: all, but for scores with alternatives)
+  // scores: beside parts, each group's sum of exp(z - peak) * (z - peak); logits for the choice of alternatives
+  float* folds;            // laid out as parts; nullptr: not a scoring call
+  float* z;                // [tokens][ld_z], entries from v0; or nullptr
+  int64_t ld_z;
+  int32_t groups, group0;  // few tokens: a token's groups in all, and those before this launch's
   // backward
   const float* lse;
   const float* grad;
   const float* loss;       // cross entropy: the losses, or nullptr: the targets' logits are formed again
+  // ... of log probabilities (then loss holds those) and entropies; a gradient that is nullptr is zeros
+  const float* entropy;    // [tokens]; nullptr: not such a call
+  const float* grad_entropy;
   bf16* dz;                // [tokens][ld_dz]; up to kTwofold tokens: [2][tokens][ld_dz]
   int64_t ld_dz;
 };
@@ -138,6 +146,52 @@ struct RowParams {
   float* lse;
 };
 
+// Scores: log probability, entropy and log sum of each token from its groups' sums.
+struct ScoreParams {
+  int64_t tokens;
+  int32_t vocab;
+  DotParams dot;           // the target's logit
+  const int64_t* targets;  // or nullptr: none is given
+  const Part* parts;       // as RowParams
+  const float* folds;
+  int64_t token_step, group_step;
+  int32_t groups;
+  float* picked;           // [tokens]: the targets' scaled logits
+  float* logp;
+  float* entropy;
+  float* lse;
+};
+
+// Alternatives a scoring call may ask for, and how many more are held until the order of those next to each
+// other is decided.
+constexpr int kMaxAlternatives = 32;
+constexpr int kSpare = 8;
+constexpr int kHeld = kMaxAlternatives + kSpare;
+
+// The choice of the largest logits of one piece of the vocabulary, joined with those of the pieces before.
+struct TopParams {
+  int64_t tokens;
+  int32_t vocab;
+  const Part* parts;       // of token t and the piece's group g at t * token_step + g * group_step
+  int64_t token_step, group_step;
+  int32_t groups;          // of the piece
+  int32_t thin_h;          // few tokens: entries per tile of 8 groups, else 0 (groups of kGroup)
+  int32_t v0, width;
+  const float* z;
+  int64_t ld_z;
+  int32_t top;
+  int32_t first, last;     // the first piece (no list yet), the last one (results)
+  const int64_t* targets;  // which the groups' peaks leave out; or nullptr
+  float* list_z;           // [tokens][kHeld], ids -1 where there are fewer
+  int32_t* list_id;
+  // last
+  const float* lse;
+  const float* logp;
+  DotParams dot;
+  int64_t* top_ids;        // [tokens][top]
+  float* top_logp;
+};
+
 struct TeacherParams {
   const int64_t* ids;
   const float* logits;
@@ -166,6 +220,8 @@ Slices dh_slices(int64_t tokens, int64_t dim, int64_t width, bool dweight, int p
 cudaError_t launch_grads(const GradParams& p, const Pipe& pipe, cudaStream_t s);
 cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t s);
 cudaError_t launch_rows(const RowParams& p, cudaStream_t s);
+cudaError_t launch_score_rows(const ScoreParams& p, cudaStream_t s);
+cudaError_t launch_top(const TopParams& p, cudaStream_t s);
 // out = bf16(gscale * *gmax * the sum of the slices of acc)
 cudaError_t launch_round(const float* acc, int slices, int64_t tokens, int32_t dim, float gscale, const float* gmax,
                          bf16* out, int64_t ld_out, cudaStream_t s);

@@ -24,6 +24,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include <cudaTypedefs.h>
 
@@ -57,7 +58,16 @@ constexpr float kLog2e = 1.4426950408889634f;
 // The thin forms of logits and dz turn the product round: vocabulary entries are the M side and the tokens
 // the N side, padded to 32. With 77 tokens the M = 256 side of the other form is two thirds empty, and the
 // launch is bound by products of zeros; turned round it is bound by reading W.
-enum Mode { kLogits, kDz, kGrads, kThinLogits, kThinDz, kThinGrads };
+//
+// Scores are logits with each group's part of the entropy, and with the logits themselves where alternatives are
+// asked for; policy dz is the gradient of log probabilities and entropies.
+enum Mode { kLogits, kDz, kGrads, kThinLogits, kThinDz, kThinGrads, kScore, kThinScore, kPolicyDz, kThinPolicyDz };
+template <int MODE>
+constexpr bool kIsThin = MODE == kThinLogits || MODE == kThinDz || MODE == kThinScore || MODE == kThinPolicyDz;
+template <int MODE>
+constexpr bool kIsPolicy = MODE == kPolicyDz || MODE == kThinPolicyDz;
+template <int MODE>
+constexpr bool kIsDz = MODE == kDz || MODE == kThinDz || kIsPolicy<MODE>;
 
 struct Params {
   CUtensorMap a[2], b[2];  // [1]: the second kind of tile of a grads launch (dW)
@@ -106,6 +116,14 @@ static_assert(sizeof(Shared) <= 1024, "barriers must fit their 1 KB");
 struct ThinTokens {
   float g[kThin];      // gradient relative to the largest, 0 for a token that does not count
   float lse[kThin];
+};
+
+// ... and thin policy dz, at the end of the ring's memory, which has a stage less for it where it was full.
+struct ThinPolicy {
+  float g[kThin];      // of the log probability
+  float ge[kThin];     // of the entropy
+  float lse[kThin];
+  float entropy[kThin];
 };
 
 // Instruction descriptor as ptx::idesc_bf16, with A MN-major too (bit 15).
@@ -199,11 +217,11 @@ __device__ __forceinline__ Where where_is(const Params& p, int w) {
   x.kind = 0;
   x.slice = 0;
   x.k0 = 0;
-  if (MODE == kThinLogits || MODE == kThinDz) {
+  if (kIsThin<MODE>) {
     x.row = 0;
     x.col = w;
     x.nk = p.nk;
-  } else if (MODE == kLogits || MODE == kDz) {
+  } else if (MODE == kLogits || MODE == kDz || MODE == kScore || MODE == kPolicyDz) {
     const int band = w / (kBand * p.cols);
     const int r = w - band * kBand * p.cols;
     const int high = min(kBand, p.rows - band * kBand);
@@ -299,6 +317,25 @@ __device__ __forceinline__ void target_logits(const LogitParams& p, int id, int6
 __device__ __forceinline__ float above(const LogitParams& p, float known, float lse, float share) {
   if (p.loss != nullptr) return expm1f(-known);
   return (known > lse ? 1.f : expf(known - lse)) - share;
+}
+
+// What a token's loss of log probability and entropy sends back (zeros where the call has no such gradient).
+__device__ __forceinline__ float grad_of(const LogitParams& p, int64_t t) {
+  if (p.grad == nullptr || p.want.targets == nullptr) return 0.f;
+  return counts(p.want, t) ? p.grad[t] : 0.f;
+}
+__device__ __forceinline__ float grad_entropy_of(const LogitParams& p, int64_t t) {
+  return p.grad_entropy != nullptr ? p.grad_entropy[t] : 0.f;
+}
+
+// Its dz at an entry that is not the target: e (a multiple of p) times what it takes off. Where p is 0, log p may be
+// -infinity and must not make it NaN.
+__device__ __forceinline__ float policy(float g, float ge, float entropy, float logp, float e) {
+  return -e * fmaf(ge, fmaxf(logp, -1e6f) + entropy, g);
+}
+// ... at the target, from its log probability, which has all the digits of 1 - p.
+__device__ __forceinline__ float policy_target(float g, float ge, float entropy, float logp) {
+  return -g * expm1f(logp) - ge * expf(logp) * (fmaxf(logp, -1e6f) + entropy);
 }
 
 // 32 x 32 values in shared memory, rows turned so that neither rows nor columns conflict.
@@ -399,23 +436,117 @@ __device__ __forceinline__ bool drain_logits(const LogitParams& p, float zscale,
   return true;
 }
 
-// One warp's part of a dz tile. Row t's gradient relative to the largest: g (p - wanted), rounded to bf16
-// as the operand of the gradients' products (the only rounding of dz).
+// exp(z - from) of 32 logits added up, alone and times z - from, which is what entropies are made of. The factor is
+// bounded where the exponential is 0, so that a logit of -infinity adds nothing.
+__device__ __forceinline__ void fold(const float (&v)[32], float from, float& sum, float& folded) {
+  float s[4] = {}, f[4] = {};
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const float d = v[k] - from, e = ex2(d * kLog2e);
+    s[k & 3] += e;
+    f[k & 3] = fmaf(e, fmaxf(d, -1e4f), f[k & 3]);
+  }
+  sum = (s[0] + s[1]) + (s[2] + s[3]);
+  folded = (f[0] + f[1]) + (f[2] + f[3]);
+}
+
+// One warp's part of a score tile: as drain_logits, with the entropy's sums, and with the logits stored where
+// alternatives are asked for.
 template <class Wait, class Free>
+__device__ __forceinline__ bool drain_score(const Params& P, int64_t t, int64_t t0, int j0, uint32_t tbase, int lane,
+                                            uint8_t* stg, uint32_t& nbox, Wait&& wait, Free&& free) {
+  const LogitParams& p = P.l;
+  const bool in = t < p.tokens;
+  Cursor c;
+  c.start(p.want, t, in && p.want.targets != nullptr, j0);
+  if (!wait()) return false;
+  ptx::tc_fence_after();
+  float peak = -INFINITY, sum = 0.f, folded = 0.f;
+#pragma unroll 1
+  for (int ch = 0; ch < 4; ++ch) {
+    const int jc = j0 + ch * 32;
+    float v[32];
+    ptx::tmem_ld_32x32b_x32(tbase + ch * 32, v);
+    if (ch == 3) free();
+    if (jc >= p.vocab) continue;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] *= P.zscale;
+    if (jc + 32 > p.vocab) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (jc + k >= p.vocab) v[k] = -INFINITY;
+    }
+    if (p.z != nullptr) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint8_t* box = stg + (nbox & 1u) * kBox;
+        if (lane == 0) ptx::bulk_wait_read<1>();  // the store that last read this box is done with it
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int k = h * 16 + q * 4;
+          *reinterpret_cast<float4*>(piece(box, lane, q)) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+        }
+        ptx::fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          if (t0 < p.tokens) ptx::tma_store_2d(&P.out[0], box, jc - p.v0 + h * 16, static_cast<int>(t0));
+          ptx::bulk_commit();
+        }
+        ++nbox;
+      }
+    }
+    if (__any_sync(0xffffffffu, c.id < jc + 32)) {
+      if (lane == 0) ptx::bulk_wait_read<0>();  // both boxes' place
+      __syncwarp();
+      wanted_of_row<false>(p, t, c, jc, v, reinterpret_cast<float*>(stg), lane,
+                           [&](float& x, float, float, int, bool) { x = -INFINITY; });
+      __syncwarp();
+    }
+    float top = v[0];
+#pragma unroll
+    for (int k = 1; k < 32; ++k) top = fmaxf(top, v[k]);
+    top = fmaxf(peak, top);
+    const float from = top == -INFINITY ? 0.f : top;  // nothing yet: every exponential is 0
+    float s, f;
+    fold(v, from, s, f);
+    const float shift = peak == -INFINITY ? 0.f : peak - from, r = ex2((peak - from) * kLog2e);
+    folded = fmaf(fmaf(sum, shift, folded), r, f);
+    sum = fmaf(sum, r, s);
+    peak = top;
+  }
+  if (in && j0 < p.vocab) {
+    const int64_t at = int64_t(j0 / kGroup) * p.tokens + t;
+    p.parts[at] = Part{peak, sum};
+    p.folds[at] = folded;
+  }
+  return true;
+}
+
+// One warp's part of a dz tile. Row t's gradient relative to the largest: g (p - wanted), rounded to bf16
+// as the operand of the gradients' products (the only rounding of dz). POLICY: of log probabilities and
+// entropies, g ([wanted] - p) - ge p (log p + entropy).
+template <bool POLICY, class Wait, class Free>
 __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t, int64_t t0, int j0, uint32_t tbase,
                                          int lane, uint8_t* stg, uint32_t& nbox, Wait&& wait, Free&& free) {
   const LogitParams& p = P.l;
   const bool in = t < p.tokens;
   Cursor c;
-  c.start(p.want, t, in, j0);
-  float g = 0.f, lse = 0.f;
+  c.start(p.want, t, in && (!POLICY || p.want.targets != nullptr), j0);
+  float g = 0.f, ge = 0.f, lse = 0.f, entropy = 0.f;
   if (in) {
     lse = p.lse[t];
-    g = counts(p.want, t) ? p.grad[t] / gmax : 0.f;
-    if (g == 0.f) c.id = INT_MAX;  // zeros, whatever z is
+    if (POLICY) {
+      g = grad_of(p, t) / gmax;
+      ge = grad_entropy_of(p, t) / gmax;
+      entropy = p.entropy[t];
+    } else {
+      g = counts(p.want, t) ? p.grad[t] / gmax : 0.f;
+    }
+    if (g == 0.f && ge == 0.f) c.id = INT_MAX;  // zeros, whatever z is
   }
-  target_logits(p, c.id, t, min(j0 + 128, p.vocab), lane);
-  const float g_low = g * kLow;
+  if (!POLICY) target_logits(p, c.id, t, min(j0 + 128, p.vocab), lane);
+  const float g_low = g * kLow, ge_low = ge * kLow;
   if (!wait()) return false;
   ptx::tc_fence_after();
 #pragma unroll 1
@@ -427,8 +558,14 @@ __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t,
     // a row that does not count, and entries past the vocabulary, give exact zeros whatever z is
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
-      const float e = g_low * exp_high(fmaf(v[k], P.zscale, -lse));
-      v[k] = g == 0.f ? 0.f : e;
+      const float x = fmaf(v[k], P.zscale, -lse);
+      if (POLICY) {
+        const float e = policy(g_low, ge_low, entropy, x, exp_high(x));
+        v[k] = g == 0.f && ge == 0.f ? 0.f : e;
+      } else {
+        const float e = g_low * exp_high(x);
+        v[k] = g == 0.f ? 0.f : e;
+      }
     }
     if (jc + 32 > p.vocab) {
 #pragma unroll
@@ -440,7 +577,8 @@ __device__ __forceinline__ bool drain_dz(const Params& P, float gmax, int64_t t,
       __syncwarp();
       wanted_of_row<true>(p, t, c, jc, v, reinterpret_cast<float*>(stg), lane,
                           [&](float& x, float share, float z, int, bool again) {
-                            x = share >= kSure && !again ? g * above(p, z, lse, share) : x - g * share;
+                            if (POLICY) x = policy_target(g, ge, entropy, z);
+                            else x = share >= kSure && !again ? g * above(p, z, lse, share) : x - g * share;
                           });
     }
     uint8_t* box = stg + (nbox & 1u) * kBox;
@@ -540,21 +678,97 @@ __device__ __forceinline__ bool drain_thin_logits(const Params& P, int first, in
   return true;
 }
 
-// One warp's part of a thin dz tile; dz[t][v - v0] as in the other form.
+// One warp's part of a thin score tile: as drain_thin_logits, with the entropy's sums and the logits.
 template <class Wait, class Free>
-__device__ __forceinline__ bool drain_thin_dz(const Params& P, const ThinTokens& tk, int first, int end, int half,
-                                              uint32_t tbase, int lane, float* sm, Wait&& wait, Free&& free) {
+__device__ __forceinline__ bool drain_thin_score(const Params& P, int first, int end, int group, int half,
+                                                 uint32_t tbase, int lane, float* sm, Wait&& wait, Free&& free) {
   const LogitParams& p = P.l;
   const int blocks = P.thin_n / 32;
   Cursor c[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int t = (half + 2 * i) * 32 + lane;
-    c[i].start(p.want, t, t < p.tokens && first < end && tk.g[t] != 0.f, first);
+    c[i].start(p.want, t, t < p.tokens && first < end && p.want.targets != nullptr, first);
+  }
+  if (!wait()) return false;
+  ptx::tc_fence_after();
+  const int v0 = first + lane;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int b = half + 2 * i;
+    if (b >= blocks) {
+      if (b < 2) free();  // this half has no tokens
+      break;
+    }
+    float v[32];
+    ptx::tmem_ld_32x32b_x32(tbase + b * 32, v);
+    if (b + 2 >= blocks) free();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = v0 < end ? v[k] * P.zscale : -INFINITY;
+    if (p.z != nullptr && v0 < end) {
+      float* z = p.z + int64_t(b) * 32 * p.ld_z + (v0 - p.v0);
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (b * 32 + k < p.tokens) z[k * p.ld_z] = v[k];
+    }
+    const int64_t t = b * 32 + lane;
+    wanted_of_tokens<false>(p, t, c[i], first, end, v, sm, lane,
+                            [&](float& x, float, float, int, bool) { x = -INFINITY; });
+    const float peak = columns(v, lane, [](float x, float y) { return fmaxf(x, y); });
+    const float from = peak == -INFINITY ? 0.f : peak;
+    float f[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float d = v[k] - __shfl_sync(0xffffffffu, from, k);
+      v[k] = ex2(d * kLog2e);
+      f[k] = v[k] * fmaxf(d, -1e4f);
+    }
+    const float sum = columns(v, lane, [](float x, float y) { return x + y; });
+    const float folded = columns(f, lane, [](float x, float y) { return x + y; });
+    if (t < p.tokens) {
+      const int64_t at = t * p.groups + p.group0 + group;
+      p.parts[at] = Part{peak, sum};
+      p.folds[at] = folded;
+    }
+  }
+  return true;
+}
+
+// What thin dz and thin policy dz know of a token.
+__device__ __forceinline__ bool none(const ThinTokens& tk, int t) { return tk.g[t] == 0.f; }
+__device__ __forceinline__ bool none(const ThinPolicy& tk, int t) { return tk.g[t] == 0.f && tk.ge[t] == 0.f; }
+__device__ __forceinline__ float dz_of(const ThinTokens& tk, int t, float z, float scale) {
+  return tk.g[t] * kLow * exp_high(fmaf(z, scale, -tk.lse[t]));
+}
+__device__ __forceinline__ float dz_of(const ThinPolicy& tk, int t, float z, float scale) {
+  const float x = fmaf(z, scale, -tk.lse[t]);
+  return policy(tk.g[t] * kLow, tk.ge[t] * kLow, tk.entropy[t], x, exp_high(x));
+}
+__device__ __forceinline__ float wanted_dz(const LogitParams& p, const ThinTokens& tk, int t, float x, float share, float z,
+                                           bool again) {
+  const float g = tk.g[t];
+  return share >= kSure && !again ? g * above(p, z, tk.lse[t], share) : x - g * share;
+}
+__device__ __forceinline__ float wanted_dz(const LogitParams&, const ThinPolicy& tk, int t, float, float, float logp, bool) {
+  return policy_target(tk.g[t], tk.ge[t], tk.entropy[t], logp);
+}
+
+// One warp's part of a thin dz tile; dz[t][v - v0] as in the other form.
+template <class Tokens, class Wait, class Free>
+__device__ __forceinline__ bool drain_thin_dz(const Params& P, const Tokens& tk, int first, int end, int half,
+                                              uint32_t tbase, int lane, float* sm, Wait&& wait, Free&& free) {
+  const LogitParams& p = P.l;
+  constexpr bool policy = std::is_same<Tokens, ThinPolicy>::value;
+  const int blocks = P.thin_n / 32;
+  Cursor c[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = (half + 2 * i) * 32 + lane;
+    c[i].start(p.want, t, t < p.tokens && first < end && !none(tk, t) && (!policy || p.want.targets != nullptr), first);
   }
 #pragma unroll 1  // one copy of its code: a short launch waits for its instructions, too
   for (int i = 0; i < 2; ++i)
-    target_logits(p, i == 0 ? c[0].id : c[1].id, (half + 2 * i) * 32 + lane, end, lane);
+    if (!policy) target_logits(p, i == 0 ? c[0].id : c[1].id, (half + 2 * i) * 32 + lane, end, lane);
   if (!wait()) return false;
   ptx::tc_fence_after();
 #pragma unroll
@@ -569,15 +783,13 @@ __device__ __forceinline__ bool drain_thin_dz(const Params& P, const ThinTokens&
     if (b + 2 >= blocks) free();
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
-      const float g = tk.g[b * 32 + k];
-      const float e = g * kLow * exp_high(fmaf(v[k], P.zscale, -tk.lse[b * 32 + k]));
-      v[k] = g == 0.f ? 0.f : e;
+      const float e = dz_of(tk, b * 32 + k, v[k], P.zscale);
+      v[k] = none(tk, b * 32 + k) ? 0.f : e;
     }
     const int t = b * 32 + lane;
     wanted_of_tokens<true>(p, t, c[i], first, end, v, sm, lane,
                            [&](float& x, float share, float z, int, bool again) {
-                             const float g = tk.g[t];
-                             x = share >= kSure && !again ? g * above(p, z, tk.lse[t], share) : x - g * share;
+                             x = wanted_dz(p, tk, t, x, share, z, again);
                            });
     // By way of shared memory, so that a lane stores 16 bytes: with 2 bytes a lane the number of stores shows in the
     // launch's time (both passes over 77 tokens x 50257 x 1024: 103 us, this way 99.7; with the tokens that there are not left
@@ -745,13 +957,14 @@ template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr bool thin = MODE == kThinLogits || MODE == kThinDz;
+  constexpr bool thin = kIsThin<MODE>;
   constexpr bool grads = MODE == kGrads || MODE == kThinGrads;
   constexpr int ring_bytes = MODE == kThinGrads ? kThinGradStages * 2 * kHalf : kRingBytes;
   constexpr int box_bytes = MODE == kThinGrads ? kWideBox : kBox;
   Shared* sh = reinterpret_cast<Shared*>(base + ring_bytes);
   uint8_t* boxes = base + ring_bytes + 1024;
   ThinTokens& tk = *reinterpret_cast<ThinTokens*>(boxes + kEpiWarps * 2 * kBox);  // thin dz only
+  ThinPolicy& tp = *reinterpret_cast<ThinPolicy*>(base + ring_bytes - sizeof(ThinPolicy));  // thin policy dz only
   // operand ring: fixed at compile time but for the thin logits and dz, whose stages hold fewer rows
   const uint32_t stages = thin ? p.stages : ring_bytes / (2 * kHalf);
   const uint32_t stage_bytes = thin ? p.stage_bytes : 2 * kHalf;
@@ -793,13 +1006,13 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
   const uint32_t tmem = sh->tmem;
   // Set up while the kernel before still runs: the first stages of W on their way to L2 (a hint: nothing is read
   // before that kernel is done, and what it may write to W passes through L2). 1 to 2 % of a call with few tokens.
-  if ((MODE == kThinLogits || MODE == kThinDz) && threadIdx.x == 0) {
+  if (thin && threadIdx.x == 0) {
     const int row = p.l.v0 + static_cast<int>(blockIdx.x >> 1) * p.thin_h + rank * (p.thin_h / 2);
     for (int kb = 0; kb < min(p.nk, 16); ++kb) tma_prefetch_2d(&p.b[0], kb * kStep, row);
   }
   // After the kernel that sorts the lists, which lets this one start once everything before it is done, only the
   // epilogue has to wait for it: loads and products of the first tile run beside it.
-  if (!p.l.after_lists || warp >= 2) follow(MODE != kLogits && MODE != kThinLogits);
+  if (!p.l.after_lists || warp >= 2) follow(grads || kIsDz<MODE>);
   const uint32_t lead_empty = ptx::mapa_shared(ptx::smem_u32(&sh->ring_empty[0]), 0);
 
   if (warp == 0) {
@@ -953,10 +1166,14 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
     float* sm = reinterpret_cast<float*>(stg);  // logits and thin dz: 32 x 32 values in the place of boxes
     static_assert(2 * kBox == 32 * 32 * 4, "a warp's two boxes");
     float gmax = 1.f;
-    if (MODE == kDz || MODE == kThinDz) {  // under the first tile's products
+    if (kIsDz<MODE>) {  // under the first tile's products
       float m = 0.f;
       for (int64_t t = threadIdx.x - 64; t < p.l.tokens; t += kEpiWarps * 32)
-        if (counts(p.l.want, t)) {
+        if (kIsPolicy<MODE>) {
+          const float g = fabsf(grad_of(p.l, t)), ge = fabsf(grad_entropy_of(p.l, t));
+          if (g < INFINITY) m = fmaxf(m, g);
+          if (ge < INFINITY) m = fmaxf(m, ge);
+        } else if (counts(p.l.want, t)) {
           const float g = fabsf(p.l.grad[t]);
           if (g < INFINITY) m = fmaxf(m, g);  // the others' gradients are relative to it, and finite
         }
@@ -977,6 +1194,17 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
         }
         tk.g[t] = g;
         tk.lse[t] = lse;
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+    }
+    if (MODE == kThinPolicyDz) {
+      const int t = threadIdx.x - 64;
+      if (t < kThin) {
+        const bool in = t < p.l.tokens;
+        tp.g[t] = in ? grad_of(p.l, t) / gmax : 0.f;
+        tp.ge[t] = in ? grad_entropy_of(p.l, t) / gmax : 0.f;
+        tp.lse[t] = in ? p.l.lse[t] : 0.f;
+        tp.entropy[t] = in ? p.l.entropy[t] : 0.f;
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
     }
@@ -1008,6 +1236,11 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
         if (MODE == kThinLogits)
           ok = drain_thin_logits(p, base_v + q * 32, last, (x.col * 2 + rank) * 4 + q, half, rows, lane, sm, wait,
                                  free);
+        else if (MODE == kThinScore)
+          ok = drain_thin_score(p, base_v + q * 32, last, (x.col * 2 + rank) * 4 + q, half, rows, lane, sm, wait,
+                                free);
+        else if (MODE == kThinPolicyDz)
+          ok = drain_thin_dz(p, tp, base_v + q * 32, last, half, rows, lane, sm, wait, free);
         else
           ok = drain_thin_dz(p, tk, base_v + q * 32, last, half, rows, lane, sm, wait, free);
       } else if (MODE == kThinGrads && x.kind == 0) {
@@ -1015,8 +1248,10 @@ __global__ void __launch_bounds__(kThreads, 1) head_pair_kernel(const __grid_con
         ok = drain_thin_dh(p, x, x.col * kTile + rank * 128 + q * 32, half, rows, lane, wait, free);
       } else if (MODE == kLogits) {
         ok = drain_logits(p.l, p.zscale, r0 + lane, c0, tbase, lane, sm, wait, free);
-      } else if (MODE == kDz) {
-        ok = drain_dz(p, gmax, r0 + lane, r0, p.l.v0 + c0, tbase, lane, stg, nbox, wait, free);
+      } else if (MODE == kScore) {
+        ok = drain_score(p, r0 + lane, r0, p.l.v0 + c0, tbase, lane, stg, nbox, wait, free);
+      } else if (MODE == kDz || MODE == kPolicyDz) {
+        ok = drain_dz<kIsPolicy<MODE>>(p, gmax, r0 + lane, r0, p.l.v0 + c0, tbase, lane, stg, nbox, wait, free);
       } else if (MODE == kThinGrads) {
         ok = drain_thin_dw(p, scale, p.l.v0 + static_cast<int>(r0), p.l.vocab, c0, tbase, lane, stg, wait, free);
       } else {
@@ -1130,7 +1365,8 @@ cudaError_t logit_launch(Params& P, const LogitParams& p, const Pipe& pipe) {
     h_rows = P.thin_n / 2;
     P.a_bytes = w_rows * kStep * 2;
     P.stage_bytes = P.a_bytes + h_rows * kStep * 2;
-    P.stages = std::min(kMaxStages, kRingBytes / P.stage_bytes);
+    const int room = kRingBytes - (p.entropy != nullptr ? static_cast<int>(sizeof(ThinPolicy)) : 0);
+    P.stages = std::min(kMaxStages, room / P.stage_bytes);
   } else {
     P.rows = cdiv(p.tokens, kTile);
     P.cols = cdiv(p.width, kTile);
@@ -1161,9 +1397,19 @@ int logit_groups(int64_t tokens, int64_t vocab, int pairs) {
 
 cudaError_t launch_logits(const LogitParams& p, const Pipe& pipe, cudaStream_t s) {
   Params P;
-  const cudaError_t e = logit_launch(P, p, pipe);
+  cudaError_t e = logit_launch(P, p, pipe);
   if (e != cudaSuccess) return e;
-  return P.thin_n != 0 ? launch_pairs<kThinLogits>(P, pipe.pairs, s) : launch_pairs<kLogits>(P, pipe.pairs, s);
+  if (p.folds == nullptr)
+    return P.thin_n != 0 ? launch_pairs<kThinLogits>(P, pipe.pairs, s) : launch_pairs<kLogits>(P, pipe.pairs, s);
+  if (P.thin_n != 0) return launch_pairs<kThinScore>(P, pipe.pairs, s);
+  if (p.z != nullptr) {
+    const cuuint64_t dims[2] = {(cuuint64_t)p.ld_z, (cuuint64_t)p.tokens};
+    const cuuint64_t strides[1] = {(cuuint64_t)p.ld_z * 4};
+    const cuuint32_t box[2] = {16, 32};
+    e = encode(&P.out[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.z, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pairs<kScore>(P, pipe.pairs, s);
 }
 
 cudaError_t launch_dz(const LogitParams& p, const Pipe& pipe, cudaStream_t s) {
@@ -1172,6 +1418,8 @@ cudaError_t launch_dz(const LogitParams& p, const Pipe& pipe, cudaStream_t s) {
   if (e == cudaSuccess && P.thin_n == 0)
     e = map_rows(&P.out[0], p.dz, p.ld_dz, p.tokens, p.ld_dz, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (e != cudaSuccess) return e;
+  if (p.entropy != nullptr)
+    return P.thin_n != 0 ? launch_pairs<kThinPolicyDz>(P, pipe.pairs, s) : launch_pairs<kPolicyDz>(P, pipe.pairs, s);
   return P.thin_n != 0 ? launch_pairs<kThinDz>(P, pipe.pairs, s) : launch_pairs<kDz>(P, pipe.pairs, s);
 }
 

@@ -53,6 +53,7 @@ EXPORTS = (
     "dmuon_selftest_wait_timeout", "dmuon_momentum_norm_noalloc", "dmuon_assign_owners", "dmuon_adamw_flat",
     "dmuon_head_create", "dmuon_head_workspace_bytes", "dmuon_head_bind", "dmuon_head_xent",
     "dmuon_head_xent_backward", "dmuon_head_xent_backward_loss", "dmuon_head_distill", "dmuon_head_distill_backward",
+    "dmuon_head_logprobs", "dmuon_head_logprobs_backward",
     "dmuon_head_read_device_status", "dmuon_head_destroy",
     "dmuon_route_workspace_bytes", "dmuon_route_sort", "dmuon_route_dispatch", "dmuon_route_combine",
     "dmuon_route_combine_backward",
@@ -121,6 +122,9 @@ def lib():
         "dmuon_head_distill": (i32, [vp, vp, i64, vp, i64, vp, vp, i32, f32, i64, vp, vp, vp]),
         "dmuon_head_distill_backward": (i32, [vp, vp, i64, vp, i64, vp, vp, i32, f32, i64, vp, vp, vp, i64, vp, i64,
                                               vp]),
+        "dmuon_head_logprobs": (i32, [vp, vp, i64, vp, i64, vp, f32, i32, i64, vp, vp, vp, vp, vp, vp]),
+        "dmuon_head_logprobs_backward": (i32, [vp, vp, i64, vp, i64, vp, f32, i64, vp, vp, vp, vp, vp, vp, i64, vp, i64,
+                                               vp]),
         "dmuon_head_read_device_status": (i32, [vp, vp, ctypes.POINTER(u32)]),
         "dmuon_head_destroy": (None, [vp]),
         "dmuon_route_workspace_bytes": (i32, [i64, i32, i32, ctypes.POINTER(sz)]),
@@ -432,6 +436,17 @@ def _run(owner, call, stream, *tensors, scratch=None):
         return call(stream.cuda_stream)
 
 
+@dataclass
+class Logprobs:
+    """What Head.logprobs returns of each token (see include/dmuon.h)."""
+
+    logp: object      # [tokens] fp32: the target's log probability, 0 where there is no target
+    entropy: object   # [tokens] fp32
+    lse: object       # [tokens] fp32
+    top_ids: object   # [tokens, top] int64, likeliest first; None where none were asked for
+    top_logp: object  # [tokens, top] fp32; None where none were asked for
+
+
 class Head:
     """Losses of a language model's head with their gradients, without the logits.
 
@@ -513,12 +528,17 @@ class Head:
             _check(fn(self._h, *args, ph, lh, pw, lw, s))
             return dh, dw
 
+        given = self._given(hidden, weight, dhidden, dweight)
+        return _run(self, call, stream, hidden, weight, lse, grad_loss, *tensors, *given, scratch=self.workspace)
+
+    def _given(self, hidden, weight, dhidden, dweight):
+        """The gradients that the caller wants written into tensors of its own, checked."""
         given = []
         for like, want, name in ((hidden, dhidden, "dhidden"), (weight, dweight, "dweight")):
             if want is not None and not isinstance(want, bool):
                 _rows(want, self.dim, _t().bfloat16, name, self.device, like.shape[0])
                 given.append(want)
-        return _run(self, call, stream, hidden, weight, lse, grad_loss, *tensors, *given, scratch=self.workspace)
+        return given
 
     def _grad(self, like, want, name):
         """The gradient of ``like`` (made where True, left out where False or None), its address and pitch."""
@@ -560,6 +580,48 @@ class Head:
         return self._backward(lib().dmuon_head_distill_backward, hidden, weight,
                               (*self._inputs(hidden, weight), *lists, float(temperature)), lse, grad_loss, dhidden,
                               dweight, stream, top_ids, top_logits)
+
+    def logprobs(self, hidden, weight, targets=None, *, top=0, temperature=1.0, stream=None) -> Logprobs:
+        """Log probability of each token's target (int64; one outside the vocabulary, or None: no target), entropy of
+        the distribution, and the ``top`` (up to 32) likeliest entries with their log probabilities."""
+        n, dev, top = hidden.shape[0], self.device, int(top)
+        y = None if targets is None else _flat(targets, hidden.shape[:1], _t().int64, "targets", dev)
+        args = (*self._inputs(hidden, weight), y, float(temperature), top, n)
+
+        def call(s):
+            empty, f32, place = _t().empty, _t().float32, hidden.device
+            out = [empty(n, dtype=f32, device=place) for _ in range(3)]
+            ids = values = None
+            if top > 0:
+                ids, values = empty((n, top), dtype=_t().int64, device=place), empty((n, top), dtype=f32, device=place)
+            _check(lib().dmuon_head_logprobs(self._h, *args, *[t.data_ptr() for t in out],
+                                             None if ids is None else ids.data_ptr(),
+                                             None if values is None else values.data_ptr(), s))
+            return Logprobs(*out, ids, values)
+
+        return _run(self, call, stream, hidden, weight, targets, scratch=self.workspace)
+
+    def logprobs_backward(self, hidden, weight, targets, scores, grad_logp=None, grad_entropy=None, *, temperature=1.0,
+                          dhidden=True, dweight=True, stream=None):
+        """(dhidden, dweight) of sum(grad_logp * logp + grad_entropy * entropy); ``scores`` as logprobs returned them
+        for the same inputs; a gradient that is None is zeros. Either result may be a tensor to write into, or False."""
+        f32, dev, shape = _t().float32, self.device, hidden.shape[:1]
+        y = None if targets is None else _flat(targets, shape, _t().int64, "targets", dev)
+        logp, entropy = _flat(scores.logp, shape, f32, "logp", dev), _flat(scores.entropy, shape, f32, "entropy", dev)
+        lse = _flat(scores.lse, shape, f32, "lse", dev)
+        gl = None if grad_logp is None else _flat(grad_logp, shape, f32, "grad_logp", dev)
+        ge = None if grad_entropy is None else _flat(grad_entropy, shape, f32, "grad_entropy", dev)
+        args = (*self._inputs(hidden, weight), y, float(temperature), shape[0], logp, entropy, lse, gl, ge)
+        given = self._given(hidden, weight, dhidden, dweight)
+
+        def call(s):
+            dh, ph, lh = self._grad(hidden, dhidden, "dhidden")
+            dw, pw, lw = self._grad(weight, dweight, "dweight")
+            _check(lib().dmuon_head_logprobs_backward(self._h, *args, ph, lh, pw, lw, s))
+            return dh, dw
+
+        return _run(self, call, stream, hidden, weight, targets, scores.logp, scores.entropy, scores.lse, grad_logp,
+                    grad_entropy, *given, scratch=self.workspace)
 
     def read_device_status(self, stream: int = 0) -> int:
         b = ctypes.c_uint32()

@@ -76,6 +76,35 @@ def distill(hidden, weight, top_ids, top_logits, temperature, grad_loss=None):
     return out
 
 
+def logprobs(hidden, weight, targets, temperature=1.0, grad_logp=None, grad_entropy=None):
+    """dict(logp, entropy, lse, z[, dz, dhidden, dweight]); dz is the gradient of z = hidden weight^T / temperature."""
+    h, w = np.asarray(hidden, np.float64), np.asarray(weight, np.float64)
+    z = h @ w.T / temperature
+    every, lse = log_softmax(z)
+    p = np.exp(every)
+    logp, entropy = np.zeros(len(h)), np.zeros(len(h))
+    dz = np.zeros_like(z)
+    for t in range(len(h)):
+        y = -1 if targets is None else int(targets[t])
+        gl = 0.0 if grad_logp is None else float(grad_logp[t])
+        ge = 0.0 if grad_entropy is None else float(grad_entropy[t])
+        # -log p of the likeliest entry from the others' ratio to it, so that a sure token keeps its digits
+        best = int(z[t].argmax())
+        others = np.delete(z[t], best) - z[t, best]
+        every[t, best] = -np.log1p(np.exp(others).sum())
+        on = p[t] > 0
+        entropy[t] = -(p[t, on] * every[t, on]).sum()
+        dz[t, on] = -ge * p[t, on] * (every[t, on] + entropy[t])
+        if 0 <= y < len(w):
+            logp[t] = every[t, y]
+            dz[t] -= gl * p[t]
+            dz[t, y] += gl * (p[t, y] - np.expm1(every[t, y]))
+    out = dict(logp=logp, entropy=entropy, lse=lse, z=z, every=every)
+    if grad_logp is not None or grad_entropy is not None:
+        out.update(dz=dz, dhidden=dz @ w / temperature, dweight=dz.T @ h / temperature)
+    return out
+
+
 def route(expert_ids, experts):
     """(dest, source, offsets): rows by expert, then by assignment."""
     ids = np.asarray(expert_ids)
