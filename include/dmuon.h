@@ -726,7 +726,7 @@ dmuon_status dmuon_route_combine_backward(const void* dy, int64_t ld_dy, const v
  * for up to 32 assignments. Sums are fp32; h is held as the sum of two bf16, so
  * that y has the one rounding of its type.
  *
- * For tokens * top <= 4096, and made for far fewer: what it costs is the reading
+ * For tokens * top <= 2048, and made for far fewer: what it costs is the reading
  * of the experts' matrices. With more tokens the experts' own products between
  * dmuon_route_dispatch and dmuon_route_combine use the tensor cores better.
  *
@@ -735,7 +735,8 @@ dmuon_status dmuon_route_combine_backward(const void* dy, int64_t ld_dy, const v
  */
 
 /* Bytes of scratch dmuon_experts_forward needs for up to these sizes (host only):
- * 0 <= tokens, 1 <= top <= 64, tokens*top <= 4096, 1 <= experts <= 4096, 1 <= dim, inner <= 2^20. */
+ * 0 <= tokens, 1 <= top <= 64, tokens*top <= 2048, 1 <= experts <= 4096, 1 <= dim, inner <= 2^20, and no matrices
+ * of more than 2^30 rows together. */
 dmuon_status dmuon_experts_workspace_bytes(int64_t tokens, int32_t top, int32_t experts, int64_t dim, int64_t inner,
                                            size_t* bytes);
 
@@ -749,13 +750,16 @@ dmuon_status dmuon_experts_workspace_bytes(int64_t tokens, int32_t top, int32_t 
  *  d_workspace device scratch, 256-byte aligned, its contents need not be
  *              initialised; free again when the call's work is done.
  * Any dim and inner: rows that start on 16 bytes and are whole 16-byte pieces
- * are read 16 bytes at a time, others element by element. The output must not
+ * stream through shared memory, others are read element by element. The output must not
  * overlap an input.
  */
 dmuon_status dmuon_experts_forward(const void* x, int64_t ld_x, const int64_t* expert_ids, const float* weights,
                                    int64_t tokens, int32_t top, int32_t experts, int64_t dim, int64_t inner,
                                    const void* up, const void* gate, const void* down, void* y, int64_t ld_y,
                                    void* d_workspace, size_t bytes, void* stream);
+
+/* The status word (DMUON_DEV_WAIT_TIMEOUT) of the last call that used a workspace; each call clears it first. */
+dmuon_status dmuon_experts_read_device_status(const void* d_workspace, void* stream, uint32_t* bits);
 
 /*
  * ---- The global gradient norm, and clipping

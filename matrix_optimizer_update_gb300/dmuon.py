@@ -57,7 +57,7 @@ EXPORTS = (
     "dmuon_head_read_device_status", "dmuon_head_destroy",
     "dmuon_route_workspace_bytes", "dmuon_route_sort", "dmuon_route_dispatch", "dmuon_route_combine",
     "dmuon_route_combine_backward",
-    "dmuon_experts_workspace_bytes", "dmuon_experts_forward",
+    "dmuon_experts_workspace_bytes", "dmuon_experts_forward", "dmuon_experts_read_device_status",
     "dmuon_clip_workspace_bytes", "dmuon_grad_norm", "dmuon_grad_clip",
     "dmuon_plan_destroy", "dmuon_last_error", "dmuon_version",
 )
@@ -134,6 +134,7 @@ def lib():
         "dmuon_route_combine_backward": (i32, [vp, i64, vp, vp, vp, vp, i64, i32, i64, i32, vp, vp, vp]),
         "dmuon_experts_workspace_bytes": (i32, [i64, i32, i32, i64, i64, ctypes.POINTER(sz)]),
         "dmuon_experts_forward": (i32, [vp, i64, vp, vp, i64, i32, i32, i64, i64, vp, vp, vp, vp, i64, vp, sz, vp]),
+        "dmuon_experts_read_device_status": (i32, [vp, vp, ctypes.POINTER(u32)]),
         "dmuon_clip_workspace_bytes": (i32, [ctypes.POINTER(sz)]),
         "dmuon_grad_norm": (i32, [vp, vp, vp, i32, vp, vp, sz, vp]),
         "dmuon_grad_clip": (i32, [vp, vp, vp, vp, i32, f32, vp, vp, sz, vp]),
@@ -758,7 +759,7 @@ class Experts:
     """A mixture's experts for a few tokens, from the router's ids and weights to the layer's output.
 
     For up to ``max_tokens`` tokens with ``top`` experts each (together at most
-    4096 assignments), beside ``Router``, which serves many tokens and training.
+    2048 assignments), beside ``Router``, which serves many tokens and training.
     Holds the scratch of a call (torch-allocated; one call uses it at a time).
     All tensors lie on the scratch's device, which is the current one or the
     stream's. See include/dmuon.h for the formulas.
@@ -801,6 +802,11 @@ class Experts:
             return y
 
         return _run(self, call, stream, x, expert_ids, weights, up, down, gate, scratch=self.workspace)
+
+    def read_device_status(self, stream: int = 0) -> int:
+        b = ctypes.c_uint32()
+        _check(lib().dmuon_experts_read_device_status(self.workspace.data_ptr(), ctypes.c_void_p(stream), ctypes.byref(b)))
+        return b.value
 
 
 class GradClip:

@@ -32,6 +32,7 @@ def check(layer, s, y=None):
     got = f64(layer.forward(**s) if y is None else y)
     want, off = ref.forward(f64(s["x"]), s["expert_ids"].cpu().numpy(), f64(s["weights"]), f64(s["up"]), f64(s["down"]),
                             f64(s["gate"]))
+    assert layer.read_device_status(torch.cuda.current_stream().cuda_stream) == 0
     assert np.all(np.abs(got - want) <= off), np.max(np.abs(got - want) / off)
 
 
@@ -41,8 +42,9 @@ def check(layer, s, y=None):
     (8, 4, 6, 512, 264, True, 0.1), (9, 1, 2, 136, 1000, True, 0.0), (13, 2, 3, 15, 520, False, 0.1),
     (16, 8, 16, 72, 64, True, 0.0), (31, 6, 60, 264, 104, True, 0.05), (33, 1, 1, 88, 80, True, 0.0),
     (64, 8, 64, 128, 88, True, 0.0), (70, 2, 2, 104, 40, False, 0.0), (100, 3, 200, 24, 56, True, 0.3),
-    (64, 64, 70, 16, 24, True, 0.0), (4096, 1, 3, 8, 16, False, 0.1), (5, 2, 4096, 16, 8, True, 0.1),
-    (6, 2, 4, 4096, 8, True, 0.0), (2, 1, 2, 8, 8960, False, 0.0)])
+    (32, 64, 70, 16, 24, True, 0.0), (2048, 1, 3, 8, 16, False, 0.1), (5, 2, 4096, 16, 8, True, 0.1),
+    (6, 2, 4, 4096, 8, True, 0.0), (2, 1, 2, 8, 8960, False, 0.0),
+    (40, 3, 3, 1000, 4000, True, 0.0), (300, 1, 2, 1032, 520, False, 0.1), (12, 4, 5, 520, 5000, False, 0.0)])
 def test_experts(tokens, top, experts, dim, inner, gated, dropped):
     check(dm.Experts.create(tokens, top, experts, dim, inner), make(tokens, top, experts, dim, inner, gated,
                                                                     tokens + dim + inner, dropped))
