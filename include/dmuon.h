@@ -714,7 +714,7 @@ dmuon_status dmuon_route_combine_backward(const void* dy, int64_t ld_dy, const v
  * ---- A mixture's experts for a few tokens
  *
  * What generating with a mixture-of-experts layer needs between its router and
- * its output, in two launches and without the rows in expert order: for
+ * its output, in three launches and without the rows in expert order: for
  * assignment i = t*top + k, which sends token t to expert e = expert_ids[i],
  *
  *   h[i] = silu(G_e x_t) * (U_e x_t)      without a gate: silu(U_e x_t)

@@ -1,5 +1,5 @@
 // experts.cu - a mixture's experts for a few tokens (include/dmuon.h, "A mixture's experts for a few
-// tokens"): from the router's ids and weights to the layer's output, in two launches.
+// tokens"): from the router's ids and weights to the layer's output, in three launches.
 //
 //   h[i] = silu(G_e x_t) * U_e x_t   (without a gate: silu(U_e x_t))     i = t*top + k, e = ids[i]
 //   y[t] = sum_k weights[i] * D_e h[i]
@@ -7,8 +7,8 @@
 // Bound by reading the matrices of the experts that the tokens reach, once: a token's products are 1 flop
 // for each byte read, 64 tokens' on 64 experts 8.
 //
-// Rows that are whole 16-byte pieces stream through shared memory: one block per SM, whose ninth warp keeps three or four
-// stages of 64 rows by 256 columns on their way by TMA, with the same columns of the expert's tokens, whatever the eight others do. A block owns a contiguous run of the row blocks
+// Rows that are whole 16-byte pieces stream through shared memory: one block per SM, whose ninth warp keeps six
+// stages of 64 rows by 256 columns on their way by TMA, whatever the eight others do. A block owns a contiguous run of the row blocks
 // of all experts in use, expert by expert, so that each has the same to read to one row block (16 rows of a matrix: 8
 // of gate and the same 8 of up, or 16), and takes up to four of them together, which read the expert's tokens once.
 // The eight warps share K. A product's sum may run over K in any order, so that a lane's 16 bytes of a row stand for
@@ -40,7 +40,6 @@ constexpr int kMaxAssignments = 2048;
 constexpr int64_t kMaxDim = int64_t(1) << 20;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRows = 16;    // rows of a unit
 constexpr int kStep = 32;    // K of a warp's step: 4 lanes of 8 elements
 constexpr int kCostRead = 8, kCostTile = 2;
 // Streaming
@@ -48,9 +47,8 @@ constexpr int kTogether = 4;                     // row blocks taken together
 constexpr int kChunk = 64;                       // columns of a TMA box, 128 bytes
 constexpr int kBoxBytes = 8 * 2 * kChunk;        // of 8 rows
 constexpr int kStageK = 4 * kChunk;              // a step of 32 for each warp
-constexpr int kMatrixBytes = 2 * kTogether * 4 * kBoxBytes;
-constexpr int kColumnPitch = 2 * kStageK + 16;   // of an assignment's columns: the next one's banks are 16 bytes on
-constexpr int kMaxStages = 4;
+constexpr int kStageBytes = 2 * kTogether * 4 * kBoxBytes;
+constexpr int kStages = 6;
 constexpr int kStreamThreads = kThreads + 32;
 constexpr int64_t kWaitNs = 2000000000LL;
 
@@ -65,7 +63,6 @@ struct ExpertsParams {
   bf16* h;             // [2][assignments][ld_h]: h as the sum of two bf16
   int64_t ld_h;
   float* part;         // [assignments][dim]: D_e h, not yet weighted
-  unsigned* arrived;   // per block of 16 entries of y: experts that are done
   bf16* y;
   int64_t ld_y;
   int32_t tokens, top, experts, n;  // n = tokens * top
@@ -73,10 +70,10 @@ struct ExpertsParams {
   unsigned* status;
 };
 
-// ... and the matrices as rows of K: gate or down, and up.
+// ... and the matrices as rows of K: gate or down, and up, in the boxes of a whole job and in boxes of 8 rows.
 struct StreamParams {
   ExpertsParams e;
-  CUtensorMap w[2];
+  CUtensorMap whole[2], part[2];
 };
 
 // What a block knows of the routing: the experts in use in ascending order, and each one's assignments.
@@ -170,51 +167,37 @@ __device__ __forceinline__ void result(const ExpertsParams& p, int assignment, i
   p.h[(p.n + assignment) * p.ld_h + o] = __float2bfloat16_rn(rest);
 }
 
-// Entries b * 16 .. of y once every expert is done with them: the assignments' products added up in the order of k.
-__device__ __forceinline__ void combine(const ExpertsParams& p, int b, int thread) {
-  for (int i = thread; i < p.tokens * kRows; i += kThreads) {
-    const int t = i / kRows, o = b * kRows + i % kRows;
-    if (o >= p.dim) continue;
+// y: the assignments' products added up in the order of k, each once its weight has been multiplied in fp32.
+__global__ void __launch_bounds__(kThreads) experts_combine_kernel(const __grid_constant__ ExpertsParams p) {
+  follow();
+  const int64_t all = int64_t(p.tokens) * p.dim;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < all; i += int64_t(gridDim.x) * kThreads) {
+    const int64_t t = i / p.dim;
+    const int o = static_cast<int>(i - t * p.dim);
     float s = 0.f;
+#pragma unroll 4
     for (int k = 0; k < p.top; ++k) {
-      const int q = t * p.top + k;
-      const int64_t id = p.ids[q];
-      if (id >= 0 && id < p.experts) s = fmaf(p.weights[q], __ldcg(&p.part[int64_t(q) * p.dim + o]), s);
+      const int64_t q = t * p.top + k, id = p.ids[q];
+      if (id >= 0 && id < p.experts) s = fmaf(p.weights[q], p.part[q * p.dim + o], s);
     }
     p.y[t * p.ld_y + o] = __float2bfloat16_rn(s);
   }
 }
 
-// y where no expert is named at all, by kThreads of each block.
-__device__ __forceinline__ void clear(const ExpertsParams& p) {
-  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < int64_t(p.tokens) * p.dim;
-       i += int64_t(gridDim.x) * kThreads)
-    p.y[i / p.dim * p.ld_y + i % p.dim] = __float2bfloat16_rn(0.f);
-}
-
-// The first launch clears what the second counts in, and the status.
-__device__ __forceinline__ void start(const ExpertsParams& p) {
-  const int first = blockIdx.x * blockDim.x + threadIdx.x;
-  if (first == 0) *p.status = 0u;
-  for (int i = first; i < (p.dim + kRows - 1) / kRows; i += gridDim.x * blockDim.x) p.arrived[i] = 0u;
-}
-
 // ------------------------------------------------------------------ element by element
-template <int TILES>
+constexpr int kPlainTiles = 2;  // tiles of 8 assignments at a time
 struct PlainShared {
   union {
     RoutingScratch scratch;
-    float sums[kWarps][TILES][4][32];
+    float sums[kWarps][kPlainTiles][4][32];
   };
   Routing r;
-  unsigned last;
 };
 
-// Tiles of 8 assignments at a time: TILES.
-template <int PHASE, int TILES>
+template <int PHASE>
 __global__ void __launch_bounds__(kThreads, 2) experts_plain_kernel(const __grid_constant__ ExpertsParams p) {
   extern __shared__ uint8_t raw[];
-  PlainShared<TILES>& sh = *reinterpret_cast<PlainShared<TILES>*>(raw);
+  PlainShared& sh = *reinterpret_cast<PlainShared*>(raw);
   const Routing& r = sh.r;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -222,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_plain_kernel(const __grid
   // there before that launch began.
   if (PHASE != kDown) {
     follow();
-    start(p);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
   }
   read_routing(p, sh.r, sh.scratch);
   const int K = PHASE == kDown ? p.inner : p.dim;
@@ -230,10 +213,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_plain_kernel(const __grid
   constexpr int kOut = PHASE == kGated ? 8 : 16;      // rows of the result per unit
   const int blocks = (rows + kOut - 1) / kOut;
   const int units = r.actives * blocks;
-  if (PHASE == kDown) {
-    follow();
-    if (units == 0) clear(p);
-  }
+  if (PHASE == kDown) follow();
   const int steps = (K + kStep - 1) / kStep;
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const int i = u / blocks, b = u % blocks;
@@ -244,12 +224,12 @@ __global__ void __launch_bounds__(kThreads, 2) experts_plain_kernel(const __grid
     const bf16* w = PHASE == kDown ? p.down : PHASE == kGated ? p.gate : p.up;
     const bf16* row0 = w + (matrix + o0) * K;
     const bf16* row1 = PHASE == kGated ? p.up + (matrix + o0) * K : w + (matrix + o1) * K;
-    for (int j0 = 0; j0 < count; j0 += 8 * TILES) {
-      const int tiles = min(TILES, (count - j0 + 7) / 8);
-      float acc[TILES][4] = {};
-      const bf16* col[TILES];  // of x or h, the row that this lane brings; nullptr: none
+    for (int j0 = 0; j0 < count; j0 += 8 * kPlainTiles) {
+      const int tiles = min(kPlainTiles, (count - j0 + 7) / 8);
+      float acc[kPlainTiles][4] = {};
+      const bf16* col[kPlainTiles];  // of x or h, the row that this lane brings; nullptr: none
 #pragma unroll
-      for (int t = 0; t < TILES; ++t) {
+      for (int t = 0; t < kPlainTiles; ++t) {
         const int j = j0 + t * 8 + g;
         col[t] = nullptr;
         if (j < count) col[t] = PHASE == kDown ? p.h + list[j] * p.ld_h : p.x + (list[j] / p.top) * p.ld_x;
@@ -258,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_plain_kernel(const __grid
         const int k = s * kStep + 8 * c;
         const uint4 a0 = piece(row0, k, K), a1 = piece(row1, k, K);
 #pragma unroll
-        for (int t = 0; t < TILES; ++t) {
+        for (int t = 0; t < kPlainTiles; ++t) {
           if (t >= tiles) break;
 #pragma unroll
           for (int q = 0; q < (PHASE == kDown ? 2 : 1); ++q) {
@@ -271,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_plain_kernel(const __grid
       }
       // the warps' sums joined; sums[.][t][v][l] is row l / 4 (+ 8 for v >= 2), column 2 * (l % 4) + v % 2
 #pragma unroll
-      for (int t = 0; t < TILES; ++t)
+      for (int t = 0; t < kPlainTiles; ++t)
         if (t < tiles)
 #pragma unroll
           for (int v = 0; v < 4; ++v) sh.sums[warp][t][v][lane] = acc[t][v];
@@ -292,43 +272,19 @@ __global__ void __launch_bounds__(kThreads, 2) experts_plain_kernel(const __grid
       }
       __syncthreads();
     }
-    if (PHASE == kDown) {
-      // the last expert's block to be done with these 16 entries of y adds them up
-      if (threadIdx.x == 0) {
-        __threadfence();
-        sh.last = atomicAdd(&p.arrived[b], 1u) == static_cast<unsigned>(r.actives - 1);
-      }
-      __syncthreads();
-      if (sh.last != 0u) {
-        __threadfence();
-        combine(p, b, threadIdx.x);
-      }
-      __syncthreads();
-    }
   }
 }
 
 // ------------------------------------------------------------------ streaming
-// A stage holds 64 rows by 256 columns of matrices and the same columns of the assignments' rows, which of h are two.
 struct StreamShared {
-  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t full[kStages], empty[kStages];
   int abort_flag;
   int from, to;                    // the block's row blocks
-  unsigned last[kTogether];
   Routing r;
   float sums[kWarps][kTogether][4][32];
 };
-constexpr int kRoom = 227 * 1024 - 1024 - static_cast<int>(sizeof(StreamShared));
-__host__ __device__ constexpr int stage_bytes(int tiles, bool down) {
-  return (kMatrixBytes + (down ? 2 : 1) * tiles * 8 * kColumnPitch + 1023) / 1024 * 1024;
-}
-__host__ __device__ constexpr int stages_of(int tiles, bool down) {
-  return kRoom / stage_bytes(tiles, down) < kMaxStages ? kRoom / stage_bytes(tiles, down) : kMaxStages;
-}
-__host__ __device__ constexpr size_t stream_smem(int tiles, bool down) {
-  return 1024 + stages_of(tiles, down) * stage_bytes(tiles, down) + sizeof(StreamShared);
-}
-static_assert(stages_of(4, true) >= 3 && sizeof(RoutingScratch) <= 3 * kMatrixBytes, "one block's shared memory");
+constexpr size_t kStreamSmem = 1024 + kStages * kStageBytes + sizeof(StreamShared);
+static_assert(kStreamSmem <= 227 * 1024 && sizeof(RoutingScratch) <= kStages * kStageBytes, "one block's shared memory");
 
 // What a row block of an expert takes: reading it, and the products with its assignments, 8 at a time. (Measured: a
 // block's time by the number of assignments, 64 rows by 2048: see the launch.)
@@ -378,21 +334,17 @@ struct Job {
   }
 };
 
-// The stages that a block fills, one after another: its jobs, 8 * TILES assignments at a time, 256 columns at a time.
-template <int TILES>
-struct Fills {
+// What a block does, one after another: its jobs, 8 * MOST assignments at a time.
+template <int MOST>
+struct Passes {
   Job job;
   const Routing* r;
-  int nk, assignments, j0, kb;
+  int assignments, j0;
   __device__ __forceinline__ bool next() {
-    if (job.rows > 0) {
-      if (++kb < nk) return true;
-      kb = 0;
-      if ((j0 += 8 * TILES) < assignments) return true;
-    }
+    if (job.rows > 0 && (j0 += 8 * MOST) < assignments) return true;
     if (!job.next()) return false;
     assignments = r->begin[job.active + 1] - r->begin[job.active];
-    j0 = kb = 0;
+    j0 = 0;
     return true;
   }
 };
@@ -407,18 +359,128 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* map, uint64_t
       : "memory");
 }
 
-// `bytes` (a multiple of 16) from global to shared memory, both on 16 bytes.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   ptx::smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(ptx::smem_u32(bar))
-               : "memory");
+// Where a warp of the products is.
+struct Ring {
+  uint8_t* base;
+  uint32_t stage, phase;
+  bool alive;
+};
+
+// Stages that an assignment's pieces are fetched ahead of their use, and what a lane holds of them.
+__host__ __device__ constexpr int ahead(int tiles) { return tiles == 1 ? 4 : tiles == 2 ? 3 : tiles == 3 ? 2 : 1; }
+template <int PHASE>
+struct Pieces {
+  static constexpr int kParts = PHASE == kDown ? 2 : 1;
+  uint4 v[6 * kParts];
+  const bf16* col[4];  // rows of x or h, from this warp's first column; nullptr: none
+
+  template <int T>
+  __device__ __forceinline__ void fetch(const ExpertsParams& p, int d, int kb, int column, int K) {
+    const int k = kb * kStageK;
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int q = 0; q < kParts; ++q)
+        v[(d * kParts + q) * T + t] = col[t] != nullptr && k + column < K
+                                          ? *reinterpret_cast<const uint4*>(col[t] + (q == 0 ? 0 : p.n * p.ld_h) + k)
+                                          : make_uint4(0, 0, 0, 0);
+  }
+
+  // A pass's first ones.
+  template <int T>
+  __device__ __forceinline__ void start(const ExpertsParams& p, const int16_t* list, int left, int column, int K) {
+    const int g = (threadIdx.x & 31) >> 2;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const int j = t * 8 + g;
+      col[t] = nullptr;
+      if (j < left) col[t] = (PHASE == kDown ? p.h + list[j] * p.ld_h : p.x + (list[j] / p.top) * p.ld_x) + column;
+    }
+#pragma unroll
+    for (int d = 0; d < ahead(T); ++d) fetch<T>(p, d, d, column, K);
+  }
+};
+
+// One pass with T tiles of 8 assignments: `left` from list on, the row blocks of the job. `then` is called once the
+// matrices have been multiplied, before the sums are joined.
+template <int PHASE, int T, class Then>
+__device__ __forceinline__ void products(const ExpertsParams& p, StreamShared& sh, Ring& ring, Pieces<PHASE>& x, const Job& job,
+                                         const int16_t* list, int left, int K, int rows, int column, uint32_t at,
+                                         Then&& then) {
+  constexpr int kParts = Pieces<PHASE>::kParts, kAhead = ahead(T), kOut = PHASE == kGated ? 8 : 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nk = (K + kStageK - 1) / kStageK;
+  float acc[kTogether][T][4] = {};
+  for (int kb0 = 0; kb0 < nk; kb0 += kAhead) {
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) {
+      const int kb = kb0 + d;
+      if (kb >= nk) break;
+      // (after a wait that ran out of time a warp only keeps the others' barriers company)
+      if (ring.alive)
+        ring.alive = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.full[ring.stage], ring.phase, &sh.abort_flag, p.status, kWaitNs));
+      // (a stage has room for all row blocks: what it holds of those that the job has not is multiplied and not used)
+      if (ring.alive && kb * kStageK + (warp >> 1) * kChunk < K) {
+        const uint8_t* s = ring.base + ring.stage * kStageBytes + at;
+        uint4 a[kTogether][2];
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) {
+          a[i][0] = *reinterpret_cast<const uint4*>(s + (PHASE == kGated ? i : 2 * i) * kBoxBytes);
+          a[i][1] = *reinterpret_cast<const uint4*>(s + (PHASE == kGated ? i + 4 : 2 * i + 1) * kBoxBytes);
+        }
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+              const uint4& v = x.v[(d * kParts + q) * T + t];
+#pragma unroll
+              for (int i = 0; i < kTogether; ++i) {
+                if (half == 0) mma(acc[i][t], a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y, v.x, v.y);
+                else mma(acc[i][t], a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w, v.z, v.w);
+              }
+            }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh.empty[ring.stage]);
+      if (++ring.stage == kStages) {
+        ring.stage = 0;
+        ring.phase ^= 1u;
+      }
+      if (kb + kAhead < nk) x.template fetch<T>(p, d, kb + kAhead, column, K);
+    }
+  }
+  then();
+  // the warps' sums joined; sums[.][i][v][l] is row l / 4 (+ 8 for v >= 2), column 2 * (l % 4) + v % 2
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+#pragma unroll
+    for (int i = 0; i < kTogether; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sh.sums[warp][i][k][lane] = acc[i][t][k];
+    consumers_sync();
+    constexpr int kEach = PHASE == kGated ? 2 : 4;
+    for (int n = threadIdx.x; n < job.rows * kEach * 32; n += kThreads) {
+      const int l = n & 31, k = (n >> 5) % kEach, i = (n >> 5) / kEach;
+      const int j = t * 8 + 2 * (l & 3) + (k & 1);
+      const int o = (job.first + i) * kOut + (l >> 2) + (k >= 2 ? 8 : 0);
+      if (j >= left || o >= rows) continue;
+      float s = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        s += sh.sums[w][i][k][l];
+        if (PHASE == kGated) s1 += sh.sums[w][i][k + 2][l];
+      }
+      result<PHASE>(p, list[j], o, s, s1);
+    }
+    consumers_sync();
+  }
 }
 
-template <int PHASE, int TILES>
+template <int PHASE, int MOST>
 __global__ void __launch_bounds__(kStreamThreads, 1) experts_stream_kernel(const __grid_constant__ StreamParams sp) {
   constexpr bool down = PHASE == kDown;
-  constexpr int kStages = stages_of(TILES, down), kStageBytes = stage_bytes(TILES, down), kParts = down ? 2 : 1;
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   StreamShared& sh = *reinterpret_cast<StreamShared*>(base + kStages * kStageBytes);
@@ -432,14 +494,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1) experts_stream_kernel(const
     }
     sh.abort_flag = 0;
     ptx::fence_mbar_init();
-    ptx::prefetch_tmap(&sp.w[0]);
-    if (PHASE == kGated) ptx::prefetch_tmap(&sp.w[1]);
+    ptx::prefetch_tmap(&sp.whole[0]);
+    if (PHASE == kGated) ptx::prefetch_tmap(&sp.whole[1]);
   }
   // The down products' launch is set up while the up products' still runs: what it reads before follow() was
   // there before that launch began.
   if (!down) {
     follow();
-    start(p);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
   }
   read_routing(p, sh.r, *reinterpret_cast<RoutingScratch*>(base));
   const int K = down ? p.inner : p.dim;
@@ -453,63 +515,48 @@ __global__ void __launch_bounds__(kStreamThreads, 1) experts_stream_kernel(const
   ptx::fence_proxy_async_shared();  // the scratch's place is the ring's
   __syncthreads();
   const int nk = (K + kStageK - 1) / kStageK;
-  Job job;
-  job.unit = sh.from;
-  job.end = sh.to;
-  job.blocks = blocks;
-  job.rows = 0;
+  Passes<MOST> pass;
+  pass.job.unit = sh.from;
+  pass.job.end = sh.to;
+  pass.job.blocks = blocks;
+  pass.job.rows = 0;
+  pass.r = &sh.r;
   uint32_t stage = 0, phase = 0;
 
   if (warp == kWarps) {
     // ---------------------------------------------------------- loads
+    // A stage: for each chunk of 64 columns 64 rows (gated, 32 of gate and then 32 of up), which boxes of 64 (or 32)
+    // rows bring where the job has all of them, else boxes of 8.
     uint32_t fills = 0;
-    Fills<TILES> f;
-    f.job = job;
-    f.r = &sh.r;
-    f.nk = nk;
-    // A stage's matrices: a box of 8 rows by 64 columns each lane. Gated, groups 0..3 are gate's rows and 4..7 up's; else
-    // the 16 rows of a row block are two groups.
-    const int group = lane >> 2, chunk = lane & 3, half = PHASE == kGated ? group & 3 : group;
-    const CUtensorMap* map = PHASE == kGated && group >= 4 ? &sp.w[1] : &sp.w[0];
-    auto matrices = [&](const Fills<TILES>& f, uint32_t stage) {
-      const int x = f.kb * kStageK, wide = min(kStageK, K - x), chunks = (wide + kChunk - 1) / kChunk;
-      const int columns = min(8 * TILES, f.assignments - f.j0);
-      if (lane == 0)
-        ptx::mbar_arrive_expect_tx(&sh.full[stage], 2 * f.job.rows * chunks * kBoxBytes + kParts * columns * 2 * wide);
-      __syncwarp();
-      if (half < (PHASE == kGated ? f.job.rows : 2 * f.job.rows) && chunk < chunks)
-        tma_load_2d(base + stage * kStageBytes + (group * 4 + chunk) * kBoxBytes, map, &sh.full[stage], x + chunk * kChunk,
-                    sh.r.active[f.job.active] * rows + f.job.first * kOut + 8 * half);
-    };
-    // ... and the assignments' columns: a row each lane, of h in two parts.
-    auto columns = [&](const Fills<TILES>& f, uint32_t stage) {
-      if (lane >= min(8 * TILES, f.assignments - f.j0)) return;
-      const int x = f.kb * kStageK, wide = min(kStageK, K - x);
-      const int i = sh.r.list[sh.r.begin[f.job.active] + f.j0 + lane];
-      const bf16* row = (down ? p.h + i * p.ld_h : p.x + (i / p.top) * p.ld_x) + x;
-      uint8_t* at = base + stage * kStageBytes + kMatrixBytes + lane * kColumnPitch;
-      for (int q = 0; q < kParts; ++q)
-        bulk_load(at + q * 8 * TILES * kColumnPitch, row + q * p.n * p.ld_h, 2 * wide, &sh.full[stage]);
-    };
-    // the first stages' matrices need not wait for the launch before, which makes h
-    const Fills<TILES> first = f;
-    bool more = true;
-    while (fills < kStages && (more = f.next())) matrices(f, fills++);
-    if (down) follow();
-    Fills<TILES> again = first;
-    for (uint32_t k = 0; k < fills; ++k) {
-      again.next();
-      columns(again, k);
-    }
-    // from the first stage on again, each once its last load has been used
-    while (more && (more = f.next())) {
-      if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sh.empty[stage], phase, abortf, p.status, kWaitNs))) break;
-      matrices(f, stage);
-      columns(f, stage);
-      ++fills;
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1u;
+    constexpr int kKinds = PHASE == kGated ? 2 : 1;
+    bool ok = true;
+    while (ok && pass.next()) {
+      const Job& job = pass.job;
+      const int y = sh.r.active[job.active] * rows + job.first * kOut;
+      for (int kb = 0; kb < nk; ++kb) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.empty[stage], phase ^ 1u, abortf, p.status, kWaitNs));
+        if (!ok) break;
+        const int x = kb * kStageK, chunks = min(4, (K - x + kChunk - 1) / kChunk);
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.full[stage], 2 * job.rows * chunks * kBoxBytes);
+        __syncwarp();
+        uint8_t* at = base + stage * kStageBytes;
+        if (job.rows == kTogether) {
+          const int chunk = lane / kKinds, kind = lane % kKinds;
+          if (chunk < chunks)
+            tma_load_2d(at + chunk * 8 * kBoxBytes + kind * 4 * kBoxBytes, &sp.whole[kind], &sh.full[stage],
+                        x + chunk * kChunk, y);
+        } else {
+          const int chunk = lane >> 3, kind = PHASE == kGated ? (lane >> 2) & 1 : 0;
+          const int group = lane & (PHASE == kGated ? 3 : 7);
+          if (chunk < chunks && group < (PHASE == kGated ? job.rows : 2 * job.rows))
+            tma_load_2d(at + (lane & 7) * kBoxBytes + chunk * 8 * kBoxBytes, &sp.part[kind], &sh.full[stage],
+                        x + chunk * kChunk, y + 8 * group);
+        }
+        ++fills;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
     }
     // nothing is in flight once every stage that was filled is full
@@ -522,102 +569,39 @@ __global__ void __launch_bounds__(kStreamThreads, 1) experts_stream_kernel(const
   }
 
   // ------------------------------------------------------------ products
-  if (down) {
-    follow();
-    if (sh.r.actives == 0) clear(p);
-  }
+  if (down) follow();
   const int g = lane >> 2, c = lane & 3;
   // this warp's 32 columns of a stage: pieces 2c + (warp & 1) of chunk warp / 2, which no two lanes of a quarter warp
-  // have in the same banks, of the swizzled rows as of the assignments' columns
-  const uint32_t at = (warp >> 1) * kBoxBytes + g * 128 + (((2 * c + (warp & 1)) ^ g) << 4);
-  const uint32_t of_column = kMatrixBytes + g * kColumnPitch + (warp >> 1) * 128 + ((2 * c + (warp & 1)) << 4);
-  bool alive = true;
-  while (job.next()) {
-    const int16_t* list = sh.r.list + sh.r.begin[job.active];
-    const int count = sh.r.begin[job.active + 1] - sh.r.begin[job.active];
-    for (int j0 = 0; j0 < count; j0 += 8 * TILES) {
-      const int tiles = min(TILES, (count - j0 + 7) / 8);
-      float acc[kTogether][TILES][4] = {};
-      for (int kb = 0; kb < nk; ++kb) {
-        // (after a wait that ran out of time a warp only keeps the others' barriers company)
-        if (alive) alive = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.full[stage], phase, abortf, p.status, kWaitNs));
-        if (alive && kb * kStageK + (warp >> 1) * kChunk < K) {
-          const uint8_t* s = base + stage * kStageBytes;
-          // zeros for what the matrix has past its last column: there, and in columns of no assignment, the stage
-          // holds what an earlier one left
-          const bool inside = kb * kStageK + (warp >> 1) * kChunk + 16 * c + 8 * (warp & 1) < K;
-          uint4 v[kParts][TILES];
-#pragma unroll
-          for (int q = 0; q < kParts; ++q)
-#pragma unroll
-            for (int t = 0; t < TILES; ++t)
-              v[q][t] = inside && j0 + t * 8 + g < count
-                            ? *reinterpret_cast<const uint4*>(s + of_column + (q * TILES + t) * 8 * kColumnPitch)
-                            : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < kTogether; ++i) {
-            if (i >= job.rows) break;
-            const uint4 a0 = *reinterpret_cast<const uint4*>(s + at + (PHASE == kGated ? i : 2 * i) * 4 * kBoxBytes);
-            const uint4 a1 =
-                *reinterpret_cast<const uint4*>(s + at + (PHASE == kGated ? i + 4 : 2 * i + 1) * 4 * kBoxBytes);
-#pragma unroll
-            for (int t = 0; t < TILES; ++t) {
-              if (t >= tiles) break;
-#pragma unroll
-              for (int q = 0; q < kParts; ++q) {
-                mma(acc[i][t], a0.x, a1.x, a0.y, a1.y, v[q][t].x, v[q][t].y);
-                mma(acc[i][t], a0.z, a1.z, a0.w, a1.w, v[q][t].z, v[q][t].w);
-              }
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh.empty[stage]);
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-      // the warps' sums joined; sums[.][i][v][l] is row l / 4 (+ 8 for v >= 2), column 2 * (l % 4) + v % 2
-#pragma unroll
-      for (int t = 0; t < TILES; ++t) {
-        if (t >= tiles) break;
-#pragma unroll
-        for (int i = 0; i < kTogether; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) sh.sums[warp][i][k][lane] = acc[i][t][k];
-        consumers_sync();
-        constexpr int kEach = PHASE == kGated ? 2 : 4;
-        for (int n = threadIdx.x; n < job.rows * kEach * 32; n += kThreads) {
-          const int l = n & 31, k = (n >> 5) % kEach, i = (n >> 5) / kEach;
-          const int j = j0 + t * 8 + 2 * (l & 3) + (k & 1);
-          const int o = (job.first + i) * kOut + (l >> 2) + (k >= 2 ? 8 : 0);
-          if (j >= count || o >= rows) continue;
-          float s = 0.f, s1 = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            s += sh.sums[w][i][k][l];
-            if (PHASE == kGated) s1 += sh.sums[w][i][k + 2][l];
-          }
-          result<PHASE>(p, list[j], o, s, s1);
-        }
-        consumers_sync();
-      }
-    }
-    if (down) {
-      // the last expert's block to be done with 16 entries of y adds them up
-      if (threadIdx.x < job.rows) {
-        __threadfence();
-        sh.last[threadIdx.x] = atomicAdd(&p.arrived[job.first + threadIdx.x], 1u) == static_cast<unsigned>(sh.r.actives - 1);
-      }
-      consumers_sync();
-      for (int i = 0; i < job.rows; ++i)
-        if (sh.last[i] != 0u) {
-          __threadfence();
-          combine(p, job.first + i, threadIdx.x);
-        }
-      consumers_sync();
-    }
+  // have in the same banks of the swizzled rows
+  const uint32_t at = (warp >> 1) * 8 * kBoxBytes + g * 128 + (((2 * c + (warp & 1)) ^ g) << 4);
+  const int column = (warp >> 1) * kChunk + 16 * c + 8 * (warp & 1);
+  Ring ring = {base, 0u, 0u, true};
+  Pieces<PHASE> x;
+  // The assignments' pieces come straight from L2, some stages before their use; a pass's first ones are sent for before
+  // the sums of the pass before are joined. Each number of tiles has a loop of its own, without branches.
+  auto start = [&](const Passes<MOST>& s) {
+    const int16_t* list = sh.r.list + sh.r.begin[s.job.active] + s.j0;
+    const int left = s.assignments - s.j0;
+    if (MOST == 1 || left <= 8) x.template start<1>(p, list, left, column, K);
+    else if (left <= 16) x.template start<2>(p, list, left, column, K);
+    else if (left <= 24) x.template start<3>(p, list, left, column, K);
+    else x.template start<4>(p, list, left, column, K);
+  };
+  bool more = pass.next();
+  if (more) start(pass);
+  while (more) {
+    Passes<MOST> after = pass;
+    more = after.next();
+    auto then = [&]() {
+      if (more) start(after);
+    };
+    const int16_t* list = sh.r.list + sh.r.begin[pass.job.active] + pass.j0;
+    const int left = pass.assignments - pass.j0;
+    if (MOST == 1 || left <= 8) products<PHASE, 1>(p, sh, ring, x, pass.job, list, left, K, rows, column, at, then);
+    else if (left <= 16) products<PHASE, 2>(p, sh, ring, x, pass.job, list, left, K, rows, column, at, then);
+    else if (left <= 24) products<PHASE, 3>(p, sh, ring, x, pass.job, list, left, K, rows, column, at, then);
+    else products<PHASE, 4>(p, sh, ring, x, pass.job, list, left, K, rows, column, at, then);
+    pass = after;
   }
 }
 
@@ -638,7 +622,7 @@ dmuon_status check_sizes(int64_t tokens, int32_t top, int32_t experts, int64_t d
 }
 
 struct Workspace {
-  size_t status, h, part, arrived, bytes;
+  size_t status, h, part, bytes;
 };
 
 Workspace workspace_of(int64_t n, int64_t dim, int64_t inner) {
@@ -652,7 +636,6 @@ Workspace workspace_of(int64_t n, int64_t dim, int64_t inner) {
   w.status = take(4);
   w.h = take(2 * 2 * n * pitch_h(inner));
   w.part = take(4 * n * dim);
-  w.arrived = take(4 * ((dim + kRows - 1) / kRows));
   w.bytes = at;
   return w;
 }
@@ -669,52 +652,48 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Matrices as rows of K, in boxes of 8 rows by 64 columns; past the last column or row a box has zeros.
-cudaError_t map_rows(CUtensorMap* m, const void* base, int64_t K, int64_t rows) {
+// Matrices as rows of K, in boxes of so many rows by 64 columns; past the last column or row a box has zeros.
+cudaError_t map_rows(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int box_rows) {
   auto fn = encode_fn();
   if (fn == nullptr) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)K * 2};
-  const cuuint32_t box[2] = {kChunk, 8}, one[2] = {1, 1};
+  const cuuint32_t box[2] = {kChunk, (cuuint32_t)box_rows}, one[2] = {1, 1};
   const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, one,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int PHASE, int TILES>
+template <int PHASE>
 cudaError_t launch(const ExpertsParams& p, bool stream, int sms, cudaStream_t s) {
   const int rows = PHASE == kDown ? p.dim : p.inner, K = PHASE == kDown ? p.inner : p.dim;
   const int out = PHASE == kGated ? 8 : 16;
   const int64_t units = int64_t(std::min(p.experts, p.n)) * ((rows + out - 1) / out);
   cudaError_t e;
+  auto shared = [](auto* kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  };
   if (!stream) {
-    e = cudaFuncSetAttribute(experts_plain_kernel<PHASE, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(sizeof(PlainShared<TILES>)));
-    if (e != cudaSuccess) return e;
-    return launch_follow(experts_plain_kernel<PHASE, TILES>, dim3(static_cast<unsigned>(std::min<int64_t>(units, 2 * sms))),
-                         kThreads, sizeof(PlainShared<TILES>), s, 1, p);
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(units, 2 * sms)));
+    if ((e = shared(experts_plain_kernel<PHASE>, sizeof(PlainShared))) != cudaSuccess) return e;
+    return launch_follow(experts_plain_kernel<PHASE>, grid, kThreads, sizeof(PlainShared), s, 1, p);
   }
-  constexpr size_t smem = stream_smem(TILES, PHASE == kDown);
   StreamParams sp;
   sp.e = p;
   const bf16* w = PHASE == kGated ? p.gate : PHASE == kUngated ? p.up : p.down;
-  e = map_rows(&sp.w[0], w, K, int64_t(p.experts) * rows);
-  if (e == cudaSuccess) e = map_rows(&sp.w[1], PHASE == kGated ? p.up : w, K, int64_t(p.experts) * rows);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(experts_stream_kernel<PHASE, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem));
+  e = cudaSuccess;
+  for (int kind = 0; kind < (PHASE == kGated ? 2 : 1) && e == cudaSuccess; ++kind) {
+    const bf16* m = kind == 0 ? w : p.up;
+    e = map_rows(&sp.whole[kind], m, K, int64_t(p.experts) * rows, kTogether * out);
+    if (e == cudaSuccess) e = map_rows(&sp.part[kind], m, K, int64_t(p.experts) * rows, 8);
+  }
   if (e != cudaSuccess) return e;
-  return launch_follow(experts_stream_kernel<PHASE, TILES>, dim3(static_cast<unsigned>(std::min<int64_t>(units, sms))),
-                       kStreamThreads, smem, s, 1, sp);
-}
-
-template <int PHASE>
-cudaError_t launch_tiles(const ExpertsParams& p, bool stream, int sms, cudaStream_t s) {
-  // as many columns as an expert may get where no token names it twice
-  if (p.tokens <= 8) return launch<PHASE, 1>(p, stream, sms, s);
-  if (p.tokens <= 16) return launch<PHASE, 2>(p, stream, sms, s);
-  return launch<PHASE, 4>(p, stream, sms, s);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(units, sms)));
+  // where no expert gets more than 8 assignments unless a token names it twice, the loops for more are left out
+  auto* kernel = p.tokens <= 8 ? experts_stream_kernel<PHASE, 1> : experts_stream_kernel<PHASE, 4>;
+  if ((e = shared(kernel, kStreamSmem)) != cudaSuccess) return e;
+  return launch_follow(kernel, grid, kStreamThreads, kStreamSmem, s, 1, sp);
 }
 
 }  // namespace
@@ -764,7 +743,6 @@ extern "C" dmuon_status dmuon_experts_forward(const void* x, int64_t ld_x, const
   p.h = reinterpret_cast<bf16*>(ws + w.h);
   p.ld_h = pitch_h(inner);
   p.part = reinterpret_cast<float*>(ws + w.part);
-  p.arrived = reinterpret_cast<unsigned*>(ws + w.arrived);
   p.status = reinterpret_cast<unsigned*>(ws + w.status);
   p.y = static_cast<bf16*>(y);
   p.ld_y = ld_y;
@@ -778,8 +756,12 @@ extern "C" dmuon_status dmuon_experts_forward(const void* x, int64_t ld_x, const
   // rows that are whole 16-byte pieces stream, others are read element by element
   const bool vec_up = dim % 8 == 0 && ld_x % 8 == 0 && !misaligned(x, 16) && !misaligned(up, 16) && !misaligned(gate, 16);
   const bool vec_down = inner % 8 == 0 && !misaligned(down, 16);
-  e = gate != nullptr ? launch_tiles<kGated>(p, vec_up, sms, s) : launch_tiles<kUngated>(p, vec_up, sms, s);
-  if (e == cudaSuccess) e = launch_tiles<kDown>(p, vec_down, sms, s);
+  e = gate != nullptr ? launch<kGated>(p, vec_up, sms, s) : launch<kUngated>(p, vec_up, sms, s);
+  if (e == cudaSuccess) e = launch<kDown>(p, vec_down, sms, s);
+  const int64_t blocks = (tokens * dim + kThreads - 1) / kThreads;
+  if (e == cudaSuccess)
+    e = launch_follow(experts_combine_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(blocks, 8 * sms))), kThreads, 0, s,
+                      1, p);
   if (e != cudaSuccess) return set_last_error(DMUON_ERR_CUDA, cudaGetErrorString(e));
   return set_last_error(DMUON_OK, "");
 }
