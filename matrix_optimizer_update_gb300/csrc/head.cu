@@ -352,13 +352,15 @@ dmuon_status score(dmuon_head_t H, const void* hidden, int64_t ld_hidden, const 
     q.last = v0 + piece >= H->vocab;
     q.first = v0 == 0;
     if ((e = head::launch_logits(p, H->pipe(), s)) != cudaSuccess) return cuda_refuse(e, "scores kernel");
-    if (q.last && (e = head::launch_score_rows(r, s)) != cudaSuccess) return cuda_refuse(e, "rows kernel");
+    const bool together = q.last && thin && top > 0;
+    if (q.last && !together && (e = head::launch_score_rows(r, s)) != cudaSuccess) return cuda_refuse(e, "rows kernel");
     const int groups = head::logit_groups(tokens, p.width, H->pairs);
     if (top > 0) {
       q.parts = parts + p.group0 * r.group_step;
       q.groups = groups;
       q.thin_h = thin ? head::thin_tiles(p.width, H->pairs).height : 0;
-      if ((e = head::launch_top(q, s)) != cudaSuccess) return cuda_refuse(e, "alternatives kernel");
+      e = together ? head::launch_score_top(r, q, s) : head::launch_top(q, s);
+      if (e != cudaSuccess) return cuda_refuse(e, "alternatives kernel");
     }
     p.group0 += groups;
   }

@@ -222,6 +222,8 @@ cudaError_t launch_teacher(const TeacherParams& p, cudaStream_t s);
 cudaError_t launch_rows(const RowParams& p, cudaStream_t s);
 cudaError_t launch_score_rows(const ScoreParams& p, cudaStream_t s);
 cudaError_t launch_top(const TopParams& p, cudaStream_t s);
+// both for the last piece of few tokens (group_step 1)
+cudaError_t launch_score_top(const ScoreParams& r, const TopParams& p, cudaStream_t s);
 // out = bf16(gscale * *gmax * the sum of the slices of acc)
 cudaError_t launch_round(const float* acc, int slices, int64_t tokens, int32_t dim, float gscale, const float* gmax,
                          bf16* out, int64_t ld_out, cudaStream_t s);

@@ -7,6 +7,7 @@
 #include "follow.cuh"
 #include "head.h"
 #include "head_dot.cuh"
+#include "head_score.cuh"
 
 namespace dmuon {
 namespace head {
@@ -238,118 +239,11 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------------ scores
-// Groups' sums joined as above, with the entropy's beside them: of sum = sum exp(z - peak) and
-// folded = sum exp(z - peak) (z - peak), the entropy is log(sum) - folded / sum, both terms positive. The target's
-// share comes apart from the others' here too, so that a sure token's log probability and entropy keep their digits.
-struct Folded {
-  float peak = kNegInf, sum = 0.f, fold = 0.f;
-  // exp(-infinity) times a distance of -infinity is nothing
-  static __device__ __forceinline__ float finite(float d) { return fmaxf(d, -1e4f); }
-  __device__ __forceinline__ void join(float peak2, float sum2, float fold2) {
-    const float m = fmaxf(peak, peak2);
-    if (!(m > kNegInf)) {  // neither has a number: zeros, or NaN to pass on
-      sum += sum2;
-      fold += fold2;
-      return;
-    }
-    const float a = peak - m, b = peak2 - m, ea = expf(a), eb = expf(b);
-    fold = ea * fmaf(sum, finite(a), fold) + eb * fmaf(sum2, finite(b), fold2);
-    sum = sum * ea + sum2 * eb;
-    peak = m;
-  }
-};
-
 template <int kTokens>
 __global__ void __launch_bounds__(kRowThreads) score_rows_kernel(const __grid_constant__ ScoreParams p) {
-  constexpr int kLanes = kRowThreads / kTokens;
-  constexpr int kWarps = kRowThreads / 32;
-  __shared__ float s_peak[kWarps][kTokens], s_sum[kWarps][kTokens], s_fold[kWarps][kTokens], s_dot[kWarps];
+  __shared__ ScoreShared<kTokens, kRowThreads> sh;
   follow();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  {
-    const int64_t t = int64_t(blockIdx.x) * kTokens + threadIdx.x % kTokens;
-    Folded f;
-    if (t < p.tokens) {
-      const int64_t at = t * p.token_step;
-      for (int g = threadIdx.x / kTokens; g < p.groups; g += 4 * kLanes) {
-        Part q[4];
-        float w[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int64_t i = at + (g + u * kLanes) * p.group_step;
-          const bool in = g + u * kLanes < p.groups;
-          q[u] = in ? p.parts[i] : Part{kNegInf, 0.f};
-          w[u] = in ? p.folds[i] : 0.f;
-        }
-        const float m = fmaxf(fmaxf(q[0].peak, q[1].peak), fmaxf(q[2].peak, q[3].peak));
-        if (!(m > kNegInf)) {
-          f.join(kNegInf, q[0].sum + q[1].sum + q[2].sum + q[3].sum, w[0] + w[1] + w[2] + w[3]);
-          continue;
-        }
-        float s = 0.f, fold = 0.f;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float d = q[u].peak - m, e = expf(d);
-          s = fmaf(q[u].sum, e, s);
-          fold = fmaf(fmaf(q[u].sum, Folded::finite(d), w[u]), e, fold);
-        }
-        f.join(m, s, fold);
-      }
-    }
-    for (int d = 16; d >= kTokens; d >>= 1) {
-      const float p2 = __shfl_xor_sync(0xffffffffu, f.peak, d), s2 = __shfl_xor_sync(0xffffffffu, f.sum, d),
-                  f2 = __shfl_xor_sync(0xffffffffu, f.fold, d);
-      f.join(p2, s2, f2);
-    }
-    if (lane < kTokens) {
-      s_peak[warp][lane] = f.peak;
-      s_sum[warp][lane] = f.sum;
-      s_fold[warp][lane] = f.fold;
-    }
-  }
-  // from here a warp per token
-  const int64_t t = int64_t(blockIdx.x) * kTokens + (kTokens == 1 ? 0 : warp);
-  float z = 0.f;
-  int64_t y = -1;
-  if (p.targets != nullptr && t < p.tokens) {
-    y = p.targets[t];
-    if (y >= p.vocab) y = -1;
-    if (y >= 0) {
-      float part[1];
-      dot_parts<1>(p.dot, {t}, {y}, kTokens == 1 ? threadIdx.x : lane, kTokens == 1 ? kRowThreads : 32, part);
-      z = warp_sum(part[0]);
-    }
-  }
-  if (lane == 0) s_dot[warp] = z;
-  __syncthreads();
-  const int mine = kTokens == 1 ? 0 : warp;
-  if (warp >= kTokens || t >= p.tokens || lane != 0) return;
-  Folded f;
-  for (int w = 0; w < kWarps; ++w) f.join(s_peak[w][mine], s_sum[w][mine], s_fold[w][mine]);
-  float lse, logp = 0.f, entropy;
-  if (y < 0) {
-    lse = f.peak + logf(f.sum);
-    entropy = logf(f.sum) - f.fold / f.sum;
-  } else {
-    if (kTokens == 1)
-      for (int w = 1; w < kWarps; ++w) z += s_dot[w];
-    z *= p.dot.scale;
-    p.picked[t] = z;
-    const float d = f.peak - z, e = expf(d), ratio = f.sum * e;  // the others' share to the target's
-    if (ratio < 1.f) {
-      logp = -log1pf(ratio);
-      lse = z - logp;
-      entropy = -logp - e * fmaf(f.sum, Folded::finite(d), f.fold) / (1.f + ratio);
-    } else {
-      const float hit = expf(-d), sum = f.sum + hit;
-      lse = f.peak + logf(sum);
-      logp = z - lse;
-      entropy = logf(sum) - fmaf(hit, Folded::finite(-d), f.fold) / sum;
-    }
-  }
-  p.lse[t] = lse;
-  p.logp[t] = logp;
-  p.entropy[t] = entropy < 0.f ? 0.f : entropy;  // off by a rounding where one entry has it all
+  score_rows<kTokens, kRowThreads>(p, int64_t(blockIdx.x) * kTokens, threadIdx.x, sh, [] { __syncthreads(); });
 }
 
 // The slices of dH's sums joined in order, scaled and rounded: 4 elements per thread and step. Bound by reading

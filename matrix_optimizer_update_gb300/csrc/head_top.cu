@@ -3,27 +3,28 @@
 // The logits of one piece of the vocabulary lie in memory, and each group's largest is known. A token's `held`
 // largest entries, in the order (logit descending, id ascending), lie in the `held` first groups in the order
 // (largest logit descending, group ascending): of an entry in another group, each of those groups has one that comes
-// before it. So a block per token reads the groups' peaks, and of the logits only those groups'.
+// before it. So of the logits only those groups' are read.
 //
 // Logits come from the tensor cores in fp32, off by about 1e-6 of themselves; alternatives nearer to each other than
 // that would change places with the way the product is cut. `top` + kSpare entries are held, and where neighbours are
 // too near to tell, their products are formed again with compensated sums, which decide the order.
+//
+// A warp per token: the search for the last of `held` peaks is a count over the warp for each bit that they differ in,
+// without a barrier. (A block per token took 105 us for 4093 tokens x 32768 entries, 15 us for one token.)
 #include <algorithm>
-#include <climits>
 #include <cmath>
 
 #include "follow.cuh"
 #include "head.h"
 #include "head_dot.cuh"
+#include "head_score.cuh"
 
 namespace dmuon {
 namespace head {
 namespace {
 
-constexpr int kTopThreads = 256;
-constexpr int kTopWarps = kTopThreads / 32;
-constexpr int kRanked = 512;       // so many candidates are put in order by counting
-constexpr int kStagedGroups = 4096;  // so many groups' peaks are kept in shared memory
+constexpr int kTopWarps = 8;
+constexpr int kCandidates = 256;  // that a warp has room for
 
 // Unsigned numbers in the order of the floats (NaN above or below all others, by its sign).
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -39,38 +40,52 @@ __device__ __forceinline__ uint64_t order_of(double v) {
 }
 
 struct TopShared {
-  int red[2][kTopWarps];
-  int wanted[kHeld];        // groups
-  int groups, candidates;
-  uint64_t sorted[kHeld + 1];
-  int cluster[kHeld + 1];   // first place of those it cannot be told from
-  uint64_t exact[kHeld + 1];
+  uint64_t cand[kCandidates];     // (logit, ~id)
+  uint64_t sorted[kHeld];
+  uint64_t exact[kHeld];
+  int wanted[kHeld];              // groups
 };
 
-// The sum over the block; `turn` alternates between calls, so that one barrier is enough.
-__device__ __forceinline__ int block_count(TopShared& sh, int n, int& turn) {
-  n = __reduce_add_sync(0xffffffffu, n);
-  int* red = sh.red[turn & 1];
-  ++turn;
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = n;
-  __syncthreads();
-  int all = 0;
-#pragma unroll
-  for (int w = 0; w < kTopWarps; ++w) all += red[w];
-  return all;
-}
-
-// The largest number that at least `want` keys reach (all keys are at least 0; there are at least `want`), found bit
-// by bit; `count(limit)` says how many of this thread's keys reach a limit. Stops where exactly `want` do.
+// The largest number that at least `want` of the warp's numbers reach (they lie between low and high, and there are
+// so many); `count(limit)` says how many of this lane's reach a limit. Stops where exactly `want` do.
 template <typename T, class Count>
-__device__ __forceinline__ T threshold(TopShared& sh, int want, int& turn, Count&& count) {
-  T at = 0;
-  for (int bit = static_cast<int>(sizeof(T)) * 8 - 1; bit >= 0; --bit) {
+__device__ __forceinline__ T threshold(int want, T low, T high, Count&& count) {
+  const T differ = low ^ high;
+  if (differ == 0) return high;
+  int bit = sizeof(T) == 8 ? 63 - __clzll(static_cast<long long>(differ)) : 31 - __clz(static_cast<int>(differ));
+  T at = bit + 1 < static_cast<int>(sizeof(T)) * 8 ? high >> (bit + 1) << (bit + 1) : 0;  // what they share
+  for (; bit >= 0; --bit) {
     const T next = at | (T(1) << bit);
-    const int n = block_count(sh, count(next), turn);
+    const int n = __reduce_add_sync(0xffffffffu, count(next));
     if (n >= want) at = next;
     if (n == want) break;
   }
+  return at;
+}
+
+// Leaves the first `held` of n candidates, in any order.
+__device__ __forceinline__ int compress(TopShared& sh, int n, int held, int lane) {
+  if (n <= held) return n;
+  __syncwarp();
+  uint64_t mine[kCandidates / 32];
+#pragma unroll
+  for (int k = 0; k < kCandidates / 32; ++k) mine[k] = k * 32 + lane < n ? sh.cand[k * 32 + lane] : 0;
+  const uint64_t least = threshold<uint64_t>(held, 0, ~uint64_t(0), [&](uint64_t limit) {
+    int c = 0;
+#pragma unroll
+    for (int k = 0; k < kCandidates / 32; ++k) c += mine[k] >= limit;
+    return c;
+  });
+  __syncwarp();
+  int at = 0;
+#pragma unroll
+  for (int k = 0; k < kCandidates / 32; ++k) {
+    const bool on = mine[k] >= least && mine[k] != 0;
+    const unsigned b = __ballot_sync(0xffffffffu, on);
+    if (on) sh.cand[at + __popc(b & ((1u << lane) - 1u))] = mine[k];
+    at += __popc(b);
+  }
+  __syncwarp();
   return at;
 }
 
@@ -103,165 +118,218 @@ __device__ __forceinline__ double exact_dot(const DotParams& d, int64_t t, int64
   return s;
 }
 
-__global__ void __launch_bounds__(kTopThreads) top_kernel(const __grid_constant__ TopParams p) {
-  extern __shared__ __align__(8) uint8_t dynamic[];
-  __shared__ TopShared sh;
-  uint32_t* peaks = reinterpret_cast<uint32_t*>(dynamic);   // the groups', then
-  uint64_t* cand = reinterpret_cast<uint64_t*>(dynamic);    // (logit, ~id) of the candidates
-  follow();
-  const int64_t t = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// KEYS: the piece has at most 32 * KEYS groups, whose peaks are held in registers; 0: any number, read again each time.
+// `scored` returns once the token's log sum and probability are there.
+template <int KEYS, class Scored>
+__device__ __forceinline__ void top_of(const TopParams& p, int64_t t, int lane, TopShared& sh, Scored&& scored) {
   const int held = p.top + kSpare;
-  int turn = 0;
-
-  // ---------------------------------------------------------- the groups with the largest peaks
+  // ---------------------------------------------------------- the groups with the largest peaks, by their number
   const Part* parts = p.parts + t * p.token_step;
-  const bool staged = p.groups <= kStagedGroups;
-  auto peak_of = [&](int g) { return staged ? peaks[g] : order_of(parts[g * p.group_step].peak); };
-  if (staged)
-    for (int g = tid; g < p.groups; g += kTopThreads) peaks[g] = order_of(parts[g * p.group_step].peak);
-  if (tid == 0) sh.groups = sh.candidates = 0;
-  __syncthreads();
-  uint32_t least = 0;      // logits below it are not among the largest
-  int up_to = INT_MAX;     // of groups whose peak is `least`, those before
+  const int turns = KEYS != 0 ? KEYS : (p.groups + 31) / 32;
+  uint32_t key[KEYS != 0 ? KEYS : 1] = {};
+  auto read = [&](int g) { return g < p.groups ? order_of(parts[g * p.group_step].peak) : 0u; };
+  auto peak = [&](int k) { return KEYS != 0 ? key[k] : read(k * 32 + lane); };
+  uint32_t low = 0xffffffffu, high = 0u;
+#pragma unroll
+  for (int k = 0; k < turns; ++k) {
+    const uint32_t v = read(k * 32 + lane);
+    if (KEYS != 0) key[k] = v;
+    if (k * 32 + lane < p.groups) low = min(low, v);
+    high = max(high, v);
+  }
+  uint32_t least = 0u;  // logits below it are not among the largest
+  int level = 0;        // of the groups whose peak is `least`, the first so many
   if (p.groups > held) {
-    least = threshold<uint32_t>(sh, held, turn, [&](uint32_t limit) {
-      int n = 0;
-      for (int g = tid; g < p.groups; g += kTopThreads) n += peak_of(g) >= limit;
-      return n;
-    });
-    int above = 0, level = 0;
-    for (int g = tid; g < p.groups; g += kTopThreads) {
-      above += peak_of(g) > least;
-      level += peak_of(g) == least;
-    }
-    above = block_count(sh, above, turn);
-    level = block_count(sh, level, turn);
-    if (above + level > held) {
-      // the first of the groups that share the last peak: `up_to` counts how many numbers may be too high
-      const uint32_t below = threshold<uint32_t>(sh, held - above, turn, [&](uint32_t limit) {
-        int n = 0;
-        for (int g = tid; g < p.groups; g += kTopThreads)
-          n += peak_of(g) == least && ~static_cast<uint32_t>(g) >= limit;
-        return n;
-      });
-      up_to = static_cast<int>(~below);  // groups 0 .. up_to
-    }
+    least = threshold<uint32_t>(held, __reduce_min_sync(0xffffffffu, low), __reduce_max_sync(0xffffffffu, high),
+                                [&](uint32_t limit) {
+                                  int n = 0;
+#pragma unroll
+                                  for (int k = 0; k < turns; ++k) n += peak(k) >= limit;
+                                  return n;
+                                });
+    int above = 0;
+#pragma unroll
+    for (int k = 0; k < turns; ++k) above += peak(k) > least;
+    level = held - __reduce_add_sync(0xffffffffu, above);
+  } else {
+    level = held;
   }
-  for (int g = tid; g < p.groups; g += kTopThreads) {
-    const uint32_t k = peak_of(g);
-    if (k > least || (k == least && g <= up_to)) {
-      const int at = atomicAdd(&sh.groups, 1);
-      if (at < held) sh.wanted[at] = g;
-    }
+  int wanted = 0;
+#pragma unroll
+  for (int k = 0; k < turns; ++k) {
+    const int g = k * 32 + lane;
+    const bool same = g < p.groups && peak(k) == least;
+    const unsigned b = __ballot_sync(0xffffffffu, same);
+    const bool on = g < p.groups && (peak(k) > least || (same && __popc(b & ((1u << lane) - 1u)) < level));
+    level -= __popc(b);
+    const unsigned w = __ballot_sync(0xffffffffu, on);
+    if (on) sh.wanted[wanted + __popc(w & ((1u << lane) - 1u))] = g;
+    wanted += __popc(w);
   }
-  __syncthreads();
+  __syncwarp();
 
-  // ---------------------------------------------------------- their entries, and the list so far
+  // ---------------------------------------------------------- their entries, the target, and the list so far
   const int64_t y = p.targets != nullptr ? p.targets[t] : -1;
-  const int per = p.thin_h != 0 ? 32 : kGroup, wanted = min(sh.groups, held);
-  auto add = [&](float z, int id) {
-    cand[atomicAdd(&sh.candidates, 1)] = (static_cast<uint64_t>(order_of(z)) << 32) | (~static_cast<uint32_t>(id));
+  const float* z = p.z + t * p.ld_z;
+  int n = 0;
+  auto add = [&](bool on, float v, int id) {
+    const unsigned b = __ballot_sync(0xffffffffu, on);
+    if (on)
+      sh.cand[n + __popc(b & ((1u << lane) - 1u))] =
+          (static_cast<uint64_t>(order_of(v)) << 32) | (~static_cast<uint32_t>(id));
+    n += __popc(b);
   };
-  for (int i = tid; i < wanted * per; i += kTopThreads) {
-    const int g = sh.wanted[i / per];
-    int id, end = p.v0 + p.width;
-    if (p.thin_h != 0) {  // tile g / 8, half g / 4 % 2, 32 entries from g % 4 * 32
-      const int first = p.v0 + (g >> 3) * p.thin_h + ((g >> 2) & 1) * (p.thin_h / 2);
-      end = min(end, first + p.thin_h / 2);
-      id = first + (g & 3) * 32 + i % per;
-    } else {
-      id = p.v0 + g * kGroup + i % per;
+  constexpr int kBatch = 4;  // groups whose loads are in flight together
+  for (int i0 = 0; i0 < wanted; i0 += kBatch) {
+    float4 v[kBatch];
+    int id[kBatch], end[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      id[u] = end[u] = 0;
+      if (i0 + u >= wanted) continue;
+      const int g = sh.wanted[i0 + u];
+      end[u] = p.v0 + p.width;
+      if (p.thin_h != 0) {  // tile g / 8, half g / 4 % 2, 32 entries from g % 4 * 32
+        const int first = p.v0 + (g >> 3) * p.thin_h + ((g >> 2) & 1) * (p.thin_h / 2);
+        end[u] = min(end[u], first + p.thin_h / 2);
+        id[u] = first + (g & 3) * 32 + lane;
+        if (id[u] < end[u]) v[u].x = z[id[u] - p.v0];
+      } else {  // four entries a lane; past the last group's the row goes on to a multiple of 256
+        id[u] = p.v0 + g * kGroup + 4 * lane;
+        v[u] = *reinterpret_cast<const float4*>(z + (id[u] - p.v0));
+      }
     }
-    if (id >= end || id == y) continue;
-    const float z = p.z[t * p.ld_z + (id - p.v0)];
-    if (order_of(z) >= least) add(z, id);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (i0 + u >= wanted) break;
+      if (n > kCandidates - kGroup) n = compress(sh, n, held, lane);
+      const float w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k > 0 && p.thin_h != 0) break;
+        add(id[u] + k < end[u] && id[u] + k != y && order_of(w[k]) >= least, w[k], id[u] + k);
+      }
+    }
   }
-  if (!p.first)
-    for (int i = tid; i < held; i += kTopThreads)
-      if (p.list_id[t * kHeld + i] >= 0) add(p.list_z[t * kHeld + i], p.list_id[t * kHeld + i]);
+  if (n > kCandidates - kHeld - 1) n = compress(sh, n, held, lane);
   // the groups' peaks leave the target out: its logit goes in by itself
-  if (tid == 0 && y >= p.v0 && y < p.v0 + p.width) add(p.z[t * p.ld_z + (y - p.v0)], static_cast<int>(y));
-  __syncthreads();
-  int n = sh.candidates;
+  const bool here = y >= p.v0 && y < p.v0 + p.width;
+  if (here) add(lane == 0, z[y - p.v0], static_cast<int>(y));
+  if (!p.first)
+    for (int i = lane; i - lane < held; i += 32) {
+      const int id = i < held ? p.list_id[t * kHeld + i] : -1;
+      add(id >= 0, id >= 0 ? p.list_z[t * kHeld + i] : 0.f, id);
+    }
+  __syncwarp();
 
   // ---------------------------------------------------------- the first of them, in order
   const int keep = min(n, held);
-  uint64_t reach = 0;
-  if (n > kRanked)
-    reach = threshold<uint64_t>(sh, keep, turn, [&](uint64_t limit) {
-      int m = 0;
-      for (int i = tid; i < n; i += kTopThreads) m += cand[i] >= limit;
-      return m;
-    });
-  for (int i = tid; i < n; i += kTopThreads) {
-    const uint64_t mine = cand[i];
-    if (mine < reach) continue;
+  for (int i = lane; i < n; i += 32) {
+    const uint64_t mine = sh.cand[i];
     int place = 0;
-    for (int j = 0; j < n; ++j) place += cand[j] > mine;
+    for (int j = 0; j < n; ++j) place += sh.cand[j] > mine;
     if (place < keep) sh.sorted[place] = mine;
   }
-  __syncthreads();
+  __syncwarp();
+  auto z_at = [&](int i) { return value_of(static_cast<uint32_t>(sh.sorted[i] >> 32)); };
+  auto id_at = [&](int i) { return static_cast<int>(~static_cast<uint32_t>(sh.sorted[i])); };
   if (!p.last) {
-    for (int i = tid; i < held; i += kTopThreads) {
-      p.list_z[t * kHeld + i] = i < keep ? value_of(static_cast<uint32_t>(sh.sorted[i] >> 32)) : 0.f;
-      p.list_id[t * kHeld + i] = i < keep ? static_cast<int>(~static_cast<uint32_t>(sh.sorted[i])) : -1;
+    for (int i = lane; i < held; i += 32) {
+      p.list_z[t * kHeld + i] = i < keep ? z_at(i) : 0.f;
+      p.list_id[t * kHeld + i] = i < keep ? id_at(i) : -1;
     }
     return;
   }
 
   // ---------------------------------------------------------- neighbours too near to tell
-  auto z_at = [&](int i) { return value_of(static_cast<uint32_t>(sh.sorted[i] >> 32)); };
-  auto id_at = [&](int i) { return static_cast<int>(~static_cast<uint32_t>(sh.sorted[i])); };
-  if (tid == 0) {
-    // what the products may be off by: 2^-14 of the logits up to 16384 dims, in proportion above (header: 2e-9 * dim)
-    const float part = 0x1p-14f * fmaxf(1.f, p.dot.dim / 16384.f);
-    for (int i = 0; i < keep; ++i) {
-      const float a = i > 0 ? z_at(i - 1) : 0.f, b = z_at(i);
-      const bool apart = i == 0 || a - b > part * (p.dot.scale + fabsf(a));
-      sh.cluster[i] = apart ? i : sh.cluster[i - 1];
+  // what the products may be off by: 2^-14 of the logits up to 16384 dims, in proportion above (header: 2e-9 * dim)
+  const float part = 0x1p-14f * fmaxf(1.f, p.dot.dim / 16384.f);
+  uint64_t starts = 0;  // places whose entry is surely below the one before
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = 32 * h + lane;
+    bool apart = true;
+    if (i > 0 && i < keep) {
+      const float a = z_at(i - 1), b = z_at(i);
+      apart = a - b > part * (p.dot.scale + fabsf(a));
     }
+    starts |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, apart)) << (32 * h);
   }
-  __syncthreads();
-  auto shared = [&](int i) {
-    const int c = sh.cluster[i];
-    return c < p.top && (c != i || (i + 1 < keep && sh.cluster[i + 1] == c));
-  };
-  for (int i = warp; i < keep; i += kTopWarps)
+  // entry i shares its place where it or the next one is not a start; its run begins at the last start up to it
+  auto begin = [&](int i) { return 63 - __clzll(static_cast<long long>(starts & ((uint64_t(2) << i) - 1))); };
+  auto shared = [&](int i) { return begin(i) < p.top && (~(starts >> i) & (i + 1 < keep ? 3 : 1)) != 0; };
+  for (int i = 0; i < keep; ++i)
     if (shared(i)) {
-      const double z = exact_dot(p.dot, t, id_at(i), lane);
-      if (lane == 0) sh.exact[i] = order_of(z + 0.0);
+      const double d = exact_dot(p.dot, t, id_at(i), lane);
+      if (lane == 0) sh.exact[i] = order_of(d + 0.0);
     }
-  __syncthreads();
-  if (tid < keep) {
-    int place = tid;
-    const int c = sh.cluster[tid];
-    if (shared(tid)) {
-      place = c;
-      for (int j = c; j < keep && sh.cluster[j] == c; ++j)
-        place += sh.exact[j] > sh.exact[tid] || (sh.exact[j] == sh.exact[tid] && id_at(j) < id_at(tid));
+  __syncwarp();
+  scored();
+  const float lse = p.lse[t], logp = p.logp[t];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = 32 * h + lane;
+    if (i >= keep) continue;
+    int place = i;
+    const int id = id_at(i);
+    if (shared(i)) {
+      place = begin(i);
+      for (int j = place; j < keep && begin(j) == begin(i); ++j)
+        place += sh.exact[j] > sh.exact[i] || (sh.exact[j] == sh.exact[i] && id_at(j) < id);
     }
     if (place < p.top) {
-      const int id = id_at(tid);
       p.top_ids[t * p.top + place] = id;
-      p.top_logp[t * p.top + place] = id == y ? p.logp[t] : z_at(tid) - p.lse[t];
+      p.top_logp[t * p.top + place] = id == y ? logp : z_at(i) - lse;
     }
   }
-  for (int i = keep + tid; i < p.top; i += kTopThreads) {
+  for (int i = keep + lane; i < p.top; i += 32) {
     p.top_ids[t * p.top + i] = -1;
     p.top_logp[t * p.top + i] = -INFINITY;
+  }
+}
+
+template <int KEYS>
+__global__ void __launch_bounds__(32 * kTopWarps) top_kernel(const __grid_constant__ TopParams p) {
+  __shared__ TopShared sh[kTopWarps];
+  follow();
+  const int warp = threadIdx.x >> 5;
+  const int64_t t = int64_t(blockIdx.x) * (blockDim.x >> 5) + warp;
+  if (t < p.tokens) top_of<KEYS>(p, t, threadIdx.x & 31, sh[warp], [] {});
+}
+
+// Few tokens: a block each, whose first warp finds the alternatives while the others join the groups' sums. (A launch
+// less: one token x 32000 x 2048 38 -> 34 us.)
+constexpr int kRestThreads = 256;  // as where no alternatives are asked for: the same sums
+template <int KEYS>
+__global__ void __launch_bounds__(32 + kRestThreads) score_top_kernel(const __grid_constant__ ScoreParams r,
+                                                                      const __grid_constant__ TopParams p) {
+  __shared__ TopShared sh;
+  __shared__ ScoreShared<1, kRestThreads> rows;
+  follow();
+  if (threadIdx.x < 32) {
+    top_of<KEYS>(p, blockIdx.x, threadIdx.x, sh, [] { __syncthreads(); });
+  } else {
+    score_rows<1, kRestThreads>(r, blockIdx.x, threadIdx.x - 32, rows, [] { asm volatile("bar.sync 1, 256;" ::: "memory"); });
+    __syncthreads();
   }
 }
 
 }  // namespace
 
 cudaError_t launch_top(const TopParams& p, cudaStream_t s) {
-  const int held = p.top + kSpare, per = p.thin_h != 0 ? 32 : kGroup;
-  const size_t staged = sizeof(uint32_t) * std::min(p.groups, kStagedGroups);
-  const size_t smem = std::max(staged, sizeof(uint64_t) * (held * per + held + 1));
-  constexpr size_t most = sizeof(uint64_t) * (kHeld * kGroup + kHeld + 1);
-  static_assert(most >= sizeof(uint32_t) * kStagedGroups && most + sizeof(TopShared) < 48 * 1024, "no opt-in needed");
-  return launch_follow(top_kernel, dim3(static_cast<unsigned>(p.tokens)), kTopThreads, smem, s, 1, p);
+  // as many warps to a block as leave each SM one: the tokens of a block lie next to each other in the groups' sums
+  const int warps = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kTopWarps, p.tokens / 128)));
+  const dim3 grid(static_cast<unsigned>((p.tokens + warps - 1) / warps));
+  if (p.groups <= 256) return launch_follow(top_kernel<8>, grid, 32 * warps, 0, s, 1, p);
+  if (p.groups <= 1024) return launch_follow(top_kernel<32>, grid, 32 * warps, 0, s, 1, p);
+  return launch_follow(top_kernel<0>, grid, 32 * warps, 0, s, 1, p);
+}
+
+cudaError_t launch_score_top(const ScoreParams& r, const TopParams& p, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(p.tokens));
+  if (p.groups <= 1024) return launch_follow(score_top_kernel<32>, grid, 32 + kRestThreads, 0, s, 1, r, p);
+  return launch_follow(score_top_kernel<0>, grid, 32 + kRestThreads, 0, s, 1, r, p);
 }
 
 }  // namespace head
