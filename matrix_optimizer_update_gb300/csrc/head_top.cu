@@ -95,21 +95,30 @@ __device__ __forceinline__ void two_sum(float& sum, float& rest, float x) {
   sum = s;
 }
 
-// A logit (unscaled) by one warp: products of bf16 are exact in fp32, their sums are compensated.
+// A logit (unscaled) by one warp: products of bf16 are exact in fp32, their sums are compensated. Four rounds of loads
+// are in flight, as the trip to memory is what it takes.
 __device__ __forceinline__ double exact_dot(const DotParams& d, int64_t t, int64_t v, int lane) {
   float sum = 0.f, rest = 0.f;
   const bf16 *h = d.hidden + t * d.ld_hidden, *w = d.weight + v * d.ld_weight;
   const int whole = d.dim / 8;
-#pragma unroll 2
-  for (int c = lane; c < whole; c += 32) {
-    const uint4 a = *reinterpret_cast<const uint4*>(h + 8 * c), b = *reinterpret_cast<const uint4*>(w + 8 * c);
-    const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162*>(&a),
-                         *y = reinterpret_cast<const __nv_bfloat162*>(&b);
+  for (int c0 = lane; c0 < whole; c0 += 4 * 32) {
+    uint4 a[4], b[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = __bfloat1622float2(x[k]), g = __bfloat1622float2(y[k]);
-      two_sum(sum, rest, f.x * g.x);
-      two_sum(sum, rest, f.y * g.y);
+    for (int u = 0; u < 4; ++u) {
+      const bool in = c0 + 32 * u < whole;
+      a[u] = in ? *reinterpret_cast<const uint4*>(h + 8 * (c0 + 32 * u)) : make_uint4(0, 0, 0, 0);
+      b[u] = in ? *reinterpret_cast<const uint4*>(w + 8 * (c0 + 32 * u)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162*>(&a[u]),
+                           *y = reinterpret_cast<const __nv_bfloat162*>(&b[u]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = __bfloat1622float2(x[k]), g = __bfloat1622float2(y[k]);
+        two_sum(sum, rest, f.x * g.x);
+        two_sum(sum, rest, f.y * g.y);
+      }
     }
   }
   for (int k = 8 * whole + lane; k < d.dim; k += 32) two_sum(sum, rest, __bfloat162float(h[k]) * __bfloat162float(w[k]));
@@ -118,56 +127,64 @@ __device__ __forceinline__ double exact_dot(const DotParams& d, int64_t t, int64
   return s;
 }
 
-// KEYS: the piece has at most 32 * KEYS groups, whose peaks are held in registers; 0: any number, read again each time.
-// `scored` returns once the token's log sum and probability are there.
-template <int KEYS, class Scored>
-__device__ __forceinline__ void top_of(const TopParams& p, int64_t t, int lane, TopShared& sh, Scored&& scored) {
-  const int held = p.top + kSpare;
-  // ---------------------------------------------------------- the groups with the largest peaks, by their number
-  const Part* parts = p.parts + t * p.token_step;
-  const int turns = KEYS != 0 ? KEYS : (p.groups + 31) / 32;
+// The first `held` of n keys in the order (key descending, number ascending): take(place, number, key) for each, by
+// ascending number. Returns how many. KEYS: n is at most 32 * KEYS, and the keys are held in registers; 0: any n,
+// read again each time. read(i) gives a key for i < n; keys of 0 are not there.
+template <int KEYS, class Read, class Take>
+__device__ __forceinline__ int pick(int n, int held, int lane, Read&& read, Take&& take) {
+  const int turns = KEYS != 0 ? KEYS : (n + 31) / 32;
   uint32_t key[KEYS != 0 ? KEYS : 1] = {};
-  auto read = [&](int g) { return g < p.groups ? order_of(parts[g * p.group_step].peak) : 0u; };
-  auto peak = [&](int k) { return KEYS != 0 ? key[k] : read(k * 32 + lane); };
+  auto at = [&](int k) { return KEYS != 0 ? key[k] : k * 32 + lane < n ? read(k * 32 + lane) : 0u; };
   uint32_t low = 0xffffffffu, high = 0u;
+  int there = 0;
 #pragma unroll
   for (int k = 0; k < turns; ++k) {
-    const uint32_t v = read(k * 32 + lane);
+    const uint32_t v = k * 32 + lane < n ? read(k * 32 + lane) : 0u;
     if (KEYS != 0) key[k] = v;
-    if (k * 32 + lane < p.groups) low = min(low, v);
+    if (v != 0u) low = min(low, v);
     high = max(high, v);
+    there += v != 0u;
   }
-  uint32_t least = 0u;  // logits below it are not among the largest
-  int level = 0;        // of the groups whose peak is `least`, the first so many
-  if (p.groups > held) {
+  uint32_t least = 1u;  // keys above it are among the first, and of those at it the first `level`
+  int level = held;
+  if (__reduce_add_sync(0xffffffffu, there) > held) {
     least = threshold<uint32_t>(held, __reduce_min_sync(0xffffffffu, low), __reduce_max_sync(0xffffffffu, high),
                                 [&](uint32_t limit) {
-                                  int n = 0;
+                                  int c = 0;
 #pragma unroll
-                                  for (int k = 0; k < turns; ++k) n += peak(k) >= limit;
-                                  return n;
+                                  for (int k = 0; k < turns; ++k) c += at(k) >= limit;
+                                  return c;
                                 });
     int above = 0;
 #pragma unroll
-    for (int k = 0; k < turns; ++k) above += peak(k) > least;
+    for (int k = 0; k < turns; ++k) above += at(k) > least;
     level = held - __reduce_add_sync(0xffffffffu, above);
-  } else {
-    level = held;
   }
-  int wanted = 0;
+  int taken = 0;
 #pragma unroll
   for (int k = 0; k < turns; ++k) {
-    const int g = k * 32 + lane;
-    const bool same = g < p.groups && peak(k) == least;
-    const unsigned b = __ballot_sync(0xffffffffu, same);
-    const bool on = g < p.groups && (peak(k) > least || (same && __popc(b & ((1u << lane) - 1u)) < level));
-    level -= __popc(b);
+    const uint32_t v = at(k);
+    const unsigned same = __ballot_sync(0xffffffffu, v == least);
+    const bool on = v > least || (v == least && __popc(same & ((1u << lane) - 1u)) < level);
+    level -= __popc(same);
     const unsigned w = __ballot_sync(0xffffffffu, on);
-    if (on) sh.wanted[wanted + __popc(w & ((1u << lane) - 1u))] = g;
-    wanted += __popc(w);
+    if (on) take(taken + __popc(w & ((1u << lane) - 1u)), k * 32 + lane, v);
+    taken += __popc(w);
   }
-  __syncwarp();
+  return taken;
+}
 
+// A group's key: its peak in order, above 0 (where only a NaN would lie).
+__device__ __forceinline__ uint32_t peak_of(const TopParams& p, int64_t t, int g) {
+  return max(order_of(p.parts[t * p.token_step + g * p.group_step].peak), 1u);
+}
+
+// A token's alternatives among the entries of `wanted` groups, whose peaks are at least `least`, the target and the
+// list so far. `scored` returns once the token's log sum and probability are there.
+template <class Scored>
+__device__ __forceinline__ void top_of(const TopParams& p, int64_t t, int lane, TopShared& sh, int wanted, uint32_t least,
+                                       Scored&& scored) {
+  const int held = p.top + kSpare;
   // ---------------------------------------------------------- their entries, the target, and the list so far
   const int64_t y = p.targets != nullptr ? p.targets[t] : -1;
   const float* z = p.z + t * p.ld_z;
@@ -243,8 +260,10 @@ __device__ __forceinline__ void top_of(const TopParams& p, int64_t t, int lane, 
   }
 
   // ---------------------------------------------------------- neighbours too near to tell
-  // what the products may be off by: 2^-14 of the logits up to 16384 dims, in proportion above (header: 2e-9 * dim)
-  const float part = 0x1p-14f * fmaxf(1.f, p.dot.dim / 16384.f);
+  // What two products may be off by against each other: at most 2.2e-9 * dim of the largest partial sum of each, which
+  // is their logit and some standard deviations of the rest; twice that (at 4096 dims 5e-4 at a logit of 12), and
+  // no less than what fp32 sums of 512 terms have.
+  const float part = 6e-9f * fmaxf(512.f, static_cast<float>(p.dot.dim));
   uint64_t starts = 0;  // places whose entry is surely below the one before
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -252,7 +271,7 @@ __device__ __forceinline__ void top_of(const TopParams& p, int64_t t, int lane, 
     bool apart = true;
     if (i > 0 && i < keep) {
       const float a = z_at(i - 1), b = z_at(i);
-      apart = a - b > part * (p.dot.scale + fabsf(a));
+      apart = a - b > part * (8.f * p.dot.scale + fabsf(a));
     }
     starts |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, apart)) << (32 * h);
   }
@@ -291,26 +310,62 @@ __device__ __forceinline__ void top_of(const TopParams& p, int64_t t, int lane, 
 
 template <int KEYS>
 __global__ void __launch_bounds__(32 * kTopWarps) top_kernel(const __grid_constant__ TopParams p) {
-  __shared__ TopShared sh[kTopWarps];
+  __shared__ TopShared all[kTopWarps];
   follow();
-  const int warp = threadIdx.x >> 5;
-  const int64_t t = int64_t(blockIdx.x) * (blockDim.x >> 5) + warp;
-  if (t < p.tokens) top_of<KEYS>(p, t, threadIdx.x & 31, sh[warp], [] {});
+  const int lane = threadIdx.x & 31;
+  TopShared& sh = all[threadIdx.x >> 5];
+  const int64_t t = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (t >= p.tokens) return;
+  uint32_t least = 0xffffffffu;
+  const int wanted = pick<KEYS>(p.groups, p.top + kSpare, lane, [&](int g) { return peak_of(p, t, g); },
+                                [&](int place, int g, uint32_t key) {
+                                  sh.wanted[place] = g;
+                                  least = min(least, key);
+                                });
+  least = __reduce_min_sync(0xffffffffu, least);
+  __syncwarp();
+  top_of(p, t, lane, sh, wanted, p.groups > wanted ? least : 0u, [] {});
 }
 
-// Few tokens: a block each, whose first warp finds the alternatives while the others join the groups' sums. (A launch
-// less: one token x 32000 x 2048 38 -> 34 us.)
-constexpr int kRestThreads = 256;  // as where no alternatives are asked for: the same sums
+// Few tokens: a block each. Eight warps find the first groups, each of an eighth of them, and the first warp of those
+// and the alternatives; meanwhile eight others join the groups' sums.
+constexpr int kJoinThreads = 256;  // as where no alternatives are asked for: the same sums
 template <int KEYS>
-__global__ void __launch_bounds__(32 + kRestThreads) score_top_kernel(const __grid_constant__ ScoreParams r,
-                                                                      const __grid_constant__ TopParams p) {
+__global__ void __launch_bounds__(32 * kTopWarps + kJoinThreads) score_top_kernel(const __grid_constant__ ScoreParams r,
+                                                                                  const __grid_constant__ TopParams p) {
   __shared__ TopShared sh;
-  __shared__ ScoreShared<1, kRestThreads> rows;
+  __shared__ ScoreShared<1, kJoinThreads> rows;
+  __shared__ uint32_t first_key[kTopWarps * kHeld];
+  __shared__ int first_group[kTopWarps * kHeld];
   follow();
-  if (threadIdx.x < 32) {
-    top_of<KEYS>(p, blockIdx.x, threadIdx.x, sh, [] { __syncthreads(); });
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp >= kTopWarps) {
+    score_rows<1, kJoinThreads>(r, t, threadIdx.x - 32 * kTopWarps, rows, [] { asm volatile("bar.sync 1, 256;" ::: "memory"); });
+    __syncthreads();
+    return;
+  }
+  const int held = p.top + kSpare, share = (p.groups + kTopWarps - 1) / kTopWarps;
+  const int begin = min(warp * share, p.groups), n = min(share, p.groups - begin);
+  for (int i = lane; i < kHeld; i += 32) first_key[warp * kHeld + i] = 0u;
+  __syncwarp();
+  pick<KEYS>(n, held, lane, [&](int i) { return peak_of(p, t, begin + i); },
+             [&](int place, int i, uint32_t key) {
+               first_key[warp * kHeld + place] = key;
+               first_group[warp * kHeld + place] = begin + i;
+             });
+  asm volatile("bar.sync 2, 256;" ::: "memory");
+  if (warp == 0) {
+    uint32_t least = 0xffffffffu;
+    const int wanted = pick<kTopWarps * kHeld / 32>(kTopWarps * kHeld, held, lane, [&](int i) { return first_key[i]; },
+                                                    [&](int place, int i, uint32_t key) {
+                                                      sh.wanted[place] = first_group[i];
+                                                      least = min(least, key);
+                                                    });
+    least = __reduce_min_sync(0xffffffffu, least);
+    __syncwarp();
+    top_of(p, t, lane, sh, wanted, p.groups > wanted ? least : 0u, [] { __syncthreads(); });
   } else {
-    score_rows<1, kRestThreads>(r, blockIdx.x, threadIdx.x - 32, rows, [] { asm volatile("bar.sync 1, 256;" ::: "memory"); });
     __syncthreads();
   }
 }
@@ -328,8 +383,10 @@ cudaError_t launch_top(const TopParams& p, cudaStream_t s) {
 
 cudaError_t launch_score_top(const ScoreParams& r, const TopParams& p, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.tokens));
-  if (p.groups <= 1024) return launch_follow(score_top_kernel<32>, grid, 32 + kRestThreads, 0, s, 1, r, p);
-  return launch_follow(score_top_kernel<0>, grid, 32 + kRestThreads, 0, s, 1, r, p);
+  const int threads = 32 * kTopWarps + kJoinThreads;
+  if (p.groups <= 256 * kTopWarps) return launch_follow(score_top_kernel<8>, grid, threads, 0, s, 1, r, p);
+  if (p.groups <= 1024 * kTopWarps) return launch_follow(score_top_kernel<32>, grid, threads, 0, s, 1, r, p);
+  return launch_follow(score_top_kernel<0>, grid, threads, 0, s, 1, r, p);
 }
 
 }  // namespace head
