@@ -70,10 +70,10 @@ struct ExpertsParams {
   unsigned* status;
 };
 
-// ... and the matrices as rows of K: gate or down, and up, in the boxes of a whole job and in boxes of 8 rows.
+// ... and the matrices as rows of K (gate or down, and up), in boxes of 1, 2 and 4 row blocks.
 struct StreamParams {
   ExpertsParams e;
-  CUtensorMap whole[2], part[2];
+  CUtensorMap boxes[2][3];
 };
 
 // What a block knows of the routing: the experts in use in ascending order, and each one's assignments.
@@ -320,7 +320,7 @@ __device__ __forceinline__ int cut(const Routing& r, int blocks, int64_t part, i
   return r.actives * blocks;
 }
 
-// A block's run of row blocks, as many at a time as one expert has in it, at most kTogether.
+// A block's run of row blocks, those of an expert in jobs of at most kTogether.
 struct Job {
   int unit, end, blocks;
   int active, first, rows;  // the expert's place among those in use, its first row block, how many
@@ -329,7 +329,9 @@ struct Job {
     if (unit >= end) return false;
     active = unit / blocks;
     first = unit - active * blocks;
-    rows = min(min(kTogether, blocks - first), end - unit);
+    // what the run has of this expert in as few jobs as possible, of about the same size
+    const int left = min(blocks - first, end - unit), jobs = (left + kTogether - 1) / kTogether;
+    rows = (left + jobs - 1) / jobs;
     return true;
   }
 };
@@ -494,8 +496,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1) experts_stream_kernel(const
     }
     sh.abort_flag = 0;
     ptx::fence_mbar_init();
-    ptx::prefetch_tmap(&sp.whole[0]);
-    if (PHASE == kGated) ptx::prefetch_tmap(&sp.whole[1]);
+    for (int k = 0; k < 3; ++k) {
+      ptx::prefetch_tmap(&sp.boxes[0][k]);
+      if (PHASE == kGated) ptx::prefetch_tmap(&sp.boxes[1][k]);
+    }
   }
   // The down products' launch is set up while the up products' still runs: what it reads before follow() was
   // there before that launch began.
@@ -525,8 +529,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) experts_stream_kernel(const
 
   if (warp == kWarps) {
     // ---------------------------------------------------------- loads
-    // A stage: for each chunk of 64 columns 64 rows (gated, 32 of gate and then 32 of up), which boxes of 64 (or 32)
-    // rows bring where the job has all of them, else boxes of 8.
+    // A stage: for each chunk of 64 columns 64 rows (gated, 32 of gate and then 32 of up). A lane to a chunk and kind,
+    // and for three row blocks another to the third.
     uint32_t fills = 0;
     constexpr int kKinds = PHASE == kGated ? 2 : 1;
     bool ok = true;
@@ -540,17 +544,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1) experts_stream_kernel(const
         if (lane == 0) ptx::mbar_arrive_expect_tx(&sh.full[stage], 2 * job.rows * chunks * kBoxBytes);
         __syncwarp();
         uint8_t* at = base + stage * kStageBytes;
-        if (job.rows == kTogether) {
-          const int chunk = lane / kKinds, kind = lane % kKinds;
-          if (chunk < chunks)
-            tma_load_2d(at + chunk * 8 * kBoxBytes + kind * 4 * kBoxBytes, &sp.whole[kind], &sh.full[stage],
-                        x + chunk * kChunk, y);
-        } else {
-          const int chunk = lane >> 3, kind = PHASE == kGated ? (lane >> 2) & 1 : 0;
-          const int group = lane & (PHASE == kGated ? 3 : 7);
-          if (chunk < chunks && group < (PHASE == kGated ? job.rows : 2 * job.rows))
-            tma_load_2d(at + (lane & 7) * kBoxBytes + chunk * 8 * kBoxBytes, &sp.part[kind], &sh.full[stage],
-                        x + chunk * kChunk, y + 8 * group);
+        const int chunk = lane & 3, kind = (lane >> 2) % kKinds, third = lane / (4 * kKinds);
+        if (chunk < chunks && third <= (job.rows == 3)) {
+          const int size = third != 0 ? 0 : job.rows == kTogether ? 2 : job.rows >= 2 ? 1 : 0;
+          constexpr int kBoxRows = PHASE == kGated ? 8 : 16;  // of a row block
+          tma_load_2d(at + chunk * 8 * kBoxBytes + kind * 4 * kBoxBytes + 2 * third * (kBoxRows / 8) * kBoxBytes,
+                      &sp.boxes[kind][size], &sh.full[stage], x + chunk * kChunk, y + 2 * third * kBoxRows);
         }
         ++fills;
         if (++stage == kStages) {
@@ -685,8 +684,8 @@ cudaError_t launch(const ExpertsParams& p, bool stream, int sms, cudaStream_t s)
   e = cudaSuccess;
   for (int kind = 0; kind < (PHASE == kGated ? 2 : 1) && e == cudaSuccess; ++kind) {
     const bf16* m = kind == 0 ? w : p.up;
-    e = map_rows(&sp.whole[kind], m, K, int64_t(p.experts) * rows, kTogether * out);
-    if (e == cudaSuccess) e = map_rows(&sp.part[kind], m, K, int64_t(p.experts) * rows, 8);
+    for (int size = 0; size < 3 && e == cudaSuccess; ++size)
+      e = map_rows(&sp.boxes[kind][size], m, K, int64_t(p.experts) * rows, out << size);
   }
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(units, sms)));
