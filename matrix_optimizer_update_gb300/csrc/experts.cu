@@ -21,6 +21,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include <cudaTypedefs.h>
 
@@ -46,9 +47,9 @@ constexpr int kCostRead = 8, kCostTile = 2;
 constexpr int kTogether = 4;                     // row blocks taken together
 constexpr int kChunk = 64;                       // columns of a TMA box, 128 bytes
 constexpr int kBoxBytes = 8 * 2 * kChunk;        // of 8 rows
-constexpr int kStageK = 4 * kChunk;              // a step of 32 for each warp
+constexpr int kStageK = 4 * kChunk;              // a chunk for each of four warps
 constexpr int kStageBytes = 2 * kTogether * 4 * kBoxBytes;
-constexpr int kStages = 6;
+constexpr int kStages = 6;                       // even: four warps have the even ones, four the odd
 constexpr int kStreamThreads = kThreads + 32;
 constexpr int64_t kWaitNs = 2000000000LL;
 
@@ -60,7 +61,7 @@ struct ExpertsParams {
   const bf16* up;
   const bf16* gate;    // or nullptr
   const bf16* down;
-  bf16* h;             // [2][assignments][ld_h]: h as the sum of two bf16
+  bf16* h;             // [assignments][ld_h / 8][2][8]: h as the sum of two bf16, eight of the first, then of the second
   int64_t ld_h;
   float* part;         // [assignments][dim]: D_e h, not yet weighted
   bf16* y;
@@ -163,8 +164,9 @@ __device__ __forceinline__ void result(const ExpertsParams& p, int assignment, i
   // as the sum of two bf16: rounded to one, h would double the squared error of y, whose own rounding is as large
   const bf16 high = __float2bfloat16_rn(f);
   const float rest = fabsf(__bfloat162float(high)) < INFINITY ? f - __bfloat162float(high) : 0.f;
-  p.h[assignment * p.ld_h + o] = high;
-  p.h[(p.n + assignment) * p.ld_h + o] = __float2bfloat16_rn(rest);
+  bf16* h = p.h + assignment * 2 * p.ld_h + (o >> 3) * 16 + (o & 7);
+  h[0] = high;
+  h[8] = __float2bfloat16_rn(rest);
 }
 
 // y: the assignments' products added up in the order of k, each once its weight has been multiplied in fp32.
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_plain_kernel(const __grid
       for (int t = 0; t < kPlainTiles; ++t) {
         const int j = j0 + t * 8 + g;
         col[t] = nullptr;
-        if (j < count) col[t] = PHASE == kDown ? p.h + list[j] * p.ld_h : p.x + (list[j] / p.top) * p.ld_x;
+        if (j < count) col[t] = PHASE == kDown ? p.h + list[j] * 2 * p.ld_h : p.x + (list[j] / p.top) * p.ld_x;
       }
       for (int s = warp; s < steps; s += kWarps) {
         const int k = s * kStep + 8 * c;
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2) experts_plain_kernel(const __grid
 #pragma unroll
           for (int q = 0; q < (PHASE == kDown ? 2 : 1); ++q) {
             uint4 v = make_uint4(0, 0, 0, 0);
-            if (col[t] != nullptr) v = piece(col[t] + q * p.n * p.ld_h, k, K);
+            if (col[t] != nullptr) v = PHASE == kDown ? piece(col[t] + 2 * k + 8 * q, 0, K - k) : piece(col[t], k, K);
             mma(acc[t], a0.x, a1.x, a0.y, a1.y, v.x, v.y);
             mma(acc[t], a0.z, a1.z, a0.w, a1.w, v.z, v.w);
           }
@@ -361,96 +363,120 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* map, uint64_t
       : "memory");
 }
 
-// Where a warp of the products is.
+// Where a warp of the products is: its next stage.
 struct Ring {
   uint8_t* base;
   uint32_t stage, phase;
   bool alive;
 };
 
-// Stages that an assignment's pieces are fetched ahead of their use, and what a lane holds of them.
-__host__ __device__ constexpr int ahead(int tiles) { return tiles == 1 ? 4 : tiles == 2 ? 3 : tiles == 3 ? 2 : 1; }
+// 32 bytes, on 32 bytes.
+__device__ __forceinline__ void load_32(uint4& a, uint4& b, const void* p) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p)
+               : "memory");
+}
+
+// Stages (of its own) that a warp's pieces of the assignments are fetched ahead of their use, and what a lane holds of
+// them: of x 16 columns to a tile and stage, of h the same twice.
+__host__ __device__ constexpr int ahead(int tiles) { return tiles == 1 ? 3 : 1; }
+constexpr int kMostTiles = 3;  // of 8 assignments in a pass: with four, what a lane holds no longer fits its registers
 template <int PHASE>
 struct Pieces {
   static constexpr int kParts = PHASE == kDown ? 2 : 1;
-  uint4 v[6 * kParts];
-  const bf16* col[4];  // rows of x or h, from this warp's first column; nullptr: none
+  uint4 v[3][2][kParts];        // [stages ahead * tiles][which 8 columns][part]
+  const bf16* col[kMostTiles];  // rows of x or h, from this lane's first column; nullptr: none
 
+  // `left` columns of the row are left from col on.
   template <int T>
-  __device__ __forceinline__ void fetch(const ExpertsParams& p, int d, int kb, int column, int K) {
+  __device__ __forceinline__ void fetch(int d, int kb, int left) {
     const int k = kb * kStageK;
 #pragma unroll
     for (int t = 0; t < T; ++t)
 #pragma unroll
-      for (int q = 0; q < kParts; ++q)
-        v[(d * kParts + q) * T + t] = col[t] != nullptr && k + column < K
-                                          ? *reinterpret_cast<const uint4*>(col[t] + (q == 0 ? 0 : p.n * p.ld_h) + k)
-                                          : make_uint4(0, 0, 0, 0);
+      for (int half = 0; half < 2; ++half) {
+        uint4(&w)[kParts] = v[d * T + t][half];
+        const bool in = col[t] != nullptr && k + 8 * half < left;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) w[q] = make_uint4(0, 0, 0, 0);
+        if (in) {
+          if (PHASE == kDown) load_32(w[0], w[kParts - 1], col[t] + 2 * (k + 8 * half));
+          else w[0] = *reinterpret_cast<const uint4*>(col[t] + k + 8 * half);
+        }
+      }
   }
 
-  // A pass's first ones.
+  // A pass's first ones, from K block kb on.
   template <int T>
-  __device__ __forceinline__ void start(const ExpertsParams& p, const int16_t* list, int left, int column, int K) {
+  __device__ __forceinline__ void start(const ExpertsParams& p, const int16_t* list, int assignments, int kb, int column,
+                                        int left) {
     const int g = (threadIdx.x & 31) >> 2;
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       const int j = t * 8 + g;
       col[t] = nullptr;
-      if (j < left) col[t] = (PHASE == kDown ? p.h + list[j] * p.ld_h : p.x + (list[j] / p.top) * p.ld_x) + column;
+      if (j < assignments)
+        col[t] = PHASE == kDown ? p.h + list[j] * 2 * p.ld_h + 2 * column : p.x + (list[j] / p.top) * p.ld_x + column;
     }
 #pragma unroll
-    for (int d = 0; d < ahead(T); ++d) fetch<T>(p, d, d, column, K);
+    for (int d = 0; d < ahead(T); ++d) fetch<T>(d, kb + 2 * d, left);
   }
 };
 
-// One pass with T tiles of 8 assignments: `left` from list on, the row blocks of the job. `then` is called once the
-// matrices have been multiplied, before the sums are joined.
+// One pass with T tiles of 8 assignments: `assignments` from list on, the row blocks of the job; this warp has every
+// other K block from kb on. `then` is called once the matrices have been multiplied, before the sums are joined.
 template <int PHASE, int T, class Then>
 __device__ __forceinline__ void products(const ExpertsParams& p, StreamShared& sh, Ring& ring, Pieces<PHASE>& x, const Job& job,
-                                         const int16_t* list, int left, int K, int rows, int column, uint32_t at,
+                                         const int16_t* list, int assignments, int kb, int K, int rows, int left, uint32_t at,
                                          Then&& then) {
   constexpr int kParts = Pieces<PHASE>::kParts, kAhead = ahead(T), kOut = PHASE == kGated ? 8 : 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nk = (K + kStageK - 1) / kStageK;
   float acc[kTogether][T][4] = {};
-  for (int kb0 = 0; kb0 < nk; kb0 += kAhead) {
+  for (; kb < nk; kb += 2 * kAhead) {
 #pragma unroll
     for (int d = 0; d < kAhead; ++d) {
-      const int kb = kb0 + d;
-      if (kb >= nk) break;
+      const int now = kb + 2 * d;
+      if (now >= nk) break;
       // (after a wait that ran out of time a warp only keeps the others' barriers company)
       if (ring.alive)
         ring.alive = __all_sync(0xffffffffu, ptx::mbar_wait(&sh.full[ring.stage], ring.phase, &sh.abort_flag, p.status, kWaitNs));
       // (a stage has room for all row blocks: what it holds of those that the job has not is multiplied and not used)
-      if (ring.alive && kb * kStageK + (warp >> 1) * kChunk < K) {
-        const uint8_t* s = ring.base + ring.stage * kStageBytes + at;
-        uint4 a[kTogether][2];
+      if (ring.alive && now * kStageK + (warp & 3) * kChunk < K) {
 #pragma unroll
-        for (int i = 0; i < kTogether; ++i) {
-          a[i][0] = *reinterpret_cast<const uint4*>(s + (PHASE == kGated ? i : 2 * i) * kBoxBytes);
-          a[i][1] = *reinterpret_cast<const uint4*>(s + (PHASE == kGated ? i + 4 : 2 * i + 1) * kBoxBytes);
-        }
+        for (int half = 0; half < 2; ++half) {
+          const uint8_t* s = ring.base + ring.stage * kStageBytes + (at ^ (half << 4));
 #pragma unroll
-        for (int q = 0; q < kParts; ++q)
+          for (int i0 = 0; i0 < kTogether; i0 += 2) {
+            uint4 a[2][2];
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int t = 0; t < T; ++t) {
-              const uint4& v = x.v[(d * kParts + q) * T + t];
-#pragma unroll
-              for (int i = 0; i < kTogether; ++i) {
-                if (half == 0) mma(acc[i][t], a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y, v.x, v.y);
-                else mma(acc[i][t], a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w, v.z, v.w);
-              }
+            for (int i = 0; i < 2; ++i) {
+              a[i][0] = *reinterpret_cast<const uint4*>(s + (PHASE == kGated ? i0 + i : 2 * (i0 + i)) * kBoxBytes);
+              a[i][1] = *reinterpret_cast<const uint4*>(s + (PHASE == kGated ? i0 + i + 4 : 2 * (i0 + i) + 1) * kBoxBytes);
             }
+#pragma unroll
+            for (int q = 0; q < kParts; ++q)
+#pragma unroll
+              for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int t = 0; t < T; ++t)
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    const uint4& v = x.v[d * T + t][half][q];
+                    if (part == 0) mma(acc[i0 + i][t], a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y, v.x, v.y);
+                    else mma(acc[i0 + i][t], a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w, v.z, v.w);
+                  }
+          }
+        }
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&sh.empty[ring.stage]);
-      if (++ring.stage == kStages) {
-        ring.stage = 0;
+      if ((ring.stage += 2) >= kStages) {
+        ring.stage -= kStages;
         ring.phase ^= 1u;
       }
-      if (kb + kAhead < nk) x.template fetch<T>(p, d, kb + kAhead, column, K);
+      if (now + 2 * kAhead < nk) x.template fetch<T>(d, now + 2 * kAhead, left);
     }
   }
   then();
@@ -467,7 +493,7 @@ __device__ __forceinline__ void products(const ExpertsParams& p, StreamShared& s
       const int l = n & 31, k = (n >> 5) % kEach, i = (n >> 5) / kEach;
       const int j = t * 8 + 2 * (l & 3) + (k & 1);
       const int o = (job.first + i) * kOut + (l >> 2) + (k >= 2 ? 8 : 0);
-      if (j >= left || o >= rows) continue;
+      if (j >= assignments || o >= rows) continue;
       float s = 0.f, s1 = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
@@ -492,7 +518,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) experts_stream_kernel(const
   if (threadIdx.x == 0) {
     for (int k = 0; k < kStages; ++k) {
       ptx::mbar_init(&sh.full[k], 1);
-      ptx::mbar_init(&sh.empty[k], kWarps);
+      ptx::mbar_init(&sh.empty[k], kWarps / 2);
     }
     sh.abort_flag = 0;
     ptx::fence_mbar_init();
@@ -570,37 +596,41 @@ __global__ void __launch_bounds__(kStreamThreads, 1) experts_stream_kernel(const
   // ------------------------------------------------------------ products
   if (down) follow();
   const int g = lane >> 2, c = lane & 3;
-  // this warp's 32 columns of a stage: pieces 2c + (warp & 1) of chunk warp / 2, which no two lanes of a quarter warp
-  // have in the same banks of the swizzled rows
-  const uint32_t at = (warp >> 1) * 8 * kBoxBytes + g * 128 + (((2 * c + (warp & 1)) ^ g) << 4);
-  const int column = (warp >> 1) * kChunk + 16 * c + 8 * (warp & 1);
-  Ring ring = {base, 0u, 0u, true};
+  // This warp's 64 columns of a stage: of chunk warp % 4 this lane has pieces 2c and 2c + 1, one after the other: 32
+  // bytes of an assignment's row, and of the swizzled rows no two lanes of a quarter warp have the same banks.
+  const uint32_t at = (warp & 3) * 8 * kBoxBytes + g * 128 + (((2 * c) ^ g) << 4);
+  const int column = (warp & 3) * kChunk + 16 * c, columns_left = K - column;
+  Ring ring = {base, static_cast<uint32_t>(warp >> 2), 0u, true};
   Pieces<PHASE> x;
   // The assignments' pieces come straight from L2, some stages before their use; a pass's first ones are sent for before
   // the sums of the pass before are joined. Each number of tiles has a loop of its own, without branches.
-  auto start = [&](const Passes<MOST>& s) {
+  int kb = warp >> 2;  // this warp's first K block of the pass
+  auto start = [&](const Passes<MOST>& s, int kb) {
     const int16_t* list = sh.r.list + sh.r.begin[s.job.active] + s.j0;
-    const int left = s.assignments - s.j0;
-    if (MOST == 1 || left <= 8) x.template start<1>(p, list, left, column, K);
-    else if (left <= 16) x.template start<2>(p, list, left, column, K);
-    else if (left <= 24) x.template start<3>(p, list, left, column, K);
-    else x.template start<4>(p, list, left, column, K);
+    const int n = s.assignments - s.j0;
+    if (MOST == 1 || n <= 8) x.template start<1>(p, list, n, kb, column, columns_left);
+    else if (n <= 16) x.template start<2>(p, list, n, kb, column, columns_left);
+    else x.template start<3>(p, list, n, kb, column, columns_left);
   };
   bool more = pass.next();
-  if (more) start(pass);
+  if (more) start(pass, kb);
   while (more) {
     Passes<MOST> after = pass;
     more = after.next();
+    const int kb_after = kb ^ (nk & 1);
     auto then = [&]() {
-      if (more) start(after);
+      if (more) start(after, kb_after);
     };
     const int16_t* list = sh.r.list + sh.r.begin[pass.job.active] + pass.j0;
-    const int left = pass.assignments - pass.j0;
-    if (MOST == 1 || left <= 8) products<PHASE, 1>(p, sh, ring, x, pass.job, list, left, K, rows, column, at, then);
-    else if (left <= 16) products<PHASE, 2>(p, sh, ring, x, pass.job, list, left, K, rows, column, at, then);
-    else if (left <= 24) products<PHASE, 3>(p, sh, ring, x, pass.job, list, left, K, rows, column, at, then);
-    else products<PHASE, 4>(p, sh, ring, x, pass.job, list, left, K, rows, column, at, then);
+    const int n = pass.assignments - pass.j0;
+    auto run = [&](auto tiles) {
+      products<PHASE, decltype(tiles)::value>(p, sh, ring, x, pass.job, list, n, kb, K, rows, columns_left, at, then);
+    };
+    if (MOST == 1 || n <= 8) run(std::integral_constant<int, 1>());
+    else if (n <= 16) run(std::integral_constant<int, 2>());
+    else run(std::integral_constant<int, 3>());
     pass = after;
+    kb = kb_after;
   }
 }
 
@@ -690,7 +720,7 @@ cudaError_t launch(const ExpertsParams& p, bool stream, int sms, cudaStream_t s)
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(units, sms)));
   // where no expert gets more than 8 assignments unless a token names it twice, the loops for more are left out
-  auto* kernel = p.tokens <= 8 ? experts_stream_kernel<PHASE, 1> : experts_stream_kernel<PHASE, 4>;
+  auto* kernel = p.tokens <= 8 ? experts_stream_kernel<PHASE, 1> : experts_stream_kernel<PHASE, kMostTiles>;
   if ((e = shared(kernel, kStreamSmem)) != cudaSuccess) return e;
   return launch_follow(kernel, grid, kStreamThreads, kStreamSmem, s, 1, sp);
 }
