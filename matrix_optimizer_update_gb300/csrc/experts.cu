@@ -42,8 +42,8 @@ constexpr int64_t kMaxDim = int64_t(1) << 20;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 32;    // K of a warp's step: 4 lanes of 8 elements
-constexpr int kCostRead = 8, kCostTile = 2;
 // Streaming
+constexpr int kMostTiles = 3;  // of 8 assignments in a pass: with four, what a lane holds no longer fits its registers
 constexpr int kTogether = 4;                     // row blocks taken together
 constexpr int kChunk = 64;                       // columns of a TMA box, 128 bytes
 constexpr int kBoxBytes = 8 * 2 * kChunk;        // of 8 rows
@@ -288,20 +288,28 @@ struct StreamShared {
 constexpr size_t kStreamSmem = 1024 + kStages * kStageBytes + sizeof(StreamShared);
 static_assert(kStreamSmem <= 227 * 1024 && sizeof(RoutingScratch) <= kStages * kStageBytes, "one block's shared memory");
 
-// What a row block of an expert takes: reading it, and the products with its assignments, 8 at a time. (Measured: a
-// block's time by the number of assignments, 64 rows by 2048: see the launch.)
-__device__ __forceinline__ int cost_of(int assignments) { return kCostRead + (assignments + 7) / 8 * kCostTile; }
+// What a row block of an expert takes, to within some percent: the time of 64 rows by 2048 (gated), and of 64 by 1408
+// (down), for 1, 8, 16, 24 and 32 assignments to each of 64 experts, was 117, 119, 126, 136 and 217 us, and 61, 64, 79,
+// 100 and 152 us. (Past 24 there is a second pass, whose matrices come out of L2.) With experts of many sizes the small
+// ones' blocks leave bandwidth to the others': 64 tokens to 8 of 64 unequally liked take 249 us with costs of 8 + 2 for
+// each tile, 205 with costs in proportion to those times, 199 with these.
+template <bool DOWN>
+__device__ __forceinline__ int cost_of(int assignments) {
+  const int tiles = (assignments + 7) / 8, passes = (tiles + kMostTiles - 1) / kMostTiles;
+  return DOWN ? 8 * passes + 4 * tiles : 16 * passes + 3 * tiles;
+}
 
 // Cuts the row blocks of all experts in use into one run for each block of the grid, of equal cost. By one warp.
+template <bool DOWN>
 __device__ __forceinline__ int cut(const Routing& r, int blocks, int64_t part, int64_t parts, int lane) {
   int64_t total = 0;
   for (int i0 = 0; i0 < r.actives; i0 += 32) {
     const int i = i0 + lane;
-    total += __reduce_add_sync(0xffffffffu, i < r.actives ? cost_of(r.begin[i + 1] - r.begin[i]) : 0);
+    total += __reduce_add_sync(0xffffffffu, i < r.actives ? cost_of<DOWN>(r.begin[i + 1] - r.begin[i]) : 0);
   }
   int64_t want = total * blocks * part / parts;  // cost before the cut
   for (int i0 = 0; i0 < r.actives; i0 += 32) {
-    const int i = i0 + lane, mine = i < r.actives ? cost_of(r.begin[i + 1] - r.begin[i]) : 0;
+    const int i = i0 + lane, mine = i < r.actives ? cost_of<DOWN>(r.begin[i + 1] - r.begin[i]) : 0;
     int before = mine;
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, before, d);
@@ -381,7 +389,6 @@ __device__ __forceinline__ void load_32(uint4& a, uint4& b, const void* p) {
 // Stages (of its own) that a warp's pieces of the assignments are fetched ahead of their use, and what a lane holds of
 // them: of x 16 columns to a tile and stage, of h the same twice.
 __host__ __device__ constexpr int ahead(int tiles) { return tiles == 1 ? 3 : 1; }
-constexpr int kMostTiles = 3;  // of 8 assignments in a pass: with four, what a lane holds no longer fits its registers
 template <int PHASE>
 struct Pieces {
   static constexpr int kParts = PHASE == kDown ? 2 : 1;
@@ -539,7 +546,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) experts_stream_kernel(const
   constexpr int kOut = PHASE == kGated ? 8 : 16;
   const int blocks = (rows + kOut - 1) / kOut;
   if (warp < 2) {
-    const int at = cut(sh.r, blocks, blockIdx.x + warp, gridDim.x, lane);
+    const int at = cut<down>(sh.r, blocks, blockIdx.x + warp, gridDim.x, lane);
     if (lane == 0) (warp == 0 ? sh.from : sh.to) = at;
   }
   ptx::fence_proxy_async_shared();  // the scratch's place is the ring's

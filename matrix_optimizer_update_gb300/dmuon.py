@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import json
 import os
+from array import array
 from dataclasses import dataclass
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -809,6 +810,21 @@ class Experts:
         return b.value
 
 
+_KINDS = {}
+
+
+def _kinds():
+    """The library's type of a torch type."""
+    if not _KINDS:
+        _KINDS.update({_t().bfloat16: BF16, _t().float32: F32})
+    return _KINDS
+
+
+def _at(a):
+    """The address of an array's elements."""
+    return a.buffer_info()[0]
+
+
 class GradClip:
     """The global norm of many gradient tensors, and their clipping.
 
@@ -831,19 +847,17 @@ class GradClip:
 
     def _table(self, tensors, name):
         """Arrays of the tensors' addresses, element counts and types."""
-        torch, device = _t(), self.device
-        kinds = {torch.bfloat16: BF16, torch.float32: F32}
-        n = len(tensors)
-        try:
-            types = (ctypes.c_int32 * n)(*[kinds[t.dtype] for t in tensors])
-        except KeyError:
-            _refuse(f"{name} must be bf16 or fp32 tensors")
+        kinds, device = _kinds(), self.device
+        types = []
         for t in tensors:
+            kind = kinds.get(t.dtype)
+            if kind is None:
+                _refuse(f"{name} must be bf16 or fp32 tensors")
             if t.get_device() != device or not t.is_contiguous():
                 _elsewhere(t, device, name)
                 _refuse(f"{name} must be contiguous CUDA tensors")
-        return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]),
-                (ctypes.c_int64 * n)(*[t.numel() for t in tensors]), types)
+            types.append(kind)
+        return (array("Q", [t.data_ptr() for t in tensors]), array("q", [t.numel() for t in tensors]), array("i", types))
 
     def norm(self, grads, *, stream=None):
         """The 2-norm over all elements of all tensors: an fp32 tensor without dimensions."""
@@ -853,7 +867,8 @@ class GradClip:
         def call(s):
             norm = _t().empty((), dtype=_t().float32, device=self.workspace.device)
             ws = self.workspace
-            _check(lib().dmuon_grad_norm(ptrs, counts, types, len(grads), norm.data_ptr(), ws.data_ptr(), ws.numel(), s))
+            _check(lib().dmuon_grad_norm(_at(ptrs), _at(counts), _at(types), len(grads), norm.data_ptr(), ws.data_ptr(),
+                                         ws.numel(), s))
             return norm
 
         return _run(self, call, stream, *grads, scratch=self.workspace)
@@ -866,15 +881,15 @@ class GradClip:
         to, results = ptrs, []
         if out is not None:
             results = list(out)
-            if [(t.shape, t.dtype) for t in results] != [(t.shape, t.dtype) for t in grads]:
+            to, counts_to, types_to = self._table(results, "out")
+            if counts_to != counts or types_to != types or any(a.shape != b.shape for a, b in zip(results, grads)):
                 _refuse("out must have the gradients' shapes and types")
-            to = self._table(results, "out")[0]
 
         def call(s):
             norm = _t().empty((), dtype=_t().float32, device=self.workspace.device)
             ws = self.workspace
-            _check(lib().dmuon_grad_clip(ptrs, to, counts, types, len(grads), float(max_norm), norm.data_ptr(),
-                                         ws.data_ptr(), ws.numel(), s))
+            _check(lib().dmuon_grad_clip(_at(ptrs), _at(to), _at(counts), _at(types), len(grads), float(max_norm),
+                                         norm.data_ptr(), ws.data_ptr(), ws.numel(), s))
             return norm
 
         return _run(self, call, stream, *grads, *results, scratch=self.workspace)
