@@ -10,6 +10,10 @@
 // captured call carries its own. A tensor is cut into units of whole 16-byte vectors; unit u of a launch
 // belongs to block u mod the grid, whatever the blocks' timing, and each block sums its units in their
 // order: the norm is the same from call to call.
+//
+// Up to 512 KB are one launch: a cluster of 8 blocks holds all of it in registers, joins its sums through shared
+// memory, and writes it back scaled. (Four matrices of 128 x 256, clipped: 7.8 us, as the two launches take, of which
+// the host pays for one less: 20 us a call against 26.)
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -19,15 +23,18 @@
 #include "dmuon.h"
 #include "follow.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace dmuon {
 namespace {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int kThreads = 256;
-constexpr int kBlocksPerSm = 8;
-constexpr int kMaxBlocks = 2048;
+// Few and large blocks: each block of the clipping pass adds up all blocks' sums in 64 bits, of which an SM does two
+// or so a cycle. (8 blocks of 256 threads to an SM took 8 us more.)
+constexpr int kThreads = 1024;
+constexpr int kBlocksPerSm = 2;
+constexpr int kMaxBlocks = 512;
 constexpr size_t kWorkspace = kMaxBlocks * sizeof(double);
 constexpr int kMostTensors = 1024;  // per launch: 28 bytes each of the 32764 that parameters may take
 constexpr int kFlight = 4;          // vectors a thread has in flight
@@ -50,12 +57,12 @@ struct Lie {
 };
 
 __host__ __device__ __forceinline__ Lie lie_of(uint64_t address, int64_t count, bool half) {
-  const int size = half ? 2 : 4, each = 16 / size;
+  const int size = half ? 1 : 2, each = half ? 3 : 2;  // logarithms
   Lie l;
-  const int64_t before = static_cast<int64_t>((16 - (address & 15)) & 15) / size;
+  const int64_t before = static_cast<int64_t>((16 - (address & 15)) & 15) >> size;
   l.head = static_cast<int32_t>(before < count ? before : count);
-  l.vectors = (count - l.head) / each;
-  l.tail = static_cast<int32_t>(count - l.head - l.vectors * each);
+  l.vectors = (count - l.head) >> each;
+  l.tail = static_cast<int32_t>(count - l.head - (l.vectors << each));
   return l;
 }
 
@@ -127,19 +134,48 @@ struct Squares {
   }
 };
 
-// The block's sum of one value per thread, in a fixed order; every thread gets it.
+// The block's sum of one value per thread, in a fixed order; the first warp gets it.
 __device__ __forceinline__ double block_sum(double v, double* red) {
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = red[0];
-#pragma unroll
-  for (int w = 1; w < kThreads / 32; ++w) v += red[w];
+  static_assert(kThreads == 32 * 32, "a lane to a warp");
+  if (threadIdx.x < 32) {
+    v = red[threadIdx.x];
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  }
   return v;
 }
 
+// This thread's element of a tensor outside its whole vectors, if it has one.
+struct Loose {
+  uint64_t from, to;
+  bool there;
+  __device__ __forceinline__ float value(bool half) const {
+    return half ? __bfloat162float(*reinterpret_cast<const bf16*>(from)) : *reinterpret_cast<const float*>(from);
+  }
+  __device__ __forceinline__ void scale(bool half, float s) const {
+    if (half) {
+      const bf16 x = *reinterpret_cast<const bf16*>(from);
+      *reinterpret_cast<bf16*>(to) = s == 1.f ? x : __float2bfloat16_rn(__bfloat162float(x) * s);
+    } else {
+      const float x = *reinterpret_cast<const float*>(from);
+      *reinterpret_cast<float*>(to) = s == 1.f ? x : x * s;
+    }
+  }
+};
 template <int N>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<N> t, double* partial, int first) {
+__device__ __forceinline__ Loose loose_of(const Table<N>& t, int i, const Lie& l, int thread, int size) {
+  Loose e;
+  e.there = thread < l.head + l.tail;
+  const int64_t at = thread < l.head ? thread : t.count[i] - l.tail + (thread - l.head);
+  e.from = (t.in[i] & ~uint64_t(1)) + at * size;
+  e.to = t.out[i] + at * size;
+  return e;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_kernel(const __grid_constant__ Table<N> t, double* partial, int first) {
   __shared__ double red[kThreads / 32];
   follow();
   Squares q;
@@ -159,27 +195,31 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
 #pragma unroll
       for (int k = 0; k < kFlight; ++k) q.vector(x[k], half);
     }
-    if (v0 == 0 && threadIdx.x < l.head + l.tail) {  // the elements outside whole vectors
-      const int64_t e = threadIdx.x < l.head ? threadIdx.x : t.count[i] - l.tail + (threadIdx.x - l.head);
-      q.one(half ? __bfloat162float(reinterpret_cast<const bf16*>(at)[e]) : reinterpret_cast<const float*>(at)[e]);
-    }
+    const Loose e = loose_of(t, i, l, threadIdx.x, half ? 2 : 4);
+    if (v0 == 0 && e.there) q.one(e.value(half));
     q.unit_done();
   }
   const double sum = block_sum(q.sum, red);
   if (threadIdx.x == 0) partial[blockIdx.x] = first ? sum : partial[blockIdx.x] + sum;
 }
 
-// The norm from the blocks' sums.
-__device__ __forceinline__ double norm_of(const double* partial, int blocks, double* red) {
+// The norm from the blocks' sums, in the first warp.
+__device__ __forceinline__ double norm_of(const double* partial, int blocks) {
   double s = 0.0;
-  for (int b = threadIdx.x; b < blocks; b += kThreads) s += partial[b];
-  return sqrt(block_sum(s, red));
+  for (int b = threadIdx.x; b < blocks; b += 32) s += partial[b];
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  return sqrt(s);
 }
 
-__global__ void __launch_bounds__(kThreads) norm_done_kernel(const double* partial, int blocks, float* norm) {
-  __shared__ double red[kThreads / 32];
+// What gradients of that norm are multiplied by. (A norm that is not finite clips nothing: the caller sees it.)
+__device__ __forceinline__ float scale_of(double norm, float max_norm) {
+  const bool clip = norm > static_cast<double>(max_norm) && norm < INFINITY;
+  return clip ? static_cast<float>(static_cast<double>(max_norm) / norm) : 1.f;
+}
+
+__global__ void __launch_bounds__(32) norm_done_kernel(const double* partial, int blocks, float* norm) {
   follow();
-  const double n = norm_of(partial, blocks, red);
+  const double n = norm_of(partial, blocks);
   if (threadIdx.x == 0) *norm = static_cast<float>(n);
 }
 
@@ -201,17 +241,37 @@ __device__ __forceinline__ uint4 scaled(const uint4& v, bool half, float s) {
   return o;
 }
 
+__device__ __forceinline__ void store_vector(uint64_t to, const uint4& v, bool half) {
+  if ((to & 15) == 0) {  // the result lies as the gradient does
+    __stcs(reinterpret_cast<uint4*>(to), v);
+    return;
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (half) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      reinterpret_cast<uint16_t*>(to)[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) reinterpret_cast<uint32_t*>(to)[e] = w[e];
+  }
+}
+
 // The last units first: they are what the norm's pass left in L2.
 template <int N>
-__global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ Table<N> t, const double* partial,
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) clip_kernel(const __grid_constant__ Table<N> t, const double* partial,
                                                         int blocks, float max_norm, float* norm) {
-  __shared__ double red[kThreads / 32];
+  __shared__ float scale;
   follow();
-  const double total = norm_of(partial, blocks, red);
-  if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(total);
-  // (a norm that is not finite clips nothing: the caller sees it)
-  const bool clip = total > static_cast<double>(max_norm) && total < INFINITY;
-  const float s = clip ? static_cast<float>(static_cast<double>(max_norm) / total) : 1.f;
+  if (threadIdx.x < 32) {
+    const double total = norm_of(partial, blocks);
+    if (threadIdx.x == 0) {
+      if (norm != nullptr && blockIdx.x == 0) *norm = static_cast<float>(total);
+      scale = scale_of(total, max_norm);
+    }
+  }
+  __syncthreads();
+  const float s = scale;
   for (int u = t.first[t.tensors] - 1 - static_cast<int>(blockIdx.x); u >= 0; u -= gridDim.x) {
     const int i = tensor_of(t, u);
     const bool half = (t.in[i] & 1u) != 0;
@@ -223,7 +283,6 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
     const int64_t v1 = min(v0 + t.per_unit, l.vectors);
     const uint4* body = reinterpret_cast<const uint4*>(at + l.head * size);
     const uint64_t body_to = to + l.head * size;
-    const bool whole = (body_to & 15) == 0;  // the result lies as the gradient does
     for (int64_t v = v0 + threadIdx.x; v < v1; v += kFlight * kThreads) {
       uint4 x[kFlight];
 #pragma unroll
@@ -234,30 +293,101 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ 
         if (v + k * kThreads >= v1) break;
         const uint4 o = s == 1.f ? x[k] : scaled(x[k], half, s);
         const uint64_t a = body_to + (v + k * kThreads) * 16;
-        if (whole) {
-          __stcs(reinterpret_cast<uint4*>(a), o);
-        } else if (half) {
-          const uint32_t w[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            reinterpret_cast<uint16_t*>(a)[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
-        } else {
-          const uint32_t w[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) reinterpret_cast<uint32_t*>(a)[e] = w[e];
-        }
+        store_vector(a, o, half);
       }
     }
-    if (v0 == 0 && threadIdx.x < l.head + l.tail) {
-      const int64_t e = threadIdx.x < l.head ? threadIdx.x : t.count[i] - l.tail + (threadIdx.x - l.head);
-      if (half) {
-        const bf16 x = reinterpret_cast<const bf16*>(at)[e];
-        reinterpret_cast<bf16*>(to)[e] = s == 1.f ? x : __float2bfloat16_rn(__bfloat162float(x) * s);
-      } else {
-        const float x = reinterpret_cast<const float*>(at)[e];
-        reinterpret_cast<float*>(to)[e] = s == 1.f ? x : x * s;
-      }
+    const Loose e = loose_of(t, i, l, threadIdx.x, size);
+    if (v0 == 0 && e.there) e.scale(half, s);
+  }
+}
+
+// ------------------------------------------------------------------ few elements
+constexpr int kCluster = 8;
+constexpr int kGroup = 256;                        // threads that have a unit at a time, a vector each
+constexpr int kGroups = kThreads / kGroup;
+constexpr int kHold = 4;                           // units a thread holds a vector of (8 take 13 us where 4 take 8)
+constexpr int kFewUnits = kCluster * kGroups * kHold;  // of kGroup vectors: 512 KB
+
+template <int N>
+__global__ void __launch_bounds__(kThreads, 1) few_kernel(const __grid_constant__ Table<N> t, int clipped, float max_norm,
+                                                                  float* norm) {
+  __shared__ double red[kThreads / 32];
+  __shared__ double sums[kCluster];
+  __shared__ float factor;
+  follow();
+  const int thread = threadIdx.x % kGroup, group = blockIdx.x * kGroups + threadIdx.x / kGroup;
+  const int units = t.first[t.tensors];
+  uint4 x[kHold];
+  float loose[kHold];
+  unsigned halves = 0u;
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) {
+    x[k] = make_uint4(0, 0, 0, 0);
+    loose[k] = 0.f;
+    const int u = k * kCluster * kGroups + group;
+    if (u >= units) continue;
+    const int i = tensor_of(t, u);
+    const bool half = (t.in[i] & 1u) != 0;
+    const uint64_t at = t.in[i] & ~uint64_t(1);
+    const Lie l = lie_of(at, t.count[i], half);
+    const int64_t v = int64_t(u - t.first[i]) * kGroup + thread;
+    if (v < l.vectors) x[k] = load_once(reinterpret_cast<const uint4*>(at + l.head * (half ? 2 : 4)) + v);
+    const Loose e = loose_of(t, i, l, thread, half ? 2 : 4);
+    if (v < kGroup && e.there) loose[k] = e.value(half);
+    halves |= static_cast<unsigned>(half) << k;
+  }
+  Squares q;
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) {
+    q.vector(x[k], (halves >> k & 1u) != 0);
+    if (loose[k] != 0.f) q.one(loose[k]);
+  }
+  // A warp's sum: in fp32 where none of its threads has anything in 64 bits, of which it would be 32 times as many.
+  double s;
+  if (__any_sync(0xffffffffu, q.sum != 0.0)) {
+    s = q.sum + static_cast<double>(q.near);
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  } else {
+    for (int d = 16; d > 0; d >>= 1) q.near += __shfl_xor_sync(0xffffffffu, q.near, d);
+    s = static_cast<double>(q.near);
+  }
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+  __syncthreads();
+  ptx::cluster_sync();  // every block is there to be written to
+  if (threadIdx.x < 32) {
+    s = red[threadIdx.x];
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (threadIdx.x < kCluster) {
+      const uint32_t to = ptx::mapa_shared(ptx::smem_u32(&sums[ptx::cluster_ctarank()]), threadIdx.x);
+      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(s) : "memory");
     }
+  }
+  __syncthreads();
+  ptx::cluster_sync();
+  if (threadIdx.x == 0) {
+    double all = sums[0];
+    for (int b = 1; b < kCluster; ++b) all += sums[b];
+    const double total = sqrt(all);
+    if (blockIdx.x == 0) *norm = static_cast<float>(total);
+    factor = scale_of(total, max_norm);
+  }
+  if (!clipped) return;
+  __syncthreads();
+  const float scale = factor;
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) {
+    const int u = k * kCluster * kGroups + group;
+    if (u >= units) break;
+    const int i = tensor_of(t, u);
+    const bool half = (t.in[i] & 1u) != 0;
+    const uint64_t at = t.in[i] & ~uint64_t(1);
+    if (scale == 1.f && at == t.out[i]) continue;
+    const int size = half ? 2 : 4;
+    const Lie l = lie_of(at, t.count[i], half);
+    const int64_t v = int64_t(u - t.first[i]) * kGroup + thread;
+    if (v < l.vectors) store_vector(t.out[i] + l.head * size + v * 16, scale == 1.f ? x[k] : scaled(x[k], half, scale), half);
+    const Loose e = loose_of(t, i, l, thread, size);
+    if (v < kGroup && e.there) e.scale(half, scale);
   }
 }
 
@@ -287,10 +417,9 @@ int64_t units_of(const Call& c, int i, int32_t per_unit) {
   return std::max<int64_t>(1, (l.vectors + per_unit - 1) / per_unit);
 }
 
-// Tensors from..to of the call (those that are empty left out), through one of its two passes.
+// Tensors from..to of the call, those that are empty left out.
 template <int N>
-cudaError_t launch(const Call& c, int from, int to, bool clip, bool first) {
-  Table<N> t;
+void fill(Table<N>& t, const Call& c, int from, int to, bool clip) {
   t.tensors = 0;
   t.per_unit = c.per_unit;
   int64_t units = 0;
@@ -303,10 +432,26 @@ cudaError_t launch(const Call& c, int from, int to, bool clip, bool first) {
     units += units_of(c, i, c.per_unit);
   }
   t.first[t.tensors] = static_cast<int32_t>(units);
+}
+
+// One of the call's two passes over them.
+template <int N>
+cudaError_t launch(const Call& c, int from, int to, bool clip, bool first) {
+  Table<N> t;
+  fill(t, c, from, to, clip);
   if (clip)
     return launch_follow(clip_kernel<N>, dim3(c.blocks), kThreads, 0, c.stream, 1, t, static_cast<const double*>(c.partial),
                          c.blocks, c.max_norm, first ? c.norm : nullptr);
   return launch_follow(norm_kernel<N>, dim3(c.blocks), kThreads, 0, c.stream, 1, t, c.partial, static_cast<int>(first));
+}
+
+template <int N>
+cudaError_t launch_few(Call c, bool clip) {
+  Table<N> t;
+  c.per_unit = kGroup;
+  fill(t, c, 0, c.n, clip);
+  return launch_follow(few_kernel<N>, dim3(kCluster), kThreads, 0, c.stream, kCluster, t, static_cast<int>(clip),
+                       c.max_norm, c.norm);
 }
 
 // Small tables have launches of their own, as larger parameters take longer to launch.
@@ -379,12 +524,20 @@ dmuon_status run(Call c, void* d_workspace, size_t bytes, void* stream, bool cli
     }
     if (bad) return refuse("a result overlaps another tensor of the call");
   }
+  c.partial = static_cast<double*>(d_workspace);
+  c.stream = reinterpret_cast<cudaStream_t>(stream);
+  if (c.n <= 128 && vectors <= kFewUnits * kGroup) {
+    int64_t units = 0;
+    for (int i = 0; i < c.n; ++i)
+      if (c.counts[i] > 0) units += units_of(c, i, kGroup);
+    if (units <= kFewUnits) return done(c.n <= 16 ? launch_few<16>(c, clip) : launch_few<128>(c, clip));
+  }
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return done(e);
-  // Units of 1 to 16 vectors a thread: as large as leaves every block several, as their start costs a search and
-  // a partly filled round of loads.
+  // Units of 1 to 16 vectors a thread: as large as leaves every block several, as their start costs a search and a
+  // partly filled round of loads.
   const int64_t most = std::min(kMaxBlocks, kBlocksPerSm * sms);
   int64_t turns = 1;
   while (turns < 16 && vectors / (kThreads * turns) > 8 * most) turns *= 2;
@@ -397,12 +550,10 @@ dmuon_status run(Call c, void* d_workspace, size_t bytes, void* stream, bool cli
       if (c.counts[i] > 0) units += units_of(c, i, c.per_unit);
     c.blocks = static_cast<int>(std::max<int64_t>(c.blocks, std::min(units, most)));
   }
-  c.partial = static_cast<double*>(d_workspace);
-  c.stream = reinterpret_cast<cudaStream_t>(stream);
   e = pass(c, false);
   if (e != cudaSuccess) return done(e);
   if (clip) return done(pass(c, true));
-  return done(launch_follow(norm_done_kernel, dim3(1), kThreads, 0, c.stream, 1, static_cast<const double*>(c.partial),
+  return done(launch_follow(norm_done_kernel, dim3(1), 32, 0, c.stream, 1, static_cast<const double*>(c.partial),
                             c.blocks, c.norm));
 }
 

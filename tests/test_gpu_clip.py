@@ -44,6 +44,9 @@ SETS = {
     "many": [(100 + i, "bf"[i % 2], i % 8) for i in range(1500)],
     "large": [(3000001, "b", 1), (2000003, "f", 2), (5, "b", 0)],
     "hundred": [(50000, "b", 0)] * 100,
+    "few": [(65536, "b", 0), (65536, "f", 1), (7, "f", 3), (60000, "f", 0)],               # just what one launch holds
+    "more": [(65536, "b", 0), (65536, "f", 1), (65537, "b", 3)],          # and a little more
+    "rows": [(2048 * (1 + i % 3), "bf"[i % 2], i % 5) for i in range(128)],
 }
 
 
