@@ -127,6 +127,76 @@ __device__ __forceinline__ double exact_dot(const DotParams& d, int64_t t, int64
   return s;
 }
 
+// The largest entries in order, as (logit, ~id), and what is done about neighbours too near to tell.
+struct Order {
+  const uint64_t* sorted;
+  uint64_t* dots;  // exact logits of those that share a run
+  int keep, top;
+
+  __device__ __forceinline__ float z(int i) const { return value_of(static_cast<uint32_t>(sorted[i] >> 32)); }
+  __device__ __forceinline__ int id(int i) const { return static_cast<int>(~static_cast<uint32_t>(sorted[i])); }
+
+  // The places whose entry is surely below the one before, as bits; by one warp.
+  __device__ __forceinline__ uint64_t starts(const TopParams& p, int lane) const {
+    // What two products may be off by against each other: at most 2.2e-9 * dim of the largest partial sum of each, which
+    // is their logit and some standard deviations of the rest; twice that (at 4096 dims 5e-4 at a logit of 12), and
+    // no less than what fp32 sums of 512 terms have.
+    const float part = 6e-9f * fmaxf(512.f, static_cast<float>(p.dot.dim));
+    uint64_t bits = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = 32 * h + lane;
+      bool apart = true;
+      if (i > 0 && i < keep) {
+        const float a = z(i - 1), b = z(i);
+        apart = a - b > part * (8.f * p.dot.scale + fabsf(a));
+      }
+      bits |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, apart)) << (32 * h);
+    }
+    return bits;
+  }
+  // The run that entry i belongs to begins at the last start up to it.
+  static __device__ __forceinline__ int run(uint64_t starts, int i) {
+    return 63 - __clzll(static_cast<long long>(starts & ((uint64_t(2) << i) - 1)));
+  }
+  // Whether it is not alone there, and the run matters.
+  __device__ __forceinline__ bool shared(uint64_t starts, int i) const {
+    return run(starts, i) < top && (~(starts >> i) & (i + 1 < keep ? 3 : 1)) != 0;
+  }
+  // The logits of such entries, of every step-th from `first` on, by a warp each.
+  __device__ __forceinline__ void exact_dots(const TopParams& p, int64_t t, uint64_t starts, int first, int step,
+                                             int lane) const {
+#pragma unroll 1
+    for (int i = first; i < keep; i += step)
+      if (shared(starts, i)) {
+        const double d = exact_dot(p.dot, t, id(i), lane);
+        if (lane == 0) dots[i] = order_of(d + 0.0);
+      }
+  }
+  __device__ __forceinline__ void results(const TopParams& p, int64_t t, int64_t y, uint64_t starts, int thread,
+                                          int threads) const {
+    const float lse = p.lse[t], logp = p.logp[t];
+    for (int i = thread; i < keep; i += threads) {
+      int place = i;
+      const int mine = id(i);
+      if (shared(starts, i)) {
+        const int begin = run(starts, i);
+        place = begin;
+        for (int j = begin; j < keep && run(starts, j) == begin; ++j)
+          place += dots[j] > dots[i] || (dots[j] == dots[i] && id(j) < mine);
+      }
+      if (place < top) {
+        p.top_ids[t * top + place] = mine;
+        p.top_logp[t * top + place] = mine == y ? logp : z(i) - lse;
+      }
+    }
+    for (int i = keep + thread; i < top; i += threads) {  // fewer entries than asked for: not finite
+      p.top_ids[t * top + i] = -1;
+      p.top_logp[t * top + i] = -INFINITY;
+    }
+  }
+};
+
 // The first `held` of n keys in the order (key descending, number ascending): take(place, number, key) for each, by
 // ascending number. Returns how many. KEYS: n is at most 32 * KEYS, and the keys are held in registers; 0: any n,
 // read again each time. read(i) gives a key for i < n; keys of 0 are not there.
@@ -180,10 +250,8 @@ __device__ __forceinline__ uint32_t peak_of(const TopParams& p, int64_t t, int g
 }
 
 // A token's alternatives among the entries of `wanted` groups, whose peaks are at least `least`, the target and the
-// list so far. `scored` returns once the token's log sum and probability are there.
-template <class Scored>
-__device__ __forceinline__ void top_of(const TopParams& p, int64_t t, int lane, TopShared& sh, int wanted, uint32_t least,
-                                       Scored&& scored) {
+// list so far; by one warp.
+__device__ __forceinline__ void top_of(const TopParams& p, int64_t t, int lane, TopShared& sh, int wanted, uint32_t least) {
   const int held = p.top + kSpare;
   // ---------------------------------------------------------- their entries, the target, and the list so far
   const int64_t y = p.targets != nullptr ? p.targets[t] : -1;
@@ -249,63 +317,18 @@ __device__ __forceinline__ void top_of(const TopParams& p, int64_t t, int lane, 
     if (place < keep) sh.sorted[place] = mine;
   }
   __syncwarp();
-  auto z_at = [&](int i) { return value_of(static_cast<uint32_t>(sh.sorted[i] >> 32)); };
-  auto id_at = [&](int i) { return static_cast<int>(~static_cast<uint32_t>(sh.sorted[i])); };
+  const Order o = {sh.sorted, sh.exact, keep, p.top};
   if (!p.last) {
     for (int i = lane; i < held; i += 32) {
-      p.list_z[t * kHeld + i] = i < keep ? z_at(i) : 0.f;
-      p.list_id[t * kHeld + i] = i < keep ? id_at(i) : -1;
+      p.list_z[t * kHeld + i] = i < keep ? o.z(i) : 0.f;
+      p.list_id[t * kHeld + i] = i < keep ? o.id(i) : -1;
     }
     return;
   }
-
-  // ---------------------------------------------------------- neighbours too near to tell
-  // What two products may be off by against each other: at most 2.2e-9 * dim of the largest partial sum of each, which
-  // is their logit and some standard deviations of the rest; twice that (at 4096 dims 5e-4 at a logit of 12), and
-  // no less than what fp32 sums of 512 terms have.
-  const float part = 6e-9f * fmaxf(512.f, static_cast<float>(p.dot.dim));
-  uint64_t starts = 0;  // places whose entry is surely below the one before
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = 32 * h + lane;
-    bool apart = true;
-    if (i > 0 && i < keep) {
-      const float a = z_at(i - 1), b = z_at(i);
-      apart = a - b > part * (8.f * p.dot.scale + fabsf(a));
-    }
-    starts |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, apart)) << (32 * h);
-  }
-  // entry i shares its place where it or the next one is not a start; its run begins at the last start up to it
-  auto begin = [&](int i) { return 63 - __clzll(static_cast<long long>(starts & ((uint64_t(2) << i) - 1))); };
-  auto shared = [&](int i) { return begin(i) < p.top && (~(starts >> i) & (i + 1 < keep ? 3 : 1)) != 0; };
-  for (int i = 0; i < keep; ++i)
-    if (shared(i)) {
-      const double d = exact_dot(p.dot, t, id_at(i), lane);
-      if (lane == 0) sh.exact[i] = order_of(d + 0.0);
-    }
+  const uint64_t starts = o.starts(p, lane);
+  o.exact_dots(p, t, starts, 0, 1, lane);
   __syncwarp();
-  scored();
-  const float lse = p.lse[t], logp = p.logp[t];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = 32 * h + lane;
-    if (i >= keep) continue;
-    int place = i;
-    const int id = id_at(i);
-    if (shared(i)) {
-      place = begin(i);
-      for (int j = place; j < keep && begin(j) == begin(i); ++j)
-        place += sh.exact[j] > sh.exact[i] || (sh.exact[j] == sh.exact[i] && id_at(j) < id);
-    }
-    if (place < p.top) {
-      p.top_ids[t * p.top + place] = id;
-      p.top_logp[t * p.top + place] = id == y ? logp : z_at(i) - lse;
-    }
-  }
-  for (int i = keep + lane; i < p.top; i += 32) {
-    p.top_ids[t * p.top + i] = -1;
-    p.top_logp[t * p.top + i] = -INFINITY;
-  }
+  o.results(p, t, y, starts, lane, 32);
 }
 
 template <int KEYS>
@@ -324,50 +347,204 @@ __global__ void __launch_bounds__(32 * kTopWarps) top_kernel(const __grid_consta
                                 });
   least = __reduce_min_sync(0xffffffffu, least);
   __syncwarp();
-  top_of(p, t, lane, sh, wanted, p.groups > wanted ? least : 0u, [] {});
+  top_of(p, t, lane, sh, wanted, p.groups > wanted ? least : 0u);
 }
 
-// Few tokens: a block each. Eight warps find the first groups, each of an eighth of them, and the first warp of those
-// and the alternatives; meanwhile eight others join the groups' sums.
+// ------------------------------------------------------------------ few tokens
+// A block each: eight warps find the alternatives together, eight others join the groups' sums meanwhile. What a
+// short launch like this takes are trips to memory and its instructions' way to the SM, so that the groups' number may
+// be up to kMoreGroups above what is needed (a search for exactly the first `held` takes twice the rounds), their
+// entries are loaded by all warps at once, and loops are not unrolled without need.
 constexpr int kJoinThreads = 256;  // as where no alternatives are asked for: the same sums
+constexpr int kFindThreads = 32 * kTopWarps;
+constexpr int kMoreGroups = 24;
+constexpr int kFewCandidates = (kHeld + kMoreGroups) * 32 + kHeld + 1;
+constexpr int kRanked = 512;  // so many candidates are put in order by counting
+
+struct FindShared {
+  int red[2][kTopWarps];
+  uint32_t low, high;
+  int groups, candidates;
+  int wanted[kHeld + kMoreGroups];
+  uint64_t cand[kFewCandidates];
+  uint64_t sorted[kHeld], exact[kHeld];
+  uint64_t starts;
+};
+
+__device__ __forceinline__ void find_sync() { asm volatile("bar.sync 2, 256;" ::: "memory"); }
+
+// The sum over the finders; `turn` alternates between calls, so that one barrier is enough.
+__device__ __forceinline__ int find_count(FindShared& sh, int n, int& turn) {
+  n = __reduce_add_sync(0xffffffffu, n);
+  int* red = sh.red[turn & 1];
+  ++turn;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = n;
+  find_sync();
+  int all = 0;
+#pragma unroll
+  for (int w = 0; w < kTopWarps; ++w) all += red[w];
+  return all;
+}
+
+// As threshold(), over the finders, and content with up to `more` above `want`.
+template <typename T, class Count>
+__device__ __forceinline__ T find_threshold(FindShared& sh, int want, int more, T low, T high, int& turn, Count&& count) {
+  const T differ = low ^ high;
+  if (differ == 0) return high;
+  int bit = sizeof(T) == 8 ? 63 - __clzll(static_cast<long long>(differ)) : 31 - __clz(static_cast<int>(differ));
+  T at = bit + 1 < static_cast<int>(sizeof(T)) * 8 ? high >> (bit + 1) << (bit + 1) : 0;
+#pragma unroll 1
+  for (; bit >= 0; --bit) {
+    const T next = at | (T(1) << bit);
+    const int n = find_count(sh, count(next), turn);
+    if (n >= want) at = next;
+    if (n >= want && n <= want + more) break;
+  }
+  return at;
+}
+
+// KEYS: the piece has at most KEYS groups to a finder, whose peaks are held in registers; 0: any number.
 template <int KEYS>
-__global__ void __launch_bounds__(32 * kTopWarps + kJoinThreads) score_top_kernel(const __grid_constant__ ScoreParams r,
-                                                                                  const __grid_constant__ TopParams p) {
-  __shared__ TopShared sh;
+__device__ __forceinline__ void find(const TopParams& p, int64_t t, FindShared& sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, held = p.top + kSpare;
+  int turn = 0;
+  const int64_t y = p.targets != nullptr ? p.targets[t] : -1;
+  const int turns = KEYS != 0 ? KEYS : (p.groups + kFindThreads - 1) / kFindThreads;
+  auto read = [&](int g) {
+    return g < p.groups ? max(order_of(p.parts[t * p.token_step + g * p.group_step].peak), 1u) : 0u;
+  };
+  uint32_t key[KEYS != 0 ? KEYS : 1] = {};
+  auto at = [&](int k) { return KEYS != 0 ? key[k] : read(k * kFindThreads + tid); };
+  if (tid == 0) {
+    sh.low = 0xffffffffu;
+    sh.high = 0u;
+    sh.groups = sh.candidates = 0;
+  }
+  uint32_t low = 0xffffffffu, high = 0u;
+#pragma unroll
+  for (int k = 0; k < turns; ++k) {
+    const uint32_t v = read(k * kFindThreads + tid);
+    if (KEYS != 0) key[k] = v;
+    if (v != 0u) low = min(low, v);
+    high = max(high, v);
+  }
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  find_sync();
+  if (lane == 0) {
+    atomicMin(&sh.low, low);
+    atomicMax(&sh.high, high);
+  }
+  find_sync();
+  uint32_t least = 1u;         // of the groups; logits below it are not among the largest
+  uint32_t up_to = 0xffffffffu;  // of groups whose peak is `least`, those up to this one
+  if (p.groups > held + kMoreGroups) {
+    least = find_threshold<uint32_t>(sh, held, kMoreGroups, sh.low, sh.high, turn, [&](uint32_t limit) {
+      int n = 0;
+#pragma unroll
+      for (int k = 0; k < turns; ++k) n += at(k) >= limit;
+      return n;
+    });
+    int above = 0, level = 0;
+#pragma unroll
+    for (int k = 0; k < turns; ++k) {
+      above += at(k) > least;
+      level += at(k) == least;
+    }
+    above = find_count(sh, above, turn);
+    level = find_count(sh, level, turn);
+    if (above + level > held + kMoreGroups) {  // many share it: the first of them by number
+      const uint32_t first = find_threshold<uint32_t>(sh, held - above, 0, 0u, 0xffffffffu, turn, [&](uint32_t limit) {
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < turns; ++k) n += at(k) == least && ~static_cast<uint32_t>(k * kFindThreads + tid) >= limit;
+        return n;
+      });
+      up_to = ~first;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < turns; ++k) {
+    const uint32_t v = at(k), g = k * kFindThreads + tid;
+    if (v > least || (v == least && g <= up_to)) sh.wanted[atomicAdd(&sh.groups, 1)] = static_cast<int>(g);
+  }
+  find_sync();
+
+  // ---------------------------------------------------------- their entries, the target, and the list so far
+  const int wanted = sh.groups;
+  if (p.groups <= wanted) least = 0u;
+  const float* z = p.z + t * p.ld_z;
+  auto add = [&](bool on, float v, int id) {
+    const unsigned b = __ballot_sync(0xffffffffu, on);
+    if (b == 0u) return;
+    int n = 0;
+    if (lane == 0) n = atomicAdd(&sh.candidates, __popc(b));
+    n = __shfl_sync(0xffffffffu, n, 0);
+    if (on)
+      sh.cand[n + __popc(b & ((1u << lane) - 1u))] =
+          (static_cast<uint64_t>(order_of(v)) << 32) | (~static_cast<uint32_t>(id));
+  };
+#pragma unroll 4
+  for (int i = warp; i < wanted; i += kTopWarps) {  // tile g / 8, half g / 4 % 2, 32 entries from g % 4 * 32
+    const int g = sh.wanted[i];
+    const int first = p.v0 + (g >> 3) * p.thin_h + ((g >> 2) & 1) * (p.thin_h / 2);
+    const int id = first + (g & 3) * 32 + lane;
+    const bool in = id < min(p.v0 + p.width, first + p.thin_h / 2) && id != y;
+    const float v = in ? z[id - p.v0] : 0.f;
+    add(in && order_of(v) >= least, v, id);
+  }
+  // the groups' peaks leave the target out: its logit goes in by itself
+  if (warp == 0 && y >= p.v0 && y < p.v0 + p.width) add(lane == 0, z[y - p.v0], static_cast<int>(y));
+  if (warp == 1 && !p.first)
+    for (int i = lane; i - lane < held; i += 32) {
+      const int id = i < held ? p.list_id[t * kHeld + i] : -1;
+      add(id >= 0, id >= 0 ? p.list_z[t * kHeld + i] : 0.f, id);
+    }
+  find_sync();
+
+  // ---------------------------------------------------------- the first of them, in order
+  const int n = sh.candidates, keep = min(n, held);
+  uint64_t reach = 0;
+  if (n > kRanked)
+    reach = find_threshold<uint64_t>(sh, keep, 0, uint64_t(0), ~uint64_t(0), turn, [&](uint64_t limit) {
+      int c = 0;
+      for (int i = tid; i < n; i += kFindThreads) c += sh.cand[i] >= limit;
+      return c;
+    });
+  for (int i = tid; i < n; i += kFindThreads) {
+    const uint64_t mine = sh.cand[i];
+    if (mine < reach) continue;
+    int place = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) place += sh.cand[j] > mine;
+    if (place < keep) sh.sorted[place] = mine;
+  }
+  find_sync();
+  const Order o = {sh.sorted, sh.exact, keep, p.top};
+  if (warp == 0) {
+    const uint64_t starts = o.starts(p, lane);
+    if (lane == 0) sh.starts = starts;
+  }
+  find_sync();
+  o.exact_dots(p, t, sh.starts, warp, kTopWarps, lane);
+  find_sync();
+  __syncthreads();  // the joined sums are there
+  o.results(p, t, y, sh.starts, tid, kFindThreads);
+}
+
+template <int KEYS>
+__global__ void __launch_bounds__(kFindThreads + kJoinThreads) score_top_kernel(const __grid_constant__ ScoreParams r,
+                                                                                const __grid_constant__ TopParams p) {
+  __shared__ FindShared sh;
   __shared__ ScoreShared<1, kJoinThreads> rows;
-  __shared__ uint32_t first_key[kTopWarps * kHeld];
-  __shared__ int first_group[kTopWarps * kHeld];
   follow();
-  const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (warp >= kTopWarps) {
-    score_rows<1, kJoinThreads>(r, t, threadIdx.x - 32 * kTopWarps, rows, [] { asm volatile("bar.sync 1, 256;" ::: "memory"); });
+  if (threadIdx.x >= kFindThreads) {
+    score_rows<1, kJoinThreads>(r, blockIdx.x, threadIdx.x - kFindThreads, rows,
+                                [] { asm volatile("bar.sync 1, 256;" ::: "memory"); });
     __syncthreads();
     return;
   }
-  const int held = p.top + kSpare, share = (p.groups + kTopWarps - 1) / kTopWarps;
-  const int begin = min(warp * share, p.groups), n = min(share, p.groups - begin);
-  for (int i = lane; i < kHeld; i += 32) first_key[warp * kHeld + i] = 0u;
-  __syncwarp();
-  pick<KEYS>(n, held, lane, [&](int i) { return peak_of(p, t, begin + i); },
-             [&](int place, int i, uint32_t key) {
-               first_key[warp * kHeld + place] = key;
-               first_group[warp * kHeld + place] = begin + i;
-             });
-  asm volatile("bar.sync 2, 256;" ::: "memory");
-  if (warp == 0) {
-    uint32_t least = 0xffffffffu;
-    const int wanted = pick<kTopWarps * kHeld / 32>(kTopWarps * kHeld, held, lane, [&](int i) { return first_key[i]; },
-                                                    [&](int place, int i, uint32_t key) {
-                                                      sh.wanted[place] = first_group[i];
-                                                      least = min(least, key);
-                                                    });
-    least = __reduce_min_sync(0xffffffffu, least);
-    __syncwarp();
-    top_of(p, t, lane, sh, wanted, p.groups > wanted ? least : 0u, [] { __syncthreads(); });
-  } else {
-    __syncthreads();
-  }
+  find<KEYS>(p, blockIdx.x, sh);
 }
 
 }  // namespace
@@ -383,9 +560,8 @@ cudaError_t launch_top(const TopParams& p, cudaStream_t s) {
 
 cudaError_t launch_score_top(const ScoreParams& r, const TopParams& p, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.tokens));
-  const int threads = 32 * kTopWarps + kJoinThreads;
-  if (p.groups <= 256 * kTopWarps) return launch_follow(score_top_kernel<8>, grid, threads, 0, s, 1, r, p);
-  if (p.groups <= 1024 * kTopWarps) return launch_follow(score_top_kernel<32>, grid, threads, 0, s, 1, r, p);
+  const int threads = kFindThreads + kJoinThreads;
+  if (p.groups <= 8 * kFindThreads) return launch_follow(score_top_kernel<8>, grid, threads, 0, s, 1, r, p);
   return launch_follow(score_top_kernel<0>, grid, threads, 0, s, 1, r, p);
 }
 
