@@ -1,12 +1,18 @@
 """A small mixture-of-experts language model trained with every operator of the library.
 
-    python -m matrix_optimizer_update_gb300.example_moe_lm [--steps N] [--distill]
+    python -m matrix_optimizer_update_gb300.example_moe_lm [--steps N] [--distill | --policy] [--max-norm X]
 
 One step: tokens -> embedding -> router -> ``Router`` sends rows to the experts
 -> experts' products -> ``Router`` combines them -> head -> ``Head`` gives the
 loss (cross entropy, or distillation from the stored top logits of a teacher)
 and its gradients, without the logits. The experts' and the router's matrices
-are updated by ``Muon``, embedding and head by AdamW (``dmuon_adamw_flat``).
+are updated by ``Muon``, embedding and head by AdamW (``dmuon_adamw_flat``),
+after ``GradClip`` has clipped all gradients where a largest norm is given.
+
+With ``--policy`` the model learns from what it generates: ``Experts`` and
+``Head.logprobs`` give its likeliest next tokens, one of them is chosen by its
+probability, and the gradient of the choice's log probability, weighted by whether
+it was right, and of the entropy trains the model.
 
 The data is synthetic: the next token is a fixed random function of the last,
 which the model has to learn by heart.
@@ -28,10 +34,10 @@ def first_derivative(backward):
     comes in has a graph, not where saved tensors have one.)"""
 
     @functools.wraps(backward)
-    def checked(ctx, grad):
+    def checked(ctx, *grads):
         if torch.is_grad_enabled():
             raise RuntimeError("the library's operators have no second derivatives")
-        return backward(ctx, grad)
+        return backward(ctx, *grads)
 
     return checked
 
@@ -101,6 +107,25 @@ class Distill(torch.autograd.Function):
                 None, None, None)
 
 
+class Logprob(torch.autograd.Function):
+    """Each token's log probability of its target, and the entropy, without the logits."""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, head, targets):
+        scores = head.logprobs(hidden, weight, targets)
+        ctx.head = head
+        ctx.save_for_backward(hidden, weight, targets, scores.logp, scores.entropy, scores.lse)
+        return scores.logp, scores.entropy
+
+    @staticmethod
+    @first_derivative
+    def backward(ctx, grad_logp, grad_entropy):
+        hidden, weight, targets, *scores = ctx.saved_tensors
+        scores = dm.Logprobs(*scores, None, None)
+        return (*ctx.head.logprobs_backward(hidden, weight, targets, scores, grad_logp.contiguous(),
+                                            grad_entropy.contiguous()), None, None)
+
+
 class Model:
     """Embedding, one mixture-of-experts layer with a residual, a norm, and a head."""
 
@@ -115,8 +140,13 @@ class Model:
         self.embedding = matrix(vocab, dim, 1.0)
         self.head_weight = matrix(vocab, dim, 0.02)
         self.router_weight = matrix(experts, dim, dim ** -0.5)
-        self.up = [matrix(inner, dim, dim ** -0.5) for _ in range(experts)]
-        self.down = [matrix(dim, inner, inner ** -0.5) for _ in range(experts)]
+        # the experts' matrices side by side, as Experts reads them; each is a parameter of its own for training
+        self.ups = torch.stack([matrix(inner, dim, dim ** -0.5).detach() for _ in range(experts)])
+        self.downs = torch.stack([matrix(dim, inner, inner ** -0.5).detach() for _ in range(experts)])
+        self.up = [m.detach().requires_grad_() for m in self.ups]
+        self.down = [m.detach().requires_grad_() for m in self.downs]
+        self.layer = dm.Experts.create(max_tokens, top, experts, dim, inner)
+        self.clip = dm.GradClip.create()
         self.router = dm.Router.create(max_tokens, top, experts)
         self.head = dm.Head.create(max_tokens, vocab, dim, max_top=max_top)
         # Muon for the matrices inside, AdamW for embedding and head
@@ -127,18 +157,38 @@ class Model:
         self.moments = [(torch.zeros(p.shape, device="cuda"), torch.zeros(p.shape, device="cuda")) for p in self.others]
         self.steps = 0
 
+    def routing(self, x):
+        probs = torch.softmax((x @ self.router_weight.T).float(), dim=1)
+        return probs.topk(self.top, dim=1)
+
+    @staticmethod
+    def norm(y):
+        y = y.float()
+        return (y * torch.rsqrt(y.square().mean(1, keepdim=True) + 1e-6)).to(torch.bfloat16)
+
     def hidden(self, tokens):
         x = self.embedding[tokens]
-        probs = torch.softmax((x @ self.router_weight.T).float(), dim=1)
-        weights, ids = probs.topk(self.top, dim=1)
+        weights, ids = self.routing(x)
         route = self.router.sort(ids)
         xs = Dispatch.apply(x, self.router, route)
         rows = [b - a for a, b in zip(route.offsets.tolist(), route.offsets[1:].tolist())]
         parts = torch.split(xs, rows)  # every assignment has an expert, so the rows add up
         ys = torch.cat([torch.nn.functional.silu(p @ u.T) @ d.T for p, u, d in zip(parts, self.up, self.down)])
-        y = x + Combine.apply(ys, weights.contiguous(), self.router, route)
-        y = y.float()
-        return (y * torch.rsqrt(y.square().mean(1, keepdim=True) + 1e-6)).to(torch.bfloat16)
+        return self.norm(x + Combine.apply(ys, weights.contiguous(), self.router, route))
+
+    @torch.no_grad()
+    def serve(self, tokens):
+        """The hidden states of tokens that are generated: nothing is read back to the host, and it can be captured."""
+        x = self.embedding[tokens]
+        weights, ids = self.routing(x)
+        return self.norm(x + self.layer.forward(x, ids, weights.contiguous(), self.ups, self.downs))
+
+    @torch.no_grad()
+    def choose(self, tokens, top=16, generator=None):
+        """A next token for each token, one of the ``top`` likeliest by its probability among them."""
+        scores = self.head.logprobs(self.serve(tokens), self.head_weight, top=top)
+        pick = torch.multinomial(scores.top_logp.exp(), 1, generator=generator)
+        return scores.top_ids.gather(1, pick)[:, 0]
 
     def losses(self, tokens, targets, teacher=None, temperature=2.0):
         """Per-token losses; ``teacher`` = (top ids, top logits) for distillation."""
@@ -147,11 +197,19 @@ class Model:
             return Xent.apply(h, self.head_weight, self.head, targets)
         return Distill.apply(h, self.head_weight, self.head, *teacher, temperature)
 
-    def step(self, lr=0.02, adamw_lr=3e-3):
-        """Update every parameter from its gradient, and clear the gradients."""
+    def policy(self, tokens, chosen):
+        """Per-token log probabilities of chosen next tokens, and entropies."""
+        return Logprob.apply(self.hidden(tokens), self.head_weight, self.head, chosen)
+
+    def step(self, lr=0.02, adamw_lr=3e-3, max_norm=None):
+        """Update every parameter from its gradient, and clear the gradients. With ``max_norm`` they are clipped to it
+        first; returns their norm before that then."""
         self.steps += 1
         stream = torch.cuda.current_stream().cuda_stream
+        norm = None
         with torch.no_grad():
+            if max_norm is not None:
+                norm = self.clip.clip([p.grad for p in (*self.matrices, *self.others) if p.grad is not None], max_norm)
             self.muon.step(self.matrices, [p.grad if p.grad is not None else torch.zeros_like(p)
                                            for p in self.matrices], self.momenta, lr=lr)
             for p, (m, v) in zip(self.others, self.moments):
@@ -159,6 +217,7 @@ class Model:
                                     lr=adamw_lr, weight_decay=0.0, step=self.steps, stream=stream)
         for p in (*self.matrices, *self.others):
             p.grad = None
+        return norm
 
 
 def batches(vocab, tokens, seed=1):
@@ -183,14 +242,35 @@ def teacher_lists(y, vocab, top, seed=2):
     return ids, logits
 
 
-def train(steps=60, distill=False, tokens=512, vocab=1000, log=print):
+def reinforce(steps=60, tokens=512, vocab=1000, bonus=0.01, max_norm=1.0, log=print):
+    """Learn from the model's own choices; returns how many of them were right, step by step."""
+    model = Model(vocab=vocab, max_tokens=tokens)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    history = []
+    for i, (x, y) in zip(range(steps), batches(vocab, tokens)):
+        chosen = model.choose(x, generator=g)
+        chosen = torch.where(y < 0, y, chosen)  # tokens that do not count have no choice
+        right = (chosen == y).float() * (y >= 0)
+        logp, entropy = model.policy(x, chosen)
+        advantage = torch.where(y >= 0, right - right.mean(), 0.0)
+        (-(advantage * logp).sum() / tokens - bonus * entropy.mean()).backward()
+        norm = model.step(max_norm=max_norm)
+        history.append(float(right.mean()))
+        if log and (i % 10 == 0 or i == steps - 1):
+            log(f"step {i}: {100 * history[-1]:.1f} % right, entropy {float(entropy.detach().mean()):.2f}, "
+                f"gradient norm {float(norm):.3f}")
+    return history
+
+
+def train(steps=60, distill=False, tokens=512, vocab=1000, max_norm=None, log=print):
     model = Model(vocab=vocab, max_tokens=tokens)
     history = []
     for i, (x, y) in zip(range(steps), batches(vocab, tokens)):
         loss = model.losses(x, y, teacher_lists(y, vocab, 16) if distill else None)
         mean = loss.sum() / (y >= 0).sum()
         mean.backward()
-        model.step()
+        model.step(max_norm=max_norm)
         history.append(float(mean.detach()))
         if log and (i % 10 == 0 or i == steps - 1):
             log(f"step {i}: {'distillation' if distill else 'cross entropy'} {history[-1]:.4f}")
@@ -200,6 +280,12 @@ def train(steps=60, distill=False, tokens=512, vocab=1000, log=print):
 if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=60)
-    ap.add_argument("--distill", action="store_true", help="learn from a teacher's top logits")
+    how = ap.add_mutually_exclusive_group()
+    how.add_argument("--distill", action="store_true", help="learn from a teacher's top logits")
+    how.add_argument("--policy", action="store_true", help="learn from the model's own choices")
+    ap.add_argument("--max-norm", type=float, default=None, help="clip the gradients to this norm")
     a = ap.parse_args()
-    train(a.steps, a.distill)
+    if a.policy:
+        reinforce(a.steps, max_norm=1.0 if a.max_norm is None else a.max_norm)
+    else:
+        train(a.steps, a.distill, max_norm=a.max_norm)
