@@ -242,13 +242,18 @@ def teacher_lists(y, vocab, top, seed=2):
     return ids, logits
 
 
-def reinforce(steps=60, tokens=512, vocab=1000, bonus=0.01, max_norm=1.0, log=print):
-    """Learn from the model's own choices; returns how many of them were right, step by step."""
+def reinforce(steps=60, tokens=512, vocab=1000, warm=15, bonus=0.01, max_norm=1.0, log=print):
+    """Learn from the model's own choices, after ``warm`` steps of cross entropy that make some of them right; returns
+    how many were, step by step."""
     model = Model(vocab=vocab, max_tokens=tokens)
     g = torch.Generator(device="cuda")
     g.manual_seed(3)
     history = []
-    for i, (x, y) in zip(range(steps), batches(vocab, tokens)):
+    data = batches(vocab, tokens)
+    for _, (x, y) in zip(range(warm), data):
+        (model.losses(x, y).sum() / (y >= 0).sum()).backward()
+        model.step(max_norm=max_norm)
+    for i, (x, y) in zip(range(steps), data):
         chosen = model.choose(x, generator=g)
         chosen = torch.where(y < 0, y, chosen)  # tokens that do not count have no choice
         right = (chosen == y).float() * (y >= 0)

@@ -122,3 +122,20 @@ def test_captured():
             s[k].copy_(v)
         graph.replay()
         check(layer, s, y)
+
+
+@pytest.mark.parametrize("tokens", [1, 7, 20])
+def test_call_after_call_without_a_wait(tokens):
+    """A call's launches are set up while those before still run, its own and the last call's, in the same workspace."""
+    layer = dm.Experts.create(tokens, 3, 10, 1100, 2000)
+    calls = [make(tokens, 3, 10, 1100, 2000, gated, 50 + k, 0.05) for k, gated in enumerate([True, False, True])]
+    first = []
+    for s in calls:
+        first.append(layer.forward(**s))
+        torch.cuda.synchronize()
+    later = [[layer.forward(**s) for s in calls] for _ in range(40)]
+    for s, y in zip(calls, first):
+        check(layer, s, y)
+    for ys in later:
+        for y, again in zip(first, ys):
+            assert torch.equal(y, again)
