@@ -722,9 +722,9 @@ dmuon_status dmuon_route_combine_backward(const void* dy, int64_t ld_dy, const v
  *
  * An id outside 0..experts-1 marks an assignment that adds nothing, whatever its
  * weight; a token without others gets zeros. A token may name an expert more
- * than once. Only the matrices of experts that are named are read, each once
- * for up to 32 assignments. Sums are fp32; h is held as the sum of two bf16, so
- * that y has the one rounding of its type.
+ * than once. Only the matrices of experts that are named are read, from memory
+ * once. Sums are fp32; h is held as the sum of two bf16, so that y has the one
+ * rounding of its type.
  *
  * For tokens * top <= 2048, and made for far fewer: what it costs is the reading
  * of the experts' matrices. With more tokens the experts' own products between
@@ -758,7 +758,8 @@ dmuon_status dmuon_experts_forward(const void* x, int64_t ld_x, const int64_t* e
                                    const void* up, const void* gate, const void* down, void* y, int64_t ld_y,
                                    void* d_workspace, size_t bytes, void* stream);
 
-/* The status word (DMUON_DEV_WAIT_TIMEOUT) of the last call that used a workspace; each call clears it first. */
+/* The status word (DMUON_DEV_WAIT_TIMEOUT) of the last call with tokens that used a workspace; each clears it first, and
+ * before any it says nothing. */
 dmuon_status dmuon_experts_read_device_status(const void* d_workspace, void* stream, uint32_t* bits);
 
 /*
@@ -772,8 +773,9 @@ dmuon_status dmuon_experts_read_device_status(const void* d_workspace, void* str
  * Squares are summed in fp32 per vector and unit and in 64 bits beyond; where
  * they leave the range of fp32 (gradients of 1e-30 or 1e30), in 64 bits
  * throughout. A norm that is infinite or NaN clips nothing: the gradients stay
- * (out becomes a copy of them), and norm says so. Elements are multiplied in
- * fp32 and rounded once.
+ * (out becomes a copy of them), and norm says so. Elements are multiplied by the
+ * quotient in fp32, in which it is held too (below 2^-126 it loses digits), and
+ * rounded once.
  *
  *  grads    host array of n device pointers; each tensor is contiguous and
  *           aligned to its elements, which is enough.

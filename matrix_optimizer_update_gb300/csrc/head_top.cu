@@ -10,7 +10,10 @@
 // too near to tell, their products are formed again with compensated sums, which decide the order.
 //
 // A warp per token: the search for the last of `held` peaks is a count over the warp for each bit that they differ in,
-// without a barrier. (A block per token took 105 us for 4093 tokens x 32768 entries, 15 us for one token.)
+// without a barrier. (A block per token took 105 us for 4093 tokens x 32768 entries, 15 us for one token.) What bounds
+// it is one warp's way through its instructions and trips to memory. 20 alternatives of 512 tokens, beside their log
+// probabilities alone: 20 us more with 32000 entries, 38 with 128000, of which writing the logits is 10 and 39 at the
+// copy rate; 61 tokens: 8 with 50257 entries, 15 with 128000.
 #include <algorithm>
 #include <cmath>
 
@@ -37,6 +40,11 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 __device__ __forceinline__ uint64_t order_of(double v) {
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v));
   return (u >> 63) != 0 ? ~u : u | (uint64_t(1) << 63);
+}
+
+// An entry as a number that is the larger the earlier it comes: by logit, then by id from the lowest.
+__device__ __forceinline__ uint64_t candidate(float z, int id) {
+  return (static_cast<uint64_t>(order_of(z)) << 32) | (~static_cast<uint32_t>(id));
 }
 
 struct TopShared {
@@ -163,15 +171,19 @@ struct Order {
   __device__ __forceinline__ bool shared(uint64_t starts, int i) const {
     return run(starts, i) < top && (~(starts >> i) & (i + 1 < keep ? 3 : 1)) != 0;
   }
-  // The logits of such entries, of every step-th from `first` on, by a warp each.
+  // The logits of such entries, of every step-th, by a warp each: `first` is this warp's number of `step`.
   __device__ __forceinline__ void exact_dots(const TopParams& p, int64_t t, uint64_t starts, int first, int step,
                                              int lane) const {
 #pragma unroll 1
-    for (int i = first; i < keep; i += step)
-      if (shared(starts, i)) {
+    for (int h = 0; h < keep; h += 32) {
+      const int mine = h + lane;
+      unsigned todo = __ballot_sync(0xffffffffu, mine < keep && mine % step == first && shared(starts, mine));
+      for (; todo != 0u; todo &= todo - 1u) {
+        const int i = h + __ffs(todo) - 1;
         const double d = exact_dot(p.dot, t, id(i), lane);
         if (lane == 0) dots[i] = order_of(d + 0.0);
       }
+    }
   }
   __device__ __forceinline__ void results(const TopParams& p, int64_t t, int64_t y, uint64_t starts, int thread,
                                           int threads) const {
@@ -234,6 +246,7 @@ __device__ __forceinline__ int pick(int n, int held, int lane, Read&& read, Take
 #pragma unroll
   for (int k = 0; k < turns; ++k) {
     const uint32_t v = at(k);
+    if (!__any_sync(0xffffffffu, v >= least)) continue;
     const unsigned same = __ballot_sync(0xffffffffu, v == least);
     const bool on = v > least || (v == least && __popc(same & ((1u << lane) - 1u)) < level);
     level -= __popc(same);
@@ -257,14 +270,16 @@ __device__ __forceinline__ void top_of(const TopParams& p, int64_t t, int lane, 
   const int64_t y = p.targets != nullptr ? p.targets[t] : -1;
   const float* z = p.z + t * p.ld_z;
   int n = 0;
-  auto add = [&](bool on, float v, int id) {
-    const unsigned b = __ballot_sync(0xffffffffu, on);
-    if (on)
-      sh.cand[n + __popc(b & ((1u << lane) - 1u))] =
-          (static_cast<uint64_t>(order_of(v)) << 32) | (~static_cast<uint32_t>(id));
-    n += __popc(b);
+  const int target = y >= p.v0 && y < p.v0 + p.width ? static_cast<int>(y) : -1;
+  // This lane's first entry of a group, and where those of its part of the vocabulary end.
+  auto first_of = [&](int g, int& end) {
+    end = p.v0 + p.width;
+    if (p.thin_h == 0) return p.v0 + g * kGroup + 4 * lane;
+    const int first = p.v0 + (g >> 3) * p.thin_h + ((g >> 2) & 1) * (p.thin_h / 2);  // tile g / 8, half g / 4 % 2
+    end = min(end, first + p.thin_h / 2);
+    return first + (g & 3) * 32 + lane;
   };
-  constexpr int kBatch = 4;  // groups whose loads are in flight together
+  constexpr int kBatch = 8;  // groups whose loads are in flight together: a bit for each of 4 entries in a word
   for (int i0 = 0; i0 < wanted; i0 += kBatch) {
     float4 v[kBatch];
     int id[kBatch], end[kBatch];
@@ -273,38 +288,62 @@ __device__ __forceinline__ void top_of(const TopParams& p, int64_t t, int lane, 
       v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       id[u] = end[u] = 0;
       if (i0 + u >= wanted) continue;
-      const int g = sh.wanted[i0 + u];
-      end[u] = p.v0 + p.width;
-      if (p.thin_h != 0) {  // tile g / 8, half g / 4 % 2, 32 entries from g % 4 * 32
-        const int first = p.v0 + (g >> 3) * p.thin_h + ((g >> 2) & 1) * (p.thin_h / 2);
-        end[u] = min(end[u], first + p.thin_h / 2);
-        id[u] = first + (g & 3) * 32 + lane;
-        if (id[u] < end[u]) v[u].x = z[id[u] - p.v0];
-      } else {  // four entries a lane; past the last group's the row goes on to a multiple of 256
-        id[u] = p.v0 + g * kGroup + 4 * lane;
+      id[u] = first_of(sh.wanted[i0 + u], end[u]);
+      if (p.thin_h == 0) {  // four entries a lane; past the last group's the row goes on to a multiple of 256
         v[u] = *reinterpret_cast<const float4*>(z + (id[u] - p.v0));
+      } else {
+        if (id[u] < end[u]) v[u].x = z[id[u] - p.v0];
+        end[u] = min(end[u], id[u] + 1);
       }
     }
+    // Which of them count, a bit each (without a branch: lanes that part and meet again for each of four conditions
+    // took 85 cycles an entry), and where this lane's come to lie: one sum over the warp for the batch.
+    unsigned on = 0u;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (i0 + u >= wanted) break;
-      if (n > kCandidates - kGroup) n = compress(sh, n, held, lane);
       const float w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (k > 0 && p.thin_h != 0) break;
-        add(id[u] + k < end[u] && id[u] + k != y && order_of(w[k]) >= least, w[k], id[u] + k);
+        const unsigned in = id[u] + k < end[u], other = id[u] + k != target, high = order_of(w[k]) >= least;
+        on |= (in & other & high) << (4 * u + k);
       }
+    }
+    int before = __popc(on);
+    const int mine = before;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, before, d);
+      if (lane >= d) before += o;
+    }
+    const int more = __shfl_sync(0xffffffffu, before, 31);
+    before -= mine;
+    // (a batch may have more than there is room for, where many entries are equal: then a part at a time)
+    for (int done = 0; done < more;) {
+      if (n + more - done > kCandidates) n = compress(sh, n, held, lane);
+      const int now = min(more - done, kCandidates - n);
+      int place = before - done;
+      for (unsigned rest = on; rest != 0u; rest &= rest - 1u, ++place) {  // few: their values are loaded again
+        const int b = __ffs(rest) - 1;
+        int unused;
+        const int entry = first_of(sh.wanted[i0 + (b >> 2)], unused) + (b & 3);
+        if (place >= 0 && place < now) sh.cand[n + place] = candidate(z[entry - p.v0], entry);
+      }
+      n += now;
+      done += now;
+      __syncwarp();
     }
   }
   if (n > kCandidates - kHeld - 1) n = compress(sh, n, held, lane);
   // the groups' peaks leave the target out: its logit goes in by itself
-  const bool here = y >= p.v0 && y < p.v0 + p.width;
-  if (here) add(lane == 0, z[y - p.v0], static_cast<int>(y));
+  if (target >= 0) {
+    if (lane == 0) sh.cand[n] = candidate(z[target - p.v0], target);
+    ++n;
+  }
   if (!p.first)
     for (int i = lane; i - lane < held; i += 32) {
       const int id = i < held ? p.list_id[t * kHeld + i] : -1;
-      add(id >= 0, id >= 0 ? p.list_z[t * kHeld + i] : 0.f, id);
+      const unsigned b = __ballot_sync(0xffffffffu, id >= 0);
+      if (id >= 0) sh.cand[n + __popc(b & ((1u << lane) - 1u))] = candidate(p.list_z[t * kHeld + i], id);
+      n += __popc(b);
     }
   __syncwarp();
 
@@ -403,18 +442,27 @@ __device__ __forceinline__ T find_threshold(FindShared& sh, int want, int more, 
   return at;
 }
 
-// KEYS: the piece has at most KEYS groups to a finder, whose peaks are held in registers; 0: any number.
-template <int KEYS>
-__device__ __forceinline__ void find(const TopParams& p, int64_t t, FindShared& sh) {
+// Where the groups' peaks are held: up to kInRegisters to a finder in its registers, up to kInShared in all in shared
+// memory, else they are read again each time. (Read again, one token x 262144 x 256 took 64 us, 128 tokens 111; from
+// shared memory 51 and 94. 34 and 53 are the log probabilities alone.)
+enum Keys { kRead, kRegisters, kShared };
+constexpr int kInRegisters = 8;
+constexpr int kInShared = 40 * 1024;
+
+template <Keys KEYS>
+__device__ __forceinline__ void find(const TopParams& p, int64_t t, FindShared& sh, uint32_t* keys) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, held = p.top + kSpare;
   int turn = 0;
   const int64_t y = p.targets != nullptr ? p.targets[t] : -1;
-  const int turns = KEYS != 0 ? KEYS : (p.groups + kFindThreads - 1) / kFindThreads;
+  const int turns = KEYS == kRegisters ? kInRegisters : (p.groups + kFindThreads - 1) / kFindThreads;
   auto read = [&](int g) {
     return g < p.groups ? max(order_of(p.parts[t * p.token_step + g * p.group_step].peak), 1u) : 0u;
   };
-  uint32_t key[KEYS != 0 ? KEYS : 1] = {};
-  auto at = [&](int k) { return KEYS != 0 ? key[k] : read(k * kFindThreads + tid); };
+  uint32_t key[KEYS == kRegisters ? kInRegisters : 1] = {};
+  auto at = [&](int k) {
+    const int g = k * kFindThreads + tid;
+    return KEYS == kRegisters ? key[k] : KEYS == kRead ? read(g) : g < p.groups ? keys[g] : 0u;
+  };
   if (tid == 0) {
     sh.low = 0xffffffffu;
     sh.high = 0u;
@@ -424,7 +472,8 @@ __device__ __forceinline__ void find(const TopParams& p, int64_t t, FindShared& 
 #pragma unroll
   for (int k = 0; k < turns; ++k) {
     const uint32_t v = read(k * kFindThreads + tid);
-    if (KEYS != 0) key[k] = v;
+    if (KEYS == kRegisters) key[k] = v;
+    if (KEYS == kShared && v != 0u) keys[k * kFindThreads + tid] = v;  // (which this thread alone reads)
     if (v != 0u) low = min(low, v);
     high = max(high, v);
   }
@@ -481,8 +530,7 @@ __device__ __forceinline__ void find(const TopParams& p, int64_t t, FindShared& 
     if (lane == 0) n = atomicAdd(&sh.candidates, __popc(b));
     n = __shfl_sync(0xffffffffu, n, 0);
     if (on)
-      sh.cand[n + __popc(b & ((1u << lane) - 1u))] =
-          (static_cast<uint64_t>(order_of(v)) << 32) | (~static_cast<uint32_t>(id));
+      sh.cand[n + __popc(b & ((1u << lane) - 1u))] = candidate(v, id);
   };
 #pragma unroll 4
   for (int i = warp; i < wanted; i += kTopWarps) {  // tile g / 8, half g / 4 % 2, 32 entries from g % 4 * 32
@@ -532,11 +580,12 @@ __device__ __forceinline__ void find(const TopParams& p, int64_t t, FindShared& 
   o.results(p, t, y, sh.starts, tid, kFindThreads);
 }
 
-template <int KEYS>
+template <Keys KEYS>
 __global__ void __launch_bounds__(kFindThreads + kJoinThreads) score_top_kernel(const __grid_constant__ ScoreParams r,
                                                                                 const __grid_constant__ TopParams p) {
   __shared__ FindShared sh;
   __shared__ ScoreShared<1, kJoinThreads> rows;
+  extern __shared__ uint32_t keys[];
   follow();
   if (threadIdx.x >= kFindThreads) {
     score_rows<1, kJoinThreads>(r, blockIdx.x, threadIdx.x - kFindThreads, rows,
@@ -544,7 +593,7 @@ __global__ void __launch_bounds__(kFindThreads + kJoinThreads) score_top_kernel(
     __syncthreads();
     return;
   }
-  find<KEYS>(p, blockIdx.x, sh);
+  find<KEYS>(p, blockIdx.x, sh, keys);
 }
 
 }  // namespace
@@ -561,8 +610,13 @@ cudaError_t launch_top(const TopParams& p, cudaStream_t s) {
 cudaError_t launch_score_top(const ScoreParams& r, const TopParams& p, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.tokens));
   const int threads = kFindThreads + kJoinThreads;
-  if (p.groups <= 8 * kFindThreads) return launch_follow(score_top_kernel<8>, grid, threads, 0, s, 1, r, p);
-  return launch_follow(score_top_kernel<0>, grid, threads, 0, s, 1, r, p);
+  if (p.groups <= kInRegisters * kFindThreads)
+    return launch_follow(score_top_kernel<kRegisters>, grid, threads, 0, s, 1, r, p);
+  if (p.groups > kInShared) return launch_follow(score_top_kernel<kRead>, grid, threads, 0, s, 1, r, p);
+  const cudaError_t e = cudaFuncSetAttribute(score_top_kernel<kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kInShared * static_cast<int>(sizeof(uint32_t)));
+  if (e != cudaSuccess) return e;
+  return launch_follow(score_top_kernel<kShared>, grid, threads, sizeof(uint32_t) * p.groups, s, 1, r, p);
 }
 
 }  // namespace head

@@ -805,6 +805,7 @@ class Experts:
         return _run(self, call, stream, x, expert_ids, weights, up, down, gate, scratch=self.workspace)
 
     def read_device_status(self, stream: int = 0) -> int:
+        """The status of the last call that had tokens."""
         b = ctypes.c_uint32()
         _check(lib().dmuon_experts_read_device_status(self.workspace.data_ptr(), ctypes.c_void_p(stream), ctypes.byref(b)))
         return b.value

@@ -395,3 +395,15 @@ def test_many_short_tiles(tokens, vocab, dim):
         assert top == 0 or torch.equal(got.top_ids, ids)
         first = first or [got.logp, got.entropy, *grads]
         assert all(torch.equal(a, b) for a, b in zip(first, [got.logp, got.entropy, *grads]))
+
+
+@pytest.mark.parametrize("tokens,vocab", [(1, 70000), (61, 140000), (2, 1 << 20), (2, 1500000)])
+def test_few_tokens_of_large_vocabularies(tokens, vocab):
+    # more groups than their finders' registers hold, and than shared memory does; one piece
+    h, w, y, _, _ = inputs(tokens, vocab, 24, 19, sure=0.0)
+    z = h.double() @ w.double().T
+    for top in (1, 32):
+        got = dm.Head.create(tokens, vocab, 24).logprobs(h, w, y, top=top)
+        assert torch.equal(got.top_ids, z.sort(dim=1, descending=True, stable=True).indices[:, :top])
+        logp = z - torch.logsumexp(z, 1, keepdim=True)
+        assert (got.top_logp - logp.gather(1, got.top_ids)).abs().max() < 1e-4
