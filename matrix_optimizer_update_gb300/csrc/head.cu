@@ -324,7 +324,8 @@ dmuon_status score(dmuon_head_t H, const void* hidden, int64_t ld_hidden, const 
     r.groups += head::logit_groups(tokens, std::min(piece, H->vocab - v0), H->pairs);
   r.token_step = thin ? r.groups : 1;
   r.group_step = thin ? 1 : tokens;
-  r.picked = p.picked;
+  r.scale = 1.f / temperature;
+  r.scale_low = static_cast<float>(1.0 / static_cast<double>(temperature) - static_cast<double>(r.scale));
   r.logp = logp;
   r.entropy = entropy;
   r.lse = lse;

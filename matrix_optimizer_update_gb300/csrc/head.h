@@ -156,7 +156,7 @@ struct ScoreParams {
   const float* folds;
   int64_t token_step, group_step;
   int32_t groups;
-  float* picked;           // [tokens]: the targets' scaled logits
+  float scale, scale_low;  // 1 / temperature, and what fp32 leaves of it
   float* logp;
   float* entropy;
   float* lse;

@@ -1,5 +1,7 @@
-// head_dot.cuh - logits formed in fp32 FMAs (see kSure in head.h).
+// head_dot.cuh - logits formed in fp32 FMAs (see kSure in head.h), or with twice the digits.
 #pragma once
+
+#include <cmath>
 
 #include "head.h"
 
@@ -47,6 +49,64 @@ __device__ __forceinline__ void dot_parts(const DotParams& d, const int64_t (&t)
 __device__ __forceinline__ float warp_sum(float v) {
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   return v;
+}
+
+// A sum with twice fp32's digits (Knuth's two-sum: what each addition rounds away is added up beside it). In 64 bits the
+// same takes longer: an SM adds two or so of those a cycle.
+struct Twice {
+  float sum, rest;
+  __device__ __forceinline__ void add(float x) {
+    const float s = sum + x, b = s - sum;
+    rest += (sum - (s - b)) + (x - b);
+    sum = s;
+  }
+  __device__ __forceinline__ void add(const Twice& o) {
+    add(o.sum);
+    rest += o.rest;
+  }
+  __device__ __forceinline__ double value() const {  // (of a sum that is infinite the rest is NaN)
+    return static_cast<double>(sum) + (fabsf(rest) < INFINITY ? static_cast<double>(rest) : 0.0);
+  }
+};
+__device__ __forceinline__ Twice warp_sum(Twice v) {
+  for (int d = 16; d > 0; d >>= 1) {
+    Twice o;
+    o.sum = __shfl_xor_sync(0xffffffffu, v.sum, d);
+    o.rest = __shfl_xor_sync(0xffffffffu, v.rest, d);
+    v.add(o);
+  }
+  return v;
+}
+
+// One thread's part of a logit with twice fp32's digits: products of bf16 are exact in fp32, their sums are compensated.
+// FLIGHT rounds of loads are in flight, as the trip to memory is what it takes.
+template <int FLIGHT>
+__device__ __forceinline__ Twice exact_part(const DotParams& d, int64_t t, int64_t v, int at, int of) {
+  Twice s = {0.f, 0.f};
+  const bf16 *h = d.hidden + t * d.ld_hidden, *w = d.weight + v * d.ld_weight;
+  const int whole = d.dim / 8;
+  for (int c0 = at; c0 < whole; c0 += FLIGHT * of) {
+    uint4 a[FLIGHT], b[FLIGHT];
+#pragma unroll
+    for (int u = 0; u < FLIGHT; ++u) {
+      const bool in = c0 + of * u < whole;
+      a[u] = in ? *reinterpret_cast<const uint4*>(h + 8 * (c0 + of * u)) : make_uint4(0, 0, 0, 0);
+      b[u] = in ? *reinterpret_cast<const uint4*>(w + 8 * (c0 + of * u)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < FLIGHT; ++u) {
+      const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162*>(&a[u]),
+                           *y = reinterpret_cast<const __nv_bfloat162*>(&b[u]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = __bfloat1622float2(x[k]), g = __bfloat1622float2(y[k]);
+        s.add(f.x * g.x);
+        s.add(f.y * g.y);
+      }
+    }
+  }
+  for (int k = 8 * whole + at; k < d.dim; k += of) s.add(__bfloat162float(h[k]) * __bfloat162float(w[k]));
+  return s;
 }
 
 }  // namespace head

@@ -97,42 +97,9 @@ __device__ __forceinline__ int compress(TopShared& sh, int n, int held, int lane
   return at;
 }
 
-__device__ __forceinline__ void two_sum(float& sum, float& rest, float x) {
-  const float s = sum + x, b = s - sum;
-  rest += (sum - (s - b)) + (x - b);
-  sum = s;
-}
-
-// A logit (unscaled) by one warp: products of bf16 are exact in fp32, their sums are compensated. Four rounds of loads
-// are in flight, as the trip to memory is what it takes.
+// A logit (unscaled) by one warp.
 __device__ __forceinline__ double exact_dot(const DotParams& d, int64_t t, int64_t v, int lane) {
-  float sum = 0.f, rest = 0.f;
-  const bf16 *h = d.hidden + t * d.ld_hidden, *w = d.weight + v * d.ld_weight;
-  const int whole = d.dim / 8;
-  for (int c0 = lane; c0 < whole; c0 += 4 * 32) {
-    uint4 a[4], b[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const bool in = c0 + 32 * u < whole;
-      a[u] = in ? *reinterpret_cast<const uint4*>(h + 8 * (c0 + 32 * u)) : make_uint4(0, 0, 0, 0);
-      b[u] = in ? *reinterpret_cast<const uint4*>(w + 8 * (c0 + 32 * u)) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162*>(&a[u]),
-                           *y = reinterpret_cast<const __nv_bfloat162*>(&b[u]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = __bfloat1622float2(x[k]), g = __bfloat1622float2(y[k]);
-        two_sum(sum, rest, f.x * g.x);
-        two_sum(sum, rest, f.y * g.y);
-      }
-    }
-  }
-  for (int k = 8 * whole + lane; k < d.dim; k += 32) two_sum(sum, rest, __bfloat162float(h[k]) * __bfloat162float(w[k]));
-  double s = static_cast<double>(sum) + static_cast<double>(rest);
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
+  return warp_sum(exact_part<4>(d, t, v, lane, 32)).value();
 }
 
 // The largest entries in order, as (logit, ~id), and what is done about neighbours too near to tell.

@@ -407,3 +407,35 @@ def test_few_tokens_of_large_vocabularies(tokens, vocab):
         assert torch.equal(got.top_ids, z.sort(dim=1, descending=True, stable=True).indices[:, :top])
         logp = z - torch.logsumexp(z, 1, keepdim=True)
         assert (got.top_logp - logp.gather(1, got.top_ids)).abs().max() < 1e-4
+
+
+@pytest.mark.parametrize("tokens,top", [(1, 0), (1, 5), (77, 0), (77, 3), (200, 0), (200, 5)])
+@pytest.mark.parametrize("dim", [64, 1003])
+def test_a_targets_logit_has_more_digits_than_fp32(tokens, top, dim):
+    # every other entry's logit is 0 exactly, so that all that can be off is the target's, 16 to 56: half a unit in its
+    # last place alone would be 1e-6 to 2e-6 of log p. Formed with twice the digits, with d = z + low: exp(d) (2 units,
+    # and its factor's one), the sum's factor, log1p (2) and their roundings are within 10 E of log p; the entropy has d
+    # and two sums more.
+    vocab, tau, half = 600, np.float32(0.7), dim // 2
+    g = torch.Generator(device="cuda")
+    g.manual_seed(tokens + dim)
+    ld = -(-dim // 8) * 8
+    h = torch.zeros(tokens, ld, device="cuda", dtype=torch.bfloat16)[:, :dim]
+    w = torch.zeros(vocab, ld, device="cuda", dtype=torch.bfloat16)[:, :dim]
+    w[:, half:] = torch.randn(vocab, dim - half, generator=g, device="cuda").to(torch.bfloat16)
+    row = torch.randn(half, generator=g, device="cuda").to(torch.bfloat16)
+    w[7], w[7, :half] = 0.0, row
+    scale = torch.linspace(11.5, 39, tokens, device="cuda")[:, None] / row.double().square().sum()
+    h[:, :half] = (row.double() * scale).to(torch.bfloat16)
+    z = f64(h) @ f64(w[7]) / np.float64(tau)
+    assert z.min() > 15 and z.max() < 58
+    got = dm.Head.create(tokens, vocab, dim).logprobs(h, w, torch.full((tokens,), 7, device="cuda"), top=top,
+                                                      temperature=float(tau))
+    ratio = (vocab - 1) * np.exp(-z)
+    logp = -np.log1p(ratio)
+    entropy = -logp + ratio * z / (1 + ratio)
+    assert np.all(np.abs(f64(got.logp) - logp) <= -10 * E * logp)
+    assert np.all(np.abs(f64(got.entropy) - entropy) <= 14 * E * entropy)
+    assert np.all(np.abs(f64(got.lse) - (z - logp)) <= 2 * E * z)
+    if top:
+        assert bool((got.top_ids[:, 0] == 7).all()) and torch.equal(got.top_logp[:, 0], got.logp)
