@@ -184,3 +184,21 @@ def test_refusals_reach_python():
         with pytest.raises(dm.DmuonError):
             call()
     assert bool((a == 1.0).all())
+
+
+def test_a_tensor_named_twice_counts_twice():
+    clip = dm.GradClip.create()
+    for n in (1000, 1 << 20):
+        a = torch.ones(n, device="cuda", dtype=torch.bfloat16)
+        assert float(clip.norm([a, a, a[:n // 2]])) == pytest.approx((2.5 * n) ** 0.5, rel=1e-6)
+
+
+@pytest.mark.parametrize("size", [500, 1 << 20])
+def test_limits_of_zero_and_infinity(size):
+    clip = dm.GradClip.create()
+    grads = [torch.randn(size, device="cuda"), torch.randn(size, device="cuda").to(torch.bfloat16)]
+    before = [g.clone() for g in grads]
+    clip.clip(grads, math.inf)
+    assert all(torch.equal(a, b) for a, b in zip(grads, before))
+    assert float(clip.clip(grads, 0.0)) > 0.0 and not any(g.any() for g in grads)
+    assert float(clip.clip(grads, 0.0)) == 0.0 and not any(g.any() for g in grads)  # 0 / 0 is not asked for

@@ -139,3 +139,48 @@ def test_call_after_call_without_a_wait(tokens):
     for ys in later:
         for y, again in zip(first, ys):
             assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("which", ["up", "gate", "down", "all"])
+def test_matrices_that_do_not_start_on_16_bytes(which):
+    s = make(6, 2, 4, 64, 48, True, 11)
+
+    def shifted(t):
+        flat = torch.full((t.numel() + 8,), float("nan"), dtype=t.dtype, device="cuda")
+        flat[1:t.numel() + 1] = t.flatten()
+        return flat[1:t.numel() + 1].view(t.shape)
+
+    names = ("up", "gate", "down") if which == "all" else (which,)
+    check(dm.Experts.create(6, 2, 4, 64, 48), {**s, **{k: shifted(s[k]) for k in names}})
+
+
+@pytest.mark.parametrize("gated", [True, False])
+def test_few_tokens_that_name_the_same_experts_over_and_over(gated):
+    # 256 assignments each to two experts, and 8 to one
+    s = make(8, 64, 3, 72, 56, gated, 12, 0.0)
+    s["expert_ids"][:, 0] = 1
+    s["expert_ids"][:, 1:] = torch.arange(63, device="cuda") % 2 * 2
+    check(dm.Experts.create(8, 64, 3, 72, 56), s)
+
+
+@pytest.mark.parametrize("dim,inner", [(1 << 20, 8), (8, 1 << 20), ((1 << 20) - 1, 3)])
+def test_the_widest_layers(dim, inner):
+    check(dm.Experts.create(2, 1, 2, dim, inner), make(2, 1, 2, dim, inner, True, 13, 0.0))
+
+
+@pytest.mark.parametrize("inner", [48, 43])
+def test_values_that_are_no_numbers_stay_in_their_token(inner):
+    s = make(12, 3, 5, 64, inner, True, 14, 0.0)
+    layer = dm.Experts.create(12, 3, 5, 64, inner)
+    want = layer.forward(**s)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        x = s["x"].clone()
+        x[7, 5] = bad
+        y = layer.forward(**{**s, "x": x})
+        assert torch.equal(y[:7], want[:7]) and torch.equal(y[8:], want[8:])
+        assert not torch.isfinite(y[7]).any()
+    # an assignment that adds nothing does so whatever its weight is
+    s["expert_ids"][4, 1] = -1
+    want = layer.forward(**s)
+    s["weights"][4, 1] = float("nan")
+    assert torch.equal(layer.forward(**s), want)

@@ -439,3 +439,17 @@ def test_a_targets_logit_has_more_digits_than_fp32(tokens, top, dim):
     assert np.all(np.abs(f64(got.lse) - (z - logp)) <= 2 * E * z)
     if top:
         assert bool((got.top_ids[:, 0] == 7).all()) and torch.equal(got.top_logp[:, 0], got.logp)
+
+
+@pytest.mark.parametrize("tokens", [1, 100, 300])
+def test_a_vocabulary_of_one(tokens):
+    h, w, _, gl, ge = inputs(tokens, 1, 40, 20)
+    head = dm.Head.create(tokens, 1, 40)
+    z = f64(h) @ f64(w).T
+    for y in (torch.zeros(tokens, dtype=torch.int64, device="cuda"), None):
+        got = head.logprobs(h, w, y, top=1)
+        assert not got.logp.any() and not got.entropy.any()
+        assert np.all(np.abs(f64(got.lse) - z[:, 0]) <= 1e-4) and not got.top_ids.any()
+        assert got.top_logp.abs().max() <= 1e-5
+        dh, dw = head.logprobs_backward(h, w, y, got, gl, ge)
+        assert dh.abs().max() <= 1e-4 and dw.abs().max() <= 1e-2
