@@ -19,9 +19,9 @@
 // its shared memory each, took 36.5 us in place of 35, and 81 in place of 72 for 7 tokens without a gate.
 //
 // A product's sum may run over K in any order, so that a lane's 16 bytes of a row stand for whatever K indices
-// mma.sync gives that lane, for the matrix and the tokens alike: nothing is transposed. mma.sync, as tcgen05 would pad
-// a few tokens' products to 128 rows that have to be in shared memory in full: the tensor pipe is at a few percent
-// here either way.
+// mma.sync gives that lane, for the matrix and the tokens alike: nothing is transposed. mma.sync, as tcgen05 wants the
+// tokens' rows, gathered anew for each expert, in shared memory in a layout of its own: with 64 tokens the tensor pipe
+// is at 13 % (up) and 23 % (down) of its cycles, and up to 8 assignments to an expert cost no more than one.
 //
 // Other rows are read element by element (experts_plain_kernel), every warp straight from memory.
 #include <cuda_bf16.h>
