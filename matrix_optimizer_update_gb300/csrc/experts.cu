@@ -82,6 +82,7 @@ struct ExpertsParams {
 struct StreamParams {
   ExpertsParams e;
   CUtensorMap boxes[2][3];
+  uint64_t share;  // 2^64 / the grid, rounded up (not used where that is one)
 };
 
 // What a block knows of the routing: the experts in use in ascending order, and each one's assignments.
@@ -306,15 +307,19 @@ __device__ __forceinline__ int cost_of(int assignments) {
   return DOWN ? 8 * passes + 4 * tiles : 16 * passes + 3 * tiles;
 }
 
-// Cuts the row blocks of all experts in use into one run for each block of the grid, of equal cost. By one warp.
+// Cuts the row blocks of all experts in use into one run for each block of the grid, of equal cost: where number `part`
+// starts. `share` is 2^64 / the grid, rounded up, for grids of more than one. By one warp. (Divisions in 64 bits took 1 us before each launch's first
+// load.)
 template <bool DOWN>
-__device__ __forceinline__ int cut(const Routing& r, int blocks, int64_t part, int64_t parts, int lane) {
-  int64_t total = 0;
+__device__ __forceinline__ int cut(const Routing& r, int blocks, unsigned part, uint64_t share, int lane) {
+  if (part == 0 || part == gridDim.x) return part == 0 ? 0 : r.actives * blocks;
+  unsigned total = 0;
   for (int i0 = 0; i0 < r.actives; i0 += 32) {
     const int i = i0 + lane;
     total += __reduce_add_sync(0xffffffffu, i < r.actives ? cost_of<DOWN>(r.begin[i + 1] - r.begin[i]) : 0);
   }
-  int64_t want = total * blocks * part / parts;  // cost before the cut
+  // cost before the cut (total * blocks is below 2^33)
+  int64_t want = static_cast<int64_t>(__umul64hi(uint64_t(total) * blocks * part, share));
   for (int i0 = 0; i0 < r.actives; i0 += 32) {
     const int i = i0 + lane, mine = i < r.actives ? cost_of<DOWN>(r.begin[i + 1] - r.begin[i]) : 0;
     int before = mine;
@@ -330,8 +335,8 @@ __device__ __forceinline__ int cut(const Routing& r, int blocks, int64_t part, i
     // the lane whose expert the cut falls into: the first that reaches it
     const unsigned reach = __ballot_sync(0xffffffffu, i < r.actives && int64_t(before) * blocks >= want);
     const int l = __ffs(reach) - 1;
-    const int64_t rest = want - int64_t(before - mine) * blocks;
-    const int block = mine > 0 ? static_cast<int>((rest + mine - 1) / mine) : 0;
+    const unsigned rest = static_cast<unsigned>(want - int64_t(before - mine) * blocks);  // on that lane, mine * blocks at most
+    const int block = mine > 0 ? static_cast<int>((rest + mine - 1u) / static_cast<unsigned>(mine)) : 0;
     return (i0 + l) * blocks + __shfl_sync(0xffffffffu, block, l);
   }
   return r.actives * blocks;
@@ -553,7 +558,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) experts_stream_kernel(const
   constexpr int kOut = PHASE == kGated ? 8 : 16;
   const int blocks = (rows + kOut - 1) / kOut;
   if (warp < 2) {
-    const int at = cut<down>(sh.r, blocks, blockIdx.x + warp, gridDim.x, lane);
+    const int at = cut<down>(sh.r, blocks, blockIdx.x + warp, sp.share, lane);
     if (lane == 0) (warp == 0 ? sh.from : sh.to) = at;
   }
   ptx::fence_proxy_async_shared();  // the scratch's place is the ring's
@@ -733,6 +738,7 @@ cudaError_t launch(const ExpertsParams& p, bool stream, int sms, cudaStream_t s)
   }
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(units, sms)));
+  sp.share = ~uint64_t(0) / grid.x + 1;
   // where no expert gets more than 8 assignments unless a token names it twice, the loops for more are left out
   auto* kernel = p.tokens <= 8 ? experts_stream_kernel<PHASE, 1> : experts_stream_kernel<PHASE, kMostTiles>;
   if ((e = shared(kernel, kStreamSmem)) != cudaSuccess) return e;
