@@ -9,14 +9,14 @@
 //
 // Rows that are whole 16-byte pieces stream through shared memory: one block per SM, whose ninth warp keeps six
 // stages of 64 rows by 256 columns on their way by TMA, whatever the eight others do. (Every warp loading its own
-// rows straight into registers took 48 us for one token to 8 of 64, 2048 x 1408, and 454 for 64 tokens; this takes 35
-// and 199, of which the matrices at the copy rate are 20 and 164.)
+// rows straight into registers took 48 us for one token to 8 of 64, 2048 x 1408, and 454 for 64 tokens; this takes 34.4
+// and 198, of which the matrices at the copy rate are 20 and 164.)
 //
 // A block owns a contiguous run of the row blocks of all experts in use, expert by expert, of the same cost to one
 // row block (16 rows of a matrix: 8 of gate and the same 8 of up, or 16), and takes up to four of them together, which
 // read the expert's tokens once. Four warps have the even stages and four the odd, each 64 of the columns. Down's
 // blocks start to read the routing while the products before still run; to have them beside up's on an SM, with half
-// its shared memory each, took 36.5 us in place of 35, and 81 in place of 72 for 7 tokens without a gate.
+// its shared memory each, took 36.5 us in place of 35.1, and 81 in place of 72 for 7 tokens without a gate.
 //
 // A product's sum may run over K in any order, so that a lane's 16 bytes of a row stand for whatever K indices
 // mma.sync gives that lane, for the matrix and the tokens alike: nothing is transposed. mma.sync, as tcgen05 wants the
@@ -308,8 +308,8 @@ __device__ __forceinline__ int cost_of(int assignments) {
 }
 
 // Cuts the row blocks of all experts in use into one run for each block of the grid, of equal cost: where number `part`
-// starts. `share` is 2^64 / the grid, rounded up, for grids of more than one. By one warp. (Divisions in 64 bits took 1 us before each launch's first
-// load.)
+// starts. `share` is 2^64 / the grid, rounded up, for grids of more than one. By one warp. (Divisions in 64 bits took
+// 0.3 us before each launch's first load.)
 template <bool DOWN>
 __device__ __forceinline__ int cut(const Routing& r, int blocks, unsigned part, uint64_t share, int lane) {
   if (part == 0 || part == gridDim.x) return part == 0 ? 0 : r.actives * blocks;
