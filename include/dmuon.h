@@ -772,10 +772,10 @@ dmuon_status dmuon_experts_read_device_status(const void* d_workspace, void* str
  *
  * Squares are summed in fp32 per vector and unit and in 64 bits beyond; where
  * they leave the range of fp32 (gradients of 1e-30 or 1e30), in 64 bits
- * throughout. A norm that is infinite or NaN clips nothing: the gradients stay
- * (out becomes a copy of them), and norm says so. Elements are multiplied by the
- * quotient in fp32, in which it is held too (below 2^-126 it loses digits), and
- * rounded once.
+ * throughout. A norm that is infinite or NaN, or above fp32's range so that norm
+ * is infinite, clips nothing: the gradients stay (out becomes a copy of them), and
+ * norm says so. Elements are multiplied by the quotient in fp32, in which it is
+ * held too (below 2^-126 it loses digits), and rounded once.
  *
  *  grads    host array of n device pointers; each tensor is contiguous and
  *           aligned to its elements, which is enough.

@@ -211,9 +211,10 @@ __device__ __forceinline__ double norm_of(const double* partial, int blocks) {
   return sqrt(s);
 }
 
-// What gradients of that norm are multiplied by. (A norm that is not finite clips nothing: the caller sees it.)
+// What gradients of that norm are multiplied by. (A norm that is not finite clips nothing: the caller sees it. So it
+// is the fp32 number which the caller gets that decides, where the one in 64 bits may still be finite.)
 __device__ __forceinline__ float scale_of(double norm, float max_norm) {
-  const bool clip = norm > static_cast<double>(max_norm) && norm < INFINITY;
+  const bool clip = norm > static_cast<double>(max_norm) && static_cast<float>(norm) < INFINITY;
   return clip ? static_cast<float>(static_cast<double>(max_norm) / norm) : 1.f;
 }
 
