@@ -12,8 +12,9 @@
 // order: the norm is the same from call to call.
 //
 // Up to 512 KB are one launch: a cluster of 8 blocks holds all of it in registers, joins its sums through shared
-// memory, and writes it back scaled. (Four matrices of 128 x 256, clipped: 7.8 us, as the two launches take, of which
-// the host pays for one less: 20 us a call against 26.)
+// memory, and writes it back scaled. The host, which is what small sets wait for, pays for a launch less: four fp32
+// matrices of 128 x 256 take 17 us a call for 22 in two launches. On the GPU it takes as long as the two up to
+// 256 KB (10 us replayed from a graph) and 2 us more beyond (12.3 for 10.3).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) clip_kernel(const __gr
 constexpr int kCluster = 8;
 constexpr int kGroup = 256;                        // threads that have a unit at a time, a vector each
 constexpr int kGroups = kThreads / kGroup;
-constexpr int kHold = 4;                           // units a thread holds a vector of (8 take 13 us where 4 take 8)
+constexpr int kHold = 4;                           // units a thread holds a vector of
 constexpr int kFewUnits = kCluster * kGroups * kHold;  // of kGroup vectors: 512 KB
 
 template <int N>
@@ -527,7 +528,7 @@ dmuon_status run(Call c, void* d_workspace, size_t bytes, void* stream, bool cli
   }
   c.partial = static_cast<double*>(d_workspace);
   c.stream = reinterpret_cast<cudaStream_t>(stream);
-  if (c.n <= 128 && vectors <= kFewUnits * kGroup) {
+  if (c.n <= 128 && vectors - c.n <= kFewUnits * kGroup) {  // too many to count otherwise
     int64_t units = 0;
     for (int i = 0; i < c.n; ++i)
       if (c.counts[i] > 0) units += units_of(c, i, kGroup);
