@@ -53,7 +53,9 @@ struct dmuon_head_s {
   int64_t piece = 0;   // vocabulary entries per piece of the backward pass, a multiple of kPieceStep
   size_t off_status = 0, off_parts = 0, off_picked = 0, off_ids = 0, off_q = 0, off_count = 0, off_entropy = 0,
          off_dz = 0, off_acc = 0, off_folds = 0, off_list = 0, bytes = 0;
-  int64_t z_bytes = 0;  // at off_dz: dz of the backward pass, logits of a scoring call
+  // at off_dz, the end of the workspace: dz of the backward pass, and a scoring call's logits, for which the caller may
+  // give more than the least
+  int64_t z_most = 0, z_bytes = 0;
   char* ws = nullptr;
   int device = -1, pairs = 0;
 
@@ -309,6 +311,9 @@ dmuon_status score(dmuon_head_t H, const void* hidden, int64_t ld_hidden, const 
   const bool thin = head::thin_tokens(tokens);
   int64_t piece = H->vocab;
   if (top > 0) {
+    if (H->z_bytes < 4 * tokens * kPieceStep)
+      return refuse(DMUON_ERR_WORKSPACE, "the workspace has room for the logits of %lld tokens",
+                    (long long)(H->z_bytes / 4 / kPieceStep));
     piece = std::min(cdiv(H->vocab, kPieceStep), H->z_bytes / (4 * tokens) / kPieceStep) * kPieceStep;
     p.z = reinterpret_cast<float*>(H->ws + H->off_dz);
     p.ld_z = piece;
@@ -393,30 +398,32 @@ extern "C" dmuon_status dmuon_head_create(int64_t max_tokens, int64_t vocab, int
     return o;
   };
   H->off_status = take(256);
+  // dz, and at least one block of entries of a scoring call's logits
+  const int64_t entries = cdiv(vocab, kPieceStep) * kPieceStep, block = 4 * max_tokens * kPieceStep;
+  const int64_t dz = 2 * std::max(max_tokens, std::min<int64_t>(2 * max_tokens, 2 * head::kTwofold)) * H->piece;
+  const int64_t z_least = std::max(dz, std::min(block, kPieceBytes)), all = 4 * max_tokens * entries;
+  H->z_most = std::max({z_least, std::min(all, kPieceBytes), block});
   // a call with few tokens has up to 8 groups for each 256 entries and for each pair of SMs and piece, of which a
-  // scoring call has one for each 2^20 entries (its logits' 512 MB over 128 tokens)
-  const int64_t parts = std::max(cdiv(vocab, head::kGroup) * max_tokens,
-                                 (cdiv(vocab, 32) + 8 * kMaxPairs * cdiv(vocab, int64_t(1) << 20)) *
-                                     std::min<int64_t>(max_tokens, kFewTokens));
+  // scoring call has as many as its logits need in the smallest workspace
+  const int64_t few = std::min<int64_t>(max_tokens, kFewTokens);
+  const int64_t pieces = cdiv(vocab, z_least / (4 * few) / kPieceStep * kPieceStep);
+  const int64_t parts =
+      std::max(cdiv(vocab, head::kGroup) * max_tokens, (cdiv(vocab, 32) + 8 * kMaxPairs * pieces) * few);
   H->off_parts = take(sizeof(head::Part) * parts);
   H->off_picked = take(4 * max_tokens * std::max(1, max_top));
   H->off_ids = take(4 * max_tokens * max_top);
   H->off_q = take(4 * max_tokens * max_top);
   H->off_count = take(max_top > 0 ? 4 * max_tokens : 0);
   H->off_entropy = take(max_top > 0 ? 4 * max_tokens : 0);
-  // logits of a scoring call: all where they take no more than 512 MB, else as many; at least one block of entries
-  const int64_t all = 4 * max_tokens * cdiv(vocab, kPieceStep) * kPieceStep;
-  H->z_bytes = std::max({2 * std::max(max_tokens, std::min<int64_t>(2 * max_tokens, 2 * head::kTwofold)) * H->piece,
-                         std::min(all, kPieceBytes), 4 * max_tokens * kPieceStep});
-  H->off_dz = take(H->z_bytes);
   // dH's sums: one set where tokens are many; where K is cut into slices, up to 2 tiles of 256 x 256 per pair
   const int64_t row = 4 * head::acc_pitch(dim);
   const int64_t folds = cdiv(sizeof(float) * parts, kAlign) * kAlign;
-  const int64_t list = all > H->z_bytes ? 8 * max_tokens * head::kHeld : 0;
+  const int64_t list = all > z_least ? 8 * max_tokens * head::kHeld : 0;
   H->off_acc = take(std::max({row * max_tokens, std::min(row * max_tokens * kMaxSlices, kSliceBytes), folds + list}));
   // in the same place, a scoring call's sums of the entropy, and the alternatives from one piece to the next
   H->off_folds = H->off_acc;
   H->off_list = H->off_acc + folds;
+  H->off_dz = take(z_least);
   H->bytes = at;
   *out = H;
   return ok();
@@ -425,6 +432,12 @@ extern "C" dmuon_status dmuon_head_create(int64_t max_tokens, int64_t vocab, int
 extern "C" dmuon_status dmuon_head_workspace_bytes(dmuon_head_t H, size_t* bytes) {
   if (H == nullptr || bytes == nullptr) return refuse(DMUON_ERR_INVALID_ARG, "NULL argument");
   *bytes = H->bytes;
+  return ok();
+}
+
+extern "C" dmuon_status dmuon_head_scores_workspace_bytes(dmuon_head_t H, size_t* bytes) {
+  if (H == nullptr || bytes == nullptr) return refuse(DMUON_ERR_INVALID_ARG, "NULL argument");
+  *bytes = std::max<size_t>(H->bytes, H->off_dz + H->z_most);
   return ok();
 }
 
@@ -452,6 +465,7 @@ extern "C" dmuon_status dmuon_head_bind(dmuon_head_t H, void* d_workspace, size_
                            reinterpret_cast<cudaStream_t>(stream))) != cudaSuccess)
     return cuda_refuse(e, "clearing the status word");
   H->ws = static_cast<char*>(d_workspace);
+  H->z_bytes = static_cast<int64_t>(std::min<size_t>(H->z_most, bytes - H->off_dz));
   H->device = device;
   H->pairs = std::min<int>(sms / 2, kMaxPairs);
   return ok();

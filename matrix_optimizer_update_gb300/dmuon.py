@@ -52,8 +52,8 @@ EXPORTS = (
     "dmuon_profile_begin", "dmuon_profile_end", "dmuon_profile_cta_times", "dmuon_read_cta_times",
     "dmuon_plan_costs", "dmuon_launch_count",
     "dmuon_selftest_wait_timeout", "dmuon_momentum_norm_noalloc", "dmuon_assign_owners", "dmuon_adamw_flat",
-    "dmuon_head_create", "dmuon_head_workspace_bytes", "dmuon_head_bind", "dmuon_head_xent",
-    "dmuon_head_xent_backward", "dmuon_head_xent_backward_loss", "dmuon_head_distill", "dmuon_head_distill_backward",
+    "dmuon_head_create", "dmuon_head_workspace_bytes", "dmuon_head_scores_workspace_bytes", "dmuon_head_bind",
+    "dmuon_head_xent", "dmuon_head_xent_backward", "dmuon_head_xent_backward_loss", "dmuon_head_distill", "dmuon_head_distill_backward",
     "dmuon_head_logprobs", "dmuon_head_logprobs_backward",
     "dmuon_head_read_device_status", "dmuon_head_destroy",
     "dmuon_route_workspace_bytes", "dmuon_route_sort", "dmuon_route_dispatch", "dmuon_route_combine",
@@ -116,6 +116,7 @@ def lib():
         "dmuon_adamw_flat": (i32, [vp, vp, vp, vp, i64, i32, i32, f32, f32, f32, f32, f32, i32, vp]),
         "dmuon_head_create": (i32, [i64, i64, i64, i32, ctypes.POINTER(vp)]),
         "dmuon_head_workspace_bytes": (i32, [vp, ctypes.POINTER(sz)]),
+        "dmuon_head_scores_workspace_bytes": (i32, [vp, ctypes.POINTER(sz)]),
         "dmuon_head_bind": (i32, [vp, vp, sz, vp]),
         "dmuon_head_xent": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, vp, vp]),
         "dmuon_head_xent_backward": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp]),
@@ -468,11 +469,13 @@ class Head:
         self.home = 0       # raw handle of the stream the workspace was allocated on
 
     @classmethod
-    def create(cls, max_tokens, vocab, dim, *, max_top=0, device=None, stream=None):
+    def create(cls, max_tokens, vocab, dim, *, max_top=0, alternatives=True, device=None, stream=None):
+        """``alternatives=False``: no room beside what the losses need, up to half the workspace; ``logprobs`` with
+        ``top`` then takes smaller pieces of the vocabulary, one after another."""
         h = ctypes.c_void_p()
         _check(lib().dmuon_head_create(int(max_tokens), int(vocab), int(dim), int(max_top), ctypes.byref(h)))
         self = cls(h, int(max_tokens), int(vocab), int(dim), int(max_top))
-        nbytes = self.workspace_bytes()
+        nbytes = self.workspace_bytes(alternatives)
         ws = _t().empty(nbytes + 1024, dtype=_t().uint8, device=device or "cuda")
         here = _here(ws.get_device())
         s = here if stream is None else stream.cuda_stream
@@ -482,9 +485,11 @@ class Head:
         self.workspace, self.home = ws, here
         return self
 
-    def workspace_bytes(self) -> int:
+    def workspace_bytes(self, alternatives=False) -> int:
+        """What ``bind`` needs at least, or with room for the logits that alternatives are chosen from."""
         n = ctypes.c_size_t()
-        _check(lib().dmuon_head_workspace_bytes(self._h, ctypes.byref(n)))
+        size = lib().dmuon_head_scores_workspace_bytes if alternatives else lib().dmuon_head_workspace_bytes
+        _check(size(self._h, ctypes.byref(n)))
         return n.value
 
     def bind(self, d_workspace: int, nbytes: int, stream: int = 0):
