@@ -617,8 +617,9 @@ dmuon_status dmuon_head_distill_backward(dmuon_head_t head, const void* hidden, 
  *  top_ids   device, tokens x top int64;  top_logp  the same, fp32.
  *
  * The target's share of the sum is kept apart from the others', as in
- * dmuon_head_xent, so that the log probability and the entropy of a token
- * predicted with near certainty keep their leading digits (other entries' log
+ * dmuon_head_xent, and the largest entry's from the rest, so that the log
+ * probability of a target predicted with near certainty and the entropy of a token
+ * with any nearly sure entry keep their leading digits (other entries' log
  * probabilities are off by about 1e-6 of their logit). Neighbours among the top
  * entries that are too near to tell in fp32 are put in order by sums with twice its
  * digits. A row whose logits are not finite has unspecified top entries (ids

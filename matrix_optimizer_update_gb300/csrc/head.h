@@ -80,7 +80,8 @@ struct LogitParams {
   int32_t after_lists;     // the launch before this one on the stream is launch_teacher's
   float* picked;           // [tokens][want.top]: scaled logits of the wanted entries
   int32_t v0, width;       // entries v0 .. v0 + width - 1 (forward: all, but for scores with alternatives)
-  // scores: beside parts, each group's sum of exp(z - peak) * (z - peak); logits for the choice of alternatives
+  // scores: parts hold the sum without one entry at the peak; beside them, each group's sum of exp(z - peak) *
+  // (z - peak); logits for the choice of alternatives
   float* folds;            // laid out as parts; nullptr: not a scoring call
   float* z;                // [tokens][ld_z], entries from v0; or nullptr
   int64_t ld_z;
@@ -152,7 +153,7 @@ struct ScoreParams {
   int32_t vocab;
   DotParams dot;           // the target's logit
   const int64_t* targets;  // or nullptr: none is given
-  const Part* parts;       // as RowParams
+  const Part* parts;       // as RowParams, but the sums go without one entry at the peak
   const float* folds;
   int64_t token_step, group_step;
   int32_t groups;

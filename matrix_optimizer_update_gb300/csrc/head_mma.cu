@@ -436,18 +436,35 @@ __device__ __forceinline__ bool drain_logits(const LogitParams& p, float zscale,
   return true;
 }
 
-// exp(z - from) of 32 logits added up, alone and times z - from, which is what entropies are made of. The factor is
-// bounded where the exponential is 0, so that a logit of -infinity adds nothing.
-__device__ __forceinline__ void fold(const float (&v)[32], float from, float& sum, float& folded) {
-  float s[4] = {}, f[4] = {};
+__device__ __forceinline__ float largest(const float (&v)[32]) {
+  float top = v[0];
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
-    const float d = v[k] - from, e = ex2(d * kLog2e);
-    s[k & 3] += e;
-    f[k & 3] = fmaf(e, fmaxf(d, -1e4f), f[k & 3]);
+  for (int k = 1; k < 32; ++k) top = fmaxf(top, v[k]);
+  return top;
+}
+
+// 0 for an exponential of 1, as the largest entry's (and one too near to tell from it) has, else 1; 0 for NaN.
+__device__ __forceinline__ float below_one(float e) { return __saturatef(fmaf(e, -0x1p30f, 0x1p30f)); }
+
+// exp(z - from) of 32 logits added up, alone and times z - from, which is what entropies are made of. `from` is the
+// largest: exponentials of 1 are counted, not added, so that the others' sum keeps its digits where one entry is nearly
+// sure (4096 tokens x 32000 x 256, where the epilogue is what takes the time, 93 us for 87; nothing from 2048 dims on).
+// The factor is bounded where the exponential is 0, so that a logit of -infinity adds nothing.
+__device__ __forceinline__ void fold(const float (&v)[32], float from, float& others, float& ones, float& folded) {
+  float2 s[2] = {}, f[2] = {}, n = {};
+#pragma unroll
+  for (int k = 0; k < 32; k += 2) {
+    const float2 d = __fadd2_rn(make_float2(v[k], v[k + 1]), make_float2(-from, -from));
+    const float2 x = __fmul2_rn(d, make_float2(kLog2e, kLog2e)), e = make_float2(ex2(x.x), ex2(x.y));
+    const float2 w = make_float2(below_one(e.x), below_one(e.y));
+    const int i = k >> 1 & 1;
+    s[i] = __ffma2_rn(e, w, s[i]);
+    n = __fadd2_rn(n, w);
+    f[i] = __ffma2_rn(e, make_float2(fmaxf(d.x, -1e4f), fmaxf(d.y, -1e4f)), f[i]);
   }
-  sum = (s[0] + s[1]) + (s[2] + s[3]);
-  folded = (f[0] + f[1]) + (f[2] + f[3]);
+  others = (s[0].x + s[0].y) + (s[1].x + s[1].y);
+  ones = 32.f - (n.x + n.y);
+  folded = (f[0].x + f[0].y) + (f[1].x + f[1].y);
 }
 
 // One warp's part of a score tile: as drain_logits, with the entropy's sums, and with the logits stored where
@@ -461,7 +478,7 @@ __device__ __forceinline__ bool drain_score(const Params& P, int64_t t, int64_t 
   c.start(p.want, t, in && p.want.targets != nullptr, j0);
   if (!wait()) return false;
   ptx::tc_fence_after();
-  float peak = -INFINITY, sum = 0.f, folded = 0.f;
+  float peak = -INFINITY, rest = 0.f, folded = 0.f;  // rest: the sum without the peak's own 1
 #pragma unroll 1
   for (int ch = 0; ch < 4; ++ch) {
     const int jc = j0 + ch * 32;
@@ -470,7 +487,10 @@ __device__ __forceinline__ bool drain_score(const Params& P, int64_t t, int64_t 
     if (ch == 3) free();
     if (jc >= p.vocab) continue;
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] *= P.zscale;
+    for (int k = 0; k < 32; k += 2) {
+      const float2 z = __fmul2_rn(make_float2(v[k], v[k + 1]), make_float2(P.zscale, P.zscale));
+      v[k] = z.x, v[k + 1] = z.y;
+    }
     if (jc + 32 > p.vocab) {
 #pragma unroll
       for (int k = 0; k < 32; ++k)
@@ -503,21 +523,18 @@ __device__ __forceinline__ bool drain_score(const Params& P, int64_t t, int64_t 
                            [&](float& x, float, float, int, bool) { x = -INFINITY; });
       __syncwarp();
     }
-    float top = v[0];
-#pragma unroll
-    for (int k = 1; k < 32; ++k) top = fmaxf(top, v[k]);
-    top = fmaxf(peak, top);
-    const float from = top == -INFINITY ? 0.f : top;  // nothing yet: every exponential is 0
-    float s, f;
-    fold(v, from, s, f);
+    const float top = fmaxf(peak, largest(v)), from = top == -INFINITY ? 0.f : top;  // nothing yet: every exponential is 0
+    float s, ones, f;
+    fold(v, from, s, ones, f);
     const float shift = peak == -INFINITY ? 0.f : peak - from, r = ex2((peak - from) * kLog2e);
-    folded = fmaf(fmaf(sum, shift, folded), r, f);
-    sum = fmaf(sum, r, s);
+    folded = fmaf(fmaf(1.f + rest, shift, folded), r, f);
+    // the peak so far stays, or one of this chunk's takes its place
+    rest = peak == top ? rest + (s + ones) : fmaf(1.f + rest, r, s + (ones - 1.f));
     peak = top;
   }
   if (in && j0 < p.vocab) {
     const int64_t at = int64_t(j0 / kGroup) * p.tokens + t;
-    p.parts[at] = Part{peak, sum};
+    p.parts[at] = Part{peak, rest};
     p.folds[at] = folded;
   }
   return true;
@@ -711,23 +728,23 @@ __device__ __forceinline__ bool drain_thin_score(const Params& P, int first, int
       for (int k = 0; k < 32; ++k)
         if (b * 32 + k < p.tokens) z[k * p.ld_z] = v[k];
     }
+    // By way of shared memory each lane gets its own token's 32 entries, and folds them as a row of the other form (three
+    // reductions over the lanes took longer: 128 tokens x 262144 x 256 64 us, this way 60).
     const int64_t t = b * 32 + lane;
-    wanted_of_tokens<false>(p, t, c[i], first, end, v, sm, lane,
-                            [&](float& x, float, float, int, bool) { x = -INFINITY; });
-    const float peak = columns(v, lane, [](float x, float y) { return fmaxf(x, y); });
-    const float from = peak == -INFINITY ? 0.f : peak;
-    float f[32];
+    __syncwarp();  // the block before has been read
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      const float d = v[k] - __shfl_sync(0xffffffffu, from, k);
-      v[k] = ex2(d * kLog2e);
-      f[k] = v[k] * fmaxf(d, -1e4f);
-    }
-    const float sum = columns(v, lane, [](float x, float y) { return x + y; });
-    const float folded = columns(f, lane, [](float x, float y) { return x + y; });
+    for (int k = 0; k < 32; ++k) cell(sm, k, lane) = v[k];
+    __syncwarp();
+    walk<false>(p, t, c[i], first, end, sm, lane, [&](float& x, float, float, int, bool) { x = -INFINITY; });
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = cell(sm, lane, k);
+    const float peak = largest(v), from = peak == -INFINITY ? 0.f : peak;
+    float rest, ones, folded;
+    fold(v, from, rest, ones, folded);
+    if (peak > -INFINITY) rest += ones - 1.f;  // one is the peak's own
     if (t < p.tokens) {
       const int64_t at = t * p.groups + p.group0 + group;
-      p.parts[at] = Part{peak, sum};
+      p.parts[at] = Part{peak, rest};
       p.folds[at] = folded;
     }
   }

@@ -1,7 +1,9 @@
 // head_score.cuh - a token's log probability, entropy and log sum from its groups' sums.
 //
 // Groups' sums are joined with the entropy's beside them: of sum = sum exp(z - peak) and
-// folded = sum exp(z - peak) (z - peak), the entropy is log(sum) - folded / sum, both terms positive. The target's
+// folded = sum exp(z - peak) (z - peak), the entropy is log(sum) - folded / sum, both terms positive. The peak's own 1 is
+// left out of sum throughout (rest = sum - 1, and log(sum) is log1p(rest)): where one entry is nearly sure, all digits of
+// the entropy are the others'. (With it inside, one entry 18 above 499 others was off by 2e-4.) The target's
 // share comes apart from the others', so that a sure token's log probability and entropy keep their digits: of those,
 // the relative error is the absolute one of the target's logit less the others' peak, which in fp32 is 1e-6 at 16 to
 // 32. So that logit has twice the digits, and of the distance a second part is kept. (24 single tokens x 123366 x 1120
@@ -17,19 +19,20 @@ namespace dmuon {
 namespace head {
 
 struct Folded {
-  float peak = -INFINITY, sum = 0.f, fold = 0.f;
+  float peak = -INFINITY, rest = 0.f, fold = 0.f;  // (without a peak rest is 0, or NaN to pass on)
   // exp(-infinity) times a distance of -infinity is nothing
   static __device__ __forceinline__ float finite(float d) { return fmaxf(d, -1e4f); }
-  __device__ __forceinline__ void join(float peak2, float sum2, float fold2) {
+  __device__ __forceinline__ void join(float peak2, float rest2, float fold2) {
     const float m = fmaxf(peak, peak2);
-    if (!(m > -INFINITY)) {  // neither has a number: zeros, or NaN to pass on
-      sum += sum2;
+    if (!(m > -INFINITY)) {  // neither has a number
+      rest += rest2;
       fold += fold2;
       return;
     }
-    const float a = peak - m, b = peak2 - m, ea = expf(a), eb = expf(b);
-    fold = ea * fmaf(sum, finite(a), fold) + eb * fmaf(sum2, finite(b), fold2);
-    sum = sum * ea + sum2 * eb;
+    const float a = peak - m, b = peak2 - m, ea = expf(a), eb = expf(b), all = 1.f + rest, all2 = 1.f + rest2;
+    fold = ea * fmaf(all, finite(a), fold) + eb * fmaf(all2, finite(b), fold2);
+    if (a == 0.f) rest = rest + (b == 0.f ? all2 : all2 * eb);
+    else rest = rest2 + all * ea;
     peak = m;
   }
 };
@@ -39,7 +42,7 @@ __device__ __forceinline__ float finite(float x) { return fabsf(x) < INFINITY ? 
 
 template <int kTokens, int kThreads>
 struct ScoreShared {
-  float peak[kThreads / 32][kTokens], sum[kThreads / 32][kTokens], fold[kThreads / 32][kTokens];
+  float peak[kThreads / 32][kTokens], rest[kThreads / 32][kTokens], fold[kThreads / 32][kTokens];
   Twice dot[kThreads / 32];
 };
 
@@ -71,24 +74,26 @@ __device__ __forceinline__ void score_rows(const ScoreParams& p, int64_t t0, int
           f.join(-INFINITY, q[0].sum + q[1].sum + q[2].sum + q[3].sum, w[0] + w[1] + w[2] + w[3]);
           continue;
         }
-        float s = 0.f, fold = 0.f;
+        float rest = 0.f, fold = 0.f;
+        int ones = -1;  // one is the peak's own
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const float d = q[u].peak - m, e = expf(d);
-          s = fmaf(q[u].sum, e, s);
-          fold = fmaf(fmaf(q[u].sum, Folded::finite(d), w[u]), e, fold);
+          const float d = q[u].peak - m, e = expf(d), all = 1.f + q[u].sum;
+          if (d == 0.f) ++ones, rest += q[u].sum;
+          else rest = fmaf(all, e, rest);
+          fold = fmaf(fmaf(all, Folded::finite(d), w[u]), e, fold);
         }
-        f.join(m, s, fold);
+        f.join(m, rest + static_cast<float>(ones), fold);
       }
     }
     for (int d = 16; d >= kTokens; d >>= 1) {
-      const float p2 = __shfl_xor_sync(0xffffffffu, f.peak, d), s2 = __shfl_xor_sync(0xffffffffu, f.sum, d),
+      const float p2 = __shfl_xor_sync(0xffffffffu, f.peak, d), s2 = __shfl_xor_sync(0xffffffffu, f.rest, d),
                   f2 = __shfl_xor_sync(0xffffffffu, f.fold, d);
       f.join(p2, s2, f2);
     }
     if (lane < kTokens) {
       sh.peak[warp][lane] = f.peak;
-      sh.sum[warp][lane] = f.sum;
+      sh.rest[warp][lane] = f.rest;
       sh.fold[warp][lane] = f.fold;
     }
   }
@@ -108,11 +113,12 @@ __device__ __forceinline__ void score_rows(const ScoreParams& p, int64_t t0, int
   const int mine = kTokens == 1 ? 0 : warp;
   if (warp >= kTokens || t >= p.tokens || lane != 0) return;
   Folded f;
-  for (int w = 0; w < kWarps; ++w) f.join(sh.peak[w][mine], sh.sum[w][mine], sh.fold[w][mine]);
+  for (int w = 0; w < kWarps; ++w) f.join(sh.peak[w][mine], sh.rest[w][mine], sh.fold[w][mine]);
   float lse, logp = 0.f, entropy;
   if (y < 0) {
-    lse = f.peak + logf(f.sum);
-    entropy = logf(f.sum) - f.fold / f.sum;
+    const float log_sum = log1pf(f.rest);
+    lse = f.peak + log_sum;
+    entropy = f.peak > -INFINITY ? log_sum - f.fold / (1.f + f.rest) : NAN;
   } else {
     if (kTokens == 1)
       for (int w = 1; w < kWarps; ++w) dot.add(sh.dot[w]);
@@ -122,16 +128,16 @@ __device__ __forceinline__ void score_rows(const ScoreParams& p, int64_t t0, int
     Twice distance = {f.peak, 0.f};
     distance.add(-z);
     const float d = distance.sum, low = finite(distance.rest - rest);
-    const float e = expf(d) * (1.f + low), ratio = f.sum * e;  // the others' share to the target's
+    const float e = expf(d) * (1.f + low), others = 1.f + f.rest, ratio = others * e;  // their share to the target's
     if (ratio < 1.f) {
       logp = -log1pf(ratio);
       lse = z + (rest - logp);
-      entropy = -logp - e * fmaf(f.sum, Folded::finite(d), f.fold) / (1.f + ratio);
+      entropy = -logp - e * fmaf(others, Folded::finite(d), f.fold) / (1.f + ratio);
     } else {
-      const float hit = expf(-d) * (1.f - low), all = f.sum + hit, log_sum = logf(all);
+      const float hit = expf(-d) * (1.f - low), rest = f.rest + hit, log_sum = log1pf(rest);
       lse = f.peak + log_sum;
       logp = -(d + (low + log_sum));
-      entropy = log_sum - fmaf(hit, Folded::finite(-d), f.fold) / all;
+      entropy = log_sum - fmaf(hit, Folded::finite(-d), f.fold) / (1.f + rest);
     }
   }
   p.lse[t] = lse;
