@@ -622,8 +622,12 @@ dmuon_status dmuon_head_distill_backward(dmuon_head_t head, const void* hidden, 
  * with any nearly sure entry keep their leading digits (other entries' log
  * probabilities are off by about 1e-6 of their logit). Neighbours among the top
  * entries that are too near to tell in fp32 are put in order by sums with twice its
- * digits. A row whose logits are not finite has unspecified top entries (ids
- * within the vocabulary or -1).
+ * digits: those nearer than what the tensor cores' sums may be off by, which goes by
+ * the products' absolute values (|hidden| . |weight|, of the target or, without one,
+ * of some entry; others' rows may have twice as much). `top` + 8 entries are looked
+ * at: where more than eight others lie within that of the last one, which of them is
+ * among the top is the tensor cores' choice. A row whose logits are not finite has
+ * unspecified top entries (ids within the vocabulary or -1).
  * Where alternatives are asked for, the logits of a piece of the vocabulary lie in
  * the workspace at a time (see dmuon_head_scores_workspace_bytes; in the smallest
  * workspace of a head for more than 2^19 tokens there is room for 2^19 at a time, and

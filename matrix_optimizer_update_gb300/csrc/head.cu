@@ -331,6 +331,7 @@ dmuon_status score(dmuon_head_t H, const void* hidden, int64_t ld_hidden, const 
   r.group_step = thin ? 1 : tokens;
   r.scale = 1.f / temperature;
   r.scale_low = static_cast<float>(1.0 / static_cast<double>(temperature) - static_cast<double>(r.scale));
+  r.sizes = top > 0 ? reinterpret_cast<float*>(H->ws + H->off_picked) : nullptr;  // a place of the losses' own
   r.logp = logp;
   r.entropy = entropy;
   r.lse = lse;
@@ -347,6 +348,7 @@ dmuon_status score(dmuon_head_t H, const void* hidden, int64_t ld_hidden, const 
   q.targets = targets;
   q.lse = lse;
   q.logp = logp;
+  q.sizes = r.sizes;
   q.dot = p.in;
   q.top_ids = top_ids;
   q.top_logp = top_logp;

@@ -158,6 +158,7 @@ struct ScoreParams {
   int64_t token_step, group_step;
   int32_t groups;
   float scale, scale_low;  // 1 / temperature, and what fp32 leaves of it
+  float* sizes;            // [tokens]: |hidden| |weight|^T / temperature at the target, or at some entry; or nullptr
   float* logp;
   float* entropy;
   float* lse;
@@ -188,6 +189,7 @@ struct TopParams {
   // last
   const float* lse;
   const float* logp;
+  const float* sizes;      // as ScoreParams
   DotParams dot;
   int64_t* top_ids;        // [tokens][top]
   float* top_logp;

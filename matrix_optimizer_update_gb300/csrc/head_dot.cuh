@@ -79,11 +79,18 @@ __device__ __forceinline__ Twice warp_sum(Twice v) {
 }
 
 // One thread's part of a logit with twice fp32's digits: products of bf16 are exact in fp32, their sums are compensated.
-// FLIGHT rounds of loads are in flight, as the trip to memory is what it takes.
-template <int FLIGHT>
-__device__ __forceinline__ Twice exact_part(const DotParams& d, int64_t t, int64_t v, int at, int of) {
+// FLIGHT rounds of loads are in flight, as the trip to memory is what it takes. With SIZE, size gets the sum of the
+// products' absolute values, too.
+template <int FLIGHT, bool SIZE = false>
+__device__ __forceinline__ Twice exact_part(const DotParams& d, int64_t t, int64_t v, int at, int of,
+                                            float* size = nullptr) {
   Twice s = {0.f, 0.f};
+  float all = 0.f;
   const bf16 *h = d.hidden + t * d.ld_hidden, *w = d.weight + v * d.ld_weight;
+  auto add = [&](float product) {
+    s.add(product);
+    if (SIZE) all += fabsf(product);
+  };
   const int whole = d.dim / 8;
   for (int c0 = at; c0 < whole; c0 += FLIGHT * of) {
     uint4 a[FLIGHT], b[FLIGHT];
@@ -100,12 +107,13 @@ __device__ __forceinline__ Twice exact_part(const DotParams& d, int64_t t, int64
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 f = __bfloat1622float2(x[k]), g = __bfloat1622float2(y[k]);
-        s.add(f.x * g.x);
-        s.add(f.y * g.y);
+        add(f.x * g.x);
+        add(f.y * g.y);
       }
     }
   }
-  for (int k = 8 * whole + at; k < d.dim; k += of) s.add(__bfloat162float(h[k]) * __bfloat162float(w[k]));
+  for (int k = 8 * whole + at; k < d.dim; k += of) add(__bfloat162float(h[k]) * __bfloat162float(w[k]));
+  if (SIZE) *size = all;
   return s;
 }
 

@@ -44,6 +44,7 @@ template <int kTokens, int kThreads>
 struct ScoreShared {
   float peak[kThreads / 32][kTokens], rest[kThreads / 32][kTokens], fold[kThreads / 32][kTokens];
   Twice dot[kThreads / 32];
+  float size[kThreads / 32];
 };
 
 // kTokens tokens from t0 on (1 or 8) by kThreads threads, `thread` among them; `sync` is their barrier.
@@ -100,15 +101,26 @@ __device__ __forceinline__ void score_rows(const ScoreParams& p, int64_t t0, int
   // from here a warp per token
   const int64_t t = t0 + (kTokens == 1 ? 0 : warp);
   Twice dot = {0.f, 0.f};
+  float size = 0.f;  // the sum of the products' absolute values
   int64_t y = -1;
-  if (p.targets != nullptr && t < p.tokens) {
-    y = p.targets[t];
-    if (y >= p.vocab) y = -1;
+  if (t < p.tokens) {
+    if (p.targets != nullptr) {
+      y = p.targets[t];
+      if (y >= p.vocab) y = -1;
+    }
+    // where sizes are asked for, a token without a target has those of some entry
+    const int64_t v = y >= 0 || p.sizes == nullptr ? y : t % p.vocab;
     // (two rounds are all of 4096 dims for a block, and less code to fetch for one token: 0.4 us)
-    if (y >= 0)
-      dot = warp_sum(kTokens == 1 ? exact_part<2>(p.dot, t, y, thread, kThreads) : exact_part<4>(p.dot, t, y, lane, 32));
+    if (v >= 0) {
+      dot = warp_sum(kTokens == 1 ? exact_part<2, true>(p.dot, t, v, thread, kThreads, &size)
+                                  : exact_part<4, true>(p.dot, t, v, lane, 32, &size));
+      size = warp_sum(size);
+    }
   }
-  if (lane == 0) sh.dot[warp] = dot;
+  if (lane == 0) {
+    sh.dot[warp] = dot;
+    sh.size[warp] = size;
+  }
   sync();
   const int mine = kTokens == 1 ? 0 : warp;
   if (warp >= kTokens || t >= p.tokens || lane != 0) return;
@@ -139,6 +151,11 @@ __device__ __forceinline__ void score_rows(const ScoreParams& p, int64_t t0, int
       logp = -(d + (low + log_sum));
       entropy = log_sum - fmaf(hit, Folded::finite(-d), f.fold) / (1.f + rest);
     }
+  }
+  if (p.sizes != nullptr) {
+    if (kTokens == 1)
+      for (int w = 1; w < kWarps; ++w) size += sh.size[w];
+    p.sizes[t] = size * p.scale;
   }
   p.lse[t] = lse;
   p.logp[t] = logp;

@@ -112,11 +112,12 @@ struct Order {
   __device__ __forceinline__ int id(int i) const { return static_cast<int>(~static_cast<uint32_t>(sorted[i])); }
 
   // The places whose entry is surely below the one before, as bits; by one warp.
-  __device__ __forceinline__ uint64_t starts(const TopParams& p, int lane) const {
+  __device__ __forceinline__ uint64_t starts(const TopParams& p, int64_t t, int lane) const {
     // What two products may be off by against each other: at most 2.2e-9 * dim of the largest partial sum of each, which
-    // is their logit and some standard deviations of the rest; twice that (at 4096 dims 5e-4 at a logit of 12), and
-    // no less than what fp32 sums of 512 terms have.
-    const float part = 6e-9f * fmaxf(512.f, static_cast<float>(p.dot.dim));
+    // is at most half of the products' absolute values and of the logit. Those are known of one entry, the target where
+    // there is one; the others' rows may have twice as much. And no less than 8 / temperature and the logit, twice
+    // over, and what fp32 sums of 512 terms have. (At 4096 dims of order 1 and weights of 0.02 1.2e-3 at a logit of 12.)
+    const float dim = fmaxf(512.f, static_cast<float>(p.dot.dim)), size = p.sizes[t];
     uint64_t bits = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -124,7 +125,8 @@ struct Order {
       bool apart = true;
       if (i > 0 && i < keep) {
         const float a = z(i - 1), b = z(i);
-        apart = a - b > part * (8.f * p.dot.scale + fabsf(a));
+        apart = a - b > dim * fmaxf(6e-9f * (8.f * p.dot.scale + fabsf(a)), 4.4e-9f * (size + fabsf(a))) &&
+                size < INFINITY;
       }
       bits |= static_cast<uint64_t>(__ballot_sync(0xffffffffu, apart)) << (32 * h);
     }
@@ -331,7 +333,7 @@ __device__ __forceinline__ void top_of(const TopParams& p, int64_t t, int lane, 
     }
     return;
   }
-  const uint64_t starts = o.starts(p, lane);
+  const uint64_t starts = o.starts(p, t, lane);
   o.exact_dots(p, t, starts, 0, 1, lane);
   __syncwarp();
   o.results(p, t, y, starts, lane, 32);
@@ -534,16 +536,15 @@ __device__ __forceinline__ void find(const TopParams& p, int64_t t, FindShared& 
     for (int j = 0; j < n; ++j) place += sh.cand[j] > mine;
     if (place < keep) sh.sorted[place] = mine;
   }
-  find_sync();
+  __syncthreads();  // and the joined sums are there
   const Order o = {sh.sorted, sh.exact, keep, p.top};
   if (warp == 0) {
-    const uint64_t starts = o.starts(p, lane);
+    const uint64_t starts = o.starts(p, t, lane);
     if (lane == 0) sh.starts = starts;
   }
   find_sync();
   o.exact_dots(p, t, sh.starts, warp, kTopWarps, lane);
   find_sync();
-  __syncthreads();  // the joined sums are there
   o.results(p, t, y, sh.starts, tid, kFindThreads);
 }
 
