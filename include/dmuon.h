@@ -606,7 +606,8 @@ dmuon_status dmuon_head_distill_backward(dmuon_head_t head, const void* hidden, 
  *   logp[t]    = zt[t][targets[t]] - lse[t]
  *   entropy[t] = - sum_v p log p,  p[t][v] = exp(zt[t][v] - lse[t])
  *   top_ids[t], top_logp[t]: the entries with the `top` largest z, largest first (of
- *                equal ones the lowest id first), and their log probabilities
+ *                equal ones the lowest id first), and their log probabilities, which
+ *                never rise along them; the target's is logp[t]
  *
  *  targets   device, tokens int64, or NULL: none is given. A target outside
  *            0..vocab-1 has the log probability 0; the rest of its token's

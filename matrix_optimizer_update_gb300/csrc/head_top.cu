@@ -41,6 +41,9 @@ __device__ __forceinline__ uint64_t order_of(double v) {
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v));
   return (u >> 63) != 0 ? ~u : u | (uint64_t(1) << 63);
 }
+__device__ __forceinline__ double value_of(uint64_t k) {
+  return __longlong_as_double(static_cast<long long>((k >> 63) != 0 ? k & ~(uint64_t(1) << 63) : ~k));
+}
 
 // An entry as a number that is the larger the earlier it comes: by logit, then by id from the lowest.
 __device__ __forceinline__ uint64_t candidate(float z, int id) {
@@ -51,6 +54,8 @@ struct TopShared {
   uint64_t cand[kCandidates];     // (logit, ~id)
   uint64_t sorted[kHeld];
   uint64_t exact[kHeld];
+  int ids[kMaxAlternatives];      // the results
+  float values[kMaxAlternatives];
   int wanted[kHeld];              // groups
 };
 
@@ -154,26 +159,47 @@ struct Order {
       }
     }
   }
-  __device__ __forceinline__ void results(const TopParams& p, int64_t t, int64_t y, uint64_t starts, int thread,
-                                          int threads) const {
+  // The results, by one warp; ids and values are its shared memory. What entries of a run have is formed from their exact
+  // logits, and values follow their order to the last digit: lse and the target's log probability are rounded by themselves.
+  __device__ __forceinline__ void results(const TopParams& p, int64_t t, int64_t y, uint64_t starts, int* ids, float* values,
+                                          int lane) const {
     const float lse = p.lse[t], logp = p.logp[t];
-    for (int i = thread; i < keep; i += threads) {
+    if (lane < top) {  // fewer entries than asked for: not finite
+      ids[lane] = -1;
+      values[lane] = -INFINITY;
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int i = lane; i < keep; i += 32) {
       int place = i;
       const int mine = id(i);
+      float value = z(i) - lse;
       if (shared(starts, i)) {
         const int begin = run(starts, i);
         place = begin;
         for (int j = begin; j < keep && run(starts, j) == begin; ++j)
           place += dots[j] > dots[i] || (dots[j] == dots[i] && id(j) < mine);
+        value = static_cast<float>(value_of(dots[i]) * p.dot.scale - lse);
       }
       if (place < top) {
-        p.top_ids[t * top + place] = mine;
-        p.top_logp[t * top + place] = mine == y ? logp : z(i) - lse;
+        ids[place] = mine;
+        values[place] = mine == y ? logp : value;
       }
     }
-    for (int i = keep + thread; i < top; i += threads) {  // fewer entries than asked for: not finite
-      p.top_ids[t * top + i] = -1;
-      p.top_logp[t * top + i] = -INFINITY;
+    __syncwarp();
+    const bool in = lane < top;
+    const int mine = in ? ids[lane] : -1;
+    float value = in ? values[lane] : 0.f;
+    const unsigned hit = __ballot_sync(0xffffffffu, in && y >= 0 && mine == y);
+    const float pivot = __shfl_sync(0xffffffffu, value, hit != 0u ? __ffs(hit) - 1 : 0);
+    if (hit != 0u && mine >= 0) value = (1u << lane) < hit ? fmaxf(value, pivot) : fminf(value, pivot);
+    for (int d = 1; d < 32; d <<= 1) {
+      const float before = __shfl_up_sync(0xffffffffu, value, d);
+      if (lane >= d) value = fminf(value, before);
+    }
+    if (in) {
+      p.top_ids[t * top + lane] = mine;
+      p.top_logp[t * top + lane] = value;
     }
   }
 };
@@ -336,7 +362,7 @@ __device__ __forceinline__ void top_of(const TopParams& p, int64_t t, int lane, 
   const uint64_t starts = o.starts(p, t, lane);
   o.exact_dots(p, t, starts, 0, 1, lane);
   __syncwarp();
-  o.results(p, t, y, starts, lane, 32);
+  o.results(p, t, y, starts, sh.ids, sh.values, lane);
 }
 
 template <int KEYS>
@@ -377,6 +403,8 @@ struct FindShared {
   uint64_t cand[kFewCandidates];
   uint64_t sorted[kHeld], exact[kHeld];
   uint64_t starts;
+  int ids[kMaxAlternatives];
+  float values[kMaxAlternatives];
 };
 
 __device__ __forceinline__ void find_sync() { asm volatile("bar.sync 2, 256;" ::: "memory"); }
@@ -545,7 +573,7 @@ __device__ __forceinline__ void find(const TopParams& p, int64_t t, FindShared& 
   find_sync();
   o.exact_dots(p, t, sh.starts, warp, kTopWarps, lane);
   find_sync();
-  o.results(p, t, y, sh.starts, tid, kFindThreads);
+  if (warp == 0) o.results(p, t, y, sh.starts, sh.ids, sh.values, lane);
 }
 
 template <Keys KEYS>
