@@ -242,9 +242,19 @@ def teacher_lists(y, vocab, top, seed=2):
     return ids, logits
 
 
+def policy_loss(logp, entropy, right, counts, bonus):
+    """The loss whose gradient makes choices that were right more likely, by how much better they did than the tokens
+    that count did on average, with a bonus for entropy; and that average."""
+    n = counts.sum().clamp(min=1)
+    right = (right & counts).float()
+    average = right.sum() / n
+    advantage = torch.where(counts, right - average, 0.0)
+    return -(advantage * logp + bonus * torch.where(counts, entropy, 0.0)).sum() / n, average
+
+
 def reinforce(steps=60, tokens=512, vocab=1000, warm=15, bonus=0.01, max_norm=1.0, log=print):
     """Learn from the model's own choices, after ``warm`` steps of cross entropy that make some of them right; returns
-    how many were, step by step."""
+    what part of those that count were, step by step."""
     model = Model(vocab=vocab, max_tokens=tokens)
     g = torch.Generator(device="cuda")
     g.manual_seed(3)
@@ -254,16 +264,16 @@ def reinforce(steps=60, tokens=512, vocab=1000, warm=15, bonus=0.01, max_norm=1.
         (model.losses(x, y).sum() / (y >= 0).sum()).backward()
         model.step(max_norm=max_norm)
     for i, (x, y) in zip(range(steps), data):
+        counts = y >= 0
         chosen = model.choose(x, generator=g)
-        chosen = torch.where(y < 0, y, chosen)  # tokens that do not count have no choice
-        right = (chosen == y).float() * (y >= 0)
+        chosen = torch.where(counts, chosen, y)  # tokens that do not count have no choice
         logp, entropy = model.policy(x, chosen)
-        advantage = torch.where(y >= 0, right - right.mean(), 0.0)
-        (-(advantage * logp).sum() / tokens - bonus * entropy.mean()).backward()
+        loss, average = policy_loss(logp, entropy, chosen == y, counts, bonus)
+        loss.backward()
         norm = model.step(max_norm=max_norm)
-        history.append(float(right.mean()))
+        history.append(float(average))
         if log and (i % 10 == 0 or i == steps - 1):
-            log(f"step {i}: {100 * history[-1]:.1f} % right, entropy {float(entropy.detach().mean()):.2f}, "
+            log(f"step {i}: {100 * history[-1]:.1f} % right, entropy {float(entropy.detach()[counts].mean()):.2f}, "
                 f"gradient norm {float(norm):.3f}")
     return history
 
