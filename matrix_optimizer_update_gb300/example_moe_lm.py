@@ -145,7 +145,8 @@ class Model:
         self.downs = torch.stack([matrix(dim, inner, inner ** -0.5).detach() for _ in range(experts)])
         self.up = [m.detach().requires_grad_() for m in self.ups]
         self.down = [m.detach().requires_grad_() for m in self.downs]
-        self.layer = dm.Experts.create(max_tokens, top, experts, dim, inner)
+        # made for few tokens: at most 2048 assignments a call
+        self.layer = dm.Experts.create(min(max_tokens, 2048 // top), top, experts, dim, inner)
         self.clip = dm.GradClip.create()
         self.router = dm.Router.create(max_tokens, top, experts)
         self.head = dm.Head.create(max_tokens, vocab, dim, max_top=max_top)
@@ -181,7 +182,8 @@ class Model:
         """The hidden states of tokens that are generated: nothing is read back to the host, and it can be captured."""
         x = self.embedding[tokens]
         weights, ids = self.routing(x)
-        return self.norm(x + self.layer.forward(x, ids, weights.contiguous(), self.ups, self.downs))
+        parts = zip(*(t.split(self.layer.max_tokens) for t in (x, ids, weights.contiguous())))
+        return self.norm(x + torch.cat([self.layer.forward(*part, self.ups, self.downs) for part in parts]))
 
     @torch.no_grad()
     def choose(self, tokens, top=16, generator=None):
