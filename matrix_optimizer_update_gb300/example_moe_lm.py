@@ -187,9 +187,11 @@ class Model:
 
     @torch.no_grad()
     def choose(self, tokens, top=16, generator=None):
-        """A next token for each token, one of the ``top`` likeliest by its probability among them."""
+        """A next token for each token, one of the ``top`` likeliest by its probability among them; anything, or -1,
+        where the logits are not finite."""
         scores = self.head.logprobs(self.serve(tokens), self.head_weight, top=top)
-        pick = torch.multinomial(scores.top_logp.exp(), 1, generator=generator)
+        # (torch ends the process on probabilities that are no numbers or all zeros)
+        pick = torch.multinomial(scores.top_logp.exp().nan_to_num(0.0, 0.0, 0.0) + 1e-30, 1, generator=generator)
         return scores.top_ids.gather(1, pick)[:, 0]
 
     def losses(self, tokens, targets, teacher=None, temperature=2.0):
