@@ -661,7 +661,7 @@ int64_t pitch_h(int64_t inner) { return (inner + 7) / 8 * 8; }
 
 dmuon_status check_sizes(int64_t tokens, int32_t top, int32_t experts, int64_t dim, int64_t inner) {
   if (top < 1 || top > kMaxTop) return refuse("top must be between 1 and 64");
-  if (tokens < 0 || tokens * top > kMaxAssignments || tokens > kMaxAssignments)
+  if (tokens < 0 || tokens > kMaxAssignments || tokens * top > kMaxAssignments)
     return refuse("tokens * top must be between 0 and 2048 (for more: sort, dispatch, the experts' products, combine)");
   if (experts < 1 || experts > kMaxExperts) return refuse("experts must be between 1 and 4096");
   if (dim < 1 || dim > kMaxDim || inner < 1 || inner > kMaxDim) return refuse("dim and inner must be between 1 and 2^20");
