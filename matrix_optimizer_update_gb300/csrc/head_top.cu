@@ -12,7 +12,7 @@
 // A warp per token: the search for the last of `held` peaks is a count over the warp for each bit that they differ in,
 // without a barrier. (A block per token took 105 us for 4093 tokens x 32768 entries, 15 us for one token.) What bounds
 // it is one warp's way through its instructions and trips to memory. 20 alternatives of 512 tokens, beside their log
-// probabilities alone: 20 us more with 32000 entries, 38 with 128000, of which writing the logits is 10 and 39 at the
+// probabilities alone: 23 us more with 32000 entries, 42 with 128000, of which writing the logits is 10 and 39 at the
 // copy rate; 61 tokens: 8 with 50257 entries, 15 with 128000.
 #include <algorithm>
 #include <cmath>
@@ -440,8 +440,8 @@ __device__ __forceinline__ T find_threshold(FindShared& sh, int want, int more, 
 }
 
 // Where the groups' peaks are held: up to kInRegisters to a finder in its registers, up to kInShared in all in shared
-// memory, else they are read again each time. (Read again, one token x 262144 x 256 took 64 us, 128 tokens 111; from
-// shared memory 51 and 94. 34 and 53 are the log probabilities alone.)
+// memory, else they are read again each time. (Read again, one token x 262144 x 256 took 13 us more, 128 tokens 17; from
+// shared memory 48 us and 83. 36 and 53 are the log probabilities alone.)
 enum Keys { kRead, kRegisters, kShared };
 constexpr int kInRegisters = 8;
 constexpr int kInShared = 40 * 1024;
