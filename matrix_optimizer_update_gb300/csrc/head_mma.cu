@@ -736,6 +736,7 @@ __device__ __forceinline__ bool drain_thin_score(const Params& P, int first, int
     for (int k = 0; k < 32; ++k) cell(sm, k, lane) = v[k];
     __syncwarp();
     walk<false>(p, t, c[i], first, end, sm, lane, [&](float& x, float, float, int, bool) { x = -INFINITY; });
+    __syncwarp();  // lanes with a target come later, and the next block's load wants them together
 #pragma unroll
     for (int k = 0; k < 32; ++k) v[k] = cell(sm, lane, k);
     const float peak = largest(v), from = peak == -INFINITY ? 0.f : peak;

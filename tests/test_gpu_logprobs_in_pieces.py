@@ -91,3 +91,20 @@ def test_equal_logits_over_pieces_come_by_id():
     w.copy_(w[:50].repeat(400, 1))
     best = head.logprobs(h, w, top=1).top_ids
     assert torch.equal(head.logprobs(h, w, top=32).top_ids, best + 50 * torch.arange(32, device="cuda"))
+
+
+def test_more_tokens_than_the_smallest_workspace_has_room_for():
+    # 512 MB are the logits of 2^19 tokens for 256 entries
+    h, w, y = inputs(1 << 20, 300, 8, 7)
+    small = dm.Head.create(1 << 20, 300, 8, alternatives=False)
+    with pytest.raises(dm.DmuonError) as e:
+        small.logprobs(h, w, y, top=3)
+    assert e.value.status == dm.ERR_WORKSPACE
+    with pytest.raises(dm.DmuonError):
+        small.logprobs(h[:(1 << 19) + 1], w, y[:(1 << 19) + 1], top=1)
+    half = slice(0, 1 << 19)
+    got, alone = small.logprobs(h[half], w, y[half], top=3), small.logprobs(h, w, y)
+    want = dm.Head.create(1 << 20, 300, 8).logprobs(h, w, y, top=3)
+    for name in ("logp", "entropy", "lse", "top_ids", "top_logp"):
+        assert torch.equal(getattr(got, name), getattr(want, name)[half])
+    assert torch.equal(alone.entropy, want.entropy) and torch.equal(alone.logp, want.logp)
